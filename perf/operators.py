@@ -1,0 +1,482 @@
+"""Cases of the experts' operators between dispatch and combine, with their plain forms.
+
+Five operators over the receive rows of a MoE layer, an expert's rows being
+one segment (normal mode) or one masked block (low-latency mode):
+
+* gated:     h = act(x Wg^T) * (x Wu^T), bf16 or FP8 rows and weights;
+* gated_bwd: its gradients dx and dw from the saved pre-activations and dh;
+* linear:    y = act(x W^T + bias) + residual, bf16 or FP8;
+* linear_bwd: its gradients dx, dw and dbias;
+* combine_bwd: the gradients of the top-k weighted sum, dy (per receive row)
+  and dweights (per token and k).
+
+``run`` computes a case in plain torch operations (32 bits throughout, the
+experts as one padded batch of products), or, where ``own`` is true, makes
+the library's calls.  Rows that belong to no expert are zero beforehand and
+stay so.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+
+
+def listed():
+    return [
+        # prompt processing at the framework's prefill width (hidden 7168, top-8): one
+        # rank's 64 experts, 2,048 rows each on average, gate and up in one product
+        dict(name="gated_prefill", op="gated", mode="normal", fp8=False, ranks=8, tokens=2048,
+             topk=8, experts=64, cin=7168, inner=2048, act="silu", train=False, skew=0.4,
+             masked=0.0),
+        # the low-latency decode step: 8 x 128 tokens over 256 experts, FP8 rows with fp32
+        # scales and FP8 weights, 32 rows an expert: bound by reading the weights
+        dict(name="gated_decode_fp8", op="gated", mode="ll", fp8=True, ue8m0=False, ranks=8,
+             tokens=128, topk=8, experts=256, cin=7168, inner=2048, act="silu", train=False, skew=0.2,
+             masked=0.0),
+        # a single token of a small model: eight rows over eight of 64 experts, latency
+        dict(name="gated_token", op="gated", mode="ll", fp8=False, ranks=1, tokens=1, topk=8,
+             experts=64, cin=2048, inner=768, act="silu", train=False, skew=0.0, masked=0.0),
+        # a training step's gradients, hidden 4096, 11 x 128 inner channels, some masked entries
+        dict(name="gated_bwd_train", op="gated_bwd", mode="normal", fp8=False, ranks=16,
+             tokens=512, topk=8, experts=32, cin=4096, inner=1408, act="silu", skew=0.4,
+             masked=0.05),
+        # odd sizes: 148 entries over 8 experts, widths that no tile divides
+        dict(name="gated_bwd_odd", op="gated_bwd", mode="normal", fp8=False, ranks=2, tokens=37,
+             topk=2, experts=8, cin=648, inner=360, act="gelu", skew=0.5, masked=0.1),
+        # the down projection of the prefill case, with the row itself as its residual
+        dict(name="linear_prefill", op="linear", mode="normal", fp8=False, ranks=8, tokens=2048,
+             topk=8, experts=64, cin=2048, inner=7168, act="none", bias=False, residual=True,
+             train=False, skew=0.4, masked=0.0),
+        # the down projection of the decode case, its rows with power-of-two scales
+        dict(name="linear_decode_fp8", op="linear", mode="ll", fp8=True, ue8m0=True, ranks=8,
+             tokens=128, topk=8, experts=256, cin=2048, inner=7168, act="none", bias=False, residual=False,
+             train=False, skew=0.2, masked=0.0),
+        # a dense layer (one expert that every token goes to): bias, activation and residual
+        dict(name="linear_dense", op="linear", mode="normal", fp8=False, ranks=1, tokens=8192,
+             topk=1, experts=1, cin=4096, inner=4096, act="gelu", bias=True, residual=True,
+             train=True, skew=0.0, masked=0.0),
+        # the down projection's gradients in the training step
+        dict(name="linear_bwd_train", op="linear_bwd", mode="normal", fp8=False, ranks=16,
+             tokens=512, topk=8, experts=32, cin=1408, inner=4096, act="none", bias=False,
+             skew=0.4, masked=0.05),
+        # a small layer with bias and activation, ragged, masked blocks
+        dict(name="linear_bwd_odd", op="linear_bwd", mode="ll", fp8=False, ranks=3, tokens=61,
+             topk=3, experts=6, cin=328, inner=520, act="silu", bias=True, skew=0.5, masked=0.1),
+        # the prefill combine, backwards: 262,144 rows of 7168 channels read and written
+        dict(name="combine_bwd_prefill", op="combine_bwd", mode="normal", ranks=8, tokens=4096,
+             topk=8, experts=256, cin=7168, skew=0.4, masked=0.0),
+        # a small ragged one, a third of the entries masked (tokens without any among them)
+        dict(name="combine_bwd_odd", op="combine_bwd", mode="ll", ranks=3, tokens=13, topk=2,
+             experts=9, cin=264, skew=0.5, masked=0.35),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    c = dict(op=rng.choice(["gated", "gated", "gated_bwd", "linear", "linear", "linear_bwd",
+                            "combine_bwd"]), mode=rng.choice(["normal", "ll"]))
+    c["fp8"] = c["op"] in ("gated", "linear") and rng.random() < 0.4
+    if c["fp8"]:
+        c["ue8m0"] = rng.random() < 0.5
+    step = 128 if c["fp8"] else 8
+    c["ranks"] = rng.choice([1, 2, 3, 4, 8])
+    c["experts"] = c["ranks"] * _log(rng, 1, 256 // c["ranks"])
+    c["topk"] = min(c["experts"], rng.choice([1, 2, 3, 4, 6, 8]))
+    c["tokens"] = max(1, _log(rng, 1, 16384) // c["ranks"])
+    c["cin"] = step * _log(rng, max(1, 256 // step), 7168 // step)
+    if c["op"] != "combine_bwd":
+        c["inner"] = step * _log(rng, max(1, 256 // step), 4096 // step)
+        c["act"] = rng.choice(["silu", "gelu", "relu", "none"])
+    if c["op"] in ("linear", "linear_bwd"):
+        c["bias"] = rng.random() < 0.5
+    if c["op"] == "linear":
+        c["residual"] = rng.random() < 0.5
+    if c["op"] in ("gated", "linear"):
+        c["train"] = rng.random() < 0.3
+    c["skew"] = round(rng.uniform(0.0, 0.6), 2)
+    c["masked"] = rng.choice([0.0, 0.0, 0.1, 0.3])
+
+    def cost(q):
+        n = q["ranks"] * q["tokens"]
+        rows = n * q["topk"] if q["mode"] == "normal" else n * q["experts"]
+        wide = q["cin"] + 3 * q.get("inner", 0)
+        weights = 2.0 * q["experts"] * q["cin"] * q.get("inner", 0) * 2
+        return max(n * q["topk"] * q["cin"] * q.get("inner", 64) / 1.5e12, weights / 4e9,
+                   2.0 * rows * wide / 6e9)
+
+    for key, least in ("tokens", 1), ("inner", step), ("cin", step):
+        while cost(c) > 1 and c.get(key, 0) // 2 >= least:
+            c[key] = c[key] // 2 // (1 if key == "tokens" else step) * (1 if key == "tokens" else step)
+    return c
+
+
+# ---- inputs ----------------------------------------------------------------
+
+def _normal(g, shape, scale=1.0, dtype=torch.bfloat16):
+    return torch.randn(shape, generator=g, device=DEV, dtype=dtype).mul_(scale)
+
+
+def _fp8_rows(g, mode, rows, c, block_rows, ue8m0):
+    """e4m3 codes (bytes) of N(0, 1) rows and their scales per 128 channels (fp32, or the
+    biased exponents of powers of two), column-major as dispatch stores them:
+    [c/128][rows], or a block's rows at a time."""
+    codes = torch.empty((rows, c), dtype=torch.uint8, device=DEV)
+    scales = torch.empty((rows, c // 128), device=DEV,
+                         dtype=torch.uint8 if ue8m0 else torch.float32)
+    step = max(1, (1 << 28) // c)
+    for i in range(0, rows, step):
+        v = torch.randn((min(step, rows - i), c // 128, 128), generator=g, device=DEV)
+        s = v.abs().amax(-1, keepdim=True).clamp_(min=1e-4) / 448.0
+        if ue8m0:  # rounded up to a power of two
+            part, power = torch.frexp(s)
+            power = power - (part == 0.5).int()
+            s = torch.ldexp(torch.ones_like(s), power)
+        codes[i:i + step] = (v / s).to(torch.float8_e4m3fn).view(torch.uint8).view(-1, c)
+        scales[i:i + step] = (power + 127).to(torch.uint8).squeeze(-1) if ue8m0 else s.squeeze(-1)
+    if mode == "normal":
+        return codes, scales.t().contiguous()
+    return codes, scales.view(-1, block_rows, c // 128).transpose(1, 2).contiguous()
+
+
+def _fp8_weights(g, e, n, c):
+    """e4m3 codes (bytes) and fp32 scales per 128 x 128 block of [e][n][c] weights."""
+    codes = torch.empty((e, n, c), dtype=torch.uint8, device=DEV)
+    scales = torch.empty((e, n // 128, c // 128), dtype=torch.float32, device=DEV)
+    step = max(1, (1 << 29) // (n * c))
+    for i in range(0, e, step):
+        v = torch.randn((min(step, e - i), n // 128, 128, c // 128, 128), generator=g, device=DEV)
+        v.mul_(c ** -0.5)
+        s = v.abs().amax((2, 4), keepdim=True).clamp_(min=1e-4) / 448.0
+        codes[i:i + step] = (v / s).to(torch.float8_e4m3fn).view(torch.uint8).view(-1, n, c)
+        scales[i:i + step] = s.view(-1, n // 128, c // 128)
+    return codes, scales
+
+
+def _routing(g, case):
+    """int32 [ranks][tokens][topk] distinct experts (Gumbel top-k over a drawn
+    popularity), a share of the entries masked with -1."""
+    n, e = case["ranks"] * case["tokens"], case["experts"]
+    pop = torch.randn(e, generator=g, device=DEV) * case["skew"]
+    u = torch.rand((n, e), generator=g, device=DEV).clamp_(1e-9, 1 - 1e-7)
+    t = torch.topk(pop - (-u.log()).log(), case["topk"], dim=1).indices.to(torch.int32)
+    t[torch.rand(t.shape, generator=g, device=DEV) < case["masked"]] = -1
+    return t.view(case["ranks"], case["tokens"], case["topk"])
+
+
+def prepare(case, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    e, topk = case["experts"], _routing(g, case)
+    n = case["ranks"] * case["tokens"]
+    ll = case["mode"] == "ll"
+    # the segments, as the layout lays them out: an expert's entries in (rank, token, k) order
+    flat = topk.view(-1).long()
+    order = torch.argsort(flat, stable=True)
+    order = order[int((flat < 0).sum()):]
+    counts = torch.bincount(flat[flat >= 0], minlength=e)
+    packed = torch.cumsum(counts, 0) - counts
+    starts = torch.arange(e, device=DEV) * n if ll else packed
+    within = torch.arange(order.numel(), device=DEV) - packed[flat[order]]
+    row = starts[flat[order]] + within
+    cap = e * n if ll else n * case["topk"]  # room for every entry, masked or not
+    most = max(1, int(counts.max()))
+    s = dict(case=case, topk=topk, counts=counts, starts=starts, cap=cap)
+    # the padded batch: row of slot (expert, i), and slot and row of every entry
+    slot = torch.arange(most, device=DEV)
+    s["pad"] = (starts[:, None] + torch.minimum(slot[None], (counts - 1).clamp_(min=0)[:, None]))
+    s["pad"] = s["pad"].clamp_(max=cap - 1)
+    s["valid"] = slot[None] < counts[:, None]
+    s["slot"], s["row"] = flat[order] * most + within, row
+    s["send_pos"] = torch.full_like(flat, -1)
+    s["send_pos"][order] = row
+
+    op, c, i = case["op"], case["cin"], case.get("inner", 0)
+    outs = {}
+    bf16 = dict(dtype=torch.bfloat16, device=DEV)
+    if op in ("gated", "linear"):
+        out_rows = 2 * i if op == "gated" else i
+        if case["fp8"]:
+            s["x"], s["x_scales"] = _fp8_rows(g, case["mode"], cap, c, n, case["ue8m0"])
+            s["w"], s["w_scales"] = _fp8_weights(g, e, out_rows, c)
+        else:
+            s["x"] = _normal(g, (cap, c))
+            s["w"] = _normal(g, (e, out_rows, c), c ** -0.5)
+        outs["y"] = torch.zeros((cap, i), **bf16)
+        if case["train"]:
+            outs["pre"] = torch.zeros((cap, out_rows), **bf16)
+    elif op in ("gated_bwd", "linear_bwd"):
+        out_rows = 2 * i if op == "gated_bwd" else i
+        s["x"] = _normal(g, (cap, c))
+        s["w"] = _normal(g, (e, out_rows, c), c ** -0.5)
+        s["dy"] = _normal(g, (cap, i))
+        if op == "gated_bwd" or case["act"] != "none":
+            s["pre"] = _normal(g, (cap, out_rows))
+            s["dpre"] = torch.zeros((cap, out_rows), **bf16)
+        outs["dx"] = torch.zeros((cap, c), **bf16)
+        outs["dw"] = torch.zeros((e, out_rows, c), **bf16)
+    else:
+        s["y"] = _normal(g, (cap, c))
+        s["dout"] = _normal(g, (n, c))
+        s["weights"] = torch.softmax(_normal(g, (n, case["topk"]), 1.0, torch.float32), -1)
+        outs["dy"] = torch.zeros((cap, c), **bf16)
+        outs["dweights"] = torch.zeros((n, case["topk"]), dtype=torch.float32, device=DEV)
+    if case.get("bias"):
+        s["bias"] = _normal(g, (e, i), 1.0, torch.float32)
+        if op == "linear_bwd":
+            outs["dbias"] = torch.zeros((e, i), dtype=torch.float32, device=DEV)
+    if case.get("residual"):
+        s["residual"] = _normal(g, (cap, i))
+    if own:
+        s["outs"] = outs
+        s["call"] = _call(s, outs)
+    return s
+
+
+def _call(s, outs):
+    """The library's layout of the routing, and the case's call on it."""
+    from combine_ep_get_layout_amd import ep
+
+    case = s["case"]
+    p = ep.Problem(case["ranks"], case["tokens"], case["cin"], case["experts"], case["topk"],
+                   mode=ep.MODE_LOW_LATENCY if case["mode"] == "ll" else ep.MODE_NORMAL,
+                   quant=(ep.QUANT_NONE if not case.get("fp8") else
+                          ep.QUANT_FP8_UE8M0 if case["ue8m0"] else ep.QUANT_FP8_F32))
+    layout = ep.Layout(p)
+    ep.get_layout(p, s["topk"], layout, ep.workspace(p))
+    op = case["op"]
+    act = getattr(ep, "ACT_" + case["act"].upper()) if "act" in case else None
+    if op == "gated":
+        return ep.prepare(ep.expert_gated, p, layout, s["x"], s["w"], outs["y"], act=act,
+                          x_scales=s.get("x_scales"), w_scales=s.get("w_scales"),
+                          pre=outs.get("pre"))
+    if op == "linear":
+        return ep.prepare(ep.expert_linear, p, layout, s["x"], s["w"], outs["y"], act=act,
+                          bias=s.get("bias"), residual=s.get("residual"),
+                          x_scales=s.get("x_scales"), w_scales=s.get("w_scales"),
+                          pre=outs.get("pre"))
+    if op == "gated_bwd":
+        return ep.prepare(ep.expert_gated_backward, p, layout, s["x"], s["w"], s["pre"], s["dy"],
+                          dpre=s["dpre"], dx=outs["dx"], dw=outs["dw"], act=act)
+    if op == "linear_bwd":
+        return ep.prepare(ep.expert_linear_backward, p, layout, s["x"], s["w"], s["dy"],
+                          pre=s.get("pre"), dpre=s.get("dpre"), dx=outs["dx"], dw=outs["dw"],
+                          dbias=outs.get("dbias"), act=act)
+    return ep.prepare(ep.combine_backward, p, layout, s["dout"], s["weights"], s["y"],
+                      dy=outs["dy"], dweights=outs["dweights"])
+
+
+# ---- the plain forms --------------------------------------------------------
+
+def _act(name, v):
+    if name == "silu":
+        return v * torch.sigmoid(v)
+    if name == "gelu":
+        return 0.5 * v * (1.0 + torch.erf(v * 0.5 ** 0.5))
+    return v.clamp(min=0) if name == "relu" else v
+
+
+def _act_grad(name, v):
+    if name == "silu":
+        t = torch.sigmoid(v)
+        return t * (1.0 + v * (1.0 - t))
+    if name == "gelu":
+        return (0.5 * (1.0 + torch.erf(v * 0.5 ** 0.5))
+                + v * torch.exp(-0.5 * v * v) * (2.0 * math.pi) ** -0.5)
+    return (v > 0).to(v.dtype) if name == "relu" else torch.ones_like(v)
+
+
+def _padded(s, rows):
+    """[experts][most rows][channels] of a row buffer in 32 bits, zero past an expert's rows."""
+    return rows[s["pad"]].float().mul_(s["valid"][:, :, None])
+
+
+def _rows(s, padded):
+    """A padded batch's rows in a bf16 row buffer, zero where no expert's row is."""
+    out = torch.zeros((s["cap"], padded.shape[2]), dtype=torch.bfloat16, device=DEV)
+    flat = padded.view(-1, padded.shape[2])
+    return out.index_copy_(0, s["row"], flat[s["slot"]].to(torch.bfloat16))
+
+
+def _inputs(s):
+    """The padded rows and the weights of a forward product in 32 bits."""
+    case = s["case"]
+    if not case["fp8"]:
+        return _padded(s, s["x"]), s["w"].float()
+    e, n, c = s["w"].shape
+    w = s["w"].view(torch.float8_e4m3fn).float().view(e, n // 128, 128, c // 128, 128)
+    w = w.mul_(s["w_scales"][:, :, None, :, None]).view(e, n, c)
+    x = s["x"].view(torch.float8_e4m3fn)[s["pad"]].float()
+    if case["mode"] == "ll":
+        scales = s["x_scales"].transpose(1, 2).reshape(-1, c // 128)
+    else:
+        scales = s["x_scales"].t()
+    if case["ue8m0"]:
+        scales = torch.ldexp(torch.ones((), device=DEV), scales.int() - 127)
+    x.view(*x.shape[:2], c // 128, 128).mul_(scales[s["pad"]][..., None])
+    return x.mul_(s["valid"][:, :, None]), w
+
+
+def _plain(s):
+    case = s["case"]
+    op, act = case["op"], case.get("act")
+    if op == "gated":
+        x, w = _inputs(s)
+        pre = torch.bmm(x, w.transpose(1, 2))
+        gate, up = pre.chunk(2, dim=2)
+        outs = dict(y=_rows(s, _act(act, gate) * up))
+        if case["train"]:
+            outs["pre"] = _rows(s, pre)
+        return outs
+    if op == "linear":
+        x, w = _inputs(s)
+        z = torch.bmm(x, w.transpose(1, 2))
+        if "bias" in s:
+            z = z + s["bias"][:, None, :]
+        y = _act(act, z)
+        if "residual" in s:
+            y = y + _padded(s, s["residual"])
+        outs = dict(y=_rows(s, y))
+        if case["train"]:
+            outs["pre"] = _rows(s, z)
+        return outs
+    if op in ("gated_bwd", "linear_bwd"):
+        dy = _padded(s, s["dy"])
+        if op == "gated_bwd":
+            gate, up = _padded(s, s["pre"]).chunk(2, dim=2)
+            dz = torch.cat([dy * up * _act_grad(act, gate), dy * _act(act, gate)], dim=2)
+        elif act != "none":
+            dz = dy * _act_grad(act, _padded(s, s["pre"]))
+        else:
+            dz = dy
+        outs = dict(dx=_rows(s, torch.bmm(dz, s["w"].float())),
+                    dw=torch.bmm(dz.transpose(1, 2), _padded(s, s["x"])).to(torch.bfloat16))
+        if "bias" in s:
+            outs["dbias"] = dz.sum(1)
+        return outs
+    # combine_bwd: an entry's gradient goes to its row, and its weight's is a dot product
+    pos = s["send_pos"]
+    k = case["topk"]
+    has = (pos >= 0)
+    dout = s["dout"].float()
+    each = dout[:, None, :] * s["weights"][:, :, None]
+    dy = torch.zeros((s["cap"] + 1, case["cin"]), dtype=torch.bfloat16, device=DEV)
+    dy.index_copy_(0, torch.where(has, pos, dy.shape[0] - 1),
+                   each.to(torch.bfloat16).view(-1, case["cin"]))
+    y = s["y"][pos.clamp(min=0)].view(-1, k, case["cin"]).float()
+    dw = (y * dout[:, None, :]).sum(-1) * has.view(-1, k)
+    return dict(dy=dy[:-1], dweights=dw)
+
+
+def run(s):
+    if own:
+        s["call"]()
+        return s["outs"]
+    return _plain(s)
+
+
+# ---- the definition in 64 bits, an expert at a time ---------------------------
+
+def _gate64(name, v):
+    """act(v) and its derivative."""
+    if name == "none":
+        return v, torch.ones_like(v)
+    if name == "relu":
+        return torch.relu(v), (v > 0).double()
+    if name == "silu":
+        t = 1.0 / (1.0 + torch.exp(-v))
+        return v * t, t + v * t * (1.0 - t)
+    cdf = 0.5 * torch.special.erfc(-v / math.sqrt(2.0))
+    return v * cdf, cdf + v * torch.exp(-v * v / 2.0) / math.sqrt(2.0 * math.pi)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    s.pop("call", None)
+    n = case["ranks"] * case["tokens"]
+    counts, starts = s["counts"].tolist(), s["starts"].tolist()
+    cap, c = s["cap"], case["cin"]
+    f64 = dict(dtype=torch.float64, device=DEV)
+    op = case["op"]
+    if op == "combine_bwd":
+        dy, dw = torch.zeros((cap, c), **f64), torch.zeros((n, case["topk"]), **f64)
+        pos = s["send_pos"].view(n, -1)
+        for k in range(case["topk"]):
+            t = torch.nonzero(pos[:, k] >= 0).view(-1)
+            for part in t.split(1 << 14):
+                rows, d = pos[part, k], s["dout"][part].double()
+                dy[rows] = d * s["weights"][part, k].double()[:, None]
+                dw[part, k] = torch.linalg.vecdot(d, s["y"][rows].double())
+        return dict(dy=dy, dweights=dw)
+    i, act = case["inner"], case["act"]
+    wide = 2 * i if op.startswith("gated") else i
+    forward = op in ("gated", "linear")
+    if forward:
+        outs = dict(y=torch.zeros((cap, i), **f64))
+        if case["train"]:
+            outs["pre"] = torch.zeros((cap, wide), **f64)
+    else:
+        outs = dict(dx=torch.zeros((cap, c), **f64), dw=torch.zeros((len(counts), wide, c), **f64))
+        if "bias" in s:
+            outs["dbias"] = torch.zeros((len(counts), i), **f64)
+    for e, count in enumerate(counts):
+        if count == 0:
+            continue
+        at = slice(starts[e], starts[e] + count)
+        x, w = s["x"][at], s["w"][e]
+        if forward and case["fp8"]:
+            each = s["x_scales"][:, at] if case["mode"] == "normal" else s["x_scales"][e][:, :count]
+            each = torch.exp2(each.double() - 127.0) if case["ue8m0"] else each.double()
+            x = x.view(torch.float8_e4m3fn).double() * each.t().repeat_interleave(128, 1)
+            per = s["w_scales"][e].double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+            w = w.view(torch.float8_e4m3fn).double() * per
+        x, w = x.double(), w.double()
+        if forward:
+            z = x @ w.t()
+            if "bias" in s:
+                z = z + s["bias"][e].double()
+            y = _gate64(act, z[:, :i])[0] * (z[:, i:] if op == "gated" else 1.0)
+            if "residual" in s:
+                y = y + s["residual"][at].double()
+            outs["y"][at] = y
+            if case["train"]:
+                outs["pre"][at] = z
+            continue
+        dz = s["dy"][at].double()
+        if op == "gated_bwd":
+            pre = s["pre"][at].double()
+            value, slope = _gate64(act, pre[:, :i])
+            dz = torch.cat([dz * slope * pre[:, i:], dz * value], 1)
+        elif act != "none":
+            dz = dz * _gate64(act, s["pre"][at].double())[1]
+        outs["dx"][at] = dz @ w
+        outs["dw"][e] = dz.t() @ x
+        if "bias" in s:
+            outs["dbias"][e] = dz.sum(0)
+    return outs
+
+
+# ---- what a pass cannot do without --------------------------------------------
+
+def work(case):
+    n, e, k, c = case["ranks"] * case["tokens"], case["experts"], case["topk"], case["cin"]
+    i = case.get("inner", 0)
+    rows = n * k * (1.0 - case["masked"])
+    hit = e * (1.0 - (1.0 - (1.0 - case["masked"]) * k / e) ** n)  # experts with a row
+    op = case["op"]
+    size = 1 if case.get("fp8") else 2
+    if op == "combine_bwd":
+        return dict(bytes=2.0 * n * c + 4.0 * rows * c + 12.0 * n * k, flops=3.0 * rows * c)
+    wide = 2 * i if op.startswith("gated") else i
+    if op in ("gated", "linear"):
+        out = i + (wide if case["train"] else 0) + (i if case.get("residual") else 0)
+        return dict(bytes=rows * (c * size + 2.0 * out) + hit * wide * c * size,
+                    flops=2.0 * rows * wide * c)
+    saved = wide if op == "gated_bwd" or case["act"] != "none" else 0
+    return dict(bytes=rows * 2.0 * (2 * c + i + saved) + 2.0 * (hit + e) * wide * c,
+                flops=4.0 * rows * wide * c)
