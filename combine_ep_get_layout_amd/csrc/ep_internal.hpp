@@ -176,4 +176,73 @@ struct UnpackArgs {
 
 hipError_t launch_unpack(const UnpackArgs& a, hipStream_t stream);
 
+// ---- the experts' products (experts.hpp) ----
+
+// Expert e's rows: [start, start + count) of the layout's segment (normal
+// mode) or the filled part of its block of block_rows rows (start NULL).
+struct Segments {
+  const int32_t* start;  // [E] or NULL
+  const int32_t* count;  // [E]
+  int64_t block_rows;
+  int64_t cap;           // rows every row buffer of the call holds
+  int E;
+  int32_t* err;
+};
+
+struct ExpertArgs {
+  Segments seg;
+  int64_t rows;            // most rows the segments hold together
+  bool gated;
+  int quant, act;
+  int C, N;                // channels in and out (gated: of one projection)
+  const char* x;
+  const void* x_scales;
+  int64_t x_cap;
+  const char* w;           // [E][N or 2 N][C]
+  const float* w_scales;
+  const float* bias;       // [E][N] or NULL
+  const uint16_t* residual;
+  uint16_t* pre;           // [cap][N or 2 N] or NULL
+  void* y;
+  void* y_scales;          // FP8 output
+  int64_t y_cap;
+  int y_quant;
+};
+
+hipError_t launch_expert_forward(const ExpertArgs& a, hipStream_t stream);
+
+struct GradArgs {
+  Segments seg;
+  int64_t rows;
+  bool gated;
+  int act;
+  int C, N, O;             // channels in; of dy; of dz (N, gated: 2 N)
+  const uint16_t* x;       // [cap][C]
+  const uint16_t* w;       // [E][O][C]
+  const uint16_t* pre;     // [cap][O]
+  const uint16_t* dy;      // [cap][N]
+  const uint16_t* dz;      // [cap][O]: dz_out, or dy where they are the same
+  uint16_t* dz_out;        // NULL: dz is dy
+  uint16_t* dx;            // [cap][C] or NULL
+  uint16_t* dw;            // [E][O][C] or NULL
+  float* dbias;            // [E][N] or NULL
+};
+
+hipError_t launch_expert_grad(const GradArgs& a, hipStream_t stream);
+
+struct CombineGradArgs {
+  Geometry g;
+  bool rank_major;
+  const uint16_t* dout;    // [N][H]
+  const uint16_t* y;       // [rows][H]
+  const float* w;          // [N][K]
+  const int32_t* send_pos;
+  int64_t rows;
+  uint16_t* dy;            // [rows][H] or NULL
+  float* dw;               // [N][K] or NULL
+  int32_t* err;
+};
+
+hipError_t launch_combine_grad(const CombineGradArgs& a, hipStream_t stream);
+
 }  // namespace ep

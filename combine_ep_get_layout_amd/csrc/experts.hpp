@@ -1,0 +1,588 @@
+// Shared parts of the experts' operators (gfx950): segments of receive rows,
+// the tile plan over them, LDS tiles filled by asynchronous loads, and the
+// matrix-core main loop.
+//
+// Every product is computed transposed, D[channel][row] = sum_k A[channel][k]
+// B[row][k], so that a lane ends up with four consecutive channels of one
+// row and stores them as one 8-byte vector.
+#pragma once
+
+#include "ep_device.hpp"
+#include "ep_internal.hpp"
+
+namespace ep {
+
+constexpr int kMaxExperts = 2048;
+constexpr int kCus = 256;        // compute units of an MI355X
+constexpr int kGemmThreads = 256;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+#define EP_LDS __attribute__((address_space(3)))
+typedef EP_LDS char lds_char;
+typedef EP_LDS float lds_float;
+
+// ---- activations -----------------------------------------------------------
+
+__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + __expf(-v)); }
+
+// Gaussian cumulative distribution, 0.5 erfc(-v / sqrt 2) (1 + erf would
+// cancel for negative v)
+__device__ __forceinline__ float gauss_cdf(float v) {
+  return 0.5f * erfcf(v * -0.70710678118654752f);
+}
+
+__device__ __forceinline__ float act_value(int act, float v) {
+  switch (act) {
+    case EP_ACT_RELU: return v > 0.0f ? v : (v != v ? v : 0.0f);
+    case EP_ACT_SILU: return v * sigmoid(v);
+    case EP_ACT_GELU: return v * gauss_cdf(v);
+    default: return v;
+  }
+}
+
+// act(v) and act'(v); relu's derivative at 0 is 0
+__device__ __forceinline__ void act_both(int act, float v, float& value, float& slope) {
+  switch (act) {
+    case EP_ACT_RELU:
+      value = v > 0.0f ? v : (v != v ? v : 0.0f);
+      slope = v > 0.0f ? 1.0f : 0.0f;
+      return;
+    case EP_ACT_SILU: {
+      const float t = sigmoid(v);
+      value = v * t;
+      slope = t * (1.0f + v * (1.0f - t));
+      return;
+    }
+    case EP_ACT_GELU: {
+      const float c = gauss_cdf(v);
+      value = v * c;
+      slope = c + v * __expf(-0.5f * v * v) * 0.39894228040143268f;  // 1 / sqrt(2 pi)
+      return;
+    }
+    default:
+      value = v;
+      slope = 1.0f;
+  }
+}
+
+// ---- bf16 ------------------------------------------------------------------
+
+// fp32 -> bf16, nearest even; a NaN stays one (the integer rounding of
+// f32_to_bf16_rne would carry some NaN patterns into infinity)
+__device__ __forceinline__ uint32_t bf16_of(float f) {
+  return f != f ? ((__float_as_uint(f) >> 16) | 0x40u) : f32_to_bf16_rne(f);
+}
+
+__device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
+  u32x4 o;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) o[q] = bf16_of(f[2 * q]) | (bf16_of(f[2 * q + 1]) << 16);
+  return o;
+}
+
+__device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    f[2 * q] = bf16_lo(v[q]);
+    f[2 * q + 1] = bf16_hi(v[q]);
+  }
+}
+
+// ---- segments --------------------------------------------------------------
+
+// What of a segment lies past the row buffers is left out and reported.
+__device__ __forceinline__ void segment_of(const Segments& s, int e, int64_t& start, int& count) {
+  int64_t c = s.count[e];
+  if (s.start) {
+    start = s.start[e];
+  } else {
+    start = e * s.block_rows;
+    c = min(c, s.block_rows);
+  }
+  if (c <= 0) c = 0;
+  if (c > 0 && (start < 0 || start + c > s.cap)) {
+    set_err(s.err, EP_DEVERR_CAPACITY);
+    c = start < 0 || start >= s.cap ? 0 : s.cap - start;
+  }
+  count = (int)c;
+}
+
+// ---- tile plan -------------------------------------------------------------
+
+// first[e] = tiles of `step` rows of the experts before e, first[E] = all of
+// them.  Every workgroup scans the counts itself (E <= 2048 of them, in the
+// shadow of its own start), so a call is one launch and needs no workspace.
+template <int THREADS>
+struct TilePlan {
+  int first[kMaxExperts + 1];
+  int wave_sum[THREADS / kWave];
+};
+
+template <int THREADS>
+__device__ void plan_tiles(const Segments& s, int step, TilePlan<THREADS>& p) {
+  constexpr int kPer = (kMaxExperts + THREADS - 1) / THREADS;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int per = (s.E + THREADS - 1) / THREADS;
+  int n[kPer], sum = 0;
+  for (int i = 0; i < per; ++i) {
+    const int e = tid * per + i;
+    n[i] = 0;
+    if (e < s.E) {
+      int64_t start;
+      int count;
+      segment_of(s, e, start, count);
+      n[i] = (count + step - 1) / step;
+    }
+    sum += n[i];
+  }
+  int upto = sum;  // inclusive scan over the wavefront
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int v = __shfl_up(upto, d);
+    if (lane >= d) upto += v;
+  }
+  if (lane == kWave - 1) p.wave_sum[tid / kWave] = upto;
+  __syncthreads();
+  int at = upto - sum;
+  for (int w = 0; w < tid / kWave; ++w) at += p.wave_sum[w];
+  for (int i = 0; i < per; ++i) {
+    const int e = tid * per + i;
+    if (e < s.E) p.first[e] = at;
+    at += n[i];
+  }
+  if (tid == THREADS - 1) p.first[s.E] = at;
+  __syncthreads();
+}
+
+// Expert of tile t (first[e] <= t < first[e + 1]): two steps of 64 lanes each.
+template <int THREADS>
+__device__ __forceinline__ int expert_of(const TilePlan<THREADS>& p, int E, int t) {
+  const int lane = lane_id();
+  const int stride = (E + kWave - 1) / kWave;  // <= 32
+  const int far = min((lane + 1) * stride, E);
+  const int skip = __popcll(__ballot(p.first[far] <= t));  // whole strides before t's
+  const int base = skip * stride;
+  const int near = min(base + lane + 1, E);
+  const bool pass = lane < stride && base + lane + 1 <= E && p.first[near] <= t;
+  return uniform(base + __popcll(__ballot(pass)));
+}
+
+// ---- LDS tiles -------------------------------------------------------------
+
+// A lane whose 16 bytes lie past the data reads these zeros instead.
+static __device__ const uint4 k_zeros[4] = {};
+
+// Asynchronous loads of 16 bytes a lane into LDS (lane i's at dst + 16 i of the
+// wave's dst), completed by wait_loads.  They are written as assembly (they
+// have no result register) because the compiler waits for every such load of
+// its own before the next LDS read, whichever buffer that reads.  M0 holds the
+// LDS address; nothing else in these kernels uses it.
+__device__ __forceinline__ int lds_offset(const lds_char* p) {
+  return uniform((int)(uintptr_t)p);
+}
+
+// The base is uniform and in scalar registers.  The compiler may have filled
+// those with vector instructions (v_readlane) just before, and does not look
+// into assembly for the five wait states that a vector-memory instruction
+// needs after such a write: every block begins with them.  M0 needs one more
+// after each change.
+
+// N (1, 2 or 4) loads from base + off[i] to dst + i * STEP
+template <int STEP, int N>
+__device__ __forceinline__ void load_lds16(const char* base, const uint32_t (&off)[N],
+                                           const lds_char* dst) {
+  static_assert(N == 1 || N == 2 || N == 4, "");
+  if constexpr (N == 4)
+    asm volatile(
+        "s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %5\n\t"
+        "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %5\n\t"
+        "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, %5\n\t"
+        "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, %5"
+        ::"s"(lds_offset(dst)), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(base),
+        "n"(STEP)
+        : "memory", "scc");
+  else if constexpr (N == 2)
+    asm volatile(
+        "s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
+        "s_add_u32 m0, m0, %4\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3"
+        ::"s"(lds_offset(dst)), "v"(off[0]), "v"(off[1]), "s"(base), "n"(STEP)
+        : "memory", "scc");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
+                 ::"s"(lds_offset(dst)), "v"(off[0]), "s"(base)
+                 : "memory");
+}
+
+// 4 bytes a lane, or one byte zero-extended to four
+template <bool BYTE>
+__device__ __forceinline__ void load_lds4(const char* base, uint32_t off, const lds_char* dst) {
+  if (BYTE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_ubyte %1, %2"
+                 ::"s"(lds_offset(dst)), "v"(off), "s"(base)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2"
+                 ::"s"(lds_offset(dst)), "v"(off), "s"(base)
+                 : "memory");
+}
+
+// from an address of the lane's own
+__device__ __forceinline__ void load_lds16(const char* src, const lds_char* dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               ::"s"(lds_offset(dst)), "v"(src)
+               : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Tile of ROWS rows x 128 bytes whose rows are contiguous along the
+// contraction.  An asynchronous load stores lane i's 16 bytes at the wave's
+// LDS base + 16 i, so the order in LDS is fixed and the lanes choose what
+// they fetch: slot j of row r holds chunk j ^ (r & 7).  Eight consecutive
+// rows' reads of one chunk then fall into eight different 16-byte columns,
+// which is every bank once.
+template <int ROWS>
+struct RowTile {
+  static constexpr int kBytes = ROWS * 128;
+  static constexpr int kPasses = (ROWS + 31) / 32;
+  static constexpr int kBlock = kPasses < 4 ? kPasses : 4;  // loads issued together
+  uint32_t off[kPasses / kBlock][kBlock];
+  int chunk;  // this lane's chunk of every row it fetches
+
+  // row_of(r): byte offset of tile row r from the tile's base
+  template <class F>
+  __device__ __forceinline__ void init(F row_of) {
+    const int tid = threadIdx.x;
+    chunk = (tid & 7) ^ ((tid >> 3) & 7);
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p)
+      off[p / kBlock][p % kBlock] = row_of((p * 32 + (tid >> 3)) % ROWS) + chunk * 16;
+  }
+  // base: the tile's first byte of this step; the second half of every
+  // PERIOD rows comes from `second` bytes further on (a gated block's ups)
+  template <int PERIOD>
+  __device__ __forceinline__ void load(const char* base, int64_t second, lds_char* lds) const {
+    const int wave = uniform(threadIdx.x >> 6);
+    if constexpr (PERIOD >= ROWS && PERIOD / 2 >= ROWS) {
+#pragma unroll
+      for (int b = 0; b < kPasses / kBlock; ++b)
+        load_lds16<4096>(base, off[b], lds + (b * kBlock * 4096 + wave * 1024) % kBytes);
+    } else {
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int r = p * 32 + wave * 8;  // 8 rows a wave, all in one half
+        const uint32_t one[1] = {off[p / kBlock][p % kBlock]};
+        load_lds16<0>(base + (r % PERIOD >= PERIOD / 2 ? second : 0), one,
+                      lds + p * 4096 + wave * 1024);
+      }
+    }
+  }
+  // the last step of rows with fewer than 128 bytes left
+  template <int PERIOD>
+  __device__ __forceinline__ void load_tail(const char* base, int64_t second, int left,
+                                            lds_char* lds) const {
+    const int wave = uniform(threadIdx.x >> 6);
+    const bool in = chunk * 16 < left;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const int r = (p * 32 + wave * 8) % ROWS;
+      const char* src =
+          base + (r % PERIOD >= PERIOD / 2 ? second : 0) + off[p / kBlock][p % kBlock];
+      load_lds16(in ? src : (const char*)k_zeros, lds + (p * 4096 + wave * 1024) % kBytes);
+    }
+  }
+};
+
+// 16-byte chunk c of row r
+__device__ __forceinline__ i32x4 row_chunk(const lds_char* lds, int r, int c) {
+  return *(const EP_LDS i32x4*)(lds + r * 128 + ((c ^ (r & 7)) << 4));
+}
+
+// Tile of 64 contraction rows x COLS bf16 whose rows run across the
+// contraction (the operand is read transposed).  Slot j of row k holds
+// 16-byte chunk j ^ 4 (k & 3): a transposed read takes 32 columns (64 bytes)
+// of four consecutive rows, which the exclusive-or sends to four different
+// quarters of the banks.
+template <int COLS>
+struct ColTile {
+  static constexpr int kBytes = 64 * COLS * 2;
+  static constexpr int kSlots = COLS / 8;
+  static constexpr int kPasses = kBytes / 4096;
+  static constexpr int kRowsPerPass = kGemmThreads / kSlots;
+  static_assert(COLS >= 128 && kRowsPerPass % 4 == 0, "a lane's rows agree modulo 4");
+  static_assert(kPasses % 4 == 0, "");
+  uint32_t off[kPasses / 4][4];
+  int row;  // this lane's row in pass 0
+
+  // cols: columns the operand has from the tile's first on (a multiple of 8)
+  __device__ __forceinline__ void init(uint32_t row_bytes, int cols) {
+    const int tid = threadIdx.x;
+    row = tid / kSlots;
+    const int chunk = (tid % kSlots) ^ ((row & 3) << 2);
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p)  // past the last column: columns not stored
+      off[p / 4][p % 4] = (row + p * kRowsPerPass) * row_bytes + min(chunk * 16, cols * 2 - 16);
+  }
+  __device__ __forceinline__ void load(const char* base, lds_char* lds) const {
+    const int wave = uniform(threadIdx.x >> 6);
+#pragma unroll
+    for (int b = 0; b < kPasses / 4; ++b)
+      load_lds16<4096>(base, off[b], lds + b * 16384 + wave * 1024);
+  }
+  // the last step, with fewer than 64 contraction rows left
+  __device__ __forceinline__ void load_tail(const char* base, int left, lds_char* lds) const {
+    const int wave = uniform(threadIdx.x >> 6);
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const char* src = base + off[p / 4][p % 4];
+      load_lds16(row + p * kRowsPerPass < left ? src : (const char*)k_zeros,
+                 lds + p * 4096 + wave * 1024);
+    }
+  }
+};
+
+__device__ __forceinline__ s16x4 read_tr(const lds_char* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((EP_LDS s16x4*)p);
+}
+
+// ---- operand fragments -------------------------------------------------------
+//
+// v_mfma 32x32x16 (MF = 32): lane l holds index l % 32, contraction elements
+// 8 (l / 32) .. + 7; 16x16x32 (MF = 16): index l % 16, elements 8 (l / 16) .. + 7.
+// Step kk covers contraction elements kk * 512 / MF .. of the tile's 64.
+
+template <int MF, int ROWS>
+__device__ __forceinline__ bf16x8 fragment(const RowTile<ROWS>&, const lds_char* lds, int first, int kk) {
+  const int lane = lane_id();
+  return __builtin_bit_cast(
+      bf16x8, row_chunk(lds, first + lane % MF, kk * (kWave / MF) + lane / MF));
+}
+
+// ds_read_b64_tr_b16: of each 16 lanes, lane s gives the address of four
+// columns of one row and lane i receives column i of the four rows that lanes
+// i / 4 + 4 j (j = 0..3) address: with lane s at row s / 4, columns
+// 4 (s % 4), lane i gets rows 0..3 of column i.
+template <int MF, int COLS>
+__device__ __forceinline__ bf16x8 fragment(const ColTile<COLS>&, const lds_char* lds, int first, int kk) {
+  const int lane = lane_id();
+  const int k = kk * (512 / MF) + 8 * (lane / MF) + (lane % 16) / 4;
+  const int col = first + (lane % MF) / 16 * 16 + 4 * (lane % 4);
+  const int slot = (col >> 3) ^ ((k & 3) << 2);
+  const lds_char* at = lds + k * (COLS * 2) + slot * 16 + (col & 4) * 2;
+  union {
+    s16x4 half[2];
+    bf16x8 all;
+  } u;
+  u.half[0] = read_tr(at);
+  u.half[1] = read_tr(at + 4 * COLS * 2);  // rows k + 4 ..: same residue modulo 4
+  return u.all;
+}
+
+// FP8: 128 contraction bytes a tile; 32x32x64 takes 32 bytes a lane, 16x16x128
+// too.  Which contraction elements a lane takes is free as long as both
+// operands agree.
+template <int MF, int ROWS>
+__device__ __forceinline__ i32x8 fragment8(const RowTile<ROWS>&, const lds_char* lds, int first, int kk) {
+  const int lane = lane_id();
+  const int r = first + lane % MF, c = 2 * (kk * (kWave / MF) + lane / MF);
+  const i32x4 a = row_chunk(lds, r, c), b = row_chunk(lds, r, c + 1);
+  return i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+template <int MF>
+struct Mfma;
+template <>
+struct Mfma<32> {
+  typedef f32x16 acc_t;
+  static __device__ __forceinline__ acc_t bf16(bf16x8 a, bf16x8 b, acc_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ acc_t fp8(i32x8 a, i32x8 b, acc_t c) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+  }
+};
+template <>
+struct Mfma<16> {
+  typedef f32x4 acc_t;
+  static __device__ __forceinline__ acc_t bf16(bf16x8 a, bf16x8 b, acc_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ acc_t fp8(i32x8 a, i32x8 b, acc_t c) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+  }
+};
+
+// First of the four consecutive channels that accumulator registers 4 q .. 4 q + 3
+// of a lane hold.
+template <int MF>
+__device__ __forceinline__ int channel_of(int q) {
+  return MF == 32 ? 8 * q + 4 * (lane_id() / 32) : 4 * (lane_id() / 16);
+}
+
+// Shape of a workgroup's tile: WC x WT waves, each CT x TT matrix-core tiles
+// of MF channels x MF rows; STAGES buffers of 64 contraction elements (128 in FP8).
+template <int MF_, int CT_, int TT_, int WC_, int WT_, int STAGES_>
+struct Shape {
+  static constexpr int MF = MF_, CT = CT_, TT = TT_, WC = WC_, WT = WT_, STAGES = STAGES_;
+  static constexpr int BN = WC * CT * MF, BM = WT * TT * MF;
+  static constexpr int KK = MF / 8;        // bf16 matrix-core steps of a stage
+  static constexpr int KK8 = MF / 16;      // FP8 steps
+  static constexpr int REGS = MF * MF / kWave;
+  static constexpr int WROWS = TT * MF;    // rows of a wave's tile
+  static constexpr int SLOADS = (WROWS + kWave - 1) / kWave;  // FP8 scale loads of a stage
+  static_assert(WC * WT * kWave == kGemmThreads, "four wavefronts");
+  typedef typename Mfma<MF>::acc_t acc_t;
+};
+
+// Tile t of mt row tiles x nt channel tiles.  Row tiles are taken in groups
+// of kGroup, a group's channel tiles one after another with its row tiles
+// fastest, so the workgroups that run together share both operands; each
+// die (block b runs on die b % kXcds) takes a run of them.
+constexpr int kGroup = 8;
+
+__device__ __forceinline__ void tile_at(int64_t t, int mt, int nt, int& m, int& n) {
+  const int64_t per = (int64_t)kGroup * nt;
+  const int g = (int)(t / per);
+  const int in = (int)(t - g * per);
+  const int rows = min(kGroup, mt - g * kGroup);
+  n = uniform(in / rows);
+  m = uniform(g * kGroup + in - n * rows);
+}
+
+// This workgroup's place among gridDim.x (a multiple of kXcds, or below it)
+__device__ __forceinline__ int block_place() {
+  const int g = gridDim.x, b = blockIdx.x;
+  return g % kXcds == 0 ? (b % kXcds) * (g / kXcds) + b / kXcds : b;
+}
+
+// ---- main loop ---------------------------------------------------------------
+
+// Waits until stage k's loads are in LDS, for every wave.  LOADS: loads a wave
+// issues per stage; stages up to k + STAGES - 2 (but the last, nk - 1) have
+// been issued.
+template <int STAGES, int LOADS>
+__device__ __forceinline__ void wait_stage(int k, int nk) {
+  if (k + STAGES - 2 < nk)
+    wait_loads<LOADS*(STAGES - 2)>();
+  else
+    wait_loads<0>();
+  barrier();
+}
+
+template <class S>
+__device__ __forceinline__ void clear(typename S::acc_t (&acc)[S::CT][S::TT]) {
+#pragma unroll
+  for (int i = 0; i < S::CT; ++i)
+#pragma unroll
+    for (int j = 0; j < S::TT; ++j)
+#pragma unroll
+      for (int q = 0; q < S::REGS; ++q) acc[i][j][q] = 0.0f;
+}
+
+// acc += the nk stages' products.  load(k, buf) issues stage k's loads into
+// buffer buf (the channel operand's tile, then the row operand's).  They are
+// issued S::STAGES stages ahead, into the buffer that the stage read last
+// leaves; a stage's last fragments are in registers before its buffer is given
+// up, so its last products cover the barrier, the new loads' issue and the
+// first reads of the next stage.
+template <class S, class Chan, class Row, class Load>
+__device__ __forceinline__ void products(const Chan& ct, const Row& rt, lds_char* lds, int nk,
+                                         Load load, typename S::acc_t (&acc)[S::CT][S::TT]) {
+  constexpr int kStage = Chan::kBytes + Row::kBytes;
+  constexpr int kLoads = Chan::kPasses + Row::kPasses;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int wc = wave % S::WC, wr = wave / S::WC;
+  barrier();  // the previous tile's reads
+#pragma unroll
+  for (int k = 0; k < S::STAGES; ++k)
+    if (k < nk) load(k, lds + k * kStage);
+  if (nk == 0) return;
+  wait_stage<S::STAGES, kLoads>(0, nk);
+  bf16x8 fa[2][S::CT], fb[2][S::TT];
+  auto read = [&](int buf, int kk, int to) {
+    const lds_char* cl = lds + buf * kStage;
+#pragma unroll
+    for (int i = 0; i < S::CT; ++i)
+      fa[to][i] = fragment<S::MF>(ct, cl, (wc * S::CT + i) * S::MF, kk);
+#pragma unroll
+    for (int j = 0; j < S::TT; ++j)
+      fb[to][j] = fragment<S::MF>(rt, cl + Chan::kBytes, (wr * S::TT + j) * S::MF, kk);
+  };
+  auto multiply = [&](int from) {
+#pragma unroll
+    for (int i = 0; i < S::CT; ++i)
+#pragma unroll
+      for (int j = 0; j < S::TT; ++j)
+        acc[i][j] = Mfma<S::MF>::bf16(fa[from][i], fb[from][j], acc[i][j]);
+  };
+  read(0, 0, 0);
+  int buf = 0;
+  for (int k = 0; k < nk; ++k) {
+#pragma unroll
+    for (int kk = 0; kk < S::KK - 1; ++kk) {
+      read(buf, kk + 1, (kk + 1) & 1);
+      multiply(kk & 1);
+    }
+    const int now = buf;
+    buf = buf + 1 == S::STAGES ? 0 : buf + 1;
+    if (k + 1 < nk) {
+      wait_stage<S::STAGES, kLoads>(k + 1, nk);
+      if (k + S::STAGES < nk) load(k + S::STAGES, lds + now * kStage);
+      read(buf, 0, 0);
+    }
+    multiply((S::KK - 1) & 1);
+  }
+}
+
+// Epilogue: a wave turns MF rows at a time around in its own part of the LDS,
+// so that eight consecutive channels of one row meet in a lane and rows leave
+// as whole 16-byte vectors.  put(r, c, from): row r of the workgroup's tile,
+// channel c of the wave's OUT channel tiles; `from` holds the eight sums of
+// channels c .. c + 7, and OUT * MF floats further on those of the wave's next
+// OUT channel tiles.
+template <class S, int OUT, class Put>
+__device__ __forceinline__ void turn_out(lds_char* lds, const typename S::acc_t (&acc)[S::CT][S::TT],
+                                         Put put) {
+  constexpr int MF = S::MF;
+  constexpr int kRowBytes = S::CT * MF * 4 + 16;  // 16: rows start four banks apart
+  constexpr int kVecs = OUT * MF / 8;
+  const int lane = lane_id(), wave = uniform(threadIdx.x >> 6);
+  const int wr = wave / S::WC;
+  barrier();
+  lds_char* mine = lds + wave * (MF * kRowBytes);
+#pragma unroll
+  for (int j = 0; j < S::TT; ++j) {
+#pragma unroll
+    for (int i = 0; i < S::CT; ++i)
+#pragma unroll
+      for (int q = 0; q < S::REGS / 4; ++q) {
+        const f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                         acc[i][j][4 * q + 3]};
+        *(EP_LDS f32x4*)(mine + (lane % MF) * kRowBytes + (i * MF + channel_of<MF>(q)) * 4) = v;
+      }
+    wave_lds_sync();
+#pragma unroll 1
+    for (int at = lane; at < MF * kVecs; at += kWave) {
+      const int r = at / kVecs, c = at % kVecs * 8;
+      put((wr * S::TT + j) * MF + r, c, (const lds_float*)(mine + r * kRowBytes) + c);
+    }
+    wave_lds_sync();
+  }
+}
+
+}  // namespace ep

@@ -1,0 +1,267 @@
+// Gradients of the experts' products (gfx950).  With z the pre-activations
+// and dz their gradient, for every expert e and the rows r of its segment:
+//   gated:   dz = [dh * u * act'(g) | dh * act(g)],  z = [g | u] = x [Wg; Wu]^T
+//   linear:  dz = dy * act'(z),                      z = x W^T + b
+//   dx[r] = sum_o dz[r][o] W_e[o],  dW_e[o] = sum_r dz[r][o] x[r],  db_e = sum_r dz[r]
+// dz is rounded to bf16 once, as the matrix cores take it; db sums the
+// unrounded values.
+#include "experts.hpp"
+
+namespace ep {
+
+// ---- dz ----------------------------------------------------------------------
+
+constexpr int kElemRows = 8;  // rows of a work item
+
+// Reads dy and the pre-activations once and writes dz: bound by memory.
+template <bool GATED>
+__global__ __launch_bounds__(256) void expert_dz(GradArgs a) {
+  __shared__ TilePlan<256> plan;
+  plan_tiles(a.seg, kElemRows, plan);
+  const int vecs = a.N / 8;
+  for (int t = blockIdx.x; t < plan.first[a.seg.E]; t += gridDim.x) {
+    const int e = expert_of(plan, a.seg.E, t);
+    int64_t start;
+    int count;
+    segment_of(a.seg, e, start, count);
+    const int row0 = (t - plan.first[e]) * kElemRows;
+    const int rows = min(count - row0, kElemRows);
+    for (int i = threadIdx.x; i < rows * vecs; i += 256) {
+      const int r = i / vecs, ch = (i - r * vecs) * 8;
+      const int64_t row = start + row0 + r;
+      float d[8], z[8], o[8];
+      unpack8(*(const u32x4*)(a.dy + row * a.N + ch), d);
+      const int64_t at = row * (GATED ? 2 : 1) * a.N + ch;
+      unpack8(*(const u32x4*)(a.pre + at), z);
+      if (GATED) {
+        float u[8], du[8];
+        unpack8(*(const u32x4*)(a.pre + at + a.N), u);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          float value, slope;
+          act_both(a.act, z[c], value, slope);
+          o[c] = d[c] * u[c] * slope;
+          du[c] = d[c] * value;
+        }
+        *(u32x4*)(a.dz_out + at + a.N) = pack8(du);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          float value, slope;
+          act_both(a.act, z[c], value, slope);
+          o[c] = d[c] * slope;
+        }
+      }
+      *(u32x4*)(a.dz_out + at) = pack8(o);
+    }
+  }
+}
+
+// ---- db ----------------------------------------------------------------------
+
+constexpr int kBiasChannels = 64;
+
+// One workgroup per expert and 64 channels: 32 rows at a time, eight channels
+// a thread, joined over LDS in a fixed order.
+__global__ __launch_bounds__(256) void expert_dbias(GradArgs a) {
+  __shared__ float part[32][kBiasChannels + 1];
+  const int e = blockIdx.y, c0 = blockIdx.x * kBiasChannels;
+  const int r0 = threadIdx.x / 8, c = (threadIdx.x % 8) * 8;
+  int64_t start;
+  int count;
+  segment_of(a.seg, e, start, count);
+  float sum[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) sum[q] = 0.0f;
+  if (c0 + c < a.N)
+    for (int r = r0; r < count; r += 32) {
+      const int64_t at = (start + r) * a.N + c0 + c;
+      float d[8], z[8];
+      unpack8(*(const u32x4*)(a.dy + at), d);
+      if (a.act != EP_ACT_NONE) {
+        unpack8(*(const u32x4*)(a.pre + at), z);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          float value, slope;
+          act_both(a.act, z[q], value, slope);
+          d[q] *= slope;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) sum[q] += d[q];
+    }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) part[r0][c + q] = sum[q];
+  __syncthreads();
+  if (threadIdx.x < kBiasChannels && c0 + (int)threadIdx.x < a.N) {
+    float s = 0.0f;
+    for (int r = 0; r < 32; ++r) s += part[r][threadIdx.x];
+    a.dbias[(int64_t)e * a.N + c0 + threadIdx.x] = s;
+  }
+}
+
+// ---- dx ----------------------------------------------------------------------
+
+// dx = dz W: the rows run along the contraction (O channels of dz), the
+// weights across it.
+template <class S>
+__global__ __launch_bounds__(kGemmThreads, 1) void expert_dx(GradArgs a) {
+  __shared__ __align__(16) char lds[S::STAGES][(S::BN + S::BM) * 128];
+  __shared__ TilePlan<kGemmThreads> plan;
+  const int wave = uniform(threadIdx.x >> 6), wc = wave % S::WC;
+  plan_tiles(a.seg, S::BM, plan);
+  const int mt = plan.first[a.seg.E];
+  const int nt = (a.C + S::BN - 1) / S::BN;
+  const int64_t tiles = (int64_t)mt * nt;
+  const int64_t z_bytes = (int64_t)a.O * 2, w_bytes = (int64_t)a.C * 2;
+  const int nk = (a.O + 63) / 64, nfull = a.O / 64;
+  for (int64_t t = block_place(); t < tiles; t += gridDim.x) {
+    int m, n;
+    tile_at(t, mt, nt, m, n);
+    const int e = expert_of(plan, a.seg.E, m);
+    int64_t start;
+    int count;
+    segment_of(a.seg, e, start, count);
+    const int row0 = (m - plan.first[e]) * S::BM;
+    const int rows = min(count - row0, S::BM);
+    const int n0 = n * S::BN;
+    ColTile<S::BN> w_tile;
+    RowTile<S::BM> z_tile;
+    const char* w_base = (const char*)a.w + (int64_t)e * a.O * w_bytes + n0 * 2;
+    const char* z_base = (const char*)a.dz + (start + row0) * z_bytes;
+    w_tile.init((uint32_t)w_bytes, a.C - n0);
+    z_tile.init([&](int r) -> uint32_t { return (uint32_t)(min(r, rows - 1) * z_bytes); });
+    auto load = [&](int k, lds_char* buf) {
+      const char* w = w_base + (int64_t)k * 64 * w_bytes;
+      const char* z = z_base + (int64_t)k * 128;
+      if (k < nfull) {
+        w_tile.load(w, buf);
+        z_tile.template load<1 << 20>(z, 0, buf + w_tile.kBytes);
+      } else {
+        w_tile.load_tail(w, a.O - k * 64, buf);
+        z_tile.template load_tail<1 << 20>(z, 0, (a.O - k * 64) * 2, buf + w_tile.kBytes);
+      }
+    };
+    typename S::acc_t acc[S::CT][S::TT];
+    clear<S>(acc);
+    products<S>(w_tile, z_tile, (lds_char*)&lds[0][0], nk, load, acc);
+    turn_out<S, S::CT>((lds_char*)&lds[0][0], acc, [&](int r, int c, const lds_float* from) {
+      const int ch = n0 + wc * S::CT * S::MF + c;
+      if (r < rows && ch < a.C) {
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = from[q];
+        *(u32x4*)(a.dx + (start + row0 + r) * a.C + ch) = pack8(v);
+      }
+    });
+  }
+}
+
+// ---- dW ----------------------------------------------------------------------
+
+// dW_e = dz_e^T x_e: both operands run across the contraction, the segment's
+// rows.  One workgroup per tile of one expert; an expert without rows gets
+// zeros.  Each die takes 32 consecutive tiles in turn, so the workgroups that
+// run on it together read the same expert's rows and long experts fall on all
+// dies alike.
+template <class S>
+__global__ __launch_bounds__(kGemmThreads, 1) void expert_dw(GradArgs a) {
+  __shared__ __align__(16) char lds[S::STAGES][(S::BN + S::BM) * 128];
+  const int wave = uniform(threadIdx.x >> 6), wc = wave % S::WC;
+  const int ct = (a.C + S::BN - 1) / S::BN, ot = (a.O + S::BM - 1) / S::BM;
+  constexpr int kRun = 32;
+  const int i = blockIdx.x / kXcds;
+  const int64_t t = ((int64_t)(i / kRun) * kXcds + blockIdx.x % kXcds) * kRun + i % kRun;
+  if (t >= (int64_t)a.seg.E * ct * ot) return;
+  const int e = uniform((int)(t / (ct * ot)));
+  int m, n;
+  tile_at(t - (int64_t)e * ct * ot, ot, ct, m, n);
+  int64_t start;
+  int count;
+  segment_of(a.seg, e, start, count);
+  const int c0 = n * S::BN, o0 = m * S::BM;
+  const int64_t x_bytes = (int64_t)a.C * 2, z_bytes = (int64_t)a.O * 2;
+  ColTile<S::BN> x_tile;
+  ColTile<S::BM> z_tile;
+  const char* x_base = (const char*)a.x + start * x_bytes + c0 * 2;
+  const char* z_base = (const char*)a.dz + start * z_bytes + o0 * 2;
+  x_tile.init((uint32_t)x_bytes, a.C - c0);
+  z_tile.init((uint32_t)z_bytes, a.O - o0);
+  const int nk = (count + 63) / 64, nfull = count / 64;
+  auto load = [&](int k, lds_char* buf) {
+    const char* x = x_base + (int64_t)k * 64 * x_bytes;
+    const char* z = z_base + (int64_t)k * 64 * z_bytes;
+    if (k < nfull) {
+      x_tile.load(x, buf);
+      z_tile.load(z, buf + x_tile.kBytes);
+    } else {
+      x_tile.load_tail(x, count - k * 64, buf);
+      z_tile.load_tail(z, count - k * 64, buf + x_tile.kBytes);
+    }
+  };
+  typename S::acc_t acc[S::CT][S::TT];
+  clear<S>(acc);
+  products<S>(x_tile, z_tile, (lds_char*)&lds[0][0], nk, load, acc);
+  uint16_t* dw = a.dw + (int64_t)e * a.O * a.C;
+  turn_out<S, S::CT>((lds_char*)&lds[0][0], acc, [&](int r, int c, const lds_float* from) {
+    const int ch = c0 + wc * S::CT * S::MF + c, o = o0 + r;
+    if (o < a.O && ch < a.C) {
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = from[q];
+      *(u32x4*)(dw + (int64_t)o * a.C + ch) = pack8(v);
+    }
+  });
+}
+
+// ---- launches ------------------------------------------------------------------
+
+typedef Shape<32, 4, 4, 2, 2, 2> Big;     // 256 channels x 256 rows
+typedef Shape<32, 2, 2, 4, 1, 3> Medium;  // 256 x 64
+typedef Shape<16, 2, 1, 4, 1, 3> Small;   // 128 x 16
+typedef Shape<32, 2, 2, 2, 2, 3> Square;  // 128 x 128
+
+template <class S>
+static void launch_dx(const GradArgs& a, hipStream_t st) {
+  const int64_t tiles = ((a.rows + S::BM - 1) / S::BM + a.seg.E) * ((a.C + S::BN - 1) / S::BN);
+  const int per_cu = S::STAGES * (S::BN + S::BM) * 128 > 70 * 1024 ? 1 : 2;
+  hipLaunchKernelGGL(expert_dx<S>, dim3((unsigned)min(tiles, (int64_t)kCus * per_cu)),
+                     dim3(kGemmThreads), 0, st, a);
+}
+
+template <class S>
+static void launch_dw(const GradArgs& a, hipStream_t st) {
+  const int64_t tiles =
+      (int64_t)a.seg.E * ((a.C + S::BN - 1) / S::BN) * ((a.O + S::BM - 1) / S::BM);
+  const int64_t run = 32 * kXcds;
+  hipLaunchKernelGGL(expert_dw<S>, dim3((unsigned)((tiles + run - 1) / run * run)),
+                     dim3(kGemmThreads), 0, st, a);
+}
+
+hipError_t launch_expert_grad(const GradArgs& a, hipStream_t st) {
+  const int64_t each = a.rows / a.seg.E;
+  if (a.dz_out && a.rows > 0) {
+    const int64_t items = a.rows / kElemRows + a.seg.E;
+    const dim3 grid((unsigned)min(items, (int64_t)kCus * 8));
+    if (a.gated)
+      hipLaunchKernelGGL(expert_dz<true>, grid, dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL(expert_dz<false>, grid, dim3(256), 0, st, a);
+  }
+  if (a.dbias)
+    hipLaunchKernelGGL(expert_dbias, dim3((a.N + kBiasChannels - 1) / kBiasChannels, a.seg.E),
+                       dim3(256), 0, st, a);
+  if (a.dx && a.rows > 0) {
+    if (each > 96) launch_dx<Big>(a, st);
+    else if (each > 8) launch_dx<Medium>(a, st);
+    else launch_dx<Small>(a, st);
+  }
+  if (a.dw) {
+    const int64_t tiles = (int64_t)a.seg.E * ((a.C + 255) / 256) * ((a.O + 255) / 256);
+    if (tiles >= kCus) launch_dw<Big>(a, st);
+    else launch_dw<Square>(a, st);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace ep

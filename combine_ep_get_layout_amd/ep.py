@@ -19,10 +19,13 @@ LIB_PATH = os.path.join(_HERE, "libep.so")
 
 MODE_NORMAL, MODE_LOW_LATENCY, MODE_MESSAGES, MODE_RANK_MAJOR = 0, 1, 2, 3
 QUANT_NONE, QUANT_FP8_F32, QUANT_FP8_UE8M0 = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = 0, 1, 2, 3
 DEVERR_TOPK_RANGE, DEVERR_LL_OVERFLOW, DEVERR_CAPACITY, DEVERR_MESSAGE = 1, 2, 4, 8
 
 EXPORTS = ["ep_workspace_bytes", "ep_max_recv_rows", "ep_messages_capacity", "ep_get_layout",
            "ep_dispatch", "ep_dispatch_fused", "ep_dispatch_fused_noalloc", "ep_combine",
+           "ep_expert_gated", "ep_expert_linear", "ep_expert_gated_backward",
+           "ep_expert_linear_backward", "ep_combine_backward",
            "ep_messages_execute", "ep_messages_unpack", "ep_status_string"]
 NOALLOC_SCRATCH_BYTES = 64 << 20  # EP_NOALLOC_SCRATCH_BYTES
 ERR_SCRATCH = -8
@@ -66,6 +69,17 @@ class CMessages(ctypes.Structure):
                 ("num_descriptors", _vp)]
 
 
+class CRows(ctypes.Structure):
+    _fields_ = [("x", _vp), ("scales", _vp), ("capacity", ctypes.c_int64),
+                ("channels", ctypes.c_int32), ("quant", ctypes.c_int32)]
+
+
+class CWeights(ctypes.Structure):
+    _fields_ = [("w", _vp), ("scales", _vp), ("bias", _vp), ("in_channels", ctypes.c_int32),
+                ("out_channels", ctypes.c_int32), ("fp8", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -97,6 +111,18 @@ def lib() -> ctypes.CDLL:
         l.ep_dispatch_fused_noalloc.restype = ctypes.c_int
         l.ep_combine.argtypes = [P, ctypes.POINTER(CLayout), _vp, ctypes.c_int64, _vp, _vp, _vp]
         l.ep_combine.restype = ctypes.c_int
+        LP, RP, WP = (ctypes.POINTER(c) for c in (CLayout, CRows, CWeights))
+        i32 = ctypes.c_int32
+        l.ep_expert_gated.argtypes = [P, LP, RP, WP, i32, RP, RP, _vp]
+        l.ep_expert_gated.restype = ctypes.c_int
+        l.ep_expert_linear.argtypes = [P, LP, RP, WP, i32, RP, RP, RP, _vp]
+        l.ep_expert_linear.restype = ctypes.c_int
+        l.ep_expert_gated_backward.argtypes = [P, LP, RP, WP, i32, RP, RP, RP, RP, _vp, _vp]
+        l.ep_expert_gated_backward.restype = ctypes.c_int
+        l.ep_expert_linear_backward.argtypes = [P, LP, RP, WP, i32, RP, RP, RP, RP, _vp, _vp, _vp]
+        l.ep_expert_linear_backward.restype = ctypes.c_int
+        l.ep_combine_backward.argtypes = [P, LP, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp, _vp]
+        l.ep_combine_backward.restype = ctypes.c_int
         l.ep_messages_execute.argtypes = [P, ctypes.POINTER(CMessages), _vp, ctypes.c_int64,
                                           ctypes.c_int32, _vp, _vp]
         l.ep_messages_execute.restype = ctypes.c_int
@@ -445,6 +471,226 @@ def _combine_args(p: Problem, layout: Layout, y: torch.Tensor, topk_weights: tor
                                 _ptr(topk_weights), _ptr(out)), (pc, cl))
 
 
+# ---- the experts' products ----
+
+def _same_device(*tensors) -> None:
+    """The library enqueues on torch's current stream: its device is the tensors'."""
+    for t in tensors:
+        _need(t is None or t.device == tensors[0].device, "tensors on one device")
+    _need(not tensors[0].is_cuda or tensors[0].device.index == torch.cuda.current_device(),
+          "tensors on the current device")
+
+
+def _rows(p: Problem, t: torch.Tensor, what: str, channels: int | None = None,
+          scales: torch.Tensor | None = None) -> CRows:
+    """A row buffer: bf16 [rows][channels], or one-byte e4m3 codes with their scales."""
+    _need(t.dim() == 2 and (channels is None or t.shape[1] == channels),
+          f"{what} [rows][{channels or 'channels'}]")
+    quant = QUANT_NONE
+    if scales is None:
+        _need(t.dtype == torch.bfloat16, f"{what} bf16 (FP8 codes come with scales)")
+    else:
+        _need(t.element_size() == 1, f"{what}: FP8 codes are bytes")
+        _need(scales.dtype in (torch.float32, torch.uint8), f"{what} scales fp32 or uint8 (UE8M0)")
+        quant = QUANT_FP8_F32 if scales.dtype == torch.float32 else QUANT_FP8_UE8M0
+        rows = t.shape[0] if p.mode == MODE_NORMAL else p.E * p.R * p.T
+        _need(scales.numel() >= t.shape[1] // 128 * rows, f"{what} scales")
+    return CRows(_ptr(t), _ptr(scales), t.shape[0], t.shape[1], quant)
+
+
+def _weights(p: Problem, w: torch.Tensor, scales: torch.Tensor | None = None,
+             bias: torch.Tensor | None = None) -> CWeights:
+    _need(w.dim() == 3 and w.shape[0] == p.E, "w [E][out channels][in channels]")
+    if scales is None:
+        _need(w.dtype == torch.bfloat16, "w bf16 (FP8 codes come with w_scales)")
+    else:
+        _need(w.element_size() == 1, "w: FP8 codes are bytes")
+        _need(scales.dtype == torch.float32
+              and scales.numel() == p.E * (w.shape[1] // 128) * (w.shape[2] // 128),
+              "w_scales [E][out/128][in/128] fp32")
+    if bias is not None:
+        _need(bias.dtype == torch.float32 and bias.numel() == p.E * w.shape[1], "bias [E][N] fp32")
+    return CWeights(_ptr(w), _ptr(scales), _ptr(bias), w.shape[2], w.shape[1],
+                    0 if scales is None else 1, 0)
+
+
+def _check_segments(p: Problem, layout: Layout) -> None:
+    _need(layout.recv_tokens_per_expert.numel() == p.E and layout.expert_start.numel() == p.E,
+          "layout buffers do not match the problem")
+
+
+def _ref(c):
+    return ctypes.byref(c) if c is not None else None
+
+
+def expert_gated(p: Problem, layout: Layout, x: torch.Tensor, w: torch.Tensor, h: torch.Tensor, *,
+                 act: int = ACT_SILU, x_scales: torch.Tensor | None = None,
+                 w_scales: torch.Tensor | None = None, h_scales: torch.Tensor | None = None,
+                 pre: torch.Tensor | None = None, stream=None) -> None:
+    """Gated feed-forward block over the receive rows: h = act(x Wg^T) * (x Wu^T).
+    x [rows][C], w [E][2 I][C] (gates first), h [rows][I]; `pre` [rows][2 I]
+    keeps both projections for expert_gated_backward.  FP8 (codes as bytes):
+    x with the dispatch's scales and w with w_scales [E][2 I/128][C/128]; h then
+    may be FP8 too (h_scales, fp32 or uint8)."""
+    _invoke(_expert_gated_args(p, layout, x, w, h, act=act, x_scales=x_scales, w_scales=w_scales,
+                               h_scales=h_scales, pre=pre), stream)
+
+
+def _expert_gated_args(p: Problem, layout: Layout, x: torch.Tensor, w: torch.Tensor,
+                       h: torch.Tensor, *, act: int = ACT_SILU,
+                       x_scales: torch.Tensor | None = None,
+                       w_scales: torch.Tensor | None = None,
+                       h_scales: torch.Tensor | None = None,
+                       pre: torch.Tensor | None = None) -> _Args:
+    _check_segments(p, layout)
+    _same_device(x, x_scales, w, w_scales, h, h_scales, pre, layout.err)
+    _need(w.dim() == 3 and w.shape[1] % 2 == 0, "w [E][2 I][C]")
+    cw = _weights(p, w, w_scales)
+    cx = _rows(p, x, "x", w.shape[2], x_scales)
+    ch = _rows(p, h, "h", w.shape[1] // 2, h_scales)
+    cpre = _rows(p, pre, "pre", w.shape[1]) if pre is not None else None
+    pc, cl = p.c(), layout.c()
+    return _Args("ep_expert_gated", (ctypes.byref(pc), ctypes.byref(cl), ctypes.byref(cx),
+                                     ctypes.byref(cw), int(act), ctypes.byref(ch), _ref(cpre)),
+                 (pc, cl, cx, cw, ch, cpre))
+
+
+def expert_linear(p: Problem, layout: Layout, x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, *,
+                  act: int = ACT_NONE, bias: torch.Tensor | None = None,
+                  residual: torch.Tensor | None = None, x_scales: torch.Tensor | None = None,
+                  w_scales: torch.Tensor | None = None, y_scales: torch.Tensor | None = None,
+                  pre: torch.Tensor | None = None, stream=None) -> None:
+    """Product with bias, activation and residual over the receive rows:
+    y = act(x W^T + bias) + residual.  x [rows][C], w [E][N][C], bias [E][N]
+    fp32, residual and y [rows][N] (residual may be y); `pre` [rows][N] keeps
+    x W^T + bias for expert_linear_backward.  FP8 as in expert_gated."""
+    _invoke(_expert_linear_args(p, layout, x, w, y, act=act, bias=bias, residual=residual,
+                                x_scales=x_scales, w_scales=w_scales, y_scales=y_scales, pre=pre),
+            stream)
+
+
+def _expert_linear_args(p: Problem, layout: Layout, x: torch.Tensor, w: torch.Tensor,
+                        y: torch.Tensor, *, act: int = ACT_NONE,
+                        bias: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                        x_scales: torch.Tensor | None = None,
+                        w_scales: torch.Tensor | None = None,
+                        y_scales: torch.Tensor | None = None,
+                        pre: torch.Tensor | None = None) -> _Args:
+    _check_segments(p, layout)
+    _same_device(x, x_scales, w, w_scales, y, y_scales, bias, residual, pre, layout.err)
+    cw = _weights(p, w, w_scales, bias)
+    cx = _rows(p, x, "x", w.shape[2], x_scales)
+    cy = _rows(p, y, "y", w.shape[1], y_scales)
+    cr = _rows(p, residual, "residual", w.shape[1]) if residual is not None else None
+    cpre = _rows(p, pre, "pre", w.shape[1]) if pre is not None else None
+    pc, cl = p.c(), layout.c()
+    return _Args("ep_expert_linear", (ctypes.byref(pc), ctypes.byref(cl), ctypes.byref(cx),
+                                      ctypes.byref(cw), int(act), _ref(cr), ctypes.byref(cy),
+                                      _ref(cpre)), (pc, cl, cx, cw, cr, cy, cpre))
+
+
+def expert_gated_backward(p: Problem, layout: Layout, x: torch.Tensor | None, w: torch.Tensor,
+                          pre: torch.Tensor, dh: torch.Tensor, *, dpre: torch.Tensor,
+                          dx: torch.Tensor | None = None, dw: torch.Tensor | None = None,
+                          act: int = ACT_SILU, stream=None) -> None:
+    """Gradients of expert_gated from its saved `pre`: dpre [rows][2 I] (always
+    written), dx [rows][C] and dw [E][2 I][C] (whole; zeros for an expert
+    without rows), each where given.  x is needed for dw alone."""
+    _invoke(_expert_gated_backward_args(p, layout, x, w, pre, dh, dpre=dpre, dx=dx, dw=dw,
+                                        act=act), stream)
+
+
+def _expert_gated_backward_args(p: Problem, layout: Layout, x: torch.Tensor | None,
+                                w: torch.Tensor, pre: torch.Tensor, dh: torch.Tensor, *,
+                                dpre: torch.Tensor, dx: torch.Tensor | None = None,
+                                dw: torch.Tensor | None = None, act: int = ACT_SILU) -> _Args:
+    _check_segments(p, layout)
+    _same_device(dh, x, w, pre, dpre, dx, dw, layout.err)
+    _need(w.dim() == 3 and w.shape[1] % 2 == 0, "w [E][2 I][C]")
+    cw = _weights(p, w)
+    cx = _rows(p, x, "x", w.shape[2]) if x is not None else None
+    cpre, cdh = _rows(p, pre, "pre", w.shape[1]), _rows(p, dh, "dh", w.shape[1] // 2)
+    cdpre = _rows(p, dpre, "dpre", w.shape[1])
+    cdx = _rows(p, dx, "dx", w.shape[2]) if dx is not None else None
+    _need(dw is None or (dw.dtype == torch.bfloat16 and dw.shape == w.shape), "dw as w, bf16")
+    pc, cl = p.c(), layout.c()
+    return _Args("ep_expert_gated_backward",
+                 (ctypes.byref(pc), ctypes.byref(cl), _ref(cx), ctypes.byref(cw), int(act),
+                  ctypes.byref(cpre), ctypes.byref(cdh), ctypes.byref(cdpre), _ref(cdx),
+                  _ptr(dw)), (pc, cl, cx, cw, cpre, cdh, cdpre, cdx))
+
+
+def expert_linear_backward(p: Problem, layout: Layout, x: torch.Tensor | None, w: torch.Tensor,
+                           dy: torch.Tensor, *, pre: torch.Tensor | None = None,
+                           dpre: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                           dw: torch.Tensor | None = None, dbias: torch.Tensor | None = None,
+                           act: int = ACT_NONE, stream=None) -> None:
+    """Gradients of expert_linear: dx [rows][C], dw [E][N][C], dbias [E][N] fp32,
+    each where given (the residual's gradient is dy).  With an activation,
+    its saved `pre` and room for dpre [rows][N] are needed."""
+    _invoke(_expert_linear_backward_args(p, layout, x, w, dy, pre=pre, dpre=dpre, dx=dx, dw=dw,
+                                         dbias=dbias, act=act), stream)
+
+
+def _expert_linear_backward_args(p: Problem, layout: Layout, x: torch.Tensor | None,
+                                 w: torch.Tensor, dy: torch.Tensor, *,
+                                 pre: torch.Tensor | None = None,
+                                 dpre: torch.Tensor | None = None,
+                                 dx: torch.Tensor | None = None, dw: torch.Tensor | None = None,
+                                 dbias: torch.Tensor | None = None, act: int = ACT_NONE) -> _Args:
+    _check_segments(p, layout)
+    _same_device(dy, x, w, pre, dpre, dx, dw, dbias, layout.err)
+    cw = _weights(p, w)
+    cx = _rows(p, x, "x", w.shape[2]) if x is not None else None
+    cpre = _rows(p, pre, "pre", w.shape[1]) if pre is not None else None
+    cdy = _rows(p, dy, "dy", w.shape[1])
+    cdpre = _rows(p, dpre, "dpre", w.shape[1]) if dpre is not None else None
+    cdx = _rows(p, dx, "dx", w.shape[2]) if dx is not None else None
+    _need(dw is None or (dw.dtype == torch.bfloat16 and dw.shape == w.shape), "dw as w, bf16")
+    _need(dbias is None or (dbias.dtype == torch.float32 and dbias.numel() == p.E * w.shape[1]),
+          "dbias [E][N] fp32")
+    pc, cl = p.c(), layout.c()
+    return _Args("ep_expert_linear_backward",
+                 (ctypes.byref(pc), ctypes.byref(cl), _ref(cx), ctypes.byref(cw), int(act),
+                  _ref(cpre), ctypes.byref(cdy), _ref(cdpre), _ref(cdx), _ptr(dw), _ptr(dbias)),
+                 (pc, cl, cx, cw, cpre, cdy, cdpre, cdx))
+
+
+def combine_backward(p: Problem, layout: Layout, dout: torch.Tensor,
+                     topk_weights: torch.Tensor | None, y: torch.Tensor | None, *,
+                     dy: torch.Tensor | None = None, dweights: torch.Tensor | None = None,
+                     stream=None) -> None:
+    """Gradient of combine: dy [rows][H] bf16 (the rows that tokens gathered) and
+    dweights [R][T][K] fp32, each where given.  y is needed for dweights alone."""
+    _invoke(_combine_backward_args(p, layout, dout, topk_weights, y, dy=dy, dweights=dweights),
+            stream)
+
+
+def _combine_backward_args(p: Problem, layout: Layout, dout: torch.Tensor,
+                           topk_weights: torch.Tensor | None, y: torch.Tensor | None, *,
+                           dy: torch.Tensor | None = None,
+                           dweights: torch.Tensor | None = None) -> _Args:
+    R, T, H, K = p.R, p.T, p.H, p.K
+    _same_device(dout, topk_weights, y, dy, dweights, layout.err)
+    _need(dout.dtype == torch.bfloat16 and dout.numel() == R * T * H, "dout [R][T][H] bf16")
+    _need(layout.send_pos is not None and layout.send_pos.numel() == R * T * K, "send_pos")
+    _need(topk_weights is None or (topk_weights.dtype == torch.float32
+          and topk_weights.numel() == R * T * K), "topk_weights [R][T][K] fp32")
+    _need(dy is not None or dweights is not None, "dy or dweights")
+    for t, name in (y, "y"), (dy, "dy"):
+        _need(t is None or (t.dtype == torch.bfloat16 and t.dim() == 2 and t.shape[1] == H),
+              f"{name} [rows][H] bf16")
+    _need(y is None or dy is None or y.shape[0] == dy.shape[0], "as many rows in dy as in y")
+    _need(dweights is None or (dweights.dtype == torch.float32 and dweights.numel() == R * T * K),
+          "dweights [R][T][K] fp32")
+    _need(dweights is None or y is not None, "dweights needs y")
+    rows = (y if y is not None else dy).shape[0]
+    pc, cl = p.c(), layout.c()
+    return _Args("ep_combine_backward", (ctypes.byref(pc), ctypes.byref(cl), _ptr(dout),
+                                         _ptr(topk_weights), _ptr(y), rows, _ptr(dy),
+                                         _ptr(dweights)), (pc, cl))
+
+
 def messages_execute(p: Problem, msgs: Messages, recv_arena: torch.Tensor, err: torch.Tensor,
                      stream=None, publish_batch: int = 0) -> None:
     """Loopback delivery of the descriptors of `msgs` into `recv_arena`
@@ -518,7 +764,10 @@ def _messages_unpack_args(p: Problem, msgs: Messages, recv_arena: torch.Tensor,
 _ARGS = {get_layout: _get_layout_args, dispatch: _dispatch_args,
          dispatch_fused: _dispatch_fused_args, dispatch_fused_noalloc: _dispatch_fused_noalloc_args,
          combine: _combine_args, messages_execute: _messages_execute_args,
-         messages_unpack: _messages_unpack_args}
+         messages_unpack: _messages_unpack_args, expert_gated: _expert_gated_args,
+         expert_linear: _expert_linear_args, expert_gated_backward: _expert_gated_backward_args,
+         expert_linear_backward: _expert_linear_backward_args,
+         combine_backward: _combine_backward_args}
 
 
 def messages_sizes(p: Problem, counts=None) -> tuple[int, int, int]:

@@ -76,6 +76,12 @@ extern "C" {
 #define EP_QUANT_FP8_F32 1   /* e4m3 codes + fp32 scale (amax / 448) per 128 channels */
 #define EP_QUANT_FP8_UE8M0 2 /* e4m3 codes + power-of-two scale stored as a biased 8-bit exponent */
 
+/* activations of the experts' products */
+#define EP_ACT_NONE 0 /* v                                                     */
+#define EP_ACT_RELU 1 /* max(v, 0); derivative 0 at 0                          */
+#define EP_ACT_SILU 2 /* v / (1 + exp(-v))                                     */
+#define EP_ACT_GELU 3 /* v Phi(v), Phi the Gaussian distribution (erf form)    */
+
 /* host-side status codes */
 #define EP_OK 0
 #define EP_ERR_NULL (-1)        /* a required pointer is NULL              */
@@ -280,6 +286,104 @@ int ep_dispatch_fused_noalloc(const ep_problem* p, const int32_t* topk_idx,
  * weights of its experts; topk_weights may be NULL. */
 int ep_combine(const ep_problem* p, const ep_layout* layout, const uint16_t* y,
                int64_t y_rows, const float* topk_weights, uint16_t* out, void* stream);
+
+/* ---- The experts' products, on the receive rows -------------------------
+ *
+ * A row buffer of these calls holds one row per receive row of `layout`:
+ * expert e's rows are its segment [expert_start[e], expert_start[e] +
+ * recv_tokens_per_expert[e]) in normal mode, and the first
+ * min(recv_tokens_per_expert[e], R*T) rows of its block [e*R*T, (e+1)*R*T)
+ * in low-latency mode and for messages unpacked by ep_messages_unpack
+ * (EP_MODE_MESSAGES; layout->recv_tokens_per_expert may be its recv_count).
+ * Rank-major problems are refused (EP_ERR_MODE): their rows are not in
+ * expert order.  Only the experts' rows are read and written; padding rows and
+ * rows behind an expert's last are left as they were, whatever they hold.
+ * A segment past the smallest capacity of the call's row buffers sets
+ * EP_DEVERR_CAPACITY (OR-ed into *layout->err) and is cut there.
+ * p->hidden and p->quant describe the dispatch and are not used: every
+ * operand has its own channel count, a multiple of 8 in [8, 32768], and
+ * 128 in FP8.  Sums are kept in fp32 and results rounded to bf16, nearest even,
+ * once.  The calls are deterministic and need no workspace.  Row buffers that
+ * a call reads must not overlap those it writes, but a residual may be the
+ * output itself. */
+
+/* One row buffer. */
+typedef struct ep_rows {
+  void* x;          /* [capacity][channels] bf16, or e4m3 codes, 16-byte aligned      */
+  void* scales;     /* FP8: as ep_recv.scales with G = channels / 128, else ignored   */
+  int64_t capacity; /* rows; low-latency and messages need >= E*R*T                   */
+  int32_t channels;
+  int32_t quant;    /* EP_QUANT_* of these rows                                       */
+} ep_rows;
+
+/* The experts' weights. */
+typedef struct ep_weights {
+  const void* w;       /* [E][out_channels][in_channels] bf16 or e4m3 codes, 16-byte aligned */
+  const float* scales; /* FP8: [E][out_channels/128][in_channels/128], the factor of each
+                          128 x 128 block; else ignored                                */
+  const float* bias;   /* [E][out_channels] fp32, 16-byte aligned, or NULL             */
+  int32_t in_channels;
+  int32_t out_channels;
+  int32_t fp8;         /* 0: bf16, 1: e4m3 codes with scales                           */
+  int32_t reserved;    /* must be 0                                                    */
+} ep_weights;
+
+/* Gated feed-forward block: both projections, the activation and their product
+ * in one launch.  w holds gate and up projection, [E][2 I][C] (out_channels =
+ * 2 I, the gates first; bias must be NULL):
+ *   g = x Wg^T,  u = x Wu^T,  h = act(g) * u      for every row x of expert e.
+ * x: bf16 rows with bf16 weights, or FP8 rows with FP8 weights.
+ * h: [capacity][I] bf16; with FP8 rows also FP8: the bf16 result quantised as
+ *   dispatch quantises a row (scale per 128 channels), for an FP8 product next.
+ * pre: [capacity][2 I] bf16 [g | u], saved for ep_expert_gated_backward, or
+ *   NULL. */
+int ep_expert_gated(const ep_problem* p, const ep_layout* layout, const ep_rows* x,
+                    const ep_weights* w, int32_t act, const ep_rows* h, const ep_rows* pre,
+                    void* stream);
+
+/* Product with bias, activation and residual:
+ *   z = x W^T + bias,  y = act(z) + residual.
+ * x, w: as above, w [E][N][C].  residual: [capacity][N] bf16 or NULL (may be y
+ * itself: y += ...).  y: [capacity][N] bf16, or FP8 as h above.  pre: [capacity][N]
+ * bf16 z, saved for the backward pass, or NULL.  With one rank, one expert and
+ * top-1 (every token to expert 0) it is a dense layer. */
+int ep_expert_linear(const ep_problem* p, const ep_layout* layout, const ep_rows* x,
+                     const ep_weights* w, int32_t act, const ep_rows* residual,
+                     const ep_rows* y, const ep_rows* pre, void* stream);
+
+/* Gradients of ep_expert_gated (bf16).  pre: the saved [g | u]; dh: [capacity][I].
+ *   dpre = [dh * u * act'(g) | dh * act(g)]   written to dpre, [capacity][2 I]
+ *   dx = dpre W,   dw[e] = sum over e's rows of dpre^T x
+ * dx: [capacity][C] or NULL (w is then not read and w->w may be NULL); dw:
+ * [E][2 I][C] bf16 or NULL (x may then be NULL).  dw is written whole: an expert
+ * without rows gets zeros. */
+int ep_expert_gated_backward(const ep_problem* p, const ep_layout* layout, const ep_rows* x,
+                             const ep_weights* w, int32_t act, const ep_rows* pre,
+                             const ep_rows* dh, const ep_rows* dpre, const ep_rows* dx,
+                             uint16_t* dw, void* stream);
+
+/* Gradients of ep_expert_linear (bf16); the residual's is dy itself.
+ *   dpre = dy * act'(pre)     dx = dpre W     dw[e] = sum dpre^T x
+ *   dbias[e] = sum of dpre, fp32, [E][N]
+ * With EP_ACT_NONE dpre = dy: pre and dpre are not used and may be NULL.  dx,
+ * dw, dbias may be NULL; as above otherwise. */
+int ep_expert_linear_backward(const ep_problem* p, const ep_layout* layout, const ep_rows* x,
+                              const ep_weights* w, int32_t act, const ep_rows* pre,
+                              const ep_rows* dy, const ep_rows* dpre, const ep_rows* dx,
+                              uint16_t* dw, float* dbias, void* stream);
+
+/* Gradient of ep_combine.  With dout[s][t] the gradient of out[s][t]:
+ *   dy[send_pos[s][t][k]] = bf16( topk_weights[s][t][k] * dout[s][t] )
+ *   dweights[s][t][k]     = sum over H of dout[s][t] * y[send_pos[s][t][k]], fp32,
+ *                           0 for an entry without a row.
+ * Rank-major: dy[row] = dout[s][t] for each of the token's rows (topk_weights
+ * unused; dweights must be NULL).  dy: [y_rows][H] bf16 or NULL; rows that no
+ * entry names are left as they were.  y may be NULL when dweights is.  A row
+ * past y_rows sets EP_DEVERR_CAPACITY and is skipped.  (The gradient of
+ * dispatch is ep_combine with weights 1.) */
+int ep_combine_backward(const ep_problem* p, const ep_layout* layout, const uint16_t* dout,
+                        const float* topk_weights, const uint16_t* y, int64_t y_rows,
+                        uint16_t* dy, float* dweights, void* stream);
 
 /* Loopback delivery of message mode's descriptors ("ibgda_device.cuh" notes,
  * sec. 1; "GPU-Initiated Communication: Dissecting Down to the Bone", WQE
