@@ -247,7 +247,7 @@ def _call(s, outs):
                    mode=ep.MODE_LOW_LATENCY if case["mode"] == "ll" else ep.MODE_NORMAL,
                    quant=(ep.QUANT_NONE if not case.get("fp8") else
                           ep.QUANT_FP8_UE8M0 if case["ue8m0"] else ep.QUANT_FP8_F32))
-    layout = ep.Layout(p)
+    layout = s["layout"] = ep.Layout(p)  # a prepared call does not keep its tensors
     ep.get_layout(p, s["topk"], layout, ep.workspace(p))
     op = case["op"]
     act = getattr(ep, "ACT_" + case["act"].upper()) if "act" in case else None
