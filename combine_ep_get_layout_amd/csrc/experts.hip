@@ -84,8 +84,8 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
     const char* w_base = a.w + (int64_t)e * (GATED ? 2 : 1) * a.N * row_bytes;
     const char* x_base = a.x + (start + row0) * row_bytes;
     // rows and channels past the end repeat the last one; they are not stored
-    const int64_t up = GATED ? (int64_t)a.N * row_bytes : 0;
     const char* gate_base = w_base + n0 * row_bytes;
+    const char* up_base = gate_base + (GATED ? (int64_t)a.N * row_bytes : 0);
     wt_tile.init([&](int r) -> uint32_t {
       const int in = r % (CT * MF);
       const int ch = (r / (CT * MF)) * (CH * MF) + in % (CH * MF);
@@ -117,17 +117,14 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
     }
 
     constexpr int kPeriod = GATED ? CT * MF : 1 << 20;
-    auto load = [&](int k, lds_char* buf) {
+    constexpr int kWBlocks = wt_tile.kBlocks, kBlocks = kWBlocks + x_tile.kBlocks;
+    auto load = [&](int k, lds_char* buf, int b) {
       const int64_t at = (int64_t)k * 128;
-      if (FP8 || k < nfull) {  // FP8 rows are whole groups of 128 channels
-        wt_tile.template load<kPeriod>(gate_base + at, up, buf);
-        x_tile.template load<1 << 20>(x_base + at, 0, buf + S::BN * 128);
-      } else {
-        const int left = (int)(row_bytes - at);
-        wt_tile.template load_tail<kPeriod>(gate_base + at, up, left, buf);
-        x_tile.template load_tail<1 << 20>(x_base + at, 0, left, buf + S::BN * 128);
-      }
-      if (FP8) {
+      if (b < kWBlocks)
+        wt_tile.template load<kPeriod>(b, gate_base + at, up_base + at, buf);
+      else
+        x_tile.template load<1 << 20>(b - kWBlocks, x_base + at, nullptr, buf + S::BN * 128);
+      if (FP8 && b == kBlocks - 1) {
 #pragma unroll
         for (int l = 0; l < S::SLOADS; ++l)
           load_lds4<Q == EP_QUANT_FP8_UE8M0>(
@@ -135,17 +132,26 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
               (const lds_char*)&lds_scales[k % S::STAGES][wave][l * kWave]);
       }
     };
+    auto tail = [&](int k, lds_char* buf) {
+      const int64_t at = (int64_t)k * 128;
+      const int left = (int)(row_bytes - at);
+      wt_tile.template load_tail<kPeriod>(gate_base + at, up_base + at, left, buf);
+      x_tile.template load_tail<1 << 20>(x_base + at, nullptr, left, buf + S::BN * 128);
+    };
 
     acc_t acc[CT][TT];
     clear<S>(acc);
     if constexpr (!FP8) {
-      products<S>(wt_tile, x_tile, (lds_char*)&lds[0][0], nk, load, acc);
+      products<S>(wt_tile, x_tile, (lds_char*)&lds[0][0], nk, nfull, load, tail, acc);
     } else {
       constexpr int kLoads = wt_tile.kPasses + x_tile.kPasses + S::SLOADS;
       barrier();  // the previous tile's reads
 #pragma unroll
       for (int k = 0; k < S::STAGES; ++k)
-        if (k < nk) load(k, (lds_char*)lds[k]);
+        if (k < nk) {
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) load(k, (lds_char*)lds[k], b);
+        }
       wait_stage<S::STAGES, kLoads>(0, nk);
       for (int k = 0; k < nk; ++k) {
         const lds_char* wl = (lds_char*)lds[k % S::STAGES];
@@ -185,7 +191,11 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
         }
         if (k + 1 < nk) {
           wait_stage<S::STAGES, kLoads>(k + 1, nk);
-          if (k + S::STAGES < nk) load(k + S::STAGES, (lds_char*)lds[k % S::STAGES]);
+          if (k + S::STAGES < nk) {
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+              load(k + S::STAGES, (lds_char*)lds[k % S::STAGES], b);
+          }
         }
       }
     }

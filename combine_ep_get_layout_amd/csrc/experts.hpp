@@ -7,6 +7,8 @@
 // row and stores them as one 8-byte vector.
 #pragma once
 
+#include <type_traits>
+
 #include "ep_device.hpp"
 #include "ep_internal.hpp"
 
@@ -193,29 +195,29 @@ __device__ __forceinline__ int lds_offset(const lds_char* p) {
 // needs after such a write: every block begins with them.  M0 needs one more
 // after each change.
 
-// N (1, 2 or 4) loads from base + off[i] to dst + i * STEP
+// N (1, 2 or 4) loads from base[i] + off[i] to dst + i * STEP
 template <int STEP, int N>
-__device__ __forceinline__ void load_lds16(const char* base, const uint32_t (&off)[N],
+__device__ __forceinline__ void load_lds16(const char* const (&base)[N], const uint32_t (&off)[N],
                                            const lds_char* dst) {
   static_assert(N == 1 || N == 2 || N == 4, "");
   if constexpr (N == 4)
     asm volatile(
         "s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %5\n\t"
-        "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %5\n\t"
-        "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, %5\n\t"
-        "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, %5"
-        ::"s"(lds_offset(dst)), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(base),
-        "n"(STEP)
+        "s_add_u32 m0, m0, %9\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %6\n\t"
+        "s_add_u32 m0, m0, %9\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, %7\n\t"
+        "s_add_u32 m0, m0, %9\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, %8"
+        ::"s"(lds_offset(dst)), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]),
+        "s"(base[0]), "s"(base[1]), "s"(base[2]), "s"(base[3]), "n"(STEP)
         : "memory", "scc");
   else if constexpr (N == 2)
     asm volatile(
         "s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
-        "s_add_u32 m0, m0, %4\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3"
-        ::"s"(lds_offset(dst)), "v"(off[0]), "v"(off[1]), "s"(base), "n"(STEP)
+        "s_add_u32 m0, m0, %5\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %4"
+        ::"s"(lds_offset(dst)), "v"(off[0]), "v"(off[1]), "s"(base[0]), "s"(base[1]), "n"(STEP)
         : "memory", "scc");
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
-                 ::"s"(lds_offset(dst)), "v"(off[0]), "s"(base)
+                 ::"s"(lds_offset(dst)), "v"(off[0]), "s"(base[0])
                  : "memory");
 }
 
@@ -261,7 +263,8 @@ struct RowTile {
   static constexpr int kBytes = ROWS * 128;
   static constexpr int kPasses = (ROWS + 31) / 32;
   static constexpr int kBlock = kPasses < 4 ? kPasses : 4;  // loads issued together
-  uint32_t off[kPasses / kBlock][kBlock];
+  static constexpr int kBlocks = kPasses / kBlock;
+  uint32_t off[kBlocks][kBlock];
   int chunk;  // this lane's chunk of every row it fetches
 
   // row_of(r): byte offset of tile row r from the tile's base
@@ -273,36 +276,31 @@ struct RowTile {
     for (int p = 0; p < kPasses; ++p)
       off[p / kBlock][p % kBlock] = row_of((p * 32 + (tid >> 3)) % ROWS) + chunk * 16;
   }
-  // base: the tile's first byte of this step; the second half of every
-  // PERIOD rows comes from `second` bytes further on (a gated block's ups)
+  // Block b's loads.  base: the tile's first byte of this step; the second
+  // half of every PERIOD rows comes from `other` (a gated block's ups).
   template <int PERIOD>
-  __device__ __forceinline__ void load(const char* base, int64_t second, lds_char* lds) const {
+  __device__ __forceinline__ void load(int b, const char* base, const char* other,
+                                       lds_char* lds) const {
     const int wave = uniform(threadIdx.x >> 6);
-    if constexpr (PERIOD >= ROWS && PERIOD / 2 >= ROWS) {
+    const char* from[kBlock];
 #pragma unroll
-      for (int b = 0; b < kPasses / kBlock; ++b)
-        load_lds16<4096>(base, off[b], lds + (b * kBlock * 4096 + wave * 1024) % kBytes);
-    } else {
-#pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        const int r = p * 32 + wave * 8;  // 8 rows a wave, all in one half
-        const uint32_t one[1] = {off[p / kBlock][p % kBlock]};
-        load_lds16<0>(base + (r % PERIOD >= PERIOD / 2 ? second : 0), one,
-                      lds + p * 4096 + wave * 1024);
-      }
+    for (int q = 0; q < kBlock; ++q) {
+      // a wave's 8 rows of a pass are all in one half
+      const int r = (b * kBlock + q) * 32 + (PERIOD / 2 % 32 == 0 ? 0 : wave * 8);
+      from[q] = r % PERIOD >= PERIOD / 2 ? other : base;
     }
+    load_lds16<4096>(from, off[b], lds + (b * kBlock * 4096 + wave * 1024) % kBytes);
   }
   // the last step of rows with fewer than 128 bytes left
   template <int PERIOD>
-  __device__ __forceinline__ void load_tail(const char* base, int64_t second, int left,
+  __device__ __forceinline__ void load_tail(const char* base, const char* other, int left,
                                             lds_char* lds) const {
     const int wave = uniform(threadIdx.x >> 6);
     const bool in = chunk * 16 < left;
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
-      const int r = (p * 32 + wave * 8) % ROWS;
-      const char* src =
-          base + (r % PERIOD >= PERIOD / 2 ? second : 0) + off[p / kBlock][p % kBlock];
+      const int r = p * 32 + wave * 8;
+      const char* src = (r % PERIOD >= PERIOD / 2 ? other : base) + off[p / kBlock][p % kBlock];
       load_lds16(in ? src : (const char*)k_zeros, lds + (p * 4096 + wave * 1024) % kBytes);
     }
   }
@@ -326,7 +324,8 @@ struct ColTile {
   static constexpr int kRowsPerPass = kGemmThreads / kSlots;
   static_assert(COLS >= 128 && kRowsPerPass % 4 == 0, "a lane's rows agree modulo 4");
   static_assert(kPasses % 4 == 0, "");
-  uint32_t off[kPasses / 4][4];
+  static constexpr int kBlocks = kPasses / 4;
+  uint32_t off[kBlocks][4];
   int row;  // this lane's row in pass 0
 
   // cols: columns the operand has from the tile's first on (a multiple of 8)
@@ -338,11 +337,10 @@ struct ColTile {
     for (int p = 0; p < kPasses; ++p)  // past the last column: columns not stored
       off[p / 4][p % 4] = (row + p * kRowsPerPass) * row_bytes + min(chunk * 16, cols * 2 - 16);
   }
-  __device__ __forceinline__ void load(const char* base, lds_char* lds) const {
+  __device__ __forceinline__ void load(int b, const char* base, lds_char* lds) const {
     const int wave = uniform(threadIdx.x >> 6);
-#pragma unroll
-    for (int b = 0; b < kPasses / 4; ++b)
-      load_lds16<4096>(base, off[b], lds + b * 16384 + wave * 1024);
+    const char* from[4] = {base, base, base, base};
+    load_lds16<4096>(from, off[b], lds + b * 16384 + wave * 1024);
   }
   // the last step, with fewer than 64 contraction rows left
   __device__ __forceinline__ void load_tail(const char* base, int left, lds_char* lds) const {
@@ -494,58 +492,97 @@ __device__ __forceinline__ void clear(typename S::acc_t (&acc)[S::CT][S::TT]) {
       for (int q = 0; q < S::REGS; ++q) acc[i][j][q] = 0.0f;
 }
 
-// acc += the nk stages' products.  load(k, buf) issues stage k's loads into
-// buffer buf (the channel operand's tile, then the row operand's).  They are
-// issued S::STAGES stages ahead, into the buffer that the stage read last
-// leaves; a stage's last fragments are in registers before its buffer is given
-// up, so its last products cover the barrier, the new loads' issue and the
-// first reads of the next stage.
-template <class S, class Chan, class Row, class Load>
+// acc += the nk stages' products.  load(k, buf, b) issues block b of stage k's
+// loads into buffer buf (first the channel operand's blocks, then the row
+// operand's); tail(k, buf) all loads of a short last stage; the first nfull
+// stages are full.
+//
+// Loads are issued S::STAGES stages ahead, into the buffer that the stage read
+// last leaves.  A stage's last fragments are in registers before its buffer is
+// given up, so its last products cover the barrier, the issue of the new loads
+// and the first reads of the next stage.  Within a step, the reads of the next
+// step's fragments and the loads are spread between the products, and the
+// order is pinned: left to itself the compiler moves the products before the
+// barrier and the reads behind it, which leaves the matrix cores idle for a
+// barrier and an LDS round trip per stage.
+template <class S, class Chan, class Row, class Load, class Tail>
 __device__ __forceinline__ void products(const Chan& ct, const Row& rt, lds_char* lds, int nk,
-                                         Load load, typename S::acc_t (&acc)[S::CT][S::TT]) {
+                                         int nfull, Load load, Tail tail,
+                                         typename S::acc_t (&acc)[S::CT][S::TT]) {
   constexpr int kStage = Chan::kBytes + Row::kBytes;
   constexpr int kLoads = Chan::kPasses + Row::kPasses;
+  constexpr int kBlocks = Chan::kBlocks + Row::kBlocks;
+  constexpr int CT = S::CT, TT = S::TT, KK = S::KK;
   const int wave = uniform(threadIdx.x >> 6);
   const int wc = wave % S::WC, wr = wave / S::WC;
+  auto load_any = [&](int k, lds_char* buf) {
+    if (k < nfull) {
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) load(k, buf, b);
+    } else {
+      tail(k, buf);
+    }
+  };
   barrier();  // the previous tile's reads
 #pragma unroll
   for (int k = 0; k < S::STAGES; ++k)
-    if (k < nk) load(k, lds + k * kStage);
+    if (k < nk) load_any(k, lds + k * kStage);
   if (nk == 0) return;
   wait_stage<S::STAGES, kLoads>(0, nk);
-  bf16x8 fa[2][S::CT], fb[2][S::TT];
-  auto read = [&](int buf, int kk, int to) {
-    const lds_char* cl = lds + buf * kStage;
-#pragma unroll
-    for (int i = 0; i < S::CT; ++i)
-      fa[to][i] = fragment<S::MF>(ct, cl, (wc * S::CT + i) * S::MF, kk);
-#pragma unroll
-    for (int j = 0; j < S::TT; ++j)
-      fb[to][j] = fragment<S::MF>(rt, cl + Chan::kBytes, (wr * S::TT + j) * S::MF, kk);
+  bf16x8 fa[2][CT], fb[2][TT];
+  auto read_chan = [&](lds_char* buf, int kk, int to, int i) {
+    fa[to][i] = fragment<S::MF>(ct, buf, (wc * CT + i) * S::MF, kk);
   };
-  auto multiply = [&](int from) {
+  auto read_row = [&](lds_char* buf, int kk, int to, int j) {
+    fb[to][j] = fragment<S::MF>(rt, buf + Chan::kBytes, (wr * TT + j) * S::MF, kk);
+  };
+  // One step: the products of the fragments `from`, and the reads of the next
+  // step's; FRESH: with block loads of stage k into `into`.
+  auto step = [&](lds_char* buf, int kk, int from, auto read_next, auto fresh, int k,
+                  lds_char* into) {
 #pragma unroll
-    for (int i = 0; i < S::CT; ++i)
+    for (int i = 0; i < CT; ++i) {
+      if constexpr (decltype(fresh)::value) {
 #pragma unroll
-      for (int j = 0; j < S::TT; ++j)
+        for (int b = i * kBlocks / CT; b < (i + 1) * kBlocks / CT; ++b) load(k, into, b);
+      }
+      if constexpr (decltype(read_next)::value) {
+        read_chan(buf, kk, from ^ 1, i);
+#pragma unroll
+        for (int j = i * TT / CT; j < (i + 1) * TT / CT; ++j) read_row(buf, kk, from ^ 1, j);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < TT; ++j)
         acc[i][j] = Mfma<S::MF>::bf16(fa[from][i], fb[from][j], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
-  read(0, 0, 0);
-  int buf = 0;
-  for (int k = 0; k < nk; ++k) {
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
 #pragma unroll
-    for (int kk = 0; kk < S::KK - 1; ++kk) {
-      read(buf, kk + 1, (kk + 1) & 1);
-      multiply(kk & 1);
-    }
-    const int now = buf;
-    buf = buf + 1 == S::STAGES ? 0 : buf + 1;
-    if (k + 1 < nk) {
-      wait_stage<S::STAGES, kLoads>(k + 1, nk);
-      if (k + S::STAGES < nk) load(k + S::STAGES, lds + now * kStage);
-      read(buf, 0, 0);
-    }
-    multiply((S::KK - 1) & 1);
+  for (int i = 0; i < CT; ++i) read_chan(lds, 0, 0, i);
+#pragma unroll
+  for (int j = 0; j < TT; ++j) read_row(lds, 0, 0, j);
+  static_assert(KK % 2 == 0, "a stage ends on the fragments it began with");
+  lds_char* buf = lds;
+  int k = 0;
+  for (; k + S::STAGES < nfull; ++k) {
+#pragma unroll
+    for (int kk = 0; kk < KK - 1; ++kk) step(buf, kk + 1, kk & 1, yes, no, 0, nullptr);
+    lds_char* now = buf;
+    buf = buf + kStage == lds + S::STAGES * kStage ? lds : buf + kStage;
+    wait_stage<S::STAGES, kLoads>(k + 1, nk);
+    step(buf, 0, 1, yes, yes, k + S::STAGES, now);
+  }
+  for (; k < nk; ++k) {  // the last stages
+#pragma unroll
+    for (int kk = 0; kk < KK - 1; ++kk) step(buf, kk + 1, kk & 1, yes, no, 0, nullptr);
+    lds_char* now = buf;
+    buf = buf + kStage == lds + S::STAGES * kStage ? lds : buf + kStage;
+    if (k + 1 < nk) wait_stage<S::STAGES, kLoads>(k + 1, nk);
+    if (k + S::STAGES < nk) tail(k + S::STAGES, now);
+    step(buf, 0, 1, yes, no, 0, nullptr);  // past the last stage the reads go unused
   }
 }
 

@@ -131,20 +131,22 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_dx(GradArgs a) {
     const char* z_base = (const char*)a.dz + (start + row0) * z_bytes;
     w_tile.init((uint32_t)w_bytes, a.C - n0);
     z_tile.init([&](int r) -> uint32_t { return (uint32_t)(min(r, rows - 1) * z_bytes); });
-    auto load = [&](int k, lds_char* buf) {
-      const char* w = w_base + (int64_t)k * 64 * w_bytes;
-      const char* z = z_base + (int64_t)k * 128;
-      if (k < nfull) {
-        w_tile.load(w, buf);
-        z_tile.template load<1 << 20>(z, 0, buf + w_tile.kBytes);
-      } else {
-        w_tile.load_tail(w, a.O - k * 64, buf);
-        z_tile.template load_tail<1 << 20>(z, 0, (a.O - k * 64) * 2, buf + w_tile.kBytes);
-      }
+    auto load = [&](int k, lds_char* buf, int b) {
+      if (b < w_tile.kBlocks)
+        w_tile.load(b, w_base + (int64_t)k * 64 * w_bytes, buf);
+      else
+        z_tile.template load<1 << 20>(b - w_tile.kBlocks, z_base + (int64_t)k * 128, nullptr,
+                                      buf + w_tile.kBytes);
+    };
+    auto tail = [&](int k, lds_char* buf) {
+      const int left = a.O - k * 64;
+      w_tile.load_tail(w_base + (int64_t)k * 64 * w_bytes, left, buf);
+      z_tile.template load_tail<1 << 20>(z_base + (int64_t)k * 128, nullptr, left * 2,
+                                         buf + w_tile.kBytes);
     };
     typename S::acc_t acc[S::CT][S::TT];
     clear<S>(acc);
-    products<S>(w_tile, z_tile, (lds_char*)&lds[0][0], nk, load, acc);
+    products<S>(w_tile, z_tile, (lds_char*)&lds[0][0], nk, nfull, load, tail, acc);
     turn_out<S, S::CT>((lds_char*)&lds[0][0], acc, [&](int r, int c, const lds_float* from) {
       const int ch = n0 + wc * S::CT * S::MF + c;
       if (r < rows && ch < a.C) {
@@ -188,20 +190,19 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_dw(GradArgs a) {
   x_tile.init((uint32_t)x_bytes, a.C - c0);
   z_tile.init((uint32_t)z_bytes, a.O - o0);
   const int nk = (count + 63) / 64, nfull = count / 64;
-  auto load = [&](int k, lds_char* buf) {
-    const char* x = x_base + (int64_t)k * 64 * x_bytes;
-    const char* z = z_base + (int64_t)k * 64 * z_bytes;
-    if (k < nfull) {
-      x_tile.load(x, buf);
-      z_tile.load(z, buf + x_tile.kBytes);
-    } else {
-      x_tile.load_tail(x, count - k * 64, buf);
-      z_tile.load_tail(z, count - k * 64, buf + x_tile.kBytes);
-    }
+  auto load = [&](int k, lds_char* buf, int b) {
+    if (b < x_tile.kBlocks)
+      x_tile.load(b, x_base + (int64_t)k * 64 * x_bytes, buf);
+    else
+      z_tile.load(b - x_tile.kBlocks, z_base + (int64_t)k * 64 * z_bytes, buf + x_tile.kBytes);
+  };
+  auto tail = [&](int k, lds_char* buf) {
+    x_tile.load_tail(x_base + (int64_t)k * 64 * x_bytes, count - k * 64, buf);
+    z_tile.load_tail(z_base + (int64_t)k * 64 * z_bytes, count - k * 64, buf + x_tile.kBytes);
   };
   typename S::acc_t acc[S::CT][S::TT];
   clear<S>(acc);
-  products<S>(x_tile, z_tile, (lds_char*)&lds[0][0], nk, load, acc);
+  products<S>(x_tile, z_tile, (lds_char*)&lds[0][0], nk, nfull, load, tail, acc);
   uint16_t* dw = a.dw + (int64_t)e * a.O * a.C;
   turn_out<S, S::CT>((lds_char*)&lds[0][0], acc, [&](int r, int c, const lds_float* from) {
     const int ch = c0 + wc * S::CT * S::MF + c, o = o0 + r;
