@@ -53,7 +53,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
   constexpr int CH = GATED ? CT / 2 : CT;      // channel tiles of the output per wave
   constexpr int ON = GATED ? S::BN / 2 : S::BN;  // output channels per workgroup tile
   typedef typename S::acc_t acc_t;
-  __shared__ __align__(16) char lds[S::STAGES][(S::BN + S::BM) * 128];
+  __shared__ __align__(16) char lds[S::STAGES][(S::BN + S::BM) * S::KB];
   // FP8: every wave's own copy of its rows' scales
   __shared__ float lds_scales[FP8 ? S::STAGES : 1][4][FP8 ? S::SLOADS * kWave : 1];
   __shared__ TilePlan<kGemmThreads> plan;
@@ -66,7 +66,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
   const int64_t tiles = (int64_t)mt * nt;
   const int esize = FP8 ? 1 : 2;
   const int64_t row_bytes = (int64_t)a.C * esize;
-  const int nk = (int)((row_bytes + 127) / 128), nfull = (int)(row_bytes / 128);
+  const int nk = (int)((row_bytes + S::KB - 1) / S::KB), nfull = (int)(row_bytes / S::KB);
 
   for (int64_t t = block_place(); t < tiles; t += gridDim.x) {
     int m, n;
@@ -79,8 +79,8 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
     const int rows = min(count - row0, S::BM);
     const int n0 = n * ON;
 
-    RowTile<S::BN> wt_tile;
-    RowTile<S::BM> x_tile;
+    RowTile<S::BN, S::KB> wt_tile;
+    RowTile<S::BM, S::KB> x_tile;
     const char* w_base = a.w + (int64_t)e * (GATED ? 2 : 1) * a.N * row_bytes;
     const char* x_base = a.x + (start + row0) * row_bytes;
     // rows and channels past the end repeat the last one; they are not stored
@@ -117,14 +117,14 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
     }
 
     constexpr int kPeriod = GATED ? CT * MF : 1 << 20;
-    constexpr int kWBlocks = wt_tile.kBlocks, kBlocks = kWBlocks + x_tile.kBlocks;
-    auto load = [&](int k, lds_char* buf, int b) {
-      const int64_t at = (int64_t)k * 128;
-      if (b < kWBlocks)
-        wt_tile.template load<kPeriod>(b, gate_base + at, up_base + at, buf);
+    constexpr int kWPasses = wt_tile.kPasses, kPasses = kWPasses + x_tile.kPasses;
+    auto load = [&](int k, lds_char* buf, int p) {
+      const int64_t at = (int64_t)k * S::KB;
+      if (p < kWPasses)
+        wt_tile.template load<kPeriod>(p, gate_base + at, up_base + at, buf);
       else
-        x_tile.template load<1 << 20>(b - kWBlocks, x_base + at, nullptr, buf + S::BN * 128);
-      if (FP8 && b == kBlocks - 1) {
+        x_tile.template load<1 << 20>(p - kWPasses, x_base + at, nullptr, buf + wt_tile.kBytes);
+      if (FP8 && p == kPasses - 1) {
 #pragma unroll
         for (int l = 0; l < S::SLOADS; ++l)
           load_lds4<Q == EP_QUANT_FP8_UE8M0>(
@@ -133,10 +133,10 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
       }
     };
     auto tail = [&](int k, lds_char* buf) {
-      const int64_t at = (int64_t)k * 128;
+      const int64_t at = (int64_t)k * S::KB;
       const int left = (int)(row_bytes - at);
       wt_tile.template load_tail<kPeriod>(gate_base + at, up_base + at, left, buf);
-      x_tile.template load_tail<1 << 20>(x_base + at, nullptr, left, buf + S::BN * 128);
+      x_tile.template load_tail<1 << 20>(x_base + at, nullptr, left, buf + wt_tile.kBytes);
     };
 
     acc_t acc[CT][TT];
@@ -150,12 +150,12 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
       for (int k = 0; k < S::STAGES; ++k)
         if (k < nk) {
 #pragma unroll
-          for (int b = 0; b < kBlocks; ++b) load(k, (lds_char*)lds[k], b);
+          for (int p = 0; p < kPasses; ++p) load(k, (lds_char*)lds[k], p);
         }
       wait_stage<S::STAGES, kLoads>(0, nk);
       for (int k = 0; k < nk; ++k) {
         const lds_char* wl = (lds_char*)lds[k % S::STAGES];
-        const lds_char* xl = wl + S::BN * 128;
+        const lds_char* xl = wl + wt_tile.kBytes;
         const float w0 = ws0[k], w1 = GATED ? ws1[k] : w0;
         float sx[TT];
 #pragma unroll
@@ -193,8 +193,8 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
           wait_stage<S::STAGES, kLoads>(k + 1, nk);
           if (k + S::STAGES < nk) {
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
-              load(k + S::STAGES, (lds_char*)lds[k % S::STAGES], b);
+            for (int p = 0; p < kPasses; ++p)
+              load(k + S::STAGES, (lds_char*)lds[k % S::STAGES], p);
           }
         }
       }
@@ -256,13 +256,13 @@ template <class S, bool GATED, int Q>
 static void launch(const ExpertArgs& a, int64_t rows, hipStream_t st) {
   const int on = GATED ? S::BN / 2 : S::BN;
   const int64_t tiles = ((rows + S::BM - 1) / S::BM + a.seg.E) * ((a.N + on - 1) / on);
-  const int per_cu = S::STAGES * (S::BN + S::BM) * 128 > 70 * 1024 ? 1 : 2;
+  const int per_cu = S::kLds > 70 * 1024 ? 1 : 2;
   const int64_t most = (int64_t)kCus * per_cu;
   hipLaunchKernelGGL((expert_forward<S, GATED, Q>), dim3((unsigned)min(tiles, most)),
                      dim3(kGemmThreads), 0, st, a);
 }
 
-typedef Shape<32, 4, 4, 2, 2, 2> Big;     // 256 channels x 256 rows
+typedef Shape<32, 4, 4, 2, 2, 4, 64> Big;  // 256 channels x 256 rows
 typedef Shape<32, 4, 2, 2, 2, 3> Big8;    // 256 x 128 (FP8 sums are scaled in vector registers)
 typedef Shape<32, 2, 2, 4, 1, 3> Medium;  // 256 x 64
 typedef Shape<16, 2, 1, 4, 1, 3> Small;   // 128 x 16

@@ -195,30 +195,11 @@ __device__ __forceinline__ int lds_offset(const lds_char* p) {
 // needs after such a write: every block begins with them.  M0 needs one more
 // after each change.
 
-// N (1, 2 or 4) loads from base[i] + off[i] to dst + i * STEP
-template <int STEP, int N>
-__device__ __forceinline__ void load_lds16(const char* const (&base)[N], const uint32_t (&off)[N],
-                                           const lds_char* dst) {
-  static_assert(N == 1 || N == 2 || N == 4, "");
-  if constexpr (N == 4)
-    asm volatile(
-        "s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %5\n\t"
-        "s_add_u32 m0, m0, %9\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %6\n\t"
-        "s_add_u32 m0, m0, %9\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, %7\n\t"
-        "s_add_u32 m0, m0, %9\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, %8"
-        ::"s"(lds_offset(dst)), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]),
-        "s"(base[0]), "s"(base[1]), "s"(base[2]), "s"(base[3]), "n"(STEP)
-        : "memory", "scc");
-  else if constexpr (N == 2)
-    asm volatile(
-        "s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
-        "s_add_u32 m0, m0, %5\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %4"
-        ::"s"(lds_offset(dst)), "v"(off[0]), "v"(off[1]), "s"(base[0]), "s"(base[1]), "n"(STEP)
-        : "memory", "scc");
-  else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
-                 ::"s"(lds_offset(dst)), "v"(off[0]), "s"(base[0])
-                 : "memory");
+// from base + off
+__device__ __forceinline__ void load_lds16(const char* base, uint32_t off, const lds_char* dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
+               ::"s"(lds_offset(dst)), "v"(off), "s"(base)
+               : "memory");
 }
 
 // 4 bytes a lane, or one byte zero-extended to four
@@ -252,46 +233,50 @@ __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
 }
 
-// Tile of ROWS rows x 128 bytes whose rows are contiguous along the
+// Tile of ROWS rows x KB bytes whose rows are contiguous along the
 // contraction.  An asynchronous load stores lane i's 16 bytes at the wave's
 // LDS base + 16 i, so the order in LDS is fixed and the lanes choose what
-// they fetch: slot j of row r holds chunk j ^ (r & 7).  Eight consecutive
-// rows' reads of one chunk then fall into eight different 16-byte columns,
-// which is every bank once.
-template <int ROWS>
+// they fetch: slot j of row r holds chunk j ^ turn(r).  The 64 banks are 256
+// bytes wide, 256 / KB rows; a 16-byte read is served 16 lanes at a time, and
+// any 16 of them that are four runs of four consecutive rows with different
+// row / 4 modulo 4, or sixteen consecutive rows, fall into sixteen different
+// columns when turn counts those groups of rows.  (With r modulo 8 alone a
+// 128-byte row's reads collided in pairs: 49% of the LDS's active cycles.)
+template <int ROWS, int KB = 128>
 struct RowTile {
-  static constexpr int kBytes = ROWS * 128;
-  static constexpr int kPasses = (ROWS + 31) / 32;
-  static constexpr int kBlock = kPasses < 4 ? kPasses : 4;  // loads issued together
-  static constexpr int kBlocks = kPasses / kBlock;
-  uint32_t off[kBlocks][kBlock];
+  static constexpr int kBytes = ROWS * KB;
+  static constexpr int kChunks = KB / 16;                     // of a row
+  static constexpr int kPassRows = 4096 / KB;                 // rows the workgroup fetches at once
+  static constexpr int kPasses = (ROWS + kPassRows - 1) / kPassRows;
+  static constexpr int kWaveRows = kPassRows / 4;
+  static __device__ __forceinline__ int turn(int r) {
+    return (r / (16 / kChunks)) & (kChunks - 1);
+  }
+  uint32_t off[kPasses];
   int chunk;  // this lane's chunk of every row it fetches
 
   // row_of(r): byte offset of tile row r from the tile's base
   template <class F>
   __device__ __forceinline__ void init(F row_of) {
     const int tid = threadIdx.x;
-    chunk = (tid & 7) ^ ((tid >> 3) & 7);
+    chunk = (tid % kChunks) ^ turn(tid / kChunks);  // every pass turns a row alike
+    static_assert(kPassRows % 16 == 0, "");
 #pragma unroll
     for (int p = 0; p < kPasses; ++p)
-      off[p / kBlock][p % kBlock] = row_of((p * 32 + (tid >> 3)) % ROWS) + chunk * 16;
+      off[p] = row_of((p * kPassRows + tid / kChunks) % ROWS) + chunk * 16;
   }
-  // Block b's loads.  base: the tile's first byte of this step; the second
-  // half of every PERIOD rows comes from `other` (a gated block's ups).
+  // Pass p's load.  base: the tile's first byte of this step; the second half
+  // of every PERIOD rows comes from `other` (a gated block's ups).
   template <int PERIOD>
-  __device__ __forceinline__ void load(int b, const char* base, const char* other,
+  __device__ __forceinline__ void load(int p, const char* base, const char* other,
                                        lds_char* lds) const {
     const int wave = uniform(threadIdx.x >> 6);
-    const char* from[kBlock];
-#pragma unroll
-    for (int q = 0; q < kBlock; ++q) {
-      // a wave's 8 rows of a pass are all in one half
-      const int r = (b * kBlock + q) * 32 + (PERIOD / 2 % 32 == 0 ? 0 : wave * 8);
-      from[q] = r % PERIOD >= PERIOD / 2 ? other : base;
-    }
-    load_lds16<4096>(from, off[b], lds + (b * kBlock * 4096 + wave * 1024) % kBytes);
+    // a wave's rows of a pass are all in one half
+    const int r = p * kPassRows + (PERIOD / 2 % kPassRows == 0 ? 0 : wave * kWaveRows);
+    load_lds16(r % PERIOD >= PERIOD / 2 ? other : base, off[p],
+               lds + (p * 4096 + wave * 1024) % kBytes);
   }
-  // the last step of rows with fewer than 128 bytes left
+  // the last step of rows with fewer than KB bytes left
   template <int PERIOD>
   __device__ __forceinline__ void load_tail(const char* base, const char* other, int left,
                                             lds_char* lds) const {
@@ -299,33 +284,32 @@ struct RowTile {
     const bool in = chunk * 16 < left;
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
-      const int r = p * 32 + wave * 8;
-      const char* src = (r % PERIOD >= PERIOD / 2 ? other : base) + off[p / kBlock][p % kBlock];
+      const int r = p * kPassRows + wave * kWaveRows;
+      const char* src = (r % PERIOD >= PERIOD / 2 ? other : base) + off[p];
       load_lds16(in ? src : (const char*)k_zeros, lds + (p * 4096 + wave * 1024) % kBytes);
     }
   }
 };
 
 // 16-byte chunk c of row r
+template <class Tile>
 __device__ __forceinline__ i32x4 row_chunk(const lds_char* lds, int r, int c) {
-  return *(const EP_LDS i32x4*)(lds + r * 128 + ((c ^ (r & 7)) << 4));
+  return *(const EP_LDS i32x4*)(lds + r * (Tile::kChunks * 16) + ((c ^ Tile::turn(r)) << 4));
 }
 
-// Tile of 64 contraction rows x COLS bf16 whose rows run across the
+// Tile of KR contraction rows x COLS bf16 whose rows run across the
 // contraction (the operand is read transposed).  Slot j of row k holds
 // 16-byte chunk j ^ 4 (k & 3): a transposed read takes 32 columns (64 bytes)
 // of four consecutive rows, which the exclusive-or sends to four different
 // quarters of the banks.
-template <int COLS>
+template <int COLS, int KR = 64>
 struct ColTile {
-  static constexpr int kBytes = 64 * COLS * 2;
+  static constexpr int kBytes = KR * COLS * 2;
   static constexpr int kSlots = COLS / 8;
   static constexpr int kPasses = kBytes / 4096;
   static constexpr int kRowsPerPass = kGemmThreads / kSlots;
   static_assert(COLS >= 128 && kRowsPerPass % 4 == 0, "a lane's rows agree modulo 4");
-  static_assert(kPasses % 4 == 0, "");
-  static constexpr int kBlocks = kPasses / 4;
-  uint32_t off[kBlocks][4];
+  uint32_t off[kPasses];
   int row;  // this lane's row in pass 0
 
   // cols: columns the operand has from the tile's first on (a multiple of 8)
@@ -335,19 +319,17 @@ struct ColTile {
     const int chunk = (tid % kSlots) ^ ((row & 3) << 2);
 #pragma unroll
     for (int p = 0; p < kPasses; ++p)  // past the last column: columns not stored
-      off[p / 4][p % 4] = (row + p * kRowsPerPass) * row_bytes + min(chunk * 16, cols * 2 - 16);
+      off[p] = (row + p * kRowsPerPass) * row_bytes + min(chunk * 16, cols * 2 - 16);
   }
-  __device__ __forceinline__ void load(int b, const char* base, lds_char* lds) const {
-    const int wave = uniform(threadIdx.x >> 6);
-    const char* from[4] = {base, base, base, base};
-    load_lds16<4096>(from, off[b], lds + b * 16384 + wave * 1024);
+  __device__ __forceinline__ void load(int p, const char* base, lds_char* lds) const {
+    load_lds16(base, off[p], lds + p * 4096 + uniform(threadIdx.x >> 6) * 1024);
   }
-  // the last step, with fewer than 64 contraction rows left
+  // the last step, with fewer than KR contraction rows left
   __device__ __forceinline__ void load_tail(const char* base, int left, lds_char* lds) const {
     const int wave = uniform(threadIdx.x >> 6);
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
-      const char* src = base + off[p / 4][p % 4];
+      const char* src = base + off[p];
       load_lds16(row + p * kRowsPerPass < left ? src : (const char*)k_zeros,
                  lds + p * 4096 + wave * 1024);
     }
@@ -364,19 +346,21 @@ __device__ __forceinline__ s16x4 read_tr(const lds_char* p) {
 // 8 (l / 32) .. + 7; 16x16x32 (MF = 16): index l % 16, elements 8 (l / 16) .. + 7.
 // Step kk covers contraction elements kk * 512 / MF .. of the tile's 64.
 
-template <int MF, int ROWS>
-__device__ __forceinline__ bf16x8 fragment(const RowTile<ROWS>&, const lds_char* lds, int first, int kk) {
+template <int MF, int ROWS, int KB>
+__device__ __forceinline__ bf16x8 fragment(const RowTile<ROWS, KB>&, const lds_char* lds, int first,
+                                           int kk) {
   const int lane = lane_id();
-  return __builtin_bit_cast(
-      bf16x8, row_chunk(lds, first + lane % MF, kk * (kWave / MF) + lane / MF));
+  return __builtin_bit_cast(bf16x8, row_chunk<RowTile<ROWS, KB>>(
+                                        lds, first + lane % MF, kk * (kWave / MF) + lane / MF));
 }
 
 // ds_read_b64_tr_b16: of each 16 lanes, lane s gives the address of four
 // columns of one row and lane i receives column i of the four rows that lanes
 // i / 4 + 4 j (j = 0..3) address: with lane s at row s / 4, columns
 // 4 (s % 4), lane i gets rows 0..3 of column i.
-template <int MF, int COLS>
-__device__ __forceinline__ bf16x8 fragment(const ColTile<COLS>&, const lds_char* lds, int first, int kk) {
+template <int MF, int COLS, int KR>
+__device__ __forceinline__ bf16x8 fragment(const ColTile<COLS, KR>&, const lds_char* lds, int first,
+                                           int kk) {
   const int lane = lane_id();
   const int k = kk * (512 / MF) + 8 * (lane / MF) + (lane % 16) / 4;
   const int col = first + (lane % MF) / 16 * 16 + 4 * (lane % 4);
@@ -397,8 +381,9 @@ __device__ __forceinline__ bf16x8 fragment(const ColTile<COLS>&, const lds_char*
 template <int MF, int ROWS>
 __device__ __forceinline__ i32x8 fragment8(const RowTile<ROWS>&, const lds_char* lds, int first, int kk) {
   const int lane = lane_id();
+  typedef RowTile<ROWS> Tile;
   const int r = first + lane % MF, c = 2 * (kk * (kWave / MF) + lane / MF);
-  const i32x4 a = row_chunk(lds, r, c), b = row_chunk(lds, r, c + 1);
+  const i32x4 a = row_chunk<Tile>(lds, r, c), b = row_chunk<Tile>(lds, r, c + 1);
   return i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
@@ -433,13 +418,15 @@ __device__ __forceinline__ int channel_of(int q) {
 }
 
 // Shape of a workgroup's tile: WC x WT waves, each CT x TT matrix-core tiles
-// of MF channels x MF rows; STAGES buffers of 64 contraction elements (128 in FP8).
-template <int MF_, int CT_, int TT_, int WC_, int WT_, int STAGES_>
+// of MF channels x MF rows; STAGES buffers of KB bytes along the contraction.
+template <int MF_, int CT_, int TT_, int WC_, int WT_, int STAGES_, int KB_ = 128>
 struct Shape {
+  static constexpr int KB = KB_, KR = KB / 2;
   static constexpr int MF = MF_, CT = CT_, TT = TT_, WC = WC_, WT = WT_, STAGES = STAGES_;
   static constexpr int BN = WC * CT * MF, BM = WT * TT * MF;
-  static constexpr int KK = MF / 8;        // bf16 matrix-core steps of a stage
-  static constexpr int KK8 = MF / 16;      // FP8 steps
+  static constexpr int KK = KR * MF / 512;  // bf16 matrix-core steps of a stage
+  static constexpr int KK8 = KB * MF / 2048;  // FP8 steps
+  static constexpr int kLds = STAGES * (BN + BM) * KB;
   static constexpr int REGS = MF * MF / kWave;
   static constexpr int WROWS = TT * MF;    // rows of a wave's tile
   static constexpr int SLOADS = (WROWS + kWave - 1) / kWave;  // FP8 scale loads of a stage
@@ -492,43 +479,44 @@ __device__ __forceinline__ void clear(typename S::acc_t (&acc)[S::CT][S::TT]) {
       for (int q = 0; q < S::REGS; ++q) acc[i][j][q] = 0.0f;
 }
 
-// acc += the nk stages' products.  load(k, buf, b) issues block b of stage k's
-// loads into buffer buf (first the channel operand's blocks, then the row
+// acc += the nk stages' products.  load(k, buf, p) issues pass p of stage k's
+// loads into buffer buf (first the channel operand's passes, then the row
 // operand's); tail(k, buf) all loads of a short last stage; the first nfull
 // stages are full.
 //
-// Loads are issued S::STAGES stages ahead, into the buffer that the stage read
-// last leaves.  A stage's last fragments are in registers before its buffer is
-// given up, so its last products cover the barrier, the issue of the new loads
-// and the first reads of the next stage.  Within a step, the reads of the next
-// step's fragments and the loads are spread between the products, and the
-// order is pinned: left to itself the compiler moves the products before the
-// barrier and the reads behind it, which leaves the matrix cores idle for a
-// barrier and an LDS round trip per stage.
+// While stage k is multiplied, stage k + STAGES - 1 is loaded into the buffer
+// that stage k - 1 left.  The loads and the reads of the next step's fragments
+// are spread evenly between the products and the order is pinned: a wave's
+// loads issued together wait for each other (four waves' sixteen 1 KiB loads
+// take the address unit about 1,000 cycles), and left to itself the compiler
+// moves the products before the barrier and the reads behind it, which leaves
+// the matrix cores idle for a barrier and an LDS round trip per stage.  A
+// stage's last products cover the barrier and the next stage's first reads.
 template <class S, class Chan, class Row, class Load, class Tail>
 __device__ __forceinline__ void products(const Chan& ct, const Row& rt, lds_char* lds, int nk,
                                          int nfull, Load load, Tail tail,
                                          typename S::acc_t (&acc)[S::CT][S::TT]) {
   constexpr int kStage = Chan::kBytes + Row::kBytes;
   constexpr int kLoads = Chan::kPasses + Row::kPasses;
-  constexpr int kBlocks = Chan::kBlocks + Row::kBlocks;
-  constexpr int CT = S::CT, TT = S::TT, KK = S::KK;
+  constexpr int CT = S::CT, TT = S::TT, KK = S::KK, STAGES = S::STAGES;
+  constexpr int kGroups = KK * CT;
+  static_assert(STAGES >= 3, "a stage is loaded while another one waits");
+  // loads issued after those of stage k + 1 by stage k's last step
+  constexpr int kAhead = kLoads * (STAGES - 3) + (KK - 1) * CT * kLoads / kGroups;
   const int wave = uniform(threadIdx.x >> 6);
   const int wc = wave % S::WC, wr = wave / S::WC;
-  auto load_any = [&](int k, lds_char* buf) {
-    if (k < nfull) {
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b) load(k, buf, b);
-    } else {
-      tail(k, buf);
-    }
-  };
   barrier();  // the previous tile's reads
 #pragma unroll
-  for (int k = 0; k < S::STAGES; ++k)
-    if (k < nk) load_any(k, lds + k * kStage);
+  for (int k = 0; k < STAGES - 1; ++k) {
+    if (k < nfull) {
+#pragma unroll
+      for (int p = 0; p < kLoads; ++p) load(k, lds + k * kStage, p);
+    } else if (k < nk) {
+      tail(k, lds + k * kStage);
+    }
+  }
   if (nk == 0) return;
-  wait_stage<S::STAGES, kLoads>(0, nk);
+  wait_stage<STAGES, kLoads>(0, nk);
   bf16x8 fa[2][CT], fb[2][TT];
   auto read_chan = [&](lds_char* buf, int kk, int to, int i) {
     fa[to][i] = fragment<S::MF>(ct, buf, (wc * CT + i) * S::MF, kk);
@@ -536,21 +524,20 @@ __device__ __forceinline__ void products(const Chan& ct, const Row& rt, lds_char
   auto read_row = [&](lds_char* buf, int kk, int to, int j) {
     fb[to][j] = fragment<S::MF>(rt, buf + Chan::kBytes, (wr * TT + j) * S::MF, kk);
   };
-  // One step: the products of the fragments `from`, and the reads of the next
-  // step's; FRESH: with block loads of stage k into `into`.
-  auto step = [&](lds_char* buf, int kk, int from, auto read_next, auto fresh, int k,
-                  lds_char* into) {
+  // Step kk's products, the reads of the next step (step `next` of buffer
+  // `buf`) and, where LOADS, its share of stage k's loads into `into`.
+  auto step = [&](int kk, lds_char* buf, int next, auto loads, int k, lds_char* into) {
+    const int from = kk & 1;
 #pragma unroll
     for (int i = 0; i < CT; ++i) {
-      if constexpr (decltype(fresh)::value) {
+      if constexpr (decltype(loads)::value) {
+        const int g = kk * CT + i;
 #pragma unroll
-        for (int b = i * kBlocks / CT; b < (i + 1) * kBlocks / CT; ++b) load(k, into, b);
+        for (int p = g * kLoads / kGroups; p < (g + 1) * kLoads / kGroups; ++p) load(k, into, p);
       }
-      if constexpr (decltype(read_next)::value) {
-        read_chan(buf, kk, from ^ 1, i);
+      read_chan(buf, next, from ^ 1, i);
 #pragma unroll
-        for (int j = i * TT / CT; j < (i + 1) * TT / CT; ++j) read_row(buf, kk, from ^ 1, j);
-      }
+      for (int j = i * TT / CT; j < (i + 1) * TT / CT; ++j) read_row(buf, next, from ^ 1, j);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < TT; ++j)
@@ -565,24 +552,30 @@ __device__ __forceinline__ void products(const Chan& ct, const Row& rt, lds_char
 #pragma unroll
   for (int j = 0; j < TT; ++j) read_row(lds, 0, 0, j);
   static_assert(KK % 2 == 0, "a stage ends on the fragments it began with");
+  auto after = [&](lds_char* b) { return b + kStage == lds + STAGES * kStage ? lds : b + kStage; };
   lds_char* buf = lds;
+  lds_char* into = lds + (STAGES - 1) * kStage;
   int k = 0;
-  for (; k + S::STAGES < nfull; ++k) {
+  for (; k + STAGES - 1 < nfull; ++k) {
 #pragma unroll
-    for (int kk = 0; kk < KK - 1; ++kk) step(buf, kk + 1, kk & 1, yes, no, 0, nullptr);
-    lds_char* now = buf;
-    buf = buf + kStage == lds + S::STAGES * kStage ? lds : buf + kStage;
-    wait_stage<S::STAGES, kLoads>(k + 1, nk);
-    step(buf, 0, 1, yes, yes, k + S::STAGES, now);
+    for (int kk = 0; kk < KK - 1; ++kk) step(kk, buf, kk + 1, yes, k + STAGES - 1, into);
+    wait_loads<kAhead>();
+    barrier();
+    step(KK - 1, after(buf), 0, yes, k + STAGES - 1, into);
+    into = buf;
+    buf = after(buf);
   }
   for (; k < nk; ++k) {  // the last stages
+    if (k + STAGES - 1 < nk) tail(k + STAGES - 1, into);
+    into = buf;
 #pragma unroll
-    for (int kk = 0; kk < KK - 1; ++kk) step(buf, kk + 1, kk & 1, yes, no, 0, nullptr);
-    lds_char* now = buf;
-    buf = buf + kStage == lds + S::STAGES * kStage ? lds : buf + kStage;
-    if (k + 1 < nk) wait_stage<S::STAGES, kLoads>(k + 1, nk);
-    if (k + S::STAGES < nk) tail(k + S::STAGES, now);
-    step(buf, 0, 1, yes, no, 0, nullptr);  // past the last stage the reads go unused
+    for (int kk = 0; kk < KK - 1; ++kk) step(kk, buf, kk + 1, no, 0, nullptr);
+    if (k + 1 < nk) {
+      wait_loads<0>();
+      barrier();
+    }
+    buf = after(buf);
+    step(KK - 1, buf, 0, no, 0, nullptr);  // past the last stage the reads go unused
   }
 }
 

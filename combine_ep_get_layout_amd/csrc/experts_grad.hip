@@ -106,7 +106,7 @@ __global__ __launch_bounds__(256) void expert_dbias(GradArgs a) {
 // weights across it.
 template <class S>
 __global__ __launch_bounds__(kGemmThreads, 1) void expert_dx(GradArgs a) {
-  __shared__ __align__(16) char lds[S::STAGES][(S::BN + S::BM) * 128];
+  __shared__ __align__(16) char lds[S::STAGES][(S::BN + S::BM) * S::KB];
   __shared__ TilePlan<kGemmThreads> plan;
   const int wave = uniform(threadIdx.x >> 6), wc = wave % S::WC;
   plan_tiles(a.seg, S::BM, plan);
@@ -114,7 +114,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_dx(GradArgs a) {
   const int nt = (a.C + S::BN - 1) / S::BN;
   const int64_t tiles = (int64_t)mt * nt;
   const int64_t z_bytes = (int64_t)a.O * 2, w_bytes = (int64_t)a.C * 2;
-  const int nk = (a.O + 63) / 64, nfull = a.O / 64;
+  const int nk = (a.O + S::KR - 1) / S::KR, nfull = a.O / S::KR;
   for (int64_t t = block_place(); t < tiles; t += gridDim.x) {
     int m, n;
     tile_at(t, mt, nt, m, n);
@@ -125,23 +125,23 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_dx(GradArgs a) {
     const int row0 = (m - plan.first[e]) * S::BM;
     const int rows = min(count - row0, S::BM);
     const int n0 = n * S::BN;
-    ColTile<S::BN> w_tile;
-    RowTile<S::BM> z_tile;
+    ColTile<S::BN, S::KR> w_tile;
+    RowTile<S::BM, S::KB> z_tile;
     const char* w_base = (const char*)a.w + (int64_t)e * a.O * w_bytes + n0 * 2;
     const char* z_base = (const char*)a.dz + (start + row0) * z_bytes;
     w_tile.init((uint32_t)w_bytes, a.C - n0);
     z_tile.init([&](int r) -> uint32_t { return (uint32_t)(min(r, rows - 1) * z_bytes); });
-    auto load = [&](int k, lds_char* buf, int b) {
-      if (b < w_tile.kBlocks)
-        w_tile.load(b, w_base + (int64_t)k * 64 * w_bytes, buf);
+    auto load = [&](int k, lds_char* buf, int p) {
+      if (p < w_tile.kPasses)
+        w_tile.load(p, w_base + (int64_t)k * S::KR * w_bytes, buf);
       else
-        z_tile.template load<1 << 20>(b - w_tile.kBlocks, z_base + (int64_t)k * 128, nullptr,
+        z_tile.template load<1 << 20>(p - w_tile.kPasses, z_base + (int64_t)k * S::KB, nullptr,
                                       buf + w_tile.kBytes);
     };
     auto tail = [&](int k, lds_char* buf) {
-      const int left = a.O - k * 64;
-      w_tile.load_tail(w_base + (int64_t)k * 64 * w_bytes, left, buf);
-      z_tile.template load_tail<1 << 20>(z_base + (int64_t)k * 128, nullptr, left * 2,
+      const int left = a.O - k * S::KR;
+      w_tile.load_tail(w_base + (int64_t)k * S::KR * w_bytes, left, buf);
+      z_tile.template load_tail<1 << 20>(z_base + (int64_t)k * S::KB, nullptr, left * 2,
                                          buf + w_tile.kBytes);
     };
     typename S::acc_t acc[S::CT][S::TT];
@@ -168,7 +168,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_dx(GradArgs a) {
 // dies alike.
 template <class S>
 __global__ __launch_bounds__(kGemmThreads, 1) void expert_dw(GradArgs a) {
-  __shared__ __align__(16) char lds[S::STAGES][(S::BN + S::BM) * 128];
+  __shared__ __align__(16) char lds[S::STAGES][(S::BN + S::BM) * S::KB];
   const int wave = uniform(threadIdx.x >> 6), wc = wave % S::WC;
   const int ct = (a.C + S::BN - 1) / S::BN, ot = (a.O + S::BM - 1) / S::BM;
   constexpr int kRun = 32;
@@ -183,22 +183,22 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_dw(GradArgs a) {
   segment_of(a.seg, e, start, count);
   const int c0 = n * S::BN, o0 = m * S::BM;
   const int64_t x_bytes = (int64_t)a.C * 2, z_bytes = (int64_t)a.O * 2;
-  ColTile<S::BN> x_tile;
-  ColTile<S::BM> z_tile;
+  ColTile<S::BN, S::KR> x_tile;
+  ColTile<S::BM, S::KR> z_tile;
   const char* x_base = (const char*)a.x + start * x_bytes + c0 * 2;
   const char* z_base = (const char*)a.dz + start * z_bytes + o0 * 2;
   x_tile.init((uint32_t)x_bytes, a.C - c0);
   z_tile.init((uint32_t)z_bytes, a.O - o0);
-  const int nk = (count + 63) / 64, nfull = count / 64;
-  auto load = [&](int k, lds_char* buf, int b) {
-    if (b < x_tile.kBlocks)
-      x_tile.load(b, x_base + (int64_t)k * 64 * x_bytes, buf);
+  const int nk = (count + S::KR - 1) / S::KR, nfull = count / S::KR;
+  auto load = [&](int k, lds_char* buf, int p) {
+    if (p < x_tile.kPasses)
+      x_tile.load(p, x_base + (int64_t)k * S::KR * x_bytes, buf);
     else
-      z_tile.load(b - x_tile.kBlocks, z_base + (int64_t)k * 64 * z_bytes, buf + x_tile.kBytes);
+      z_tile.load(p - x_tile.kPasses, z_base + (int64_t)k * S::KR * z_bytes, buf + x_tile.kBytes);
   };
   auto tail = [&](int k, lds_char* buf) {
-    x_tile.load_tail(x_base + (int64_t)k * 64 * x_bytes, count - k * 64, buf);
-    z_tile.load_tail(z_base + (int64_t)k * 64 * z_bytes, count - k * 64, buf + x_tile.kBytes);
+    x_tile.load_tail(x_base + (int64_t)k * S::KR * x_bytes, count - k * S::KR, buf);
+    z_tile.load_tail(z_base + (int64_t)k * S::KR * z_bytes, count - k * S::KR, buf + x_tile.kBytes);
   };
   typename S::acc_t acc[S::CT][S::TT];
   clear<S>(acc);
@@ -217,7 +217,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_dw(GradArgs a) {
 
 // ---- launches ------------------------------------------------------------------
 
-typedef Shape<32, 4, 4, 2, 2, 2> Big;     // 256 channels x 256 rows
+typedef Shape<32, 4, 4, 2, 2, 4, 64> Big;  // 256 channels x 256 rows
 typedef Shape<32, 2, 2, 4, 1, 3> Medium;  // 256 x 64
 typedef Shape<16, 2, 1, 4, 1, 3> Small;   // 128 x 16
 typedef Shape<32, 2, 2, 2, 2, 3> Square;  // 128 x 128
@@ -225,7 +225,7 @@ typedef Shape<32, 2, 2, 2, 2, 3> Square;  // 128 x 128
 template <class S>
 static void launch_dx(const GradArgs& a, hipStream_t st) {
   const int64_t tiles = ((a.rows + S::BM - 1) / S::BM + a.seg.E) * ((a.C + S::BN - 1) / S::BN);
-  const int per_cu = S::STAGES * (S::BN + S::BM) * 128 > 70 * 1024 ? 1 : 2;
+  const int per_cu = S::kLds > 70 * 1024 ? 1 : 2;
   hipLaunchKernelGGL(expert_dx<S>, dim3((unsigned)min(tiles, (int64_t)kCus * per_cu)),
                      dim3(kGemmThreads), 0, st, a);
 }
