@@ -262,7 +262,7 @@ static void launch(const ExpertArgs& a, int64_t rows, hipStream_t st) {
                      dim3(kGemmThreads), 0, st, a);
 }
 
-typedef Shape<32, 4, 4, 2, 2, 4, 64> Big;  // 256 channels x 256 rows
+typedef Shape<32, 4, 4, 2, 2, 2> Big;     // 256 channels x 256 rows
 typedef Shape<32, 4, 2, 2, 2, 3> Big8;    // 256 x 128 (FP8 sums are scaled in vector registers)
 typedef Shape<32, 2, 2, 4, 1, 3> Medium;  // 256 x 64
 typedef Shape<16, 2, 1, 4, 1, 3> Small;   // 128 x 16

@@ -493,7 +493,7 @@ __device__ __forceinline__ void clear(typename S::acc_t (&acc)[S::CT][S::TT]) {
 // the matrix cores idle for a barrier and an LDS round trip per stage.  A
 // stage's last products cover the barrier and the next stage's first reads.
 template <class S, class Chan, class Row, class Load, class Tail>
-__device__ __forceinline__ void products(const Chan& ct, const Row& rt, lds_char* lds, int nk,
+__device__ __forceinline__ void products_ring(const Chan& ct, const Row& rt, lds_char* lds, int nk,
                                          int nfull, Load load, Tail tail,
                                          typename S::acc_t (&acc)[S::CT][S::TT]) {
   constexpr int kStage = Chan::kBytes + Row::kBytes;
@@ -577,6 +577,117 @@ __device__ __forceinline__ void products(const Chan& ct, const Row& rt, lds_char
     buf = after(buf);
     step(KK - 1, buf, 0, no, 0, nullptr);  // past the last stage the reads go unused
   }
+}
+
+// The same for tiles so large that only two stages fit (256 x 256: their
+// fragments, 128 registers a lane, are the third).  Fragment set s (the
+// operands of step s, four steps a stage) is read one step after the products
+// that used its registers:
+//   step 0 of stage k:  reads set 3 of stage k; then buffer k is read out
+//   barrier:            ... and stage k + 1 has arrived in the other one
+//   steps 1, 2, 3:      read sets 0, 1, 2 of stage k + 1; steps 1 and 2 load
+//                       stage k + 2 into buffer k
+// so a load has two to four steps (16 products of 32 cycles a wave each) to
+// arrive and rows are fetched as whole 128-byte lines.  64-byte stages, four
+// of which fit, were tried first: their loads alone take 1.54 ms at 16
+// experts x 2,048 rows x 7168 x 4096, those of 128 bytes 1.04 ms.
+template <class S, class Chan, class Row, class Load, class Tail>
+__device__ __forceinline__ void products_deep(const Chan& ct, const Row& rt, lds_char* lds, int nk,
+                                              int nfull, Load load, Tail tail,
+                                              typename S::acc_t (&acc)[S::CT][S::TT]) {
+  constexpr int kStage = Chan::kBytes + Row::kBytes;
+  constexpr int kLoads = Chan::kPasses + Row::kPasses;
+  constexpr int CT = S::CT, TT = S::TT;
+  static_assert(S::STAGES == 2 && S::KK == 4, "");
+  const int wave = uniform(threadIdx.x >> 6);
+  const int wc = wave % S::WC, wr = wave / S::WC;
+  auto load_any = [&](int k, lds_char* buf) {
+    if (k < nfull) {
+#pragma unroll
+      for (int p = 0; p < kLoads; ++p) load(k, buf, p);
+    } else if (k < nk) {
+      tail(k, buf);
+    }
+  };
+  if (nk == 0) return;
+  barrier();  // the previous tile's reads
+  load_any(0, lds);
+  load_any(1, lds + kStage);
+  if (nk > 1)
+    wait_loads<kLoads>();
+  else
+    wait_loads<0>();
+  barrier();
+  bf16x8 fa[4][CT], fb[4][TT];
+  auto read = [&](lds_char* buf, int set, int n) {  // the n-th fragment of a set
+    if (n < CT)
+      fa[set][n] = fragment<S::MF>(ct, buf, (wc * CT + n) * S::MF, set);
+    else
+      fb[set][n - CT] = fragment<S::MF>(rt, buf + Chan::kBytes, (wr * TT + n - CT) * S::MF, set);
+  };
+  constexpr int kFrags = CT + TT;
+  // Step s's products in CT groups; group i first reads its share of `set`
+  // (all in the first half of step 0, whose barrier waits for them) and, where
+  // LOADS, issues its share of stage k's loads.
+  auto step = [&](int s, lds_char* buf, int set, auto loads, int k, lds_char* into) {
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+      if constexpr (decltype(loads)::value) {
+        const int g = (s - 1) * CT + i;
+#pragma unroll
+        for (int p = g * kLoads / (2 * CT); p < (g + 1) * kLoads / (2 * CT); ++p) load(k, into, p);
+      }
+      const int first = s == 0 ? min(2 * i, CT) : i, last = s == 0 ? min(2 * i + 2, CT) : i + 1;
+#pragma unroll
+      for (int n = first * kFrags / CT; n < last * kFrags / CT; ++n) read(buf, set, n);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < TT; ++j) acc[i][j] = Mfma<S::MF>::bf16(fa[s][i], fb[s][j], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
+#pragma unroll
+  for (int set = 0; set < 3; ++set)
+#pragma unroll
+    for (int n = 0; n < kFrags; ++n) read(lds, set, n);
+  lds_char* buf = lds;
+  lds_char* other = lds + kStage;
+  int k = 0;
+  for (; k + 2 < nfull; ++k) {
+    step(0, buf, 3, no, 0, nullptr);
+    wait_loads<0>();
+    barrier();
+    step(1, other, 0, yes, k + 2, buf);
+    step(2, other, 1, yes, k + 2, buf);
+    step(3, other, 2, no, 0, nullptr);
+    lds_char* t = buf;
+    buf = other;
+    other = t;
+  }
+  for (; k < nk; ++k) {  // the last stages; past the last one the reads go unused
+    step(0, buf, 3, no, 0, nullptr);
+    wait_loads<0>();
+    barrier();
+    if (k + 2 < nk) tail(k + 2, buf);
+    step(1, other, 0, no, 0, nullptr);
+    step(2, other, 1, no, 0, nullptr);
+    step(3, other, 2, no, 0, nullptr);
+    lds_char* t = buf;
+    buf = other;
+    other = t;
+  }
+}
+
+template <class S, class Chan, class Row, class Load, class Tail>
+__device__ __forceinline__ void products(const Chan& ct, const Row& rt, lds_char* lds, int nk,
+                                         int nfull, Load load, Tail tail,
+                                         typename S::acc_t (&acc)[S::CT][S::TT]) {
+  if constexpr (S::STAGES == 2)
+    products_deep<S>(ct, rt, lds, nk, nfull, load, tail, acc);
+  else
+    products_ring<S>(ct, rt, lds, nk, nfull, load, tail, acc);
 }
 
 // Epilogue: a wave turns MF rows at a time around in its own part of the LDS,

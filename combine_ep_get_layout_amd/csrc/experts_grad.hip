@@ -217,7 +217,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_dw(GradArgs a) {
 
 // ---- launches ------------------------------------------------------------------
 
-typedef Shape<32, 4, 4, 2, 2, 4, 64> Big;  // 256 channels x 256 rows
+typedef Shape<32, 4, 4, 2, 2, 2> Big;     // 256 channels x 256 rows
 typedef Shape<32, 2, 2, 4, 1, 3> Medium;  // 256 x 64
 typedef Shape<16, 2, 1, 4, 1, 3> Small;   // 128 x 16
 typedef Shape<32, 2, 2, 2, 2, 3> Square;  // 128 x 128
