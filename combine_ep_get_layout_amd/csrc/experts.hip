@@ -10,35 +10,47 @@
 
 namespace ep {
 
-// Eight consecutive channels of one row: the epilogue's arithmetic.  v: the
-// product (gated: the gates); u: gated, the ups.  Returns the result in bf16.
-template <bool GATED>
-__device__ __forceinline__ u32x4 finish8(const ExpertArgs& a, int e, int64_t row, int ch,
-                                         f32x4 v0, f32x4 v1, f32x4 u0, f32x4 u1) {
-  float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+// Where a workgroup's tile starts in the row buffers (row 0, channel 0 of the
+// tile) and the bias of its channels; offsets from there fit 32 bits.
+struct TileOut {
+  uint16_t* y;
+  uint16_t* pre;
+  const uint16_t* residual;
+  const float* bias;
+};
+
+// Eight consecutive channels of one row: the epilogue's arithmetic.  at: the
+// vector's offset in a buffer of N channels; gated: r, ch its row and channel.
+// Returns the result in bf16.
+template <bool GATED, class T>
+__device__ __forceinline__ u32x4 finish8(const ExpertArgs& a, const TileOut& o, uint32_t at, int r,
+                                         int ch, int further, const T& turned) {
+  float v[8];
+  turned.get(0, v);
   if (GATED) {
-    const float u[8] = {u0[0], u0[1], u0[2], u0[3], u1[0], u1[1], u1[2], u1[3]};
-    if (a.pre) {
-      uint16_t* at = a.pre + row * 2 * a.N + ch;
-      *(u32x4*)at = pack8(v);
-      *(u32x4*)(at + a.N) = pack8(u);
+    float u[8];
+    turned.get(further, u);
+    if (o.pre) {
+      uint16_t* to = o.pre + ((uint32_t)r * 2u * (uint32_t)a.N + ch);
+      *(u32x4*)to = pack8(v);
+      *(u32x4*)(to + a.N) = pack8(u);
     }
+    act_each(a.act, v);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] = act_value(a.act, v[c]) * u[c];
+    for (int c = 0; c < 8; ++c) v[c] *= u[c];
   } else {
-    if (a.bias) {
-      const f32x4* b = (const f32x4*)(a.bias + (int64_t)e * a.N + ch);
+    if (o.bias) {
+      const f32x4 b0 = *(const f32x4*)(o.bias + ch), b1 = *(const f32x4*)(o.bias + ch + 4);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] += b[c / 4][c % 4];
+      for (int c = 0; c < 4; ++c) v[c] += b0[c], v[4 + c] += b1[c];
     }
-    if (a.pre) *(u32x4*)(a.pre + row * a.N + ch) = pack8(v);
+    if (o.pre) *(u32x4*)(o.pre + at) = pack8(v);
+    act_each(a.act, v);
+    if (o.residual) {
+      float add[8];
+      unpack8(*(const u32x4*)(o.residual + at), add);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] = act_value(a.act, v[c]);
-    if (a.residual) {
-      float r[8];
-      unpack8(*(const u32x4*)(a.residual + row * a.N + ch), r);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] += r[c];
+      for (int c = 0; c < 8; ++c) v[c] += add[c];
     }
   }
   return pack8(v);
@@ -200,22 +212,27 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
       }
     }
 
-    constexpr int kTurn = 4 * MF * (CT * MF * 4 + 16);
+    constexpr int kTurn = 4 * MF * Turned<S>::kRowBytes;
     constexpr int kRow = ON * 2 + 16;  // FP8 output: a row of the tile in bf16
     static_assert(kTurn + (FP8 && ON >= 128 ? S::BM * kRow : 0) <= sizeof(lds),
                   "the epilogue fits the tile buffers");
     lds_char* base = (lds_char*)&lds[0][0];
     const bool codes = FP8 && ON >= 128 && a.y_quant != EP_QUANT_NONE;
-    turn_out<S, CH>(base, acc, [&](int r, int c, const lds_float* from) {
-      const int ch = n0 + wc * CH * MF + c;
-      if (r < rows && ch < a.N) {
-        const EP_LDS f32x4* v = (const EP_LDS f32x4*)from;
-        const EP_LDS f32x4* u = (const EP_LDS f32x4*)(GATED ? from + CH * MF : from);
-        const u32x4 y = finish8<GATED>(a, e, start + row0 + r, ch, v[0], v[1], u[0], u[1]);
+    const int64_t first = (start + row0) * a.N + n0;
+    TileOut out;
+    out.y = (uint16_t*)a.y + first;
+    out.pre = a.pre ? a.pre + (GATED ? (start + row0) * 2 * a.N + n0 : first) : nullptr;
+    out.residual = a.residual ? a.residual + first : nullptr;
+    out.bias = a.bias ? a.bias + (int64_t)e * a.N + n0 : nullptr;
+    turn_out<S, CH>(base, acc, [&](int r, int c, const Turned<S>& turned) {
+      const int ch = wc * CH * MF + c;
+      if (r < rows && n0 + ch < a.N) {
+        const uint32_t at = (uint32_t)r * (uint32_t)a.N + ch;
+        const u32x4 y = finish8<GATED>(a, out, at, r, ch, CH * MF, turned);
         if (codes)
-          *(EP_LDS u32x4*)(base + kTurn + r * kRow + (ch - n0) * 2) = y;
+          *(EP_LDS u32x4*)(base + kTurn + r * kRow + ch * 2) = y;
         else
-          *(u32x4*)((uint16_t*)a.y + (start + row0 + r) * a.N + ch) = y;
+          *(u32x4*)(out.y + at) = y;
       }
     });
     if (codes) {

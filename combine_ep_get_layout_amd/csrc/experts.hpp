@@ -31,7 +31,12 @@ typedef EP_LDS float lds_float;
 
 // ---- activations -----------------------------------------------------------
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + __expf(-v)); }
+// 1 / (1 + exp(-v)) by the hardware's exponential and reciprocal (one unit in
+// the last place each): the epilogues have one wave per SIMD, where every
+// instruction counts, and a correctly rounded division is ten of them.
+__device__ __forceinline__ float sigmoid(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+}
 
 // Gaussian cumulative distribution, 0.5 erfc(-v / sqrt 2) (1 + erf would
 // cancel for negative v)
@@ -39,12 +44,15 @@ __device__ __forceinline__ float gauss_cdf(float v) {
   return 0.5f * erfcf(v * -0.70710678118654752f);
 }
 
-__device__ __forceinline__ float act_value(int act, float v) {
-  switch (act) {
-    case EP_ACT_RELU: return v > 0.0f ? v : (v != v ? v : 0.0f);
-    case EP_ACT_SILU: return v * sigmoid(v);
-    case EP_ACT_GELU: return v * gauss_cdf(v);
-    default: return v;
+// one branch for eight values
+__device__ __forceinline__ void act_each(int act, float (&v)[8]) {
+  if (act == EP_ACT_SILU) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = v[c] * sigmoid(v[c]);
+  } else if (act != EP_ACT_NONE) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      v[c] = act == EP_ACT_RELU ? (v[c] < 0.0f ? 0.0f : v[c]) : v[c] * gauss_cdf(v[c]);
   }
 }
 
@@ -75,16 +83,16 @@ __device__ __forceinline__ void act_both(int act, float v, float& value, float& 
 
 // ---- bf16 ------------------------------------------------------------------
 
-// fp32 -> bf16, nearest even; a NaN stays one (the integer rounding of
-// f32_to_bf16_rne would carry some NaN patterns into infinity)
-__device__ __forceinline__ uint32_t bf16_of(float f) {
-  return f != f ? ((__float_as_uint(f) >> 16) | 0x40u) : f32_to_bf16_rne(f);
-}
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
+// fp32 -> bf16 nearest even by v_cvt_pk_bf16_f32 (NaN stays NaN)
 __device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
   u32x4 o;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) o[q] = bf16_of(f[2 * q]) | (bf16_of(f[2 * q + 1]) << 16);
+  for (int q = 0; q < 4; ++q)
+    o[q] = __builtin_bit_cast(
+        uint32_t, __builtin_convertvector((f32x2){f[2 * q], f[2 * q + 1]}, bf16x2));
   return o;
 }
 
@@ -692,35 +700,54 @@ __device__ __forceinline__ void products(const Chan& ct, const Row& rt, lds_char
 
 // Epilogue: a wave turns MF rows at a time around in its own part of the LDS,
 // so that eight consecutive channels of one row meet in a lane and rows leave
-// as whole 16-byte vectors.  put(r, c, from): row r of the workgroup's tile,
-// channel c of the wave's OUT channel tiles; `from` holds the eight sums of
-// channels c .. c + 7, and OUT * MF floats further on those of the wave's next
-// OUT channel tiles.
+// as whole 16-byte vectors.  A row's quads of channels lie in two halves, the
+// even ones and the odd ones: both a lane's two reads and the writes then
+// fall into all banks once.
+template <class S>
+struct Turned {
+  static constexpr int kHalf = S::CT * S::MF * 2;        // bytes
+  static constexpr int kRowBytes = 2 * kHalf + 16;       // 16: rows start four banks apart
+  const lds_char* at;
+  // eight channels, `further` channels on (a multiple of 8)
+  __device__ __forceinline__ void get(int further, float (&f)[8]) const {
+    const f32x4 a = *(const EP_LDS f32x4*)(at + further * 2);
+    const f32x4 b = *(const EP_LDS f32x4*)(at + kHalf + further * 2);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) f[q] = a[q], f[4 + q] = b[q];
+  }
+};
+
+// put(r, c, turned): row r of the workgroup's tile, channel c (a multiple of 8)
+// of the wave's first OUT channel tiles.  A lane's channels are the same in
+// every call.
 template <class S, int OUT, class Put>
 __device__ __forceinline__ void turn_out(lds_char* lds, const typename S::acc_t (&acc)[S::CT][S::TT],
                                          Put put) {
+  typedef Turned<S> T;
   constexpr int MF = S::MF;
-  constexpr int kRowBytes = S::CT * MF * 4 + 16;  // 16: rows start four banks apart
-  constexpr int kVecs = OUT * MF / 8;
+  constexpr int kVecs = OUT * MF / 8, kRows = kWave / kVecs;  // vectors of a row; rows at once
   const int lane = lane_id(), wave = uniform(threadIdx.x >> 6);
   const int wr = wave / S::WC;
   barrier();
-  lds_char* mine = lds + wave * (MF * kRowBytes);
+  lds_char* mine = lds + wave * (MF * T::kRowBytes);
+  const int r0 = lane / kVecs, c = lane % kVecs * 8;
 #pragma unroll
   for (int j = 0; j < S::TT; ++j) {
+    lds_char* to = mine + (lane % MF) * T::kRowBytes;
 #pragma unroll
     for (int i = 0; i < S::CT; ++i)
 #pragma unroll
       for (int q = 0; q < S::REGS / 4; ++q) {
         const f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
                          acc[i][j][4 * q + 3]};
-        *(EP_LDS f32x4*)(mine + (lane % MF) * kRowBytes + (i * MF + channel_of<MF>(q)) * 4) = v;
+        const int quad = (i * MF + channel_of<MF>(q)) / 4;
+        *(EP_LDS f32x4*)(to + (quad & 1) * T::kHalf + (quad >> 1) * 16) = v;
       }
     wave_lds_sync();
-#pragma unroll 1
-    for (int at = lane; at < MF * kVecs; at += kWave) {
-      const int r = at / kVecs, c = at % kVecs * 8;
-      put((wr * S::TT + j) * MF + r, c, (const lds_float*)(mine + r * kRowBytes) + c);
+    if (kRows <= MF || r0 < MF) {
+#pragma unroll 2
+      for (int r = r0; r < MF; r += kRows)
+        put((wr * S::TT + j) * MF + r, c, T{mine + r * T::kRowBytes + c * 2});
     }
     wave_lds_sync();
   }

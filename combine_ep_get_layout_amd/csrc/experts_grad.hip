@@ -147,13 +147,13 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_dx(GradArgs a) {
     typename S::acc_t acc[S::CT][S::TT];
     clear<S>(acc);
     products<S>(w_tile, z_tile, (lds_char*)&lds[0][0], nk, nfull, load, tail, acc);
-    turn_out<S, S::CT>((lds_char*)&lds[0][0], acc, [&](int r, int c, const lds_float* from) {
-      const int ch = n0 + wc * S::CT * S::MF + c;
-      if (r < rows && ch < a.C) {
+    uint16_t* out = a.dx + (start + row0) * a.C + n0;
+    turn_out<S, S::CT>((lds_char*)&lds[0][0], acc, [&](int r, int c, const Turned<S>& turned) {
+      const int ch = wc * S::CT * S::MF + c;
+      if (r < rows && n0 + ch < a.C) {
         float v[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = from[q];
-        *(u32x4*)(a.dx + (start + row0 + r) * a.C + ch) = pack8(v);
+        turned.get(0, v);
+        *(u32x4*)(out + ((uint32_t)r * (uint32_t)a.C + ch)) = pack8(v);
       }
     });
   }
@@ -203,14 +203,13 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_dw(GradArgs a) {
   typename S::acc_t acc[S::CT][S::TT];
   clear<S>(acc);
   products<S>(x_tile, z_tile, (lds_char*)&lds[0][0], nk, nfull, load, tail, acc);
-  uint16_t* dw = a.dw + (int64_t)e * a.O * a.C;
-  turn_out<S, S::CT>((lds_char*)&lds[0][0], acc, [&](int r, int c, const lds_float* from) {
-    const int ch = c0 + wc * S::CT * S::MF + c, o = o0 + r;
-    if (o < a.O && ch < a.C) {
+  uint16_t* out = a.dw + ((int64_t)e * a.O + o0) * a.C + c0;
+  turn_out<S, S::CT>((lds_char*)&lds[0][0], acc, [&](int r, int c, const Turned<S>& turned) {
+    const int ch = wc * S::CT * S::MF + c;
+    if (o0 + r < a.O && c0 + ch < a.C) {
       float v[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = from[q];
-      *(u32x4*)(dw + (int64_t)o * a.C + ch) = pack8(v);
+      turned.get(0, v);
+      *(u32x4*)(out + ((uint32_t)r * (uint32_t)a.C + ch)) = pack8(v);
     }
   });
 }
