@@ -200,26 +200,31 @@ __device__ __forceinline__ int lds_offset(const lds_char* p) {
 // The base is uniform and in scalar registers.  The compiler may have filled
 // those with vector instructions (v_readlane) just before, and does not look
 // into assembly for the five wait states that a vector-memory instruction
-// needs after such a write: every block begins with them.  M0 needs one more
-// after each change.
+// needs after such a write; a scalar one needs none, so every block copies the
+// base first.  The copy is also the wait state that M0 needs.
 
 // from base + off
 __device__ __forceinline__ void load_lds16(const char* base, uint32_t off, const lds_char* dst) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
-               ::"s"(lds_offset(dst)), "v"(off), "s"(base)
+  const char* from;
+  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
+               : "=&s"(from)
+               : "s"(lds_offset(dst)), "v"(off), "s"(base)
                : "memory");
 }
 
 // 4 bytes a lane, or one byte zero-extended to four
 template <bool BYTE>
 __device__ __forceinline__ void load_lds4(const char* base, uint32_t off, const lds_char* dst) {
+  const char* from;
   if (BYTE)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_ubyte %1, %2"
-                 ::"s"(lds_offset(dst)), "v"(off), "s"(base)
+    asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_ubyte %2, %0"
+                 : "=&s"(from)
+                 : "s"(lds_offset(dst)), "v"(off), "s"(base)
                  : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2"
-                 ::"s"(lds_offset(dst)), "v"(off), "s"(base)
+    asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dword %2, %0"
+                 : "=&s"(from)
+                 : "s"(lds_offset(dst)), "v"(off), "s"(base)
                  : "memory");
 }
 
@@ -606,7 +611,8 @@ __device__ __forceinline__ void products_deep(const Chan& ct, const Row& rt, lds
   constexpr int kStage = Chan::kBytes + Row::kBytes;
   constexpr int kLoads = Chan::kPasses + Row::kPasses;
   constexpr int CT = S::CT, TT = S::TT;
-  static_assert(S::STAGES == 2 && S::KK == 4, "");
+  constexpr int KK = S::KK;
+  static_assert(S::STAGES == 2 && KK % 2 == 0, "");
   const int wave = uniform(threadIdx.x >> 6);
   const int wc = wave % S::WC, wr = wave / S::WC;
   auto load_any = [&](int k, lds_char* buf) {
@@ -626,7 +632,7 @@ __device__ __forceinline__ void products_deep(const Chan& ct, const Row& rt, lds
   else
     wait_loads<0>();
   barrier();
-  bf16x8 fa[4][CT], fb[4][TT];
+  bf16x8 fa[KK][CT], fb[KK][TT];
   auto read = [&](lds_char* buf, int set, int n) {  // the n-th fragment of a set
     if (n < CT)
       fa[set][n] = fragment<S::MF>(ct, buf, (wc * CT + n) * S::MF, set);
@@ -634,54 +640,59 @@ __device__ __forceinline__ void products_deep(const Chan& ct, const Row& rt, lds
       fb[set][n - CT] = fragment<S::MF>(rt, buf + Chan::kBytes, (wr * TT + n - CT) * S::MF, set);
   };
   constexpr int kFrags = CT + TT;
-  // Step s's products in CT groups; group i first reads its share of `set`
-  // (all in the first half of step 0, whose barrier waits for them) and, where
-  // LOADS, issues its share of stage k's loads.
+  // Step s's products, one at a time: before each at most one read of `set`
+  // (all in the first half of step 0, whose barrier waits for them) or one of
+  // stage k's loads.  With one wave per SIMD the few instructions between two
+  // products have to fit into the time of one, 32 cycles.
+  constexpr int kProducts = CT * TT, kStepLoads = kLoads / (KK / 2);
+  static_assert(kLoads % (KK / 2) == 0 && kStepLoads <= kProducts, "");
   auto step = [&](int s, lds_char* buf, int set, auto loads, int k, lds_char* into) {
 #pragma unroll
-    for (int i = 0; i < CT; ++i) {
+    for (int m = 0; m < kProducts; ++m) {
+      const int i = m / TT, j = m % TT;
+      const int span = s == 0 ? kProducts / 2 : kProducts;
+#pragma unroll
+      for (int n = 0; n < kFrags; ++n)
+        if (n * span / kFrags == m) read(buf, set, n);
       if constexpr (decltype(loads)::value) {
-        const int g = (s - 1) * CT + i;
 #pragma unroll
-        for (int p = g * kLoads / (2 * CT); p < (g + 1) * kLoads / (2 * CT); ++p) load(k, into, p);
+        for (int l = 0; l < kStepLoads; ++l)
+          if ((2 * l + 1) * kProducts / (2 * kStepLoads) == m)
+            load(k, into, (s - 1) * kStepLoads + l);
       }
-      const int first = s == 0 ? min(2 * i, CT) : i, last = s == 0 ? min(2 * i + 2, CT) : i + 1;
-#pragma unroll
-      for (int n = first * kFrags / CT; n < last * kFrags / CT; ++n) read(buf, set, n);
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int j = 0; j < TT; ++j) acc[i][j] = Mfma<S::MF>::bf16(fa[s][i], fb[s][j], acc[i][j]);
+      acc[i][j] = Mfma<S::MF>::bf16(fa[s][i], fb[s][j], acc[i][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
   constexpr std::true_type yes{};
   constexpr std::false_type no{};
 #pragma unroll
-  for (int set = 0; set < 3; ++set)
+  for (int set = 0; set < KK - 1; ++set)
 #pragma unroll
     for (int n = 0; n < kFrags; ++n) read(lds, set, n);
   lds_char* buf = lds;
   lds_char* other = lds + kStage;
   int k = 0;
   for (; k + 2 < nfull; ++k) {
-    step(0, buf, 3, no, 0, nullptr);
+    step(0, buf, KK - 1, no, 0, nullptr);
     wait_loads<0>();
     barrier();
-    step(1, other, 0, yes, k + 2, buf);
-    step(2, other, 1, yes, k + 2, buf);
-    step(3, other, 2, no, 0, nullptr);
+#pragma unroll
+    for (int s = 1; s <= KK / 2; ++s) step(s, other, s - 1, yes, k + 2, buf);
+#pragma unroll
+    for (int s = KK / 2 + 1; s < KK; ++s) step(s, other, s - 1, no, 0, nullptr);
     lds_char* t = buf;
     buf = other;
     other = t;
   }
   for (; k < nk; ++k) {  // the last stages; past the last one the reads go unused
-    step(0, buf, 3, no, 0, nullptr);
+    step(0, buf, KK - 1, no, 0, nullptr);
     wait_loads<0>();
     barrier();
     if (k + 2 < nk) tail(k + 2, buf);
-    step(1, other, 0, no, 0, nullptr);
-    step(2, other, 1, no, 0, nullptr);
-    step(3, other, 2, no, 0, nullptr);
+#pragma unroll
+    for (int s = 1; s < KK; ++s) step(s, other, s - 1, no, 0, nullptr);
     lds_char* t = buf;
     buf = other;
     other = t;
