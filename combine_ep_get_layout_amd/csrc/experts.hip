@@ -66,8 +66,11 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
   constexpr int ON = GATED ? S::BN / 2 : S::BN;  // output channels per workgroup tile
   typedef typename S::acc_t acc_t;
   __shared__ __align__(16) char lds[S::STAGES][(S::BN + S::BM) * S::KB];
-  // FP8: every wave's own copy of its rows' scales
-  __shared__ float lds_scales[FP8 ? S::STAGES : 1][4][FP8 ? S::SLOADS * kWave : 1];
+  // FP8: every wave's own copy of its rows' scales and, behind them, of its two
+  // weight blocks'.  They come by the same asynchronous loads as the tiles: a
+  // load into a register would have to be waited for, and with it every
+  // load issued before it.
+  __shared__ float lds_scales[FP8 ? S::STAGES : 1][4][FP8 ? (S::SLOADS + 1) * kWave : 1];
   __shared__ TilePlan<kGemmThreads> plan;
 
   const int lane = lane_id(), wave = uniform(threadIdx.x >> 6);
@@ -111,8 +114,8 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
     const char* xs = nullptr;
     int64_t xs_stride = 0;
     uint32_t xs_off[S::SLOADS];
-    const float* ws0 = nullptr;
-    const float* ws1 = nullptr;
+    const char* ws = nullptr;
+    uint32_t ws_off = 0;
     if (FP8) {
       const int G = a.C / 128;
       const int64_t group = a.seg.start ? a.x_cap : a.seg.block_rows;
@@ -124,8 +127,8 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
         xs_off[l] = min(wt * S::WROWS + l * kWave + lane, rows - 1) * kScaleBytes;
       const int blocks = (GATED ? 2 : 1) * a.N / 128;
       const int ch = min(n0 + wc * CH * MF, a.N - 1) / 128;
-      ws0 = a.w_scales + ((int64_t)e * blocks + ch) * G;
-      ws1 = GATED ? ws0 + (int64_t)(a.N / 128) * G : ws0;
+      ws = (const char*)(a.w_scales + ((int64_t)e * blocks + ch) * G);
+      ws_off = GATED && lane % 2 ? (uint32_t)(a.N / 128) * G * 4 : 0;  // odd lanes: the ups'
     }
 
     constexpr int kPeriod = GATED ? CT * MF : 1 << 20;
@@ -142,6 +145,8 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
           load_lds4<Q == EP_QUANT_FP8_UE8M0>(
               xs + k * xs_stride, xs_off[l],
               (const lds_char*)&lds_scales[k % S::STAGES][wave][l * kWave]);
+        load_lds4<false>(ws + (int64_t)k * 4, ws_off,
+                         (const lds_char*)&lds_scales[k % S::STAGES][wave][S::SLOADS * kWave]);
       }
     };
     auto tail = [&](int k, lds_char* buf) {
@@ -156,7 +161,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
     if constexpr (!FP8) {
       products<S>(wt_tile, x_tile, (lds_char*)&lds[0][0], nk, nfull, load, tail, acc);
     } else {
-      constexpr int kLoads = wt_tile.kPasses + x_tile.kPasses + S::SLOADS;
+      constexpr int kLoads = wt_tile.kPasses + x_tile.kPasses + S::SLOADS + 1;
       barrier();  // the previous tile's reads
 #pragma unroll
       for (int k = 0; k < S::STAGES; ++k)
@@ -165,14 +170,16 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
           for (int p = 0; p < kPasses; ++p) load(k, (lds_char*)lds[k], p);
         }
       wait_stage<S::STAGES, kLoads>(0, nk);
+      int buf = 0;
       for (int k = 0; k < nk; ++k) {
-        const lds_char* wl = (lds_char*)lds[k % S::STAGES];
+        const lds_char* wl = (lds_char*)lds[buf];
         const lds_char* xl = wl + wt_tile.kBytes;
-        const float w0 = ws0[k], w1 = GATED ? ws1[k] : w0;
+        const float* scales = lds_scales[buf][wave];
+        const float w0 = scales[S::SLOADS * kWave], w1 = scales[S::SLOADS * kWave + 1];
         float sx[TT];
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
-          const float s = lds_scales[k % S::STAGES][wave][j * MF + lane % MF];
+          const float s = scales[j * MF + lane % MF];
           sx[j] = Q == EP_QUANT_FP8_F32 ? s : __builtin_ldexpf(1.0f, __float_as_int(s) - 127);
         }
         i32x8 fb[TT][S::KK8];
@@ -205,10 +212,10 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
           wait_stage<S::STAGES, kLoads>(k + 1, nk);
           if (k + S::STAGES < nk) {
 #pragma unroll
-            for (int p = 0; p < kPasses; ++p)
-              load(k + S::STAGES, (lds_char*)lds[k % S::STAGES], p);
+            for (int p = 0; p < kPasses; ++p) load(k + S::STAGES, (lds_char*)lds[buf], p);
           }
         }
+        buf = buf + 1 == S::STAGES ? 0 : buf + 1;
       }
     }
 
