@@ -56,66 +56,84 @@ __device__ __forceinline__ u32x4 finish8(const ExpertArgs& a, const TileOut& o, 
   return pack8(v);
 }
 
-// Q: EP_QUANT_*
+// What a tile's epilogue needs of it.
+struct Tile {
+  int64_t row;     // first row in the row buffers
+  int64_t block;   // that row within its low-latency block
+  int e, rows, n0;
+};
+
+// One workgroup's state: where its loads read, and the epilogue.  Q: EP_QUANT_*
 template <class S, bool GATED, int Q>
-__global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) {
-  constexpr bool FP8 = Q != EP_QUANT_NONE;
-  constexpr int MF = S::MF, CT = S::CT, TT = S::TT;
+struct Forward {
+  static constexpr bool FP8 = Q != EP_QUANT_NONE;
+  static constexpr int MF = S::MF, CT = S::CT;
   // gated: a wave's channel tiles are half gates and half ups of the same channels
-  constexpr int CH = GATED ? CT / 2 : CT;      // channel tiles of the output per wave
-  constexpr int ON = GATED ? S::BN / 2 : S::BN;  // output channels per workgroup tile
-  typedef typename S::acc_t acc_t;
-  __shared__ __align__(16) char lds[S::STAGES][(S::BN + S::BM) * S::KB];
-  // FP8: every wave's own copy of its rows' scales and, behind them, of its two
-  // weight blocks'.  They come by the same asynchronous loads as the tiles: a
-  // load into a register would have to be waited for, and with it every
-  // load issued before it.
-  __shared__ float lds_scales[FP8 ? S::STAGES : 1][4][FP8 ? (S::SLOADS + 1) * kWave : 1];
-  __shared__ TilePlan<kGemmThreads> plan;
+  static constexpr int CH = GATED ? CT / 2 : CT;         // channel tiles of the output per wave
+  static constexpr int ON = GATED ? S::BN / 2 : S::BN;   // output channels per workgroup tile
+  static constexpr int GS = S::KB / 128;                 // FP8 scale groups of a stage
+  static constexpr int kPeriod = GATED ? CT * MF : 1 << 20;
+  typedef RowTile<S::BN, S::KB> Chan;
+  typedef RowTile<S::BM, S::KB> Row;
+  static constexpr int kSlot = Chan::kBytes + Row::kBytes;
+  static constexpr int kPasses = Chan::kPasses + Row::kPasses;
+  static constexpr int kLoads = kPasses + (FP8 ? GS * S::SLOADS + 1 : 0);
+  static constexpr int kScales = (GS * S::SLOADS + 1) * kWave;
+  static constexpr int kScaleBytes = Q == EP_QUANT_FP8_F32 ? 4 : 1;
+  static constexpr int kTurn = 4 * MF * Turned<S>::kRowBytes;
+  static constexpr int kRow = ON * 2 + 16;  // FP8 output: a row of the tile in bf16
 
-  const int lane = lane_id(), wave = uniform(threadIdx.x >> 6);
-  const int wc = wave % S::WC, wt = wave / S::WC;
-  plan_tiles(a.seg, S::BM, plan);
-  const int mt = plan.first[a.seg.E];
-  const int nt = (a.N + ON - 1) / ON;
-  const int64_t tiles = (int64_t)mt * nt;
-  const int esize = FP8 ? 1 : 2;
-  const int64_t row_bytes = (int64_t)a.C * esize;
-  const int nk = (int)((row_bytes + S::KB - 1) / S::KB), nfull = (int)(row_bytes / S::KB);
+  const ExpertArgs& a;
+  const TilePlan<kGemmThreads>& plan;
+  lds_char* lds;
+  lds_float* scales;
+  int nk, nfull, wave, wc, wr;
+  int mt, nt;
+  int64_t row_bytes;
+  Chan w_tile;
+  Row x_tile;
+  const char *gate_base, *up_base, *x_base;
+  // FP8: scales of this wave's rows (column-major: a contraction group's side
+  // by side) and of the weights' 128 x 128 blocks
+  const char *xs, *ws;
+  int64_t xs_stride;
+  uint32_t xs_off[S::SLOADS], ws_off;
+  typename S::acc_t (*acc)[S::TT];
 
-  for (int64_t t = block_place(); t < tiles; t += gridDim.x) {
+  __device__ __forceinline__ Forward(const ExpertArgs& a_, const TilePlan<kGemmThreads>& p,
+                                     lds_char* l, lds_float* s)
+      : a(a_), plan(p), lds(l), scales(s) {
+    wave = uniform(threadIdx.x >> 6);
+    wc = wave % S::WC;
+    wr = wave / S::WC;
+    row_bytes = (int64_t)a.C * (FP8 ? 1 : 2);
+    nk = (int)((row_bytes + S::KB - 1) / S::KB);
+    nfull = (int)(row_bytes / S::KB);
+    mt = uniform(plan.first[a.seg.E]);
+    nt = (a.N + ON - 1) / ON;
+  }
+
+  __device__ __forceinline__ Tile setup(int64_t t) {
+    const int lane = lane_id();
     int m, n;
     tile_at(t, mt, nt, m, n);
     const int e = expert_of(plan, a.seg.E, m);
     int64_t start;
     int count;
-    segment_of(a.seg, e, start, count);
-    const int row0 = (m - plan.first[e]) * S::BM;  // within the segment
+    segment_at(a.seg, e, start, count);
+    const int row0 = (m - uniform(plan.first[e])) * S::BM;  // within the segment
     const int rows = min(count - row0, S::BM);
     const int n0 = n * ON;
-
-    RowTile<S::BN, S::KB> wt_tile;
-    RowTile<S::BM, S::KB> x_tile;
-    const char* w_base = a.w + (int64_t)e * (GATED ? 2 : 1) * a.N * row_bytes;
-    const char* x_base = a.x + (start + row0) * row_bytes;
     // rows and channels past the end repeat the last one; they are not stored
-    const char* gate_base = w_base + n0 * row_bytes;
-    const char* up_base = gate_base + (GATED ? (int64_t)a.N * row_bytes : 0);
-    wt_tile.init([&](int r) -> uint32_t {
+    gate_base = a.w + ((int64_t)e * (GATED ? 2 : 1) * a.N + n0) * row_bytes;
+    up_base = gate_base + (GATED ? (int64_t)a.N * row_bytes : 0);
+    x_base = a.x + (start + row0) * row_bytes;
+    w_tile.init([&](int r) -> uint32_t {
       const int in = r % (CT * MF);
       const int ch = (r / (CT * MF)) * (CH * MF) + in % (CH * MF);
-      return (uint32_t)(min(ch, a.N - 1 - n0) * row_bytes);
+      return (uint32_t)min(ch, a.N - 1 - n0) * (uint32_t)row_bytes;
     });
-    x_tile.init([&](int r) -> uint32_t { return (uint32_t)(min(r, rows - 1) * row_bytes); });
-
-    // FP8: scales of this wave's rows (column-major: a contraction group's
-    // side by side) and of the weights' 128 x 128 blocks
-    constexpr int kScaleBytes = Q == EP_QUANT_FP8_F32 ? 4 : 1;
-    const char* xs = nullptr;
-    int64_t xs_stride = 0;
-    uint32_t xs_off[S::SLOADS];
-    const char* ws = nullptr;
-    uint32_t ws_off = 0;
+    x_tile.init([&](int r) -> uint32_t { return (uint32_t)min(r, rows - 1) * (uint32_t)row_bytes; });
     if (FP8) {
       const int G = a.C / 128;
       const int64_t group = a.seg.start ? a.x_cap : a.seg.block_rows;
@@ -124,116 +142,62 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
       xs_stride = group * kScaleBytes;
 #pragma unroll
       for (int l = 0; l < S::SLOADS; ++l)
-        xs_off[l] = min(wt * S::WROWS + l * kWave + lane, rows - 1) * kScaleBytes;
+        xs_off[l] = min(wr * S::WROWS + l * kWave + lane, rows - 1) * kScaleBytes;
       const int blocks = (GATED ? 2 : 1) * a.N / 128;
       const int ch = min(n0 + wc * CH * MF, a.N - 1) / 128;
       ws = (const char*)(a.w_scales + ((int64_t)e * blocks + ch) * G);
       ws_off = GATED && lane % 2 ? (uint32_t)(a.N / 128) * G * 4 : 0;  // odd lanes: the ups'
     }
+    return Tile{start + row0, row0, e, rows, n0};
+  }
 
-    constexpr int kPeriod = GATED ? CT * MF : 1 << 20;
-    constexpr int kWPasses = wt_tile.kPasses, kPasses = kWPasses + x_tile.kPasses;
-    auto load = [&](int k, lds_char* buf, int p) {
-      const int64_t at = (int64_t)k * S::KB;
-      if (p < kWPasses)
-        wt_tile.template load<kPeriod>(p, gate_base + at, up_base + at, buf);
-      else
-        x_tile.template load<1 << 20>(p - kWPasses, x_base + at, nullptr, buf + wt_tile.kBytes);
-      if (FP8 && p == kPasses - 1) {
+  __device__ __forceinline__ void load_scales(int k, int slot) {
+    // a short last stage repeats the last group's; its products are zero
+    const int last = a.C / 128 - 1;
+    lds_float* to = scales + (slot * 4 + wave) * kScales;
 #pragma unroll
-        for (int l = 0; l < S::SLOADS; ++l)
-          load_lds4<Q == EP_QUANT_FP8_UE8M0>(
-              xs + k * xs_stride, xs_off[l],
-              (const lds_char*)&lds_scales[k % S::STAGES][wave][l * kWave]);
-        load_lds4<false>(ws + (int64_t)k * 4, ws_off,
-                         (const lds_char*)&lds_scales[k % S::STAGES][wave][S::SLOADS * kWave]);
-      }
-    };
-    auto tail = [&](int k, lds_char* buf) {
-      const int64_t at = (int64_t)k * S::KB;
-      const int left = (int)(row_bytes - at);
-      wt_tile.template load_tail<kPeriod>(gate_base + at, up_base + at, left, buf);
-      x_tile.template load_tail<1 << 20>(x_base + at, nullptr, left, buf + wt_tile.kBytes);
-    };
+    for (int g = 0; g < GS; ++g)
+#pragma unroll
+      for (int l = 0; l < S::SLOADS; ++l)
+        load_lds4<Q == EP_QUANT_FP8_UE8M0>(xs + min(k * GS + g, last) * xs_stride, xs_off[l],
+                                           (const lds_char*)(to + (g * S::SLOADS + l) * kWave));
+    load_lds4<false>(ws, ws_off + 4 * min(k * GS + lane_id() / 2 % GS, last),
+                     (const lds_char*)(to + GS * S::SLOADS * kWave));
+  }
+  __device__ __forceinline__ void load_at(int k, lds_char* buf, int p) {
+    const int64_t at = (int64_t)k * S::KB;
+    if (p < Chan::kPasses)
+      w_tile.template load<kPeriod>(p, gate_base + at, up_base + at, buf);
+    else
+      x_tile.template load<1 << 20>(p - Chan::kPasses, x_base + at, nullptr, buf + Chan::kBytes);
+  }
+  __device__ __forceinline__ void tail_at(int k, lds_char* buf) {
+    const int64_t at = (int64_t)k * S::KB;
+    const int left = (int)(row_bytes - at);
+    w_tile.template load_tail<kPeriod>(gate_base + at, up_base + at, left, buf);
+    x_tile.template load_tail<1 << 20>(x_base + at, nullptr, left, buf + Chan::kBytes);
+  }
+  __device__ __forceinline__ void load(int k, int slot, int p) {
+    load_at(k, lds + slot * kSlot, p);
+    if (FP8 && p == kPasses - 1) load_scales(k, slot);
+  }
+  __device__ __forceinline__ void tail(int k, int slot) {
+    tail_at(k, lds + slot * kSlot);
+    if (FP8) load_scales(k, slot);
+  }
 
-    acc_t acc[CT][TT];
-    clear<S>(acc);
-    if constexpr (!FP8) {
-      products<S>(wt_tile, x_tile, (lds_char*)&lds[0][0], nk, nfull, load, tail, acc);
-    } else {
-      constexpr int kLoads = wt_tile.kPasses + x_tile.kPasses + S::SLOADS + 1;
-      barrier();  // the previous tile's reads
-#pragma unroll
-      for (int k = 0; k < S::STAGES; ++k)
-        if (k < nk) {
-#pragma unroll
-          for (int p = 0; p < kPasses; ++p) load(k, (lds_char*)lds[k], p);
-        }
-      wait_stage<S::STAGES, kLoads>(0, nk);
-      int buf = 0;
-      for (int k = 0; k < nk; ++k) {
-        const lds_char* wl = (lds_char*)lds[buf];
-        const lds_char* xl = wl + wt_tile.kBytes;
-        const float* scales = lds_scales[buf][wave];
-        const float w0 = scales[S::SLOADS * kWave], w1 = scales[S::SLOADS * kWave + 1];
-        float sx[TT];
-#pragma unroll
-        for (int j = 0; j < TT; ++j) {
-          const float s = scales[j * MF + lane % MF];
-          sx[j] = Q == EP_QUANT_FP8_F32 ? s : __builtin_ldexpf(1.0f, __float_as_int(s) - 127);
-        }
-        i32x8 fb[TT][S::KK8];
-#pragma unroll
-        for (int j = 0; j < TT; ++j)
-#pragma unroll
-          for (int kk = 0; kk < S::KK8; ++kk)
-            fb[j][kk] = fragment8<MF>(x_tile, xl, (wt * TT + j) * MF, kk);
-#pragma unroll
-        for (int i = 0; i < CT; ++i) {
-          i32x8 fa[S::KK8];
-#pragma unroll
-          for (int kk = 0; kk < S::KK8; ++kk)
-            fa[kk] = fragment8<MF>(wt_tile, wl, (wc * CT + i) * MF, kk);
-          const float w = GATED && i >= CH ? w1 : w0;
-#pragma unroll
-          for (int j = 0; j < TT; ++j) {
-            acc_t part;
-#pragma unroll
-            for (int q = 0; q < S::REGS; ++q) part[q] = 0.0f;
-#pragma unroll
-            for (int kk = 0; kk < S::KK8; ++kk) part = Mfma<MF>::fp8(fa[kk], fb[j][kk], part);
-            const float s = sx[j] * w;
-#pragma unroll
-            for (int q = 0; q < S::REGS; ++q)
-              acc[i][j][q] = __builtin_fmaf(part[q], s, acc[i][j][q]);
-          }
-        }
-        if (k + 1 < nk) {
-          wait_stage<S::STAGES, kLoads>(k + 1, nk);
-          if (k + S::STAGES < nk) {
-#pragma unroll
-            for (int p = 0; p < kPasses; ++p) load(k + S::STAGES, (lds_char*)lds[buf], p);
-          }
-        }
-        buf = buf + 1 == S::STAGES ? 0 : buf + 1;
-      }
-    }
-
-    constexpr int kTurn = 4 * MF * Turned<S>::kRowBytes;
-    constexpr int kRow = ON * 2 + 16;  // FP8 output: a row of the tile in bf16
-    static_assert(kTurn + (FP8 && ON >= 128 ? S::BM * kRow : 0) <= sizeof(lds),
-                  "the epilogue fits the tile buffers");
-    lds_char* base = (lds_char*)&lds[0][0];
+  __device__ __forceinline__ void epilogue(const Tile& t, lds_char* base) {
     const bool codes = FP8 && ON >= 128 && a.y_quant != EP_QUANT_NONE;
-    const int64_t first = (start + row0) * a.N + n0;
+    const int64_t first = t.row * a.N + t.n0;
     TileOut out;
     out.y = (uint16_t*)a.y + first;
-    out.pre = a.pre ? a.pre + (GATED ? (start + row0) * 2 * a.N + n0 : first) : nullptr;
+    out.pre = a.pre ? a.pre + (GATED ? t.row * 2 * a.N + t.n0 : first) : nullptr;
     out.residual = a.residual ? a.residual + first : nullptr;
-    out.bias = a.bias ? a.bias + (int64_t)e * a.N + n0 : nullptr;
-    turn_out<S, CH>(base, acc, [&](int r, int c, const Turned<S>& turned) {
+    out.bias = a.bias ? a.bias + (int64_t)t.e * a.N + t.n0 : nullptr;
+    turn_out<S, CH>(base, *(typename S::acc_t(*)[S::CT][S::TT])acc,
+                    [&](int r, int c, const Turned<S>& turned) {
       const int ch = wc * CH * MF + c;
-      if (r < rows && n0 + ch < a.N) {
+      if (r < t.rows && t.n0 + ch < a.N) {
         const uint32_t at = (uint32_t)r * (uint32_t)a.N + ch;
         const u32x4 y = finish8<GATED>(a, out, at, r, ch, CH * MF, turned);
         if (codes)
@@ -242,37 +206,77 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
           *(u32x4*)(out.y + at) = y;
       }
     });
-    if (codes) {
-      // eight lanes take 128 channels of a row: quantised as dispatch does
-      // a bf16 row
-      barrier();
-      constexpr int kGroups = ON / 128;
-      for (int at = threadIdx.x / 8; at < S::BM * kGroups; at += kGemmThreads / 8) {
-        const int r = at / kGroups, g = at % kGroups, l = threadIdx.x % 8;
-        const EP_LDS u32x4* from =
-            (const EP_LDS u32x4*)(base + kTurn + r * kRow + g * 256 + l * 32);
-        const u32x4 lo = from[0], hi = from[1];
-        u32x4 out;
-        float scale;
-        uint32_t exponent;
-        if (a.y_quant == EP_QUANT_FP8_F32)
-          quantise_pair<EP_QUANT_FP8_F32>(lo, hi, out, scale, exponent);
-        else
-          quantise_pair<EP_QUANT_FP8_UE8M0>(lo, hi, out, scale, exponent);
-        const int ch = n0 + g * 128;
-        if (r < rows && ch < a.N) {
-          const int64_t row = start + row0 + r;
-          *(u32x4*)((char*)a.y + row * a.N + ch + l * 16) = out;
-          const int64_t at_scale =
-              a.seg.start ? (int64_t)(ch / 128) * a.y_cap + row
-                          : ((int64_t)e * (a.N / 128) + ch / 128) * a.seg.block_rows + row0 + r;
-          if (l == 0) {
-            if (a.y_quant == EP_QUANT_FP8_F32) ((float*)a.y_scales)[at_scale] = scale;
-            else ((uint8_t*)a.y_scales)[at_scale] = (uint8_t)exponent;
-          }
+    if (codes) store_codes(t, base);
+  }
+
+  // FP8 output: eight lanes take 128 channels of a row, quantised as dispatch
+  // does a bf16 row
+  __device__ __forceinline__ void store_codes(const Tile& t, lds_char* base) {
+    barrier();
+    constexpr int kGroups = ON >= 128 ? ON / 128 : 1;
+    for (int at = threadIdx.x / 8; at < S::BM * kGroups; at += kGemmThreads / 8) {
+      const int r = at / kGroups, g = at % kGroups, l = threadIdx.x % 8;
+      const EP_LDS u32x4* from = (const EP_LDS u32x4*)(base + kTurn + r * kRow + g * 256 + l * 32);
+      const u32x4 lo = from[0], hi = from[1];
+      u32x4 out;
+      float scale;
+      uint32_t exponent;
+      if (a.y_quant == EP_QUANT_FP8_F32)
+        quantise_pair<EP_QUANT_FP8_F32>(lo, hi, out, scale, exponent);
+      else
+        quantise_pair<EP_QUANT_FP8_UE8M0>(lo, hi, out, scale, exponent);
+      const int ch = t.n0 + g * 128;
+      if (r < t.rows && ch < a.N) {
+        *(u32x4*)((char*)a.y + (t.row + r) * a.N + ch + l * 16) = out;
+        const int64_t at_scale =
+            a.seg.start ? (int64_t)(ch / 128) * a.y_cap + t.row + r
+                        : ((int64_t)t.e * (a.N / 128) + ch / 128) * a.seg.block_rows + t.block + r;
+        if (l == 0) {
+          if (a.y_quant == EP_QUANT_FP8_F32) ((float*)a.y_scales)[at_scale] = scale;
+          else ((uint8_t*)a.y_scales)[at_scale] = (uint8_t)exponent;
         }
       }
     }
+  }
+};
+
+template <class S, bool GATED, int Q>
+__global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) {
+  typedef Forward<S, GATED, Q> F;
+  __shared__ __align__(16) char lds[S::STAGES][F::kSlot];
+  // FP8: every wave's own copy of its rows' scales and, behind them, of its two
+  // weight blocks'.  They come by the same asynchronous loads as the tiles: a
+  // load into a register would have to be waited for, and with it every
+  // load issued before it.
+  __shared__ float scales[F::FP8 ? S::STAGES * 4 * F::kScales : 1];
+  __shared__ TilePlan<kGemmThreads> plan;
+  static_assert(F::kTurn + (F::FP8 && F::ON >= 128 ? S::BM * F::kRow : 0) <= sizeof(lds),
+                "the epilogue fits the tile buffers");
+  plan_tiles(a.seg, S::BM, plan);
+  lds_char* base = (lds_char*)&lds[0][0];
+  F f(a, plan, base, (lds_float*)scales);
+  const int64_t tiles = (int64_t)f.mt * f.nt;
+  if constexpr (S::STAGES == 2) {
+    typename S::acc_t acc[S::CT][S::TT];
+    f.acc = acc;
+    for (int64_t t = block_place(); t < tiles; t += gridDim.x) {
+      const Tile tile = f.setup(t);
+      clear<S>(acc);
+      products_deep<S>(
+          f.w_tile, f.x_tile, base, f.nk, f.nfull,
+          [&](int k, lds_char* buf, int p) { f.load_at(k, buf, p); },
+          [&](int k, lds_char* buf) { f.tail_at(k, buf); }, acc);
+      f.epilogue(tile, base);
+    }
+  } else if constexpr (F::FP8) {
+    RingEngine8<S, typename F::Chan, typename F::Row, GATED, Q> engine(base, (lds_float*)scales);
+    f.acc = engine.acc;
+    run_ring<S, F::kTurn <= F::kSlot>(f, engine, base, block_place(), tiles,
+                                      a.y_quant == EP_QUANT_NONE);
+  } else {
+    RingEngine<S, typename F::Chan, typename F::Row> engine(base);
+    f.acc = engine.acc;
+    run_ring<S, F::kTurn <= F::kSlot>(f, engine, base, block_place(), tiles, true);
   }
 }
 

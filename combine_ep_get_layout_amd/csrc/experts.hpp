@@ -124,10 +124,10 @@ __device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8]) {
 // ---- segments --------------------------------------------------------------
 
 // What of a segment lies past the row buffers is left out and reported.
-__device__ __forceinline__ void segment_of(const Segments& s, int e, int64_t& start, int& count) {
-  int64_t c = s.count[e];
+__device__ __forceinline__ void cut_segment(const Segments& s, int e, int64_t first, int64_t c,
+                                            int64_t& start, int& count) {
   if (s.start) {
-    start = s.start[e];
+    start = first;
   } else {
     start = e * s.block_rows;
     c = min(c, s.block_rows);
@@ -138,6 +138,19 @@ __device__ __forceinline__ void segment_of(const Segments& s, int e, int64_t& st
     c = start < 0 || start >= s.cap ? 0 : s.cap - start;
   }
   count = (int)c;
+}
+
+__device__ __forceinline__ void segment_of(const Segments& s, int e, int64_t& start, int& count) {
+  cut_segment(s, e, s.start ? s.start[e] : 0, s.count[e], start, count);
+}
+
+// The same for a uniform e.  The arrays do not change during the call, so the
+// loads are scalar: a vector load would be waited for together with every
+// asynchronous load issued before it.
+__device__ __forceinline__ void segment_at(const Segments& s, int e, int64_t& start, int& count) {
+  typedef const __attribute__((address_space(4))) int32_t* fixed;
+  const int32_t c = ((fixed)s.count)[e], first = s.start ? ((fixed)s.start)[e] : 0;
+  cut_segment(s, e, first, c, start, count);
 }
 
 // ---- tile plan -------------------------------------------------------------
@@ -408,10 +421,10 @@ __device__ __forceinline__ bf16x8 fragment(const ColTile<COLS, KR>&, const lds_c
 // FP8: 128 contraction bytes a tile; 32x32x64 takes 32 bytes a lane, 16x16x128
 // too.  Which contraction elements a lane takes is free as long as both
 // operands agree.
-template <int MF, int ROWS>
-__device__ __forceinline__ i32x8 fragment8(const RowTile<ROWS>&, const lds_char* lds, int first, int kk) {
+template <int MF, int ROWS, int KB>
+__device__ __forceinline__ i32x8 fragment8(const RowTile<ROWS, KB>&, const lds_char* lds, int first, int kk) {
   const int lane = lane_id();
-  typedef RowTile<ROWS> Tile;
+  typedef RowTile<ROWS, KB> Tile;
   const int r = first + lane % MF, c = 2 * (kk * (kWave / MF) + lane / MF);
   const i32x4 a = row_chunk<Tile>(lds, r, c), b = row_chunk<Tile>(lds, r, c + 1);
   return i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
@@ -487,18 +500,6 @@ __device__ __forceinline__ int block_place() {
 
 // ---- main loop ---------------------------------------------------------------
 
-// Waits until stage k's loads are in LDS, for every wave.  LOADS: loads a wave
-// issues per stage; stages up to k + STAGES - 2 (but the last, nk - 1) have
-// been issued.
-template <int STAGES, int LOADS>
-__device__ __forceinline__ void wait_stage(int k, int nk) {
-  if (k + STAGES - 2 < nk)
-    wait_loads<LOADS*(STAGES - 2)>();
-  else
-    wait_loads<0>();
-  barrier();
-}
-
 template <class S>
 __device__ __forceinline__ void clear(typename S::acc_t (&acc)[S::CT][S::TT]) {
 #pragma unroll
@@ -509,108 +510,246 @@ __device__ __forceinline__ void clear(typename S::acc_t (&acc)[S::CT][S::TT]) {
       for (int q = 0; q < S::REGS; ++q) acc[i][j][q] = 0.0f;
 }
 
-// acc += the nk stages' products.  load(k, buf, p) issues pass p of stage k's
-// loads into buffer buf (first the channel operand's passes, then the row
-// operand's); tail(k, buf) all loads of a short last stage; the first nfull
-// stages are full.
+// One tile after another with STAGES >= 3 buffers in a ring.  While stage k is
+// multiplied, stage k + STAGES - 1 is loaded into the buffer that stage k - 1
+// left; towards a tile's end those are the next tile's first stages, so the
+// loads never stop and the epilogue (which turns its sums around in the last
+// stage's buffer) runs while they arrive.  With 16 stages a tile (FP8, 2,048
+// channels) a third of the time had gone into starting and ending tiles.
 //
-// While stage k is multiplied, stage k + STAGES - 1 is loaded into the buffer
-// that stage k - 1 left.  The loads and the reads of the next step's fragments
-// are spread evenly between the products and the order is pinned: a wave's
-// loads issued together wait for each other (four waves' sixteen 1 KiB loads
-// take the address unit about 1,000 cycles), and left to itself the compiler
-// moves the products before the barrier and the reads behind it, which leaves
-// the matrix cores idle for a barrier and an LDS round trip per stage.  A
-// stage's last products cover the barrier and the next stage's first reads.
-template <class S, class Chan, class Row, class Load, class Tail>
-__device__ __forceinline__ void products_ring(const Chan& ct, const Row& rt, lds_char* lds, int nk,
-                                         int nfull, Load load, Tail tail,
-                                         typename S::acc_t (&acc)[S::CT][S::TT]) {
-  constexpr int kStage = Chan::kBytes + Row::kBytes;
-  constexpr int kLoads = Chan::kPasses + Row::kPasses;
-  constexpr int CT = S::CT, TT = S::TT, KK = S::KK, STAGES = S::STAGES;
-  constexpr int kGroups = KK * CT;
-  static_assert(STAGES >= 3, "a stage is loaded while another one waits");
-  // loads issued after those of stage k + 1 by stage k's last step
-  constexpr int kAhead = kLoads * (STAGES - 3) + (KK - 1) * CT * kLoads / kGroups;
-  const int wave = uniform(threadIdx.x >> 6);
-  const int wc = wave % S::WC, wr = wave / S::WC;
-  barrier();  // the previous tile's reads
+// Job: nk stages a tile, the first nfull of them full; setup(t) points the
+//   loads at tile t and returns what its epilogue needs; load(k, slot, p) issues
+//   pass p (of kPasses) of stage k's loads into a buffer, kLoads a wave in all;
+//   tail(k, slot) a short last stage's; epilogue(tile, region) stores.
+// Engine: first(slot) reads what the first stage begins with; stage(slot, next,
+//   issue, mid) multiplies the stage in `slot`, calls issue(p) for p = 0 ..
+//   kPasses - 1 spread between the products, and mid() once this stage's
+//   buffer is read out and before it reads from buffer `next`.  By then it has
+//   made kIssued of the issue calls.
+template <class S, bool CHAIN, class Job, class Engine>
+__device__ __forceinline__ void run_ring(Job& job, Engine& engine, lds_char* lds, int64_t t,
+                                         int64_t tiles, bool may_chain) {
+  constexpr int N = S::STAGES, kSlot = (S::BN + S::BM) * S::KB;
+  static_assert(N >= 3, "a stage is loaded while another one waits");
+  if (t >= tiles) return;
+  auto after = [](int slot) { return slot + 1 == N ? 0 : slot + 1; };
+  auto before = [](int slot) { return slot == 0 ? N - 1 : slot - 1; };
+  auto load_any = [&](int k, int slot) {
+    if (k < job.nfull) {
 #pragma unroll
-  for (int k = 0; k < STAGES - 1; ++k) {
-    if (k < nfull) {
-#pragma unroll
-      for (int p = 0; p < kLoads; ++p) load(k, lds + k * kStage, p);
-    } else if (k < nk) {
-      tail(k, lds + k * kStage);
-    }
-  }
-  if (nk == 0) return;
-  wait_stage<STAGES, kLoads>(0, nk);
-  bf16x8 fa[2][CT], fb[2][TT];
-  auto read_chan = [&](lds_char* buf, int kk, int to, int i) {
-    fa[to][i] = fragment<S::MF>(ct, buf, (wc * CT + i) * S::MF, kk);
-  };
-  auto read_row = [&](lds_char* buf, int kk, int to, int j) {
-    fb[to][j] = fragment<S::MF>(rt, buf + Chan::kBytes, (wr * TT + j) * S::MF, kk);
-  };
-  // Step kk's products, the reads of the next step (step `next` of buffer
-  // `buf`) and, where LOADS, its share of stage k's loads into `into`.
-  auto step = [&](int kk, lds_char* buf, int next, auto loads, int k, lds_char* into) {
-    const int from = kk & 1;
-#pragma unroll
-    for (int i = 0; i < CT; ++i) {
-      if constexpr (decltype(loads)::value) {
-        const int g = kk * CT + i;
-#pragma unroll
-        for (int p = g * kLoads / kGroups; p < (g + 1) * kLoads / kGroups; ++p) load(k, into, p);
-      }
-      read_chan(buf, next, from ^ 1, i);
-#pragma unroll
-      for (int j = i * TT / CT; j < (i + 1) * TT / CT; ++j) read_row(buf, next, from ^ 1, j);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int j = 0; j < TT; ++j)
-        acc[i][j] = Mfma<S::MF>::bf16(fa[from][i], fb[from][j], acc[i][j]);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int p = 0; p < Job::kPasses; ++p) job.load(k, slot, p);
+    } else {
+      job.tail(k, slot);
     }
   };
-  constexpr std::true_type yes{};
-  constexpr std::false_type no{};
+  const bool chain = CHAIN && may_chain && job.nk >= N;
+  auto tile = job.setup(t);
+  bool fresh = true;
+  int slot = 0;
+  for (;;) {
+    if (fresh) {
+      barrier();  // the previous tile's epilogue
+      slot = 0;
 #pragma unroll
-  for (int i = 0; i < CT; ++i) read_chan(lds, 0, 0, i);
-#pragma unroll
-  for (int j = 0; j < TT; ++j) read_row(lds, 0, 0, j);
-  static_assert(KK % 2 == 0, "a stage ends on the fragments it began with");
-  auto after = [&](lds_char* b) { return b + kStage == lds + STAGES * kStage ? lds : b + kStage; };
-  lds_char* buf = lds;
-  lds_char* into = lds + (STAGES - 1) * kStage;
-  int k = 0;
-  for (; k + STAGES - 1 < nfull; ++k) {
-#pragma unroll
-    for (int kk = 0; kk < KK - 1; ++kk) step(kk, buf, kk + 1, yes, k + STAGES - 1, into);
-    wait_loads<kAhead>();
-    barrier();
-    step(KK - 1, after(buf), 0, yes, k + STAGES - 1, into);
-    into = buf;
-    buf = after(buf);
-  }
-  for (; k < nk; ++k) {  // the last stages
-    if (k + STAGES - 1 < nk) tail(k + STAGES - 1, into);
-    into = buf;
-#pragma unroll
-    for (int kk = 0; kk < KK - 1; ++kk) step(kk, buf, kk + 1, no, 0, nullptr);
-    if (k + 1 < nk) {
-      wait_loads<0>();
+      for (int k = 0; k < N - 1; ++k)
+        if (k < job.nk) load_any(k, k);
+      if (N - 2 < job.nk) wait_loads<Job::kLoads*(N - 2)>();
+      else wait_loads<0>();
       barrier();
+      engine.first(slot);
     }
-    buf = after(buf);
-    step(KK - 1, buf, 0, no, 0, nullptr);  // past the last stage the reads go unused
+    engine.clear();
+    const int64_t then = t + gridDim.x;
+    const bool more = chain && then < tiles;
+    auto next = tile;
+    int k = 0;
+    for (; k + N - 1 < job.nfull; ++k) {
+      const int into = before(slot);
+      engine.template stage<true>(
+          slot, after(slot), [&](int p) { job.load(k + N - 1, into, p); },
+          [&]() {
+            // stage k + 1 has arrived; younger: the stages between and what
+            // of stage k + N - 1 has been issued
+            wait_loads<Job::kLoads*(N - 3) + Engine::kIssued>();
+            barrier();
+          });
+      slot = after(slot);
+    }
+    for (; k < job.nk; ++k) {
+      const int ahead = k + N - 1;
+      if (ahead < job.nk) {
+        job.tail(ahead, before(slot));
+      } else if (more) {
+        if (ahead == job.nk) next = job.setup(then);
+        load_any(ahead - job.nk, before(slot));
+      }
+      engine.template stage<false>(
+          slot, after(slot), [](int) {},
+          [&]() {
+            if (more) wait_loads<Job::kLoads*(N - 2)>();
+            else wait_loads<0>();
+            barrier();
+          });
+      slot = after(slot);
+    }
+    job.epilogue(tile, chain ? lds + before(slot) * kSlot : lds);
+    t = then;
+    if (t >= tiles) return;
+    fresh = !chain;
+    if (chain) {
+      tile = next;
+      barrier();  // the epilogue's buffer is loaded next
+    } else {
+      tile = job.setup(t);
+    }
   }
 }
 
-// The same for tiles so large that only two stages fit (256 x 256: their
-// fragments, 128 registers a lane, are the third).  Fragment set s (the
+// bf16.  The loads and the reads of the next step's fragments are spread evenly
+// between the products and the order is pinned: a wave's loads issued together
+// wait for each other, and left to itself the compiler moves the products
+// before the barrier and the reads behind it, which leaves the matrix cores
+// idle for a barrier and an LDS round trip per stage.  A stage's last products
+// cover the barrier and the next stage's first reads.
+template <class S, class Chan, class Row>
+struct RingEngine {
+  static constexpr int CT = S::CT, TT = S::TT, KK = S::KK;
+  static constexpr int kSlot = Chan::kBytes + Row::kBytes;
+  static constexpr int kPasses = Chan::kPasses + Row::kPasses;
+  static constexpr int kGroups = KK * CT;
+  static constexpr int kIssued = (KK - 1) * CT * kPasses / kGroups;
+  static_assert(KK % 2 == 0, "a stage ends on the fragments it began with");
+  typename S::acc_t acc[CT][TT];
+  bf16x8 fa[2][CT], fb[2][TT];
+  lds_char* lds;
+  int wc, wr;
+
+  __device__ __forceinline__ explicit RingEngine(lds_char* l) : lds(l) {
+    const int wave = uniform(threadIdx.x >> 6);
+    wc = wave % S::WC;
+    wr = wave / S::WC;
+  }
+  __device__ __forceinline__ void read_chan(int slot, int kk, int to, int i) {
+    fa[to][i] = fragment<S::MF>(Chan(), lds + slot * kSlot, (wc * CT + i) * S::MF, kk);
+  }
+  __device__ __forceinline__ void read_row(int slot, int kk, int to, int j) {
+    fb[to][j] =
+        fragment<S::MF>(Row(), lds + slot * kSlot + Chan::kBytes, (wr * TT + j) * S::MF, kk);
+  }
+  __device__ __forceinline__ void clear() { ep::clear<S>(acc); }
+  __device__ __forceinline__ void first(int slot) {
+#pragma unroll
+    for (int i = 0; i < CT; ++i) read_chan(slot, 0, 0, i);
+#pragma unroll
+    for (int j = 0; j < TT; ++j) read_row(slot, 0, 0, j);
+  }
+  template <bool LOADS, class Issue, class Mid>
+  __device__ __forceinline__ void stage(int slot, int next, Issue issue, Mid mid) {
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      const int from = kk & 1;
+      if (kk == KK - 1) mid();
+#pragma unroll
+      for (int i = 0; i < CT; ++i) {
+        if constexpr (LOADS) {
+          const int g = kk * CT + i;
+#pragma unroll
+          for (int p = g * kPasses / kGroups; p < (g + 1) * kPasses / kGroups; ++p) issue(p);
+        }
+        const int s = kk == KK - 1 ? next : slot, n = kk == KK - 1 ? 0 : kk + 1;
+        read_chan(s, n, from ^ 1, i);
+#pragma unroll
+        for (int j = i * TT / CT; j < (i + 1) * TT / CT; ++j) read_row(s, n, from ^ 1, j);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < TT; ++j)
+          acc[i][j] = Mfma<S::MF>::bf16(fa[from][i], fb[from][j], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+};
+
+// FP8: the products of a 128-channel group are summed on the matrix cores and
+// added to the fp32 sums times the row's and the weight block's scale.
+template <class S, class Chan, class Row, bool GATED, int Q>
+struct RingEngine8 {
+  static constexpr int CT = S::CT, TT = S::TT, MF = S::MF;
+  static constexpr int kSlot = Chan::kBytes + Row::kBytes;
+  static constexpr int kPasses = Chan::kPasses + Row::kPasses;
+  static constexpr int GS = S::KB / 128, kSteps = S::KK8 / GS;
+  static constexpr int kScales = (GS * S::SLOADS + 1) * kWave;  // floats of a wave and stage
+  static constexpr int kIssued = kPasses + GS * S::SLOADS + 1;  // all loads
+  typename S::acc_t acc[CT][TT];
+  lds_char* lds;
+  lds_float* scales;
+  int wc, wr, wave;
+
+  __device__ __forceinline__ RingEngine8(lds_char* l, lds_float* s) : lds(l), scales(s) {
+    wave = uniform(threadIdx.x >> 6);
+    wc = wave % S::WC;
+    wr = wave / S::WC;
+  }
+  __device__ __forceinline__ void clear() { ep::clear<S>(acc); }
+  __device__ __forceinline__ void first(int) {}
+  template <bool LOADS, class Issue, class Mid>
+  __device__ __forceinline__ void stage(int slot, int, Issue issue, Mid mid) {
+    const lds_char* wl = lds + slot * kSlot;
+    const lds_char* xl = wl + Chan::kBytes;
+    const lds_float* sc = scales + (slot * 4 + wave) * kScales;
+    const int lane = lane_id();
+#pragma unroll
+    for (int g = 0; g < GS; ++g) {
+      const float w0 = sc[GS * S::SLOADS * kWave + 2 * g];
+      const float w1 = sc[GS * S::SLOADS * kWave + 2 * g + 1];
+      float sx[TT];
+#pragma unroll
+      for (int j = 0; j < TT; ++j) {
+        const float s = sc[g * S::SLOADS * kWave + j * MF + lane % MF];
+        sx[j] = Q == EP_QUANT_FP8_F32 ? s : __builtin_ldexpf(1.0f, __float_as_int(s) - 127);
+      }
+      i32x8 fb[TT][kSteps];
+#pragma unroll
+      for (int j = 0; j < TT; ++j)
+#pragma unroll
+        for (int kk = 0; kk < kSteps; ++kk)
+          fb[j][kk] = fragment8<MF>(Row(), xl, (wr * TT + j) * MF, g * kSteps + kk);
+#pragma unroll
+      for (int i = 0; i < CT; ++i) {
+        if constexpr (LOADS) {
+          constexpr int kGroups = GS * CT;
+          const int u = g * CT + i;
+#pragma unroll
+          for (int p = u * kPasses / kGroups; p < (u + 1) * kPasses / kGroups; ++p) issue(p);
+        }
+        i32x8 fa[kSteps];
+#pragma unroll
+        for (int kk = 0; kk < kSteps; ++kk)
+          fa[kk] = fragment8<MF>(Chan(), wl, (wc * CT + i) * MF, g * kSteps + kk);
+        const float w = GATED && i >= CT / 2 ? w1 : w0;
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+          typename S::acc_t part;
+#pragma unroll
+          for (int q = 0; q < S::REGS; ++q) part[q] = 0.0f;
+#pragma unroll
+          for (int kk = 0; kk < kSteps; ++kk) part = Mfma<MF>::fp8(fa[kk], fb[j][kk], part);
+          const float s = sx[j] * w;
+#pragma unroll
+          for (int q = 0; q < S::REGS; ++q)
+            acc[i][j][q] = __builtin_fmaf(part[q], s, acc[i][j][q]);
+        }
+      }
+    }
+    mid();
+  }
+};
+
+// acc += a tile's nk stages, for tiles so large that only two stages fit (256 x
+// 256: their fragments, 128 registers a lane, are the third).  load(k, buf, p)
+// issues pass p of stage k's loads into buffer buf (first the channel operand's
+// passes, then the row operand's); tail(k, buf) all loads of a short last
+// stage; the first nfull stages are full.  Fragment set s (the
 // operands of step s, four steps a stage) is read one step after the products
 // that used its registers:
 //   step 0 of stage k:  reads set 3 of stage k; then buffer k is read out
@@ -714,16 +853,6 @@ __device__ __forceinline__ void products_deep(const Chan& ct, const Row& rt, lds
     buf = other;
     other = t;
   }
-}
-
-template <class S, class Chan, class Row, class Load, class Tail>
-__device__ __forceinline__ void products(const Chan& ct, const Row& rt, lds_char* lds, int nk,
-                                         int nfull, Load load, Tail tail,
-                                         typename S::acc_t (&acc)[S::CT][S::TT]) {
-  if constexpr (S::STAGES == 2)
-    products_deep<S>(ct, rt, lds, nk, nfull, load, tail, acc);
-  else
-    products_ring<S>(ct, rt, lds, nk, nfull, load, tail, acc);
 }
 
 // Epilogue: a wave turns MF rows at a time around in its own part of the LDS,

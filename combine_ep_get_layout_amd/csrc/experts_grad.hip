@@ -104,58 +104,110 @@ __global__ __launch_bounds__(256) void expert_dbias(GradArgs a) {
 
 // dx = dz W: the rows run along the contraction (O channels of dz), the
 // weights across it.
+struct DxTile {
+  int64_t row;
+  int rows, n0;
+};
+
 template <class S>
-__global__ __launch_bounds__(kGemmThreads, 1) void expert_dx(GradArgs a) {
-  __shared__ __align__(16) char lds[S::STAGES][(S::BN + S::BM) * S::KB];
-  __shared__ TilePlan<kGemmThreads> plan;
-  const int wave = uniform(threadIdx.x >> 6), wc = wave % S::WC;
-  plan_tiles(a.seg, S::BM, plan);
-  const int mt = plan.first[a.seg.E];
-  const int nt = (a.C + S::BN - 1) / S::BN;
-  const int64_t tiles = (int64_t)mt * nt;
-  const int64_t z_bytes = (int64_t)a.O * 2, w_bytes = (int64_t)a.C * 2;
-  const int nk = (a.O + S::KR - 1) / S::KR, nfull = a.O / S::KR;
-  for (int64_t t = block_place(); t < tiles; t += gridDim.x) {
+struct Dx {
+  typedef ColTile<S::BN, S::KR> Chan;
+  typedef RowTile<S::BM, S::KB> Row;
+  static constexpr int kSlot = Chan::kBytes + Row::kBytes;
+  static constexpr int kPasses = Chan::kPasses + Row::kPasses, kLoads = kPasses;
+  static constexpr int kTurn = 4 * S::MF * Turned<S>::kRowBytes;
+
+  const GradArgs& a;
+  const TilePlan<kGemmThreads>& plan;
+  lds_char* lds;
+  int nk, nfull, wc, mt, nt;
+  int64_t z_bytes, w_bytes;
+  Chan w_tile;
+  Row z_tile;
+  const char *w_base, *z_base;
+  typename S::acc_t (*acc)[S::TT];
+
+  __device__ __forceinline__ Dx(const GradArgs& a_, const TilePlan<kGemmThreads>& p, lds_char* l)
+      : a(a_), plan(p), lds(l) {
+    wc = uniform(threadIdx.x >> 6) % S::WC;
+    z_bytes = (int64_t)a.O * 2;
+    w_bytes = (int64_t)a.C * 2;
+    nk = (a.O + S::KR - 1) / S::KR;
+    nfull = a.O / S::KR;
+    mt = uniform(plan.first[a.seg.E]);
+    nt = (a.C + S::BN - 1) / S::BN;
+  }
+  __device__ __forceinline__ DxTile setup(int64_t t) {
     int m, n;
     tile_at(t, mt, nt, m, n);
     const int e = expert_of(plan, a.seg.E, m);
     int64_t start;
     int count;
-    segment_of(a.seg, e, start, count);
-    const int row0 = (m - plan.first[e]) * S::BM;
+    segment_at(a.seg, e, start, count);
+    const int row0 = (m - uniform(plan.first[e])) * S::BM;
     const int rows = min(count - row0, S::BM);
     const int n0 = n * S::BN;
-    ColTile<S::BN, S::KR> w_tile;
-    RowTile<S::BM, S::KB> z_tile;
-    const char* w_base = (const char*)a.w + (int64_t)e * a.O * w_bytes + n0 * 2;
-    const char* z_base = (const char*)a.dz + (start + row0) * z_bytes;
+    w_base = (const char*)a.w + (int64_t)e * a.O * w_bytes + n0 * 2;
+    z_base = (const char*)a.dz + (start + row0) * z_bytes;
     w_tile.init((uint32_t)w_bytes, a.C - n0);
-    z_tile.init([&](int r) -> uint32_t { return (uint32_t)(min(r, rows - 1) * z_bytes); });
-    auto load = [&](int k, lds_char* buf, int p) {
-      if (p < w_tile.kPasses)
-        w_tile.load(p, w_base + (int64_t)k * S::KR * w_bytes, buf);
-      else
-        z_tile.template load<1 << 20>(p - w_tile.kPasses, z_base + (int64_t)k * S::KB, nullptr,
-                                      buf + w_tile.kBytes);
-    };
-    auto tail = [&](int k, lds_char* buf) {
-      const int left = a.O - k * S::KR;
-      w_tile.load_tail(w_base + (int64_t)k * S::KR * w_bytes, left, buf);
-      z_tile.template load_tail<1 << 20>(z_base + (int64_t)k * S::KB, nullptr, left * 2,
-                                         buf + w_tile.kBytes);
-    };
-    typename S::acc_t acc[S::CT][S::TT];
-    clear<S>(acc);
-    products<S>(w_tile, z_tile, (lds_char*)&lds[0][0], nk, nfull, load, tail, acc);
-    uint16_t* out = a.dx + (start + row0) * a.C + n0;
-    turn_out<S, S::CT>((lds_char*)&lds[0][0], acc, [&](int r, int c, const Turned<S>& turned) {
+    z_tile.init([&](int r) -> uint32_t { return (uint32_t)min(r, rows - 1) * (uint32_t)z_bytes; });
+    return DxTile{start + row0, rows, n0};
+  }
+  __device__ __forceinline__ void load_at(int k, lds_char* buf, int p) {
+    if (p < Chan::kPasses)
+      w_tile.load(p, w_base + (int64_t)k * S::KR * w_bytes, buf);
+    else
+      z_tile.template load<1 << 20>(p - Chan::kPasses, z_base + (int64_t)k * S::KB, nullptr,
+                                    buf + Chan::kBytes);
+  }
+  __device__ __forceinline__ void tail_at(int k, lds_char* buf) {
+    const int left = a.O - k * S::KR;
+    w_tile.load_tail(w_base + (int64_t)k * S::KR * w_bytes, left, buf);
+    z_tile.template load_tail<1 << 20>(z_base + (int64_t)k * S::KB, nullptr, left * 2,
+                                       buf + Chan::kBytes);
+  }
+  __device__ __forceinline__ void load(int k, int slot, int p) { load_at(k, lds + slot * kSlot, p); }
+  __device__ __forceinline__ void tail(int k, int slot) { tail_at(k, lds + slot * kSlot); }
+
+  __device__ __forceinline__ void epilogue(const DxTile& t, lds_char* base) {
+    uint16_t* out = a.dx + t.row * a.C + t.n0;
+    turn_out<S, S::CT>(base, *(typename S::acc_t(*)[S::CT][S::TT])acc,
+                       [&](int r, int c, const Turned<S>& turned) {
       const int ch = wc * S::CT * S::MF + c;
-      if (r < rows && n0 + ch < a.C) {
+      if (r < t.rows && t.n0 + ch < a.C) {
         float v[8];
         turned.get(0, v);
         *(u32x4*)(out + ((uint32_t)r * (uint32_t)a.C + ch)) = pack8(v);
       }
     });
+  }
+};
+
+template <class S>
+__global__ __launch_bounds__(kGemmThreads, 1) void expert_dx(GradArgs a) {
+  typedef Dx<S> D;
+  __shared__ __align__(16) char lds[S::STAGES][D::kSlot];
+  __shared__ TilePlan<kGemmThreads> plan;
+  plan_tiles(a.seg, S::BM, plan);
+  lds_char* base = (lds_char*)&lds[0][0];
+  D d(a, plan, base);
+  const int64_t tiles = (int64_t)d.mt * d.nt;
+  if constexpr (S::STAGES == 2) {
+    typename S::acc_t acc[S::CT][S::TT];
+    d.acc = acc;
+    for (int64_t t = block_place(); t < tiles; t += gridDim.x) {
+      const DxTile tile = d.setup(t);
+      clear<S>(acc);
+      products_deep<S>(
+          d.w_tile, d.z_tile, base, d.nk, d.nfull,
+          [&](int k, lds_char* buf, int p) { d.load_at(k, buf, p); },
+          [&](int k, lds_char* buf) { d.tail_at(k, buf); }, acc);
+      d.epilogue(tile, base);
+    }
+  } else {
+    RingEngine<S, typename D::Chan, typename D::Row> engine(base);
+    d.acc = engine.acc;
+    run_ring<S, D::kTurn <= D::kSlot>(d, engine, base, block_place(), tiles, true);
   }
 }
 
@@ -167,51 +219,97 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_dx(GradArgs a) {
 // run on it together read the same expert's rows and long experts fall on all
 // dies alike.
 template <class S>
+struct Dw {
+  typedef ColTile<S::BN, S::KR> Chan;
+  typedef ColTile<S::BM, S::KR> Row;
+  static constexpr int kSlot = Chan::kBytes + Row::kBytes;
+  static constexpr int kPasses = Chan::kPasses + Row::kPasses, kLoads = kPasses;
+
+  const GradArgs& a;
+  lds_char* lds;
+  int nk, nfull, wc, e, count, c0, o0;
+  int64_t x_bytes, z_bytes;
+  Chan x_tile;
+  Row z_tile;
+  const char *x_base, *z_base;
+  typename S::acc_t (*acc)[S::TT];
+
+  __device__ __forceinline__ Dw(const GradArgs& a_, lds_char* l) : a(a_), lds(l) {
+    wc = uniform(threadIdx.x >> 6) % S::WC;
+    x_bytes = (int64_t)a.C * 2;
+    z_bytes = (int64_t)a.O * 2;
+  }
+  __device__ __forceinline__ int setup(int64_t t) {
+    const int ct = (a.C + S::BN - 1) / S::BN, ot = (a.O + S::BM - 1) / S::BM;
+    e = uniform((int)(t / (ct * ot)));
+    int m, n;
+    tile_at(t - (int64_t)e * ct * ot, ot, ct, m, n);
+    int64_t start;
+    segment_at(a.seg, e, start, count);
+    c0 = n * S::BN;
+    o0 = m * S::BM;
+    nk = (count + S::KR - 1) / S::KR;
+    nfull = count / S::KR;
+    x_base = (const char*)a.x + start * x_bytes + c0 * 2;
+    z_base = (const char*)a.dz + start * z_bytes + o0 * 2;
+    x_tile.init((uint32_t)x_bytes, a.C - c0);
+    z_tile.init((uint32_t)z_bytes, a.O - o0);
+    return 0;
+  }
+  __device__ __forceinline__ void load_at(int k, lds_char* buf, int p) {
+    if (p < Chan::kPasses)
+      x_tile.load(p, x_base + (int64_t)k * S::KR * x_bytes, buf);
+    else
+      z_tile.load(p - Chan::kPasses, z_base + (int64_t)k * S::KR * z_bytes, buf + Chan::kBytes);
+  }
+  __device__ __forceinline__ void tail_at(int k, lds_char* buf) {
+    const int left = count - k * S::KR;
+    x_tile.load_tail(x_base + (int64_t)k * S::KR * x_bytes, left, buf);
+    z_tile.load_tail(z_base + (int64_t)k * S::KR * z_bytes, left, buf + Chan::kBytes);
+  }
+  __device__ __forceinline__ void load(int k, int slot, int p) { load_at(k, lds + slot * kSlot, p); }
+  __device__ __forceinline__ void tail(int k, int slot) { tail_at(k, lds + slot * kSlot); }
+
+  __device__ __forceinline__ void epilogue(int, lds_char* base) {
+    uint16_t* out = a.dw + ((int64_t)e * a.O + o0) * a.C + c0;
+    turn_out<S, S::CT>(base, *(typename S::acc_t(*)[S::CT][S::TT])acc,
+                       [&](int r, int c, const Turned<S>& turned) {
+      const int ch = wc * S::CT * S::MF + c;
+      if (o0 + r < a.O && c0 + ch < a.C) {
+        float v[8];
+        turned.get(0, v);
+        *(u32x4*)(out + ((uint32_t)r * (uint32_t)a.C + ch)) = pack8(v);
+      }
+    });
+  }
+};
+
+template <class S>
 __global__ __launch_bounds__(kGemmThreads, 1) void expert_dw(GradArgs a) {
-  __shared__ __align__(16) char lds[S::STAGES][(S::BN + S::BM) * S::KB];
-  const int wave = uniform(threadIdx.x >> 6), wc = wave % S::WC;
-  const int ct = (a.C + S::BN - 1) / S::BN, ot = (a.O + S::BM - 1) / S::BM;
+  typedef Dw<S> D;
+  __shared__ __align__(16) char lds[S::STAGES][D::kSlot];
+  lds_char* base = (lds_char*)&lds[0][0];
+  D d(a, base);
   constexpr int kRun = 32;
   const int i = blockIdx.x / kXcds;
   const int64_t t = ((int64_t)(i / kRun) * kXcds + blockIdx.x % kXcds) * kRun + i % kRun;
-  if (t >= (int64_t)a.seg.E * ct * ot) return;
-  const int e = uniform((int)(t / (ct * ot)));
-  int m, n;
-  tile_at(t - (int64_t)e * ct * ot, ot, ct, m, n);
-  int64_t start;
-  int count;
-  segment_of(a.seg, e, start, count);
-  const int c0 = n * S::BN, o0 = m * S::BM;
-  const int64_t x_bytes = (int64_t)a.C * 2, z_bytes = (int64_t)a.O * 2;
-  ColTile<S::BN, S::KR> x_tile;
-  ColTile<S::BM, S::KR> z_tile;
-  const char* x_base = (const char*)a.x + start * x_bytes + c0 * 2;
-  const char* z_base = (const char*)a.dz + start * z_bytes + o0 * 2;
-  x_tile.init((uint32_t)x_bytes, a.C - c0);
-  z_tile.init((uint32_t)z_bytes, a.O - o0);
-  const int nk = (count + S::KR - 1) / S::KR, nfull = count / S::KR;
-  auto load = [&](int k, lds_char* buf, int p) {
-    if (p < x_tile.kPasses)
-      x_tile.load(p, x_base + (int64_t)k * S::KR * x_bytes, buf);
-    else
-      z_tile.load(p - x_tile.kPasses, z_base + (int64_t)k * S::KR * z_bytes, buf + x_tile.kBytes);
-  };
-  auto tail = [&](int k, lds_char* buf) {
-    x_tile.load_tail(x_base + (int64_t)k * S::KR * x_bytes, count - k * S::KR, buf);
-    z_tile.load_tail(z_base + (int64_t)k * S::KR * z_bytes, count - k * S::KR, buf + x_tile.kBytes);
-  };
-  typename S::acc_t acc[S::CT][S::TT];
-  clear<S>(acc);
-  products<S>(x_tile, z_tile, (lds_char*)&lds[0][0], nk, nfull, load, tail, acc);
-  uint16_t* out = a.dw + ((int64_t)e * a.O + o0) * a.C + c0;
-  turn_out<S, S::CT>((lds_char*)&lds[0][0], acc, [&](int r, int c, const Turned<S>& turned) {
-    const int ch = wc * S::CT * S::MF + c;
-    if (o0 + r < a.O && c0 + ch < a.C) {
-      float v[8];
-      turned.get(0, v);
-      *(u32x4*)(out + ((uint32_t)r * (uint32_t)a.C + ch)) = pack8(v);
-    }
-  });
+  const int64_t tiles = (int64_t)a.seg.E * ((a.C + S::BN - 1) / S::BN) * ((a.O + S::BM - 1) / S::BM);
+  if (t >= tiles) return;
+  if constexpr (S::STAGES == 2) {
+    typename S::acc_t acc[S::CT][S::TT];
+    d.acc = acc;
+    d.setup(t);
+    clear<S>(acc);
+    products_deep<S>(
+        d.x_tile, d.z_tile, base, d.nk, d.nfull,
+        [&](int k, lds_char* buf, int p) { d.load_at(k, buf, p); },
+        [&](int k, lds_char* buf) { d.tail_at(k, buf); }, acc);
+    d.epilogue(0, base);
+  } else {
+    RingEngine<S, typename D::Chan, typename D::Row> engine(base);
+    d.acc = engine.acc;
+    run_ring<S, false>(d, engine, base, t, t + 1, false);
+  }
 }
 
 // ---- launches ------------------------------------------------------------------
