@@ -3,6 +3,7 @@
 // and the product with bias, activation and residual
 //   y = act(x W^T + b) + r
 // over the rows of each expert's segment, one launch each.
+#include <algorithm>
 #include <type_traits>
 
 #include "experts.hpp"
@@ -71,7 +72,7 @@ struct Forward {
   // gated: a wave's channel tiles are half gates and half ups of the same channels
   static constexpr int CH = GATED ? CT / 2 : CT;         // channel tiles of the output per wave
   static constexpr int ON = GATED ? S::BN / 2 : S::BN;   // output channels per workgroup tile
-  static constexpr int GS = S::KB / 128;                 // FP8 scale groups of a stage
+  static constexpr int GS = S::GS;                       // FP8 scale groups of a wave's stage
   static constexpr int kPeriod = GATED ? CT * MF : 1 << 20;
   typedef RowTile<S::BN, S::KB> Chan;
   typedef RowTile<S::BM, S::KB> Row;
@@ -87,6 +88,7 @@ struct Forward {
   const TilePlan<kGemmThreads>& plan;
   lds_char* lds;
   lds_float* scales;
+  S place;
   int nk, nfull, wave, wc, wr;
   int mt, nt;
   int64_t row_bytes;
@@ -104,8 +106,8 @@ struct Forward {
                                      lds_char* l, lds_float* s)
       : a(a_), plan(p), lds(l), scales(s) {
     wave = uniform(threadIdx.x >> 6);
-    wc = wave % S::WC;
-    wr = wave / S::WC;
+    wc = place.wc;
+    wr = place.wr;
     row_bytes = (int64_t)a.C * (FP8 ? 1 : 2);
     nk = (int)((row_bytes + S::KB - 1) / S::KB);
     nfull = (int)(row_bytes / S::KB);
@@ -153,15 +155,15 @@ struct Forward {
 
   __device__ __forceinline__ void load_scales(int k, int slot) {
     // a short last stage repeats the last group's; its products are zero
-    const int last = a.C / 128 - 1;
+    const int last = a.C / 128 - 1, first = k * (S::KB / 128) + place.wk * GS;
     lds_float* to = scales + (slot * 4 + wave) * kScales;
 #pragma unroll
     for (int g = 0; g < GS; ++g)
 #pragma unroll
       for (int l = 0; l < S::SLOADS; ++l)
-        load_lds4<Q == EP_QUANT_FP8_UE8M0>(xs + min(k * GS + g, last) * xs_stride, xs_off[l],
+        load_lds4<Q == EP_QUANT_FP8_UE8M0>(xs + min(first + g, last) * xs_stride, xs_off[l],
                                            (const lds_char*)(to + (g * S::SLOADS + l) * kWave));
-    load_lds4<false>(ws, ws_off + 4 * min(k * GS + lane_id() / 2 % GS, last),
+    load_lds4<false>(ws, ws_off + 4 * min(first + lane_id() / 2 % GS, last),
                      (const lds_char*)(to + GS * S::SLOADS * kWave));
   }
   __device__ __forceinline__ void load_at(int k, lds_char* buf, int p) {
@@ -294,6 +296,7 @@ typedef Shape<32, 4, 4, 2, 2, 2> Big;     // 256 channels x 256 rows
 typedef Shape<32, 4, 2, 2, 2, 3> Big8;    // 256 x 128 (FP8 sums are scaled in vector registers)
 typedef Shape<32, 2, 2, 4, 1, 3> Medium;  // 256 x 64
 typedef Shape<16, 2, 1, 4, 1, 3> Small;   // 128 x 16
+typedef Shape<16, 2, 1, 1, 1, 3, 512, 4> Tiny;  // 32 x 16, the waves share the contraction
 
 template <bool GATED, int Q>
 static void choose(const ExpertArgs& a, hipStream_t st) {
@@ -301,7 +304,9 @@ static void choose(const ExpertArgs& a, hipStream_t st) {
   const int64_t each = a.rows / a.seg.E;
   if (each > 96) launch<Large, GATED, Q>(a, a.rows, st);
   else if (each > 8 || a.y_quant != EP_QUANT_NONE) launch<Medium, GATED, Q>(a, a.rows, st);
-  else launch<Small, GATED, Q>(a, a.rows, st);
+  else if (std::min<int64_t>(a.seg.E, a.rows) * ((a.N + 63) / 64) * (GATED ? 1 : 1) >= 2 * kCus)
+    launch<Small, GATED, Q>(a, a.rows, st);
+  else launch<Tiny, GATED, Q>(a, a.rows, st);
 }
 
 template <bool GATED>

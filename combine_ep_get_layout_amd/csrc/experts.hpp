@@ -293,20 +293,22 @@ struct RowTile {
   static constexpr int kPasses = (ROWS + kPassRows - 1) / kPassRows;
   static constexpr int kWaveRows = kPassRows / 4;
   static __device__ __forceinline__ int turn(int r) {
-    return (r / (16 / kChunks)) & (kChunks - 1);
+    return kChunks >= 16 ? r & 15 : (r / (16 / (kChunks < 16 ? kChunks : 16))) & (kChunks - 1);
+  }
+  // the chunk that this lane fetches in pass p
+  static __device__ __forceinline__ int chunk(int p) {
+    const int tid = threadIdx.x;
+    return (tid % kChunks) ^ turn(p * kPassRows + tid / kChunks);
   }
   uint32_t off[kPasses];
-  int chunk;  // this lane's chunk of every row it fetches
 
   // row_of(r): byte offset of tile row r from the tile's base
   template <class F>
   __device__ __forceinline__ void init(F row_of) {
     const int tid = threadIdx.x;
-    chunk = (tid % kChunks) ^ turn(tid / kChunks);  // every pass turns a row alike
-    static_assert(kPassRows % 16 == 0, "");
 #pragma unroll
     for (int p = 0; p < kPasses; ++p)
-      off[p] = row_of((p * kPassRows + tid / kChunks) % ROWS) + chunk * 16;
+      off[p] = row_of((p * kPassRows + tid / kChunks) % ROWS) + chunk(p) * 16;
   }
   // Pass p's load.  base: the tile's first byte of this step; the second half
   // of every PERIOD rows comes from `other` (a gated block's ups).
@@ -324,9 +326,9 @@ struct RowTile {
   __device__ __forceinline__ void load_tail(const char* base, const char* other, int left,
                                             lds_char* lds) const {
     const int wave = uniform(threadIdx.x >> 6);
-    const bool in = chunk * 16 < left;
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
+      const bool in = chunk(p) * 16 < left;
       const int r = p * kPassRows + wave * kWaveRows;
       const char* src = (r % PERIOD >= PERIOD / 2 ? other : base) + off[p];
       load_lds16(in ? src : (const char*)k_zeros, lds + (p * 4096 + wave * 1024) % kBytes);
@@ -460,21 +462,32 @@ __device__ __forceinline__ int channel_of(int q) {
   return MF == 32 ? 8 * q + 4 * (lane_id() / 32) : 4 * (lane_id() / 16);
 }
 
-// Shape of a workgroup's tile: WC x WT waves, each CT x TT matrix-core tiles
-// of MF channels x MF rows; STAGES buffers of KB bytes along the contraction.
-template <int MF_, int CT_, int TT_, int WC_, int WT_, int STAGES_, int KB_ = 128>
+// Shape of a workgroup's tile: WC x WT x WK waves, each CT x TT matrix-core
+// tiles of MF channels x MF rows; STAGES buffers of KB bytes along the
+// contraction, of which WK waves take a part each.
+template <int MF_, int CT_, int TT_, int WC_, int WT_, int STAGES_, int KB_ = 128, int WK_ = 1>
 struct Shape {
   static constexpr int KB = KB_, KR = KB / 2;
-  static constexpr int MF = MF_, CT = CT_, TT = TT_, WC = WC_, WT = WT_, STAGES = STAGES_;
+  static constexpr int MF = MF_, CT = CT_, TT = TT_, WC = WC_, WT = WT_, WK = WK_;
+  static constexpr int STAGES = STAGES_;
   static constexpr int BN = WC * CT * MF, BM = WT * TT * MF;
-  static constexpr int KK = KR * MF / 512;  // bf16 matrix-core steps of a stage
-  static constexpr int KK8 = KB * MF / 2048;  // FP8 steps
+  static constexpr int KK = KR * MF / 512 / WK;     // bf16 matrix-core steps of a wave's stage
+  static constexpr int GS = KB / 128 / WK;          // FP8 scale groups of a wave's stage
+  static constexpr int KK8 = KB * MF / 2048 / WK;   // FP8 steps
   static constexpr int kLds = STAGES * (BN + BM) * KB;
   static constexpr int REGS = MF * MF / kWave;
   static constexpr int WROWS = TT * MF;    // rows of a wave's tile
-  static constexpr int SLOADS = (WROWS + kWave - 1) / kWave;  // FP8 scale loads of a stage
-  static_assert(WC * WT * kWave == kGemmThreads, "four wavefronts");
+  static constexpr int SLOADS = (WROWS + kWave - 1) / kWave;  // FP8 scale loads of a group
+  static_assert(WC * WT * WK * kWave == kGemmThreads, "four wavefronts");
   typedef typename Mfma<MF>::acc_t acc_t;
+  // this wave's place
+  int wc, wr, wk;
+  __device__ __forceinline__ Shape() {
+    const int wave = uniform(threadIdx.x >> 6);
+    wc = wave % WC;
+    wr = wave / WC % WT;
+    wk = wave / (WC * WT);
+  }
 };
 
 // Tile t of mt row tiles x nt channel tiles.  Row tiles are taken in groups
@@ -622,19 +635,16 @@ struct RingEngine {
   typename S::acc_t acc[CT][TT];
   bf16x8 fa[2][CT], fb[2][TT];
   lds_char* lds;
-  int wc, wr;
+  S at;
 
-  __device__ __forceinline__ explicit RingEngine(lds_char* l) : lds(l) {
-    const int wave = uniform(threadIdx.x >> 6);
-    wc = wave % S::WC;
-    wr = wave / S::WC;
-  }
+  __device__ __forceinline__ explicit RingEngine(lds_char* l) : lds(l) {}
   __device__ __forceinline__ void read_chan(int slot, int kk, int to, int i) {
-    fa[to][i] = fragment<S::MF>(Chan(), lds + slot * kSlot, (wc * CT + i) * S::MF, kk);
+    fa[to][i] = fragment<S::MF>(Chan(), lds + slot * kSlot, (at.wc * CT + i) * S::MF,
+                                at.wk * KK + kk);
   }
   __device__ __forceinline__ void read_row(int slot, int kk, int to, int j) {
-    fb[to][j] =
-        fragment<S::MF>(Row(), lds + slot * kSlot + Chan::kBytes, (wr * TT + j) * S::MF, kk);
+    fb[to][j] = fragment<S::MF>(Row(), lds + slot * kSlot + Chan::kBytes, (at.wr * TT + j) * S::MF,
+                                at.wk * KK + kk);
   }
   __device__ __forceinline__ void clear() { ep::clear<S>(acc); }
   __device__ __forceinline__ void first(int slot) {
@@ -677,27 +687,23 @@ struct RingEngine8 {
   static constexpr int CT = S::CT, TT = S::TT, MF = S::MF;
   static constexpr int kSlot = Chan::kBytes + Row::kBytes;
   static constexpr int kPasses = Chan::kPasses + Row::kPasses;
-  static constexpr int GS = S::KB / 128, kSteps = S::KK8 / GS;
+  static constexpr int GS = S::GS, kSteps = S::KK8 / GS;
   static constexpr int kScales = (GS * S::SLOADS + 1) * kWave;  // floats of a wave and stage
   static constexpr int kIssued = kPasses + GS * S::SLOADS + 1;  // all loads
   typename S::acc_t acc[CT][TT];
   lds_char* lds;
   lds_float* scales;
-  int wc, wr, wave;
+  S at;
 
-  __device__ __forceinline__ RingEngine8(lds_char* l, lds_float* s) : lds(l), scales(s) {
-    wave = uniform(threadIdx.x >> 6);
-    wc = wave % S::WC;
-    wr = wave / S::WC;
-  }
+  __device__ __forceinline__ RingEngine8(lds_char* l, lds_float* s) : lds(l), scales(s) {}
   __device__ __forceinline__ void clear() { ep::clear<S>(acc); }
   __device__ __forceinline__ void first(int) {}
   template <bool LOADS, class Issue, class Mid>
   __device__ __forceinline__ void stage(int slot, int, Issue issue, Mid mid) {
     const lds_char* wl = lds + slot * kSlot;
     const lds_char* xl = wl + Chan::kBytes;
-    const lds_float* sc = scales + (slot * 4 + wave) * kScales;
-    const int lane = lane_id();
+    const lds_float* sc = scales + (slot * 4 + uniform(threadIdx.x >> 6)) * kScales;
+    const int lane = lane_id(), first = at.wk * GS;
 #pragma unroll
     for (int g = 0; g < GS; ++g) {
       const float w0 = sc[GS * S::SLOADS * kWave + 2 * g];
@@ -713,7 +719,7 @@ struct RingEngine8 {
       for (int j = 0; j < TT; ++j)
 #pragma unroll
         for (int kk = 0; kk < kSteps; ++kk)
-          fb[j][kk] = fragment8<MF>(Row(), xl, (wr * TT + j) * MF, g * kSteps + kk);
+          fb[j][kk] = fragment8<MF>(Row(), xl, (at.wr * TT + j) * MF, (first + g) * kSteps + kk);
 #pragma unroll
       for (int i = 0; i < CT; ++i) {
         if constexpr (LOADS) {
@@ -725,7 +731,7 @@ struct RingEngine8 {
         i32x8 fa[kSteps];
 #pragma unroll
         for (int kk = 0; kk < kSteps; ++kk)
-          fa[kk] = fragment8<MF>(Chan(), wl, (wc * CT + i) * MF, g * kSteps + kk);
+          fa[kk] = fragment8<MF>(Chan(), wl, (at.wc * CT + i) * MF, (first + g) * kSteps + kk);
         const float w = GATED && i >= CT / 2 ? w1 : w0;
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
@@ -769,8 +775,8 @@ __device__ __forceinline__ void products_deep(const Chan& ct, const Row& rt, lds
   constexpr int CT = S::CT, TT = S::TT;
   constexpr int KK = S::KK;
   static_assert(S::STAGES == 2 && KK % 2 == 0, "");
-  const int wave = uniform(threadIdx.x >> 6);
-  const int wc = wave % S::WC, wr = wave / S::WC;
+  const S at;
+  const int wc = at.wc, wr = at.wr;
   auto load_any = [&](int k, lds_char* buf) {
     if (k < nfull) {
 #pragma unroll
@@ -865,10 +871,16 @@ struct Turned {
   static constexpr int kHalf = S::CT * S::MF * 2;        // bytes
   static constexpr int kRowBytes = 2 * kHalf + 16;       // 16: rows start four banks apart
   const lds_char* at;
-  // eight channels, `further` channels on (a multiple of 8)
+  // eight channels, `further` channels on (a multiple of 8); the sum of the
+  // waves' parts of the contraction, in their order
   __device__ __forceinline__ void get(int further, float (&f)[8]) const {
-    const f32x4 a = *(const EP_LDS f32x4*)(at + further * 2);
-    const f32x4 b = *(const EP_LDS f32x4*)(at + kHalf + further * 2);
+    f32x4 a = *(const EP_LDS f32x4*)(at + further * 2);
+    f32x4 b = *(const EP_LDS f32x4*)(at + kHalf + further * 2);
+#pragma unroll
+    for (int w = 1; w < S::WK; ++w) {
+      a += *(const EP_LDS f32x4*)(at + w * (S::MF * kRowBytes) + further * 2);
+      b += *(const EP_LDS f32x4*)(at + w * (S::MF * kRowBytes) + kHalf + further * 2);
+    }
 #pragma unroll
     for (int q = 0; q < 4; ++q) f[q] = a[q], f[4 + q] = b[q];
   }
@@ -884,7 +896,7 @@ __device__ __forceinline__ void turn_out(lds_char* lds, const typename S::acc_t 
   constexpr int MF = S::MF;
   constexpr int kVecs = OUT * MF / 8, kRows = kWave / kVecs;  // vectors of a row; rows at once
   const int lane = lane_id(), wave = uniform(threadIdx.x >> 6);
-  const int wr = wave / S::WC;
+  const int wr = S().wr;
   barrier();
   lds_char* mine = lds + wave * (MF * T::kRowBytes);
   const int r0 = lane / kVecs, c = lane % kVecs * 8;
@@ -900,6 +912,13 @@ __device__ __forceinline__ void turn_out(lds_char* lds, const typename S::acc_t 
         const int quad = (i * MF + channel_of<MF>(q)) / 4;
         *(EP_LDS f32x4*)(to + (quad & 1) * T::kHalf + (quad >> 1) * 16) = v;
       }
+    if constexpr (S::WK > 1) {
+      static_assert(S::TT == 1 && S::WC == 1 && S::WT == 1, "one tile that the waves share");
+      barrier();
+      const int r = threadIdx.x / kVecs, ch = threadIdx.x % kVecs * 8;
+      if (r < MF) put(r, ch, T{lds + r * T::kRowBytes + ch * 2});
+      return;
+    }
     wave_lds_sync();
     if (kRows <= MF || r0 < MF) {
 #pragma unroll 2

@@ -129,7 +129,7 @@ struct Dx {
 
   __device__ __forceinline__ Dx(const GradArgs& a_, const TilePlan<kGemmThreads>& p, lds_char* l)
       : a(a_), plan(p), lds(l) {
-    wc = uniform(threadIdx.x >> 6) % S::WC;
+    wc = S().wc;
     z_bytes = (int64_t)a.O * 2;
     w_bytes = (int64_t)a.C * 2;
     nk = (a.O + S::KR - 1) / S::KR;
@@ -235,7 +235,7 @@ struct Dw {
   typename S::acc_t (*acc)[S::TT];
 
   __device__ __forceinline__ Dw(const GradArgs& a_, lds_char* l) : a(a_), lds(l) {
-    wc = uniform(threadIdx.x >> 6) % S::WC;
+    wc = S().wc;
     x_bytes = (int64_t)a.C * 2;
     z_bytes = (int64_t)a.O * 2;
   }
