@@ -85,7 +85,7 @@ struct Forward {
   static constexpr int kRow = ON * 2 + 16;  // FP8 output: a row of the tile in bf16
 
   const ExpertArgs& a;
-  const TilePlan<kGemmThreads>& plan;
+  const TilePlan& plan;
   lds_char* lds;
   lds_float* scales;
   S place;
@@ -102,7 +102,7 @@ struct Forward {
   uint32_t xs_off[S::SLOADS], ws_off;
   typename S::acc_t (*acc)[S::TT];
 
-  __device__ __forceinline__ Forward(const ExpertArgs& a_, const TilePlan<kGemmThreads>& p,
+  __device__ __forceinline__ Forward(const ExpertArgs& a_, const TilePlan& p,
                                      lds_char* l, lds_float* s)
       : a(a_), plan(p), lds(l), scales(s) {
     wave = uniform(threadIdx.x >> 6);
@@ -111,7 +111,7 @@ struct Forward {
     row_bytes = (int64_t)a.C * (FP8 ? 1 : 2);
     nk = (int)((row_bytes + S::KB - 1) / S::KB);
     nfull = (int)(row_bytes / S::KB);
-    mt = uniform(plan.first[a.seg.E]);
+    mt = uniform(plan.upto[a.seg.E - 1]);
     nt = (a.N + ON - 1) / ON;
   }
 
@@ -123,7 +123,7 @@ struct Forward {
     int64_t start;
     int count;
     segment_at(a.seg, e, start, count);
-    const int row0 = (m - uniform(plan.first[e])) * S::BM;  // within the segment
+    const int row0 = (m - uniform(plan.first(e))) * S::BM;  // within the segment
     const int rows = min(count - row0, S::BM);
     const int n0 = n * ON;
     // rows and channels past the end repeat the last one; they are not stored
@@ -251,10 +251,10 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
   // load into a register would have to be waited for, and with it every
   // load issued before it.
   __shared__ float scales[F::FP8 ? S::STAGES * 4 * F::kScales : 1];
-  __shared__ TilePlan<kGemmThreads> plan;
+  __shared__ TilePlan plan;
   static_assert(F::kTurn + (F::FP8 && F::ON >= 128 ? S::BM * F::kRow : 0) <= sizeof(lds),
                 "the epilogue fits the tile buffers");
-  plan_tiles(a.seg, S::BM, plan);
+  plan_tiles<kGemmThreads>(a.seg, S::BM, plan, (int*)lds);
   lds_char* base = (lds_char*)&lds[0][0];
   F f(a, plan, base, (lds_float*)scales);
   const int64_t tiles = (int64_t)f.mt * f.nt;
@@ -286,7 +286,7 @@ template <class S, bool GATED, int Q>
 static void launch(const ExpertArgs& a, int64_t rows, hipStream_t st) {
   const int on = GATED ? S::BN / 2 : S::BN;
   const int64_t tiles = ((rows + S::BM - 1) / S::BM + a.seg.E) * ((a.N + on - 1) / on);
-  const int per_cu = S::kLds > 70 * 1024 ? 1 : 2;
+  const int per_cu = S::kLds > 72 * 1024 ? 1 : 2;
   const int64_t most = (int64_t)kCus * per_cu;
   hipLaunchKernelGGL((expert_forward<S, GATED, Q>), dim3((unsigned)min(tiles, most)),
                      dim3(kGemmThreads), 0, st, a);
@@ -302,9 +302,10 @@ template <bool GATED, int Q>
 static void choose(const ExpertArgs& a, hipStream_t st) {
   typedef typename std::conditional<Q == EP_QUANT_NONE, Big, Big8>::type Large;
   const int64_t each = a.rows / a.seg.E;
+  constexpr int on = GATED ? Small::BN / 2 : Small::BN;
   if (each > 96) launch<Large, GATED, Q>(a, a.rows, st);
   else if (each > 8 || a.y_quant != EP_QUANT_NONE) launch<Medium, GATED, Q>(a, a.rows, st);
-  else if (std::min<int64_t>(a.seg.E, a.rows) * ((a.N + 63) / 64) * (GATED ? 1 : 1) >= 2 * kCus)
+  else if (std::min<int64_t>(a.seg.E, a.rows) * ((a.N + on - 1) / on) >= 2 * kCus)
     launch<Small, GATED, Q>(a, a.rows, st);
   else launch<Tiny, GATED, Q>(a, a.rows, st);
 }

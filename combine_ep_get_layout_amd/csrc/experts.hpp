@@ -155,17 +155,17 @@ __device__ __forceinline__ void segment_at(const Segments& s, int e, int64_t& st
 
 // ---- tile plan -------------------------------------------------------------
 
-// first[e] = tiles of `step` rows of the experts before e, first[E] = all of
-// them.  Every workgroup scans the counts itself (E <= 2048 of them, in the
-// shadow of its own start), so a call is one launch and needs no workspace.
-template <int THREADS>
+// upto[e] = tiles of `step` rows of the experts up to e.  Every workgroup scans
+// the counts itself (E <= 2048 of them, in the shadow of its own start), so a
+// call is one launch and needs no workspace.
 struct TilePlan {
-  int first[kMaxExperts + 1];
-  int wave_sum[THREADS / kWave];
+  int upto[kMaxExperts];
+  __device__ __forceinline__ int first(int e) const { return e == 0 ? 0 : upto[e - 1]; }
 };
 
+// sums: LDS for an int per wavefront, free afterwards
 template <int THREADS>
-__device__ void plan_tiles(const Segments& s, int step, TilePlan<THREADS>& p) {
+__device__ void plan_tiles(const Segments& s, int step, TilePlan& p, int* sums) {
   constexpr int kPer = (kMaxExperts + THREADS - 1) / THREADS;
   const int tid = threadIdx.x, lane = tid & 63;
   const int per = (s.E + THREADS - 1) / THREADS;
@@ -187,29 +187,27 @@ __device__ void plan_tiles(const Segments& s, int step, TilePlan<THREADS>& p) {
     const int v = __shfl_up(upto, d);
     if (lane >= d) upto += v;
   }
-  if (lane == kWave - 1) p.wave_sum[tid / kWave] = upto;
+  if (lane == kWave - 1) sums[tid / kWave] = upto;
   __syncthreads();
   int at = upto - sum;
-  for (int w = 0; w < tid / kWave; ++w) at += p.wave_sum[w];
+  for (int w = 0; w < tid / kWave; ++w) at += sums[w];
   for (int i = 0; i < per; ++i) {
     const int e = tid * per + i;
-    if (e < s.E) p.first[e] = at;
     at += n[i];
+    if (e < s.E) p.upto[e] = at;
   }
-  if (tid == THREADS - 1) p.first[s.E] = at;
   __syncthreads();
 }
 
-// Expert of tile t (first[e] <= t < first[e + 1]): two steps of 64 lanes each.
-template <int THREADS>
-__device__ __forceinline__ int expert_of(const TilePlan<THREADS>& p, int E, int t) {
+// Expert of tile t (first(e) <= t < upto[e]): two steps of 64 lanes each.
+__device__ __forceinline__ int expert_of(const TilePlan& p, int E, int t) {
   const int lane = lane_id();
   const int stride = (E + kWave - 1) / kWave;  // <= 32
-  const int far = min((lane + 1) * stride, E);
-  const int skip = __popcll(__ballot(p.first[far] <= t));  // whole strides before t's
+  const int far = (lane + 1) * stride - 1;     // the last expert of this lane's stride
+  const int skip = __popcll(__ballot(far < E && p.upto[min(far, E - 1)] <= t));
   const int base = skip * stride;
-  const int near = min(base + lane + 1, E);
-  const bool pass = lane < stride && base + lane + 1 <= E && p.first[near] <= t;
+  const int near = base + lane;
+  const bool pass = lane < stride && near < E && p.upto[min(near, E - 1)] <= t;
   return uniform(base + __popcll(__ballot(pass)));
 }
 

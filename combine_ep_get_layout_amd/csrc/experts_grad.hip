@@ -16,15 +16,16 @@ constexpr int kElemRows = 8;  // rows of a work item
 // Reads dy and the pre-activations once and writes dz: bound by memory.
 template <bool GATED>
 __global__ __launch_bounds__(256) void expert_dz(GradArgs a) {
-  __shared__ TilePlan<256> plan;
-  plan_tiles(a.seg, kElemRows, plan);
+  __shared__ TilePlan plan;
+  __shared__ int sums[4];
+  plan_tiles<256>(a.seg, kElemRows, plan, sums);
   const int vecs = a.N / 8;
-  for (int t = blockIdx.x; t < plan.first[a.seg.E]; t += gridDim.x) {
+  for (int t = blockIdx.x; t < plan.upto[a.seg.E - 1]; t += gridDim.x) {
     const int e = expert_of(plan, a.seg.E, t);
     int64_t start;
     int count;
     segment_of(a.seg, e, start, count);
-    const int row0 = (t - plan.first[e]) * kElemRows;
+    const int row0 = (t - plan.first(e)) * kElemRows;
     const int rows = min(count - row0, kElemRows);
     for (int i = threadIdx.x; i < rows * vecs; i += 256) {
       const int r = i / vecs, ch = (i - r * vecs) * 8;
@@ -118,7 +119,7 @@ struct Dx {
   static constexpr int kTurn = 4 * S::MF * Turned<S>::kRowBytes;
 
   const GradArgs& a;
-  const TilePlan<kGemmThreads>& plan;
+  const TilePlan& plan;
   lds_char* lds;
   int nk, nfull, wc, mt, nt;
   int64_t z_bytes, w_bytes;
@@ -127,14 +128,14 @@ struct Dx {
   const char *w_base, *z_base;
   typename S::acc_t (*acc)[S::TT];
 
-  __device__ __forceinline__ Dx(const GradArgs& a_, const TilePlan<kGemmThreads>& p, lds_char* l)
+  __device__ __forceinline__ Dx(const GradArgs& a_, const TilePlan& p, lds_char* l)
       : a(a_), plan(p), lds(l) {
     wc = S().wc;
     z_bytes = (int64_t)a.O * 2;
     w_bytes = (int64_t)a.C * 2;
     nk = (a.O + S::KR - 1) / S::KR;
     nfull = a.O / S::KR;
-    mt = uniform(plan.first[a.seg.E]);
+    mt = uniform(plan.upto[a.seg.E - 1]);
     nt = (a.C + S::BN - 1) / S::BN;
   }
   __device__ __forceinline__ DxTile setup(int64_t t) {
@@ -144,7 +145,7 @@ struct Dx {
     int64_t start;
     int count;
     segment_at(a.seg, e, start, count);
-    const int row0 = (m - uniform(plan.first[e])) * S::BM;
+    const int row0 = (m - uniform(plan.first(e))) * S::BM;
     const int rows = min(count - row0, S::BM);
     const int n0 = n * S::BN;
     w_base = (const char*)a.w + (int64_t)e * a.O * w_bytes + n0 * 2;
@@ -187,8 +188,8 @@ template <class S>
 __global__ __launch_bounds__(kGemmThreads, 1) void expert_dx(GradArgs a) {
   typedef Dx<S> D;
   __shared__ __align__(16) char lds[S::STAGES][D::kSlot];
-  __shared__ TilePlan<kGemmThreads> plan;
-  plan_tiles(a.seg, S::BM, plan);
+  __shared__ TilePlan plan;
+  plan_tiles<kGemmThreads>(a.seg, S::BM, plan, (int*)lds);
   lds_char* base = (lds_char*)&lds[0][0];
   D d(a, plan, base);
   const int64_t tiles = (int64_t)d.mt * d.nt;
