@@ -89,7 +89,7 @@ struct Forward {
   lds_char* lds;
   lds_float* scales;
   S place;
-  int nk, nfull, wave, wc, wr;
+  int nk, nfull, wave, wc, wr, turn;
   int mt, nt;
   int64_t row_bytes;
   Chan w_tile;
@@ -126,6 +126,13 @@ struct Forward {
     const int row0 = (m - uniform(plan.first(e))) * S::BM;  // within the segment
     const int rows = min(count - row0, S::BM);
     const int n0 = n * ON;
+    // Few rows an expert: the weights are read once, by workgroups that would
+    // all be at the same channel of their rows at the same time, and where a
+    // row's length is a power of two those addresses share few memory
+    // channels.  So every tile begins somewhere else (64 experts x 64 rows,
+    // 4096 x 4096: 520 -> 403 us; 3584 channels: 344 -> 350 us).  Large tiles
+    // share their operands in the die's cache and stay in step.
+    turn = S::STAGES > 2 && nk == nfull ? (n * 11 + e * 7) % nk : 0;
     // rows and channels past the end repeat the last one; they are not stored
     gate_base = a.w + ((int64_t)e * (GATED ? 2 : 1) * a.N + n0) * row_bytes;
     up_base = gate_base + (GATED ? (int64_t)a.N * row_bytes : 0);
@@ -153,9 +160,13 @@ struct Forward {
     return Tile{start + row0, row0, e, rows, n0};
   }
 
+  // the stage of the rows that is multiplied k-th
+  __device__ __forceinline__ int turned(int k) const {
+    return S::STAGES == 2 ? k : k + turn >= nk ? k + turn - nk : k + turn;
+  }
   __device__ __forceinline__ void load_scales(int k, int slot) {
     // a short last stage repeats the last group's; its products are zero
-    const int last = a.C / 128 - 1, first = k * (S::KB / 128) + place.wk * GS;
+    const int last = a.C / 128 - 1, first = turned(k) * (S::KB / 128) + place.wk * GS;
     lds_float* to = scales + (slot * 4 + wave) * kScales;
 #pragma unroll
     for (int g = 0; g < GS; ++g)
@@ -167,7 +178,7 @@ struct Forward {
                      (const lds_char*)(to + GS * S::SLOADS * kWave));
   }
   __device__ __forceinline__ void load_at(int k, lds_char* buf, int p) {
-    const int64_t at = (int64_t)k * S::KB;
+    const int64_t at = (int64_t)turned(k) * S::KB;
     if (p < Chan::kPasses)
       w_tile.template load<kPeriod>(p, gate_base + at, up_base + at, buf);
     else
@@ -197,7 +208,7 @@ struct Forward {
     out.residual = a.residual ? a.residual + first : nullptr;
     out.bias = a.bias ? a.bias + (int64_t)t.e * a.N + t.n0 : nullptr;
     turn_out<S, CH>(base, *(typename S::acc_t(*)[S::CT][S::TT])acc,
-                    [&](int r, int c, const Turned<S>& turned) {
+                    [&](int wc, int r, int c, const Turned<S>& turned) {
       const int ch = wc * CH * MF + c;
       if (r < t.rows && t.n0 + ch < a.N) {
         const uint32_t at = (uint32_t)r * (uint32_t)a.N + ch;
@@ -282,32 +293,61 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
   }
 }
 
-template <class S, bool GATED, int Q>
-static void launch(const ExpertArgs& a, int64_t rows, hipStream_t st) {
-  const int on = GATED ? S::BN / 2 : S::BN;
-  const int64_t tiles = ((rows + S::BM - 1) / S::BM + a.seg.E) * ((a.N + on - 1) / on);
-  const int per_cu = S::kLds > 72 * 1024 ? 1 : 2;
-  const int64_t most = (int64_t)kCus * per_cu;
-  hipLaunchKernelGGL((expert_forward<S, GATED, Q>), dim3((unsigned)min(tiles, most)),
-                     dim3(kGemmThreads), 0, st, a);
-}
-
 typedef Shape<32, 4, 4, 2, 2, 2> Big;     // 256 channels x 256 rows
 typedef Shape<32, 4, 2, 2, 2, 3> Big8;    // 256 x 128 (FP8 sums are scaled in vector registers)
 typedef Shape<32, 2, 2, 4, 1, 3> Medium;  // 256 x 64
 typedef Shape<16, 2, 1, 4, 1, 3> Small;   // 128 x 16
 typedef Shape<16, 2, 1, 1, 1, 3, 512, 4> Tiny;  // 32 x 16, the waves share the contraction
 
+// Workgroups of a shape on the chip: by LDS, two a compute unit or one.
+template <class S, int Q>
+constexpr int slots() {
+  const int lds = S::kLds + (int)sizeof(TilePlan) +
+                  (Q == EP_QUANT_NONE ? 0 : S::STAGES * 4 * (S::GS * S::SLOADS + 1) * kWave * 4);
+  return lds <= 80 * 1024 ? 2 * kCus : kCus;
+}
+
+template <class S, bool GATED, int Q>
+static void launch(const ExpertArgs& a, hipStream_t st) {
+  const int on = GATED ? S::BN / 2 : S::BN;
+  const int64_t tiles = ((a.rows + S::BM - 1) / S::BM + a.seg.E) * ((a.N + on - 1) / on);
+  hipLaunchKernelGGL((expert_forward<S, GATED, Q>),
+                     dim3((unsigned)std::min(tiles, (int64_t)slots<S, Q>())), dim3(kGemmThreads), 0,
+                     st, a);
+}
+
+template <class S, bool GATED, int Q>
+static double time_of(const ExpertArgs& a, double stage, double tile) {
+  return shape_time<S>(a.seg, a.rows, (int64_t)a.N * (GATED ? 2 : 1),
+                       (int64_t)a.C * (Q == EP_QUANT_NONE ? 2 : 1), slots<S, Q>(), stage, tile);
+}
+
+// The shape with the least expected time, in units of a stage of Medium; the
+// stages' times are fitted to measurements of every shape at 1 to 128 experts, 1 to
+// 512 rows each (random routing), 648 to 8192 channels.  The choice is 2% off the
+// best shape on average and 28% at worst (FP8 1% and 17%); by rows per expert alone
+// it was 24% off, and 4.9 times at worst (FP8 21%, 4.0 times).  us, bf16, Big / Medium
+// / Small / Tiny:
+//   1 expert, 2048 x 2048, 8 rows:       39 /  20 /   12 /    7
+//   1 expert, 4096 x 8192, 512 rows:     82 /  44 /  124 /  149
+//   8 experts, 1024 x 1024, 512 rows:    33 /  17 /   38 /   60
+//   64 experts, 4096 x 4096, 64 rows:   553 / 400 /  762 /  801
+//   64 experts, 4096 x 4096, 256 rows:  638 / 846 / 2663 / 2646
+// A result in FP8 needs its groups of 128 channels whole in a tile, gated or not:
+// only the two larger shapes have them.
 template <bool GATED, int Q>
 static void choose(const ExpertArgs& a, hipStream_t st) {
-  typedef typename std::conditional<Q == EP_QUANT_NONE, Big, Big8>::type Large;
-  const int64_t each = a.rows / a.seg.E;
-  constexpr int on = GATED ? Small::BN / 2 : Small::BN;
-  if (each > 96) launch<Large, GATED, Q>(a, a.rows, st);
-  else if (each > 8 || a.y_quant != EP_QUANT_NONE) launch<Medium, GATED, Q>(a, a.rows, st);
-  else if (std::min<int64_t>(a.seg.E, a.rows) * ((a.N + on - 1) / on) >= 2 * kCus)
-    launch<Small, GATED, Q>(a, a.rows, st);
-  else launch<Tiny, GATED, Q>(a, a.rows, st);
+  constexpr bool FP8 = Q != EP_QUANT_NONE;
+  typedef typename std::conditional<FP8, Big8, Big>::type Large;
+  const double large = time_of<Large, GATED, Q>(a, FP8 ? 1.55 : 2.0, FP8 ? 0.0 : 1.0);
+  const double medium = time_of<Medium, GATED, Q>(a, 1.0, FP8 ? 0.3 : 0.0);
+  const double small = time_of<Small, GATED, Q>(a, FP8 ? 0.9 : 0.95, 0.0);
+  const double tiny = time_of<Tiny, GATED, Q>(a, FP8 ? 0.4 : 1.1, FP8 ? 3.5 : 1.5);
+  const bool any = a.y_quant == EP_QUANT_NONE;
+  if (any && tiny < std::min({large, medium, small})) launch<Tiny, GATED, Q>(a, st);
+  else if (any && small < std::min(large, medium)) launch<Small, GATED, Q>(a, st);
+  else if (medium < large) launch<Medium, GATED, Q>(a, st);
+  else launch<Large, GATED, Q>(a, st);
 }
 
 template <bool GATED>

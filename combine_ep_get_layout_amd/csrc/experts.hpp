@@ -7,6 +7,8 @@
 // row and stores them as one 8-byte vector.
 #pragma once
 
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "ep_device.hpp"
@@ -509,6 +511,27 @@ __device__ __forceinline__ int block_place() {
   return g % kXcds == 0 ? (b % kXcds) * (g / kXcds) + b / kXcds : b;
 }
 
+// ---- choice of a shape ---------------------------------------------------------
+
+// Row tiles of `step` rows that the segments are expected to make.  The counts
+// are on the device: an expert that is hit has the mean number of rows and, unless
+// it has all of them, half a tile more.
+inline double row_tiles(const Segments& s, int64_t rows, int step) {
+  const double hit = (double)std::min<int64_t>(rows, s.E);
+  if (hit <= 1.0) return (double)((rows + step - 1) / step);
+  return hit * std::max(1.0, (double)rows / hit / step + 0.5);
+}
+
+// Relative time of shape S: whole rounds of its workgroups (`slots` of them on the
+// chip) over a product of `channels` results a row and `bytes` of contraction.
+// stage, tile: the time of one of its stages, and of a tile's start and end.
+template <class S>
+inline double shape_time(const Segments& s, int64_t rows, int64_t channels, int64_t bytes,
+                         int slots, double stage, double tile) {
+  const double tiles = row_tiles(s, rows, S::BM) * (double)((channels + S::BN - 1) / S::BN);
+  return std::ceil(tiles / slots) * ((double)((bytes + S::KB - 1) / S::KB) * stage + tile);
+}
+
 // ---- main loop ---------------------------------------------------------------
 
 template <class S>
@@ -876,17 +899,18 @@ struct Turned {
     f32x4 b = *(const EP_LDS f32x4*)(at + kHalf + further * 2);
 #pragma unroll
     for (int w = 1; w < S::WK; ++w) {
-      a += *(const EP_LDS f32x4*)(at + w * (S::MF * kRowBytes) + further * 2);
-      b += *(const EP_LDS f32x4*)(at + w * (S::MF * kRowBytes) + kHalf + further * 2);
+      constexpr int kPart = S::WC * S::WT * S::MF * kRowBytes;  // the waves of one part
+      a += *(const EP_LDS f32x4*)(at + w * kPart + further * 2);
+      b += *(const EP_LDS f32x4*)(at + w * kPart + kHalf + further * 2);
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) f[q] = a[q], f[4 + q] = b[q];
   }
 };
 
-// put(r, c, turned): row r of the workgroup's tile, channel c (a multiple of 8)
-// of the wave's first OUT channel tiles.  A lane's channels are the same in
-// every call.
+// put(wc, r, c, turned): row r of the workgroup's tile, channel c (a multiple of
+// 8) of the first OUT channel tiles of the waves in column wc.  A lane's
+// channels are the same in every call.
 template <class S, int OUT, class Put>
 __device__ __forceinline__ void turn_out(lds_char* lds, const typename S::acc_t (&acc)[S::CT][S::TT],
                                          Put put) {
@@ -894,7 +918,7 @@ __device__ __forceinline__ void turn_out(lds_char* lds, const typename S::acc_t 
   constexpr int MF = S::MF;
   constexpr int kVecs = OUT * MF / 8, kRows = kWave / kVecs;  // vectors of a row; rows at once
   const int lane = lane_id(), wave = uniform(threadIdx.x >> 6);
-  const int wr = S().wr;
+  const S place;
   barrier();
   lds_char* mine = lds + wave * (MF * T::kRowBytes);
   const int r0 = lane / kVecs, c = lane % kVecs * 8;
@@ -910,18 +934,22 @@ __device__ __forceinline__ void turn_out(lds_char* lds, const typename S::acc_t 
         const int quad = (i * MF + channel_of<MF>(q)) / 4;
         *(EP_LDS f32x4*)(to + (quad & 1) * T::kHalf + (quad >> 1) * 16) = v;
       }
-    if constexpr (S::WK > 1) {
-      static_assert(S::TT == 1 && S::WC == 1 && S::WT == 1, "one tile that the waves share");
+    if constexpr (S::WK > 1) {  // the waves that share a tile store parts of it
+      static_assert(S::WT == 1, "");
       barrier();
-      const int r = threadIdx.x / kVecs, ch = threadIdx.x % kVecs * 8;
-      if (r < MF) put(r, ch, T{lds + r * T::kRowBytes + ch * 2});
-      return;
+      constexpr int kThreads = kGemmThreads / S::WC;  // of one column
+      const int column = uniform(threadIdx.x / kThreads), id = threadIdx.x % kThreads;
+      const lds_char* from = lds + column * (MF * T::kRowBytes);
+      for (int r = id / kVecs; r < MF; r += kThreads / kVecs)
+        put(column, j * MF + r, id % kVecs * 8, T{from + r * T::kRowBytes + id % kVecs * 16});
+      if (j + 1 < S::TT) barrier();
+      continue;
     }
     wave_lds_sync();
     if (kRows <= MF || r0 < MF) {
 #pragma unroll 2
       for (int r = r0; r < MF; r += kRows)
-        put((wr * S::TT + j) * MF + r, c, T{mine + r * T::kRowBytes + c * 2});
+        put(place.wc, (place.wr * S::TT + j) * MF + r, c, T{mine + r * T::kRowBytes + c * 2});
     }
     wave_lds_sync();
   }

@@ -173,7 +173,7 @@ struct Dx {
   __device__ __forceinline__ void epilogue(const DxTile& t, lds_char* base) {
     uint16_t* out = a.dx + t.row * a.C + t.n0;
     turn_out<S, S::CT>(base, *(typename S::acc_t(*)[S::CT][S::TT])acc,
-                       [&](int r, int c, const Turned<S>& turned) {
+                       [&](int wc, int r, int c, const Turned<S>& turned) {
       const int ch = wc * S::CT * S::MF + c;
       if (r < t.rows && t.n0 + ch < a.C) {
         float v[8];
@@ -274,7 +274,7 @@ struct Dw {
   __device__ __forceinline__ void epilogue(int, lds_char* base) {
     uint16_t* out = a.dw + ((int64_t)e * a.O + o0) * a.C + c0;
     turn_out<S, S::CT>(base, *(typename S::acc_t(*)[S::CT][S::TT])acc,
-                       [&](int r, int c, const Turned<S>& turned) {
+                       [&](int wc, int r, int c, const Turned<S>& turned) {
       const int ch = wc * S::CT * S::MF + c;
       if (o0 + r < a.O && c0 + ch < a.C) {
         float v[8];
@@ -321,11 +321,18 @@ typedef Shape<16, 2, 1, 4, 1, 3> Small;   // 128 x 16
 typedef Shape<32, 2, 2, 2, 2, 3> Square;  // 128 x 128
 
 template <class S>
+constexpr int dx_slots() { return S::kLds > 70 * 1024 ? kCus : 2 * kCus; }
+
+template <class S>
 static void launch_dx(const GradArgs& a, hipStream_t st) {
   const int64_t tiles = ((a.rows + S::BM - 1) / S::BM + a.seg.E) * ((a.C + S::BN - 1) / S::BN);
-  const int per_cu = S::kLds > 70 * 1024 ? 1 : 2;
-  hipLaunchKernelGGL(expert_dx<S>, dim3((unsigned)min(tiles, (int64_t)kCus * per_cu)),
+  hipLaunchKernelGGL(expert_dx<S>, dim3((unsigned)min(tiles, (int64_t)dx_slots<S>())),
                      dim3(kGemmThreads), 0, st, a);
+}
+
+template <class S>
+static double dx_time(const GradArgs& a, double stage, double tile) {
+  return shape_time<S>(a.seg, a.rows, a.C, (int64_t)a.O * 2, dx_slots<S>(), stage, tile);
 }
 
 template <class S>
@@ -338,7 +345,6 @@ static void launch_dw(const GradArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_expert_grad(const GradArgs& a, hipStream_t st) {
-  const int64_t each = a.rows / a.seg.E;
   if (a.dz_out && a.rows > 0) {
     const int64_t items = a.rows / kElemRows + a.seg.E;
     const dim3 grid((unsigned)min(items, (int64_t)kCus * 8));
@@ -351,9 +357,15 @@ hipError_t launch_expert_grad(const GradArgs& a, hipStream_t st) {
     hipLaunchKernelGGL(expert_dbias, dim3((a.N + kBiasChannels - 1) / kBiasChannels, a.seg.E),
                        dim3(256), 0, st, a);
   if (a.dx && a.rows > 0) {
-    if (each > 96) launch_dx<Big>(a, st);
-    else if (each > 8) launch_dx<Medium>(a, st);
-    else launch_dx<Small>(a, st);
+    // as in the forward products, in units of a stage of Medium: 1% off the best
+    // shape on average over the same sizes, 18% by rows per expert alone.  us, Big
+    // / Medium / Small: 1 expert, 2048 x 2048, 512 rows 41 / 20 / 20; 64 experts,
+    // 2048 x 2048, 64 rows 139 / 106 / 215, 512 rows 282 / 432 / 1378.
+    const double big = dx_time<Big>(a, 2.0, 1.0), medium = dx_time<Medium>(a, 1.0, 0.0);
+    const double small = dx_time<Small>(a, 0.95, 0.0);
+    if (small < min(big, medium)) launch_dx<Small>(a, st);
+    else if (medium < big) launch_dx<Medium>(a, st);
+    else launch_dx<Big>(a, st);
   }
   if (a.dw) {
     const int64_t tiles = (int64_t)a.seg.E * ((a.C + 255) / 256) * ((a.O + 255) / 256);
