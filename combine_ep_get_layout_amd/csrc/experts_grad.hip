@@ -11,22 +11,28 @@ namespace ep {
 
 // ---- dz ----------------------------------------------------------------------
 
-constexpr int kElemRows = 8;  // rows of a work item
+// Rows of a work item: 256 vectors of 8 channels at least, one a thread (16 experts x
+// 2,048 rows x 4096 channels 146 us, eight rows an item 170; 1 expert x 512 rows 8.6 and
+// 22 us).
+__host__ __device__ __forceinline__ int dz_rows(int channels) {
+  return channels >= 2048 ? 1 : 2048 / channels;
+}
 
 // Reads dy and the pre-activations once and writes dz: bound by memory.
 template <bool GATED>
 __global__ __launch_bounds__(256) void expert_dz(GradArgs a) {
   __shared__ TilePlan plan;
   __shared__ int sums[4];
-  plan_tiles<256>(a.seg, kElemRows, plan, sums);
+  const int step = dz_rows(a.N);
+  plan_tiles<256>(a.seg, step, plan, sums);
   const int vecs = a.N / 8;
   for (int t = blockIdx.x; t < plan.upto[a.seg.E - 1]; t += gridDim.x) {
     const int e = expert_of(plan, a.seg.E, t);
     int64_t start;
     int count;
     segment_of(a.seg, e, start, count);
-    const int row0 = (t - plan.first(e)) * kElemRows;
-    const int rows = min(count - row0, kElemRows);
+    const int row0 = (t - plan.first(e)) * step;
+    const int rows = min(count - row0, step);
     for (int i = threadIdx.x; i < rows * vecs; i += 256) {
       const int r = i / vecs, ch = (i - r * vecs) * 8;
       const int64_t row = start + row0 + r;
@@ -60,14 +66,17 @@ __global__ __launch_bounds__(256) void expert_dz(GradArgs a) {
 
 // ---- db ----------------------------------------------------------------------
 
-constexpr int kBiasChannels = 64;
+constexpr int kBiasWaves = 16, kBiasRows = 4;
 
-// One workgroup per expert and 64 channels: 32 rows at a time, eight channels
-// a thread, joined over LDS in a fixed order.
-__global__ __launch_bounds__(256) void expert_dbias(GradArgs a) {
-  __shared__ float part[32][kBiasChannels + 1];
-  const int e = blockIdx.y, c0 = blockIdx.x * kBiasChannels;
-  const int r0 = threadIdx.x / 8, c = (threadIdx.x % 8) * 8;
+// One workgroup per expert and CH channels: eight channels a thread, 8192 / CH
+// rows at a time and four such loads in flight, joined over lanes and LDS in a fixed
+// order.
+template <int CH>
+__global__ __launch_bounds__(kBiasWaves* kWave) void expert_dbias(GradArgs a) {
+  __shared__ float part[kBiasWaves][CH];
+  constexpr int kLanes = CH / 8, kStep = kBiasWaves * kWave / kLanes;
+  const int e = blockIdx.y, c0 = blockIdx.x * CH, lane = lane_id();
+  const int r0 = threadIdx.x / kLanes, c = (threadIdx.x % kLanes) * 8;
   int64_t start;
   int count;
   segment_of(a.seg, e, start, count);
@@ -75,28 +84,43 @@ __global__ __launch_bounds__(256) void expert_dbias(GradArgs a) {
 #pragma unroll
   for (int q = 0; q < 8; ++q) sum[q] = 0.0f;
   if (c0 + c < a.N)
-    for (int r = r0; r < count; r += 32) {
-      const int64_t at = (start + r) * a.N + c0 + c;
-      float d[8], z[8];
-      unpack8(*(const u32x4*)(a.dy + at), d);
-      if (a.act != EP_ACT_NONE) {
-        unpack8(*(const u32x4*)(a.pre + at), z);
+    for (int r = r0; r < count; r += kStep * kBiasRows) {
+      u32x4 d8[kBiasRows], z8[kBiasRows];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          float value, slope;
-          act_both(a.act, z[q], value, slope);
-          d[q] *= slope;
-        }
+      for (int i = 0; i < kBiasRows; ++i) {  // rows past the end repeat the last one
+        const int64_t at = (start + min(r + i * kStep, count - 1)) * a.N + c0 + c;
+        d8[i] = *(const u32x4*)(a.dy + at);
+        z8[i] = a.act == EP_ACT_NONE ? d8[i] : *(const u32x4*)(a.pre + at);
       }
 #pragma unroll
-      for (int q = 0; q < 8; ++q) sum[q] += d[q];
+      for (int i = 0; i < kBiasRows; ++i) {
+        if (r + i * kStep >= count) break;
+        float d[8], z[8];
+        unpack8(d8[i], d);
+        unpack8(z8[i], z);
+        if (a.act != EP_ACT_NONE)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float value, slope;
+            act_both(a.act, z[q], value, slope);
+            d[q] *= slope;
+          }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum[q] += d[q];
+      }
     }
 #pragma unroll
-  for (int q = 0; q < 8; ++q) part[r0][c + q] = sum[q];
+  for (int q = 0; q < 8; ++q)
+#pragma unroll
+    for (int d = kLanes; d < kWave; d <<= 1) sum[q] += __shfl_xor(sum[q], d);
+  if (lane < kLanes)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) part[threadIdx.x / kWave][c + q] = sum[q];
   __syncthreads();
-  if (threadIdx.x < kBiasChannels && c0 + (int)threadIdx.x < a.N) {
+  if (threadIdx.x < CH && c0 + (int)threadIdx.x < a.N) {
     float s = 0.0f;
-    for (int r = 0; r < 32; ++r) s += part[r][threadIdx.x];
+#pragma unroll
+    for (int w = 0; w < kBiasWaves; ++w) s += part[w][threadIdx.x];
     a.dbias[(int64_t)e * a.N + c0 + threadIdx.x] = s;
   }
 }
@@ -320,6 +344,12 @@ typedef Shape<32, 2, 2, 4, 1, 3> Medium;  // 256 x 64
 typedef Shape<16, 2, 1, 4, 1, 3> Small;   // 128 x 16
 typedef Shape<32, 2, 2, 2, 2, 3> Square;  // 128 x 128
 
+template <int CH>
+static void launch_dbias(const GradArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL(expert_dbias<CH>, dim3((a.N + CH - 1) / CH, a.seg.E),
+                     dim3(kBiasWaves * kWave), 0, st, a);
+}
+
 template <class S>
 constexpr int dx_slots() { return S::kLds > 70 * 1024 ? kCus : 2 * kCus; }
 
@@ -346,16 +376,22 @@ static void launch_dw(const GradArgs& a, hipStream_t st) {
 
 hipError_t launch_expert_grad(const GradArgs& a, hipStream_t st) {
   if (a.dz_out && a.rows > 0) {
-    const int64_t items = a.rows / kElemRows + a.seg.E;
+    const int64_t items = a.rows / dz_rows(a.N) + a.seg.E;
     const dim3 grid((unsigned)min(items, (int64_t)kCus * 8));
     if (a.gated)
       hipLaunchKernelGGL(expert_dz<true>, grid, dim3(256), 0, st, a);
     else
       hipLaunchKernelGGL(expert_dz<false>, grid, dim3(256), 0, st, a);
   }
-  if (a.dbias)
-    hipLaunchKernelGGL(expert_dbias, dim3((a.N + kBiasChannels - 1) / kBiasChannels, a.seg.E),
-                       dim3(256), 0, st, a);
+  if (a.dbias) {
+    // Channels of a workgroup, so that there are enough of them and each has a few
+    // rows a thread.  us, 32 / 64 / 256 channels: 1 expert x 8,192 rows x 4096 channels
+    // 67 / 123 / 479; 4 x 2,048 x 4096 52 / 38 / 128; 64 x 4 x 4096 48 / 22 / 7.
+    const int64_t groups = (int64_t)a.seg.E * ((a.N + 63) / 64);
+    if (groups <= kCus / 2) launch_dbias<32>(a, st);
+    else if (groups >= 4 * kCus && a.rows <= (int64_t)a.seg.E * 128) launch_dbias<256>(a, st);
+    else launch_dbias<64>(a, st);
+  }
   if (a.dx && a.rows > 0) {
     // as in the forward products, in units of a stage of Medium: 1% off the best
     // shape on average over the same sizes, 18% by rows per expert alone.  us, Big

@@ -811,3 +811,45 @@ def test_expert_counts_at_the_limit():
         wx, ex, ww, ew = backward64(x[s:s + c].double(), w[e].double(), dz, dz * 0)
         held(dx[s:s + c], wx, ex, ("dx", e))
         held(dw[e], ww, ew, ("dw", e))
+
+
+# more tiles than the chip holds at once, of every kind of tile: from one row an
+# expert (32 channels x 16 rows) to segments of 256 x 256; short and long
+# contractions, with and without a rest
+WIDE = [
+    (1, 1500, 2, 2, N, 0.1, 200, 1304),
+    (1, 1500, 2, 2, N, 0.1, 200, 2600),
+    (1, 1500, 2, 2, N, 0.1, 2600, 72),
+    (2, 40, 64, 4, N, 0.0, 840, 328),
+    (1, 60, 64, 4, L, 0.0, 264, 1032),
+    (1, 300, 32, 4, N, 0.1, 328, 1032),
+    (1, 260, 4, 2, N, 0.1, 2056, 1032),
+    (1, 400, 16, 4, N, 0.1, 2056, 136),
+]
+WIDE_IDS = ["-".join(map(str, s)) for s in WIDE]
+
+
+@pytest.mark.parametrize("shape", WIDE, ids=WIDE_IDS)
+def test_wide_products(shape):
+    test_gated(shape, "silu")
+    test_linear(shape, "all")
+
+
+@pytest.mark.parametrize("shape", WIDE, ids=WIDE_IDS)
+def test_wide_gradients(shape):
+    test_backward(shape, "gated", "gelu")
+    test_backward(shape, "linear", "silu")
+
+
+@pytest.mark.parametrize("quant", [ep.QUANT_FP8_F32, ep.QUANT_FP8_UE8M0])
+@pytest.mark.parametrize("shape", [
+    (1, 1500, 2, 2, N, 256, 1280),
+    (2, 300, 8, 2, L, 512, 1152),
+    (1, 40, 64, 4, N, 640, 384),
+    (1, 256, 16, 4, N, 1664, 640),
+    (1, 200, 64, 4, L, 384, 640),
+    (1, 10, 64, 2, L, 2688, 256),
+], ids=lambda s: "-".join(map(str, s)))
+def test_wide_fp8(shape, quant):
+    test_fp8_rows_of_a_dispatch(shape, "gated", quant)
+    test_fp8_rows_of_a_dispatch(shape, "linear", quant)
