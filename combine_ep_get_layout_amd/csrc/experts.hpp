@@ -179,7 +179,7 @@ __device__ void plan_tiles(const Segments& s, int step, TilePlan& p, int* sums) 
       int64_t start;
       int count;
       segment_of(s, e, start, count);
-      n[i] = (count + step - 1) / step;
+      n[i] = (int)(((uint32_t)count + step - 1) / step);  // count + step may pass 2^31
     }
     sum += n[i];
   }

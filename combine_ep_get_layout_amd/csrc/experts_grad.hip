@@ -84,11 +84,11 @@ __global__ __launch_bounds__(kBiasWaves* kWave) void expert_dbias(GradArgs a) {
 #pragma unroll
   for (int q = 0; q < 8; ++q) sum[q] = 0.0f;
   if (c0 + c < a.N)
-    for (int r = r0; r < count; r += kStep * kBiasRows) {
+    for (int64_t r = r0; r < count; r += kStep * kBiasRows) {
       u32x4 d8[kBiasRows], z8[kBiasRows];
 #pragma unroll
       for (int i = 0; i < kBiasRows; ++i) {  // rows past the end repeat the last one
-        const int64_t at = (start + min(r + i * kStep, count - 1)) * a.N + c0 + c;
+        const int64_t at = (start + min(r + i * kStep, (int64_t)count - 1)) * a.N + c0 + c;
         d8[i] = *(const u32x4*)(a.dy + at);
         z8[i] = a.act == EP_ACT_NONE ? d8[i] : *(const u32x4*)(a.pre + at);
       }
@@ -273,7 +273,7 @@ struct Dw {
     segment_at(a.seg, e, start, count);
     c0 = n * S::BN;
     o0 = m * S::BM;
-    nk = (count + S::KR - 1) / S::KR;
+    nk = (int)(((uint32_t)count + S::KR - 1) / S::KR);
     nfull = count / S::KR;
     x_base = (const char*)a.x + start * x_bytes + c0 * 2;
     z_base = (const char*)a.dz + start * z_bytes + o0 * 2;

@@ -481,6 +481,9 @@ def _same_device(*tensors) -> None:
           "tensors on the current device")
 
 
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
 def _rows(p: Problem, t: torch.Tensor, what: str, channels: int | None = None,
           scales: torch.Tensor | None = None) -> CRows:
     """A row buffer: bf16 [rows][channels], or one-byte e4m3 codes with their scales."""
@@ -490,7 +493,7 @@ def _rows(p: Problem, t: torch.Tensor, what: str, channels: int | None = None,
     if scales is None:
         _need(t.dtype == torch.bfloat16, f"{what} bf16 (FP8 codes come with scales)")
     else:
-        _need(t.element_size() == 1, f"{what}: FP8 codes are bytes")
+        _need(t.dtype in _CODES, f"{what}: FP8 codes are e4m3, or bytes")
         _need(scales.dtype in (torch.float32, torch.uint8), f"{what} scales fp32 or uint8 (UE8M0)")
         quant = QUANT_FP8_F32 if scales.dtype == torch.float32 else QUANT_FP8_UE8M0
         rows = t.shape[0] if p.mode == MODE_NORMAL else p.E * p.R * p.T
@@ -504,7 +507,7 @@ def _weights(p: Problem, w: torch.Tensor, scales: torch.Tensor | None = None,
     if scales is None:
         _need(w.dtype == torch.bfloat16, "w bf16 (FP8 codes come with w_scales)")
     else:
-        _need(w.element_size() == 1, "w: FP8 codes are bytes")
+        _need(w.dtype in _CODES, "w: FP8 codes are e4m3, or bytes")
         _need(scales.dtype == torch.float32
               and scales.numel() == p.E * (w.shape[1] // 128) * (w.shape[2] // 128),
               "w_scales [E][out/128][in/128] fp32")
@@ -515,6 +518,7 @@ def _weights(p: Problem, w: torch.Tensor, scales: torch.Tensor | None = None,
 
 
 def _check_segments(p: Problem, layout: Layout) -> None:
+    _same_device(layout.err, layout.recv_tokens_per_expert, layout.expert_start)
     _need(layout.recv_tokens_per_expert.numel() == p.E and layout.expert_start.numel() == p.E,
           "layout buffers do not match the problem")
 

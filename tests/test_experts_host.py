@@ -215,3 +215,13 @@ def test_the_binding_checks_shapes_and_types():
         with pytest.raises(ValueError):
             call()
             pytest.fail(str(i))
+
+
+@pytest.mark.parametrize("dtype", [torch.float8_e5m2, torch.float8_e4m3fnuz, torch.int8, torch.bool])
+def test_codes_of_another_kind_are_refused(dtype):
+    """A byte type that is not e4m3 codes would be read as if it were."""
+    x, w = torch.zeros((32, 128), dtype=torch.uint8), torch.zeros((4, 256, 128), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="e4m3"):
+        ep._rows(problem(), x.view(dtype), "x", 128, torch.zeros(32))
+    with pytest.raises(ValueError, match="e4m3"):
+        ep._weights(problem(), w.view(dtype), torch.zeros(4, 2, 1))
