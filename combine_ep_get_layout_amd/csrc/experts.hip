@@ -11,51 +11,8 @@
 
 namespace ep {
 
-// Where a workgroup's tile starts in the row buffers (row 0, channel 0 of the
-// tile) and the bias of its channels; offsets from there fit 32 bits.
-struct TileOut {
-  uint16_t* y;
-  uint16_t* pre;
-  const uint16_t* residual;
-  const float* bias;
-};
-
-// Eight consecutive channels of one row: the epilogue's arithmetic.  at: the
-// vector's offset in a buffer of N channels; gated: r, ch its row and channel.
-// Returns the result in bf16.
-template <bool GATED, class T>
-__device__ __forceinline__ u32x4 finish8(const ExpertArgs& a, const TileOut& o, uint32_t at, int r,
-                                         int ch, int further, const T& turned) {
-  float v[8];
-  turned.get(0, v);
-  if (GATED) {
-    float u[8];
-    turned.get(further, u);
-    if (o.pre) {
-      uint16_t* to = o.pre + ((uint32_t)r * 2u * (uint32_t)a.N + ch);
-      *(u32x4*)to = pack8(v);
-      *(u32x4*)(to + a.N) = pack8(u);
-    }
-    act_each(a.act, v);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] *= u[c];
-  } else {
-    if (o.bias) {
-      const f32x4 b0 = *(const f32x4*)(o.bias + ch), b1 = *(const f32x4*)(o.bias + ch + 4);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] += b0[c], v[4 + c] += b1[c];
-    }
-    if (o.pre) *(u32x4*)(o.pre + at) = pack8(v);
-    act_each(a.act, v);
-    if (o.residual) {
-      float add[8];
-      unpack8(*(const u32x4*)(o.residual + at), add);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] += add[c];
-    }
-  }
-  return pack8(v);
-}
+// Nothing to load for a row's result.
+struct NoRow {};
 
 // What a tile's epilogue needs of it.
 struct Tile {
@@ -199,26 +156,84 @@ struct Forward {
     if (FP8) load_scales(k, slot);
   }
 
+  // Offsets within a tile's rows fit 32 bits.
   __device__ __forceinline__ void epilogue(const Tile& t, lds_char* base) {
+    typedef TurnLane<S, CH> Lane;
+    constexpr int B = Lane::kBatch, kStep = Lane::kRows;
+    typedef typename std::conditional<GATED, NoRow, u32x4>::type Row8;
     const bool codes = FP8 && ON >= 128 && a.y_quant != EP_QUANT_NONE;
+    const Lane lane;
+    const int ch = lane.wc * CH * MF + lane.channel;  // within the tile
+    const bool in = t.n0 + ch < a.N;
     const int64_t first = t.row * a.N + t.n0;
-    TileOut out;
-    out.y = (uint16_t*)a.y + first;
-    out.pre = a.pre ? a.pre + (GATED ? t.row * 2 * a.N + t.n0 : first) : nullptr;
-    out.residual = a.residual ? a.residual + first : nullptr;
-    out.bias = a.bias ? a.bias + (int64_t)t.e * a.N + t.n0 : nullptr;
-    turn_out<S, CH>(base, *(typename S::acc_t(*)[S::CT][S::TT])acc,
-                    [&](int wc, int r, int c, const Turned<S>& turned) {
-      const int ch = wc * CH * MF + c;
-      if (r < t.rows && t.n0 + ch < a.N) {
-        const uint32_t at = (uint32_t)r * (uint32_t)a.N + ch;
-        const u32x4 y = finish8<GATED>(a, out, at, r, ch, CH * MF, turned);
-        if (codes)
-          *(EP_LDS u32x4*)(base + kTurn + r * kRow + ch * 2) = y;
-        else
-          *(u32x4*)(out.y + at) = y;
-      }
-    });
+    uint16_t* const y = (uint16_t*)a.y + first;
+    uint16_t* const pre = a.pre ? a.pre + (GATED ? t.row * 2 * a.N + t.n0 : first) : nullptr;
+    f32x4 bias[2] = {};
+    if (!GATED && a.bias && in) {
+      const float* b = a.bias + (int64_t)t.e * a.N + t.n0 + ch;
+      bias[0] = *(const f32x4*)b;
+      bias[1] = *(const f32x4*)(b + 4);
+    }
+    turn_out<S, CH>(
+        base, *(typename S::acc_t(*)[S::CT][S::TT])acc,
+        [&](int r) {
+          Row8 row = {};
+          if constexpr (!GATED)
+            if (a.residual && r < t.rows && in)
+              row = *(const u32x4*)(a.residual + first + (uint32_t)r * (uint32_t)a.N + ch);
+          return row;
+        },
+        [&](int r, const Turned<S>(&turned)[B], const Row8(&add)[B]) {
+          float v[B][8];
+#pragma unroll
+          for (int b = 0; b < B; ++b) turned[b].get(0, v[b]);
+          if constexpr (GATED) {
+            float u[B][8];
+#pragma unroll
+            for (int b = 0; b < B; ++b) turned[b].get(CH * MF, u[b]);
+            if (pre)
+#pragma unroll
+              for (int b = 0; b < B; ++b)
+                if (r + b * kStep < t.rows && in) {
+                  uint16_t* to = pre + ((uint32_t)(r + b * kStep) * 2u * (uint32_t)a.N + ch);
+                  *(u32x4*)to = pack8(v[b]);
+                  *(u32x4*)(to + a.N) = pack8(u[b]);
+                }
+            act_each(a.act, v);
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+#pragma unroll
+              for (int c = 0; c < 8; ++c) v[b][c] *= u[b][c];
+          } else {
+            if (a.bias)
+#pragma unroll
+              for (int b = 0; b < B; ++b)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) v[b][c] += bias[c / 4][c % 4];
+            if (pre)
+#pragma unroll
+              for (int b = 0; b < B; ++b)
+                if (r + b * kStep < t.rows && in)
+                  *(u32x4*)(pre + ((uint32_t)(r + b * kStep) * (uint32_t)a.N + ch)) = pack8(v[b]);
+            act_each(a.act, v);
+            if (a.residual)
+#pragma unroll
+              for (int b = 0; b < B; ++b) {
+                float more[8];
+                unpack8(add[b], more);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) v[b][c] += more[c];
+              }
+          }
+#pragma unroll
+          for (int b = 0; b < B; ++b)
+            if (r + b * kStep < t.rows && in) {
+              if (codes)
+                *(EP_LDS u32x4*)(base + kTurn + (r + b * kStep) * kRow + ch * 2) = pack8(v[b]);
+              else
+                *(u32x4*)(y + ((uint32_t)(r + b * kStep) * (uint32_t)a.N + ch)) = pack8(v[b]);
+            }
+        });
     if (codes) store_codes(t, base);
   }
 

@@ -63,15 +63,24 @@ __device__ __forceinline__ float gauss_cdf(float v) {
   return v < 0.0f ? tail : 1.0f - tail;
 }
 
-// one branch for eight values
-__device__ __forceinline__ void act_each(int act, float (&v)[8]) {
+// one branch for all values
+template <int B>
+__device__ __forceinline__ void act_each(int act, float (&v)[B][8]) {
   if (act == EP_ACT_SILU) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] = v[c] * sigmoid(v[c]);
-  } else if (act != EP_ACT_NONE) {
+    for (int b = 0; b < B; ++b)
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      v[c] = act == EP_ACT_RELU ? (v[c] < 0.0f ? 0.0f : v[c]) : v[c] * gauss_cdf(v[c]);
+      for (int c = 0; c < 8; ++c) v[b][c] = v[b][c] * sigmoid(v[b][c]);
+  } else if (act == EP_ACT_GELU) {
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[b][c] = v[b][c] * gauss_cdf(v[b][c]);
+  } else if (act == EP_ACT_RELU) {
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[b][c] = v[b][c] < 0.0f ? 0.0f : v[b][c];
   }
 }
 
@@ -908,22 +917,55 @@ struct Turned {
   }
 };
 
-// put(wc, r, c, turned): row r of the workgroup's tile, channel c (a multiple of
-// 8) of the first OUT channel tiles of the waves in column wc.  A lane's
-// channels are the same in every call.
-template <class S, int OUT, class Put>
+// What a lane of turn_out stores: channels from `channel` on of the first OUT channel
+// tiles of the waves in column wc, the same for all its rows.
+template <class S, int OUT>
+struct TurnLane {
+  static constexpr int kVecs = OUT * S::MF / 8;  // vectors of a row
+  // threads that turn a region together: a wave, or those that share a tile
+  static constexpr int kThreads = S::WK > 1 ? kGemmThreads / S::WC : kWave;
+  static constexpr int kRows = kThreads / kVecs;  // rows at once
+  static constexpr int kTurns = kRows >= S::MF ? 1 : S::MF / kRows;
+  static constexpr int kBatch = kTurns < 4 ? kTurns : 4;  // rows that a lane stores together
+  int wc, row, channel;
+  __device__ __forceinline__ TurnLane() {
+    const int id = threadIdx.x % kThreads;
+    wc = S::WK > 1 ? uniform(threadIdx.x / kThreads) : S().wc;
+    row = id / kVecs;
+    channel = id % kVecs * 8;
+  }
+};
+
+// Rows r, r + kRows, ..: fetch(r) loads what a row's result needs from memory;
+// put(r, turned, fetched) takes kBatch rows.  With two stages the loads go out one
+// turn ahead: a load behind a store waits for the store as well (linear product with
+// residual, 64 experts x 2,048 rows, 2048 x 7168: 4.23 -> 3.72 ms).  The ring's
+// loads of the next tile are already under way and are waited for in any case; there
+// the registers for it cost more (FP8 decode 744 -> 812 us).
+template <class S, int OUT, class Fetch, class Put>
 __device__ __forceinline__ void turn_out(lds_char* lds, const typename S::acc_t (&acc)[S::CT][S::TT],
-                                         Put put) {
+                                         Fetch fetch, Put put) {
   typedef Turned<S> T;
-  constexpr int MF = S::MF;
-  constexpr int kVecs = OUT * MF / 8, kRows = kWave / kVecs;  // vectors of a row; rows at once
+  typedef TurnLane<S, OUT> Lane;
+  constexpr int MF = S::MF, kTurns = Lane::kTurns, kBatch = Lane::kBatch;
   const int lane = lane_id(), wave = uniform(threadIdx.x >> 6);
   const S place;
+  const Lane at;
+  constexpr int kAhead = S::STAGES == 2 ? 1 : 0;
+  decltype(fetch(0)) fetched[kAhead + 1][kTurns];
+  auto fetch_all = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i)
+      fetched[j & kAhead][i] = fetch((place.wr * S::TT + j) * MF + at.row + i * Lane::kRows);
+  };
+  if (kAhead) fetch_all(0);
   barrier();
   lds_char* mine = lds + wave * (MF * T::kRowBytes);
-  const int r0 = lane / kVecs, c = lane % kVecs * 8;
+  const lds_char* from =
+      (S::WK > 1 ? lds + at.wc * (MF * T::kRowBytes) : mine) + at.row * T::kRowBytes + at.channel * 2;
 #pragma unroll
   for (int j = 0; j < S::TT; ++j) {
+    if (j + kAhead < S::TT) fetch_all(j + kAhead);
     lds_char* to = mine + (lane % MF) * T::kRowBytes;
 #pragma unroll
     for (int i = 0; i < S::CT; ++i)
@@ -934,24 +976,23 @@ __device__ __forceinline__ void turn_out(lds_char* lds, const typename S::acc_t 
         const int quad = (i * MF + channel_of<MF>(q)) / 4;
         *(EP_LDS f32x4*)(to + (quad & 1) * T::kHalf + (quad >> 1) * 16) = v;
       }
-    if constexpr (S::WK > 1) {  // the waves that share a tile store parts of it
-      static_assert(S::WT == 1, "");
-      barrier();
-      constexpr int kThreads = kGemmThreads / S::WC;  // of one column
-      const int column = uniform(threadIdx.x / kThreads), id = threadIdx.x % kThreads;
-      const lds_char* from = lds + column * (MF * T::kRowBytes);
-      for (int r = id / kVecs; r < MF; r += kThreads / kVecs)
-        put(column, j * MF + r, id % kVecs * 8, T{from + r * T::kRowBytes + id % kVecs * 16});
-      if (j + 1 < S::TT) barrier();
-      continue;
+    static_assert(S::WK == 1 || (S::WT == 1 && S::TT == 1), "one region for the waves of a tile");
+    if (S::WK > 1) barrier();
+    else wave_lds_sync();
+    if (Lane::kRows <= MF || at.row < MF) {
+#pragma unroll
+      for (int i = 0; i < kTurns; i += kBatch) {
+        T turned[kBatch];
+        decltype(fetch(0)) own[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          turned[b].at = from + (i + b) * Lane::kRows * T::kRowBytes;
+          own[b] = fetched[j & kAhead][i + b];
+        }
+        put((place.wr * S::TT + j) * MF + at.row + i * Lane::kRows, turned, own);
+      }
     }
-    wave_lds_sync();
-    if (kRows <= MF || r0 < MF) {
-#pragma unroll 2
-      for (int r = r0; r < MF; r += kRows)
-        put(place.wc, (place.wr * S::TT + j) * MF + r, c, T{mine + r * T::kRowBytes + c * 2});
-    }
-    wave_lds_sync();
+    if (S::WK == 1) wave_lds_sync();
   }
 }
 

@@ -196,13 +196,18 @@ struct Dx {
 
   __device__ __forceinline__ void epilogue(const DxTile& t, lds_char* base) {
     uint16_t* out = a.dx + t.row * a.C + t.n0;
-    turn_out<S, S::CT>(base, *(typename S::acc_t(*)[S::CT][S::TT])acc,
-                       [&](int wc, int r, int c, const Turned<S>& turned) {
-      const int ch = wc * S::CT * S::MF + c;
-      if (r < t.rows && t.n0 + ch < a.C) {
-        float v[8];
-        turned.get(0, v);
-        *(u32x4*)(out + ((uint32_t)r * (uint32_t)a.C + ch)) = pack8(v);
+    const TurnLane<S, S::CT> lane;
+    const int ch = lane.wc * S::CT * S::MF + lane.channel;
+    turn_out<S, S::CT>(base, *(typename S::acc_t(*)[S::CT][S::TT])acc, [](int) { return 0; },
+                       [&](int r, const Turned<S>(&turned)[lane.kBatch], const int(&)[lane.kBatch]) {
+#pragma unroll
+      for (int b = 0; b < lane.kBatch; ++b) {
+        const int row = r + b * lane.kRows;
+        if (row < t.rows && t.n0 + ch < a.C) {
+          float v[8];
+          turned[b].get(0, v);
+          *(u32x4*)(out + ((uint32_t)row * (uint32_t)a.C + ch)) = pack8(v);
+        }
       }
     });
   }
@@ -297,13 +302,18 @@ struct Dw {
 
   __device__ __forceinline__ void epilogue(int, lds_char* base) {
     uint16_t* out = a.dw + ((int64_t)e * a.O + o0) * a.C + c0;
-    turn_out<S, S::CT>(base, *(typename S::acc_t(*)[S::CT][S::TT])acc,
-                       [&](int wc, int r, int c, const Turned<S>& turned) {
-      const int ch = wc * S::CT * S::MF + c;
-      if (o0 + r < a.O && c0 + ch < a.C) {
-        float v[8];
-        turned.get(0, v);
-        *(u32x4*)(out + ((uint32_t)r * (uint32_t)a.C + ch)) = pack8(v);
+    const TurnLane<S, S::CT> lane;
+    const int ch = lane.wc * S::CT * S::MF + lane.channel;
+    turn_out<S, S::CT>(base, *(typename S::acc_t(*)[S::CT][S::TT])acc, [](int) { return 0; },
+                       [&](int r, const Turned<S>(&turned)[lane.kBatch], const int(&)[lane.kBatch]) {
+#pragma unroll
+      for (int b = 0; b < lane.kBatch; ++b) {
+        const int row = r + b * lane.kRows;
+        if (o0 + row < a.O && c0 + ch < a.C) {
+          float v[8];
+          turned[b].get(0, v);
+          *(u32x4*)(out + ((uint32_t)row * (uint32_t)a.C + ch)) = pack8(v);
+        }
       }
     });
   }
