@@ -355,7 +355,8 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_dw(GradArgs a) {
 typedef Shape<32, 4, 4, 2, 2, 2> Big;     // 256 channels x 256 rows
 typedef Shape<32, 2, 2, 4, 1, 3> Medium;  // 256 x 64
 typedef Shape<16, 2, 1, 4, 1, 3> Small;   // 128 x 16
-typedef Shape<32, 2, 2, 2, 2, 3> Square;  // 128 x 128
+typedef Shape<32, 2, 2, 2, 2, 3> Square;  // 128 x 128, one on a compute unit
+typedef Shape<32, 2, 2, 2, 2, 4, 64> Pair;  // the same in 64 KiB, two on one
 
 template <int CH>
 static void launch_dbias(const GradArgs& a, hipStream_t st) {
@@ -417,9 +418,18 @@ hipError_t launch_expert_grad(const GradArgs& a, hipStream_t st) {
     else launch_dx<Big>(a, st);
   }
   if (a.dw) {
-    const int64_t tiles = (int64_t)a.seg.E * ((a.C + 255) / 256) * ((a.O + 255) / 256);
-    if (tiles >= kCus) launch_dw<Big>(a, st);
-    else launch_dw<Square>(a, st);
+    // The largest tiles that fill the chip; of the smaller ones two on a compute unit
+    // where there are more of them than compute units.  us, Square / Pair: 8 experts of
+    // 1024 x 1024 (512 tiles), 16 rows 12.1 / 8.4, 512 rows 16.3 / 14.6; 1 expert of
+    // 2048 x 2048 (256 tiles), 16 rows 5.7 / 5.4, 8,192 rows 74 / 87.  8 experts of 4096 x
+    // 4096, Big / Square: 64 rows 76 / 118, 2,048 rows 470 / 749; 1 of 2048 x 2048 (64 of
+    // Big's tiles): 12 / 6 and 60 / 22.
+    const auto tiles = [&](int side) {
+      return (int64_t)a.seg.E * ((a.C + side - 1) / side) * ((a.O + side - 1) / side);
+    };
+    if (tiles(Big::BN) >= kCus) launch_dw<Big>(a, st);
+    else if (tiles(Square::BN) <= kCus) launch_dw<Square>(a, st);
+    else launch_dw<Pair>(a, st);
   }
   return hipGetLastError();
 }

@@ -825,6 +825,7 @@ WIDE = [
     (1, 300, 32, 4, N, 0.1, 328, 1032),
     (1, 260, 4, 2, N, 0.1, 2056, 1032),
     (1, 400, 16, 4, N, 0.1, 2056, 136),
+    (1, 900, 4, 2, N, 0.1, 648, 1096),
 ]
 WIDE_IDS = ["-".join(map(str, s)) for s in WIDE]
 
