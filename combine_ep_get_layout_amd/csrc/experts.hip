@@ -168,7 +168,13 @@ struct Forward {
   __device__ __forceinline__ void epilogue(const Tile& t, lds_char* base) {
     typedef TurnLane<S, CH> Lane;
     constexpr int B = Lane::kBatch, kStep = Lane::kRows;
-    typedef typename std::conditional<GATED, NoRow, u32x4>::type Row8;
+    // With two stages the residual is loaded ahead of its use (turn_out).  In the
+    // ring it is loaded and used in one branch: a load that some path leaves
+    // unused is waited for where its registers are next written, in the main loop,
+    // and with it every load of the stages in flight (1 expert, 4096 x 8192, 64
+    // rows of Medium: 35 -> 55 us).
+    constexpr bool kAhead = S::STAGES == 2 && !GATED;
+    typedef typename std::conditional<kAhead, u32x4, NoRow>::type Row8;
     const bool codes = FP8 && ON >= 128 && a.y_quant != EP_QUANT_NONE;
     const Lane lane;
     const int ch = lane.wc * CH * MF + lane.channel;  // within the tile
@@ -176,17 +182,12 @@ struct Forward {
     const int64_t first = t.row * a.N + t.n0;
     uint16_t* const y = (uint16_t*)a.y + first;
     uint16_t* const pre = a.pre ? a.pre + (GATED ? t.row * 2 * a.N + t.n0 : first) : nullptr;
-    f32x4 bias[2] = {};
-    if (!GATED && a.bias && in) {
-      const float* b = a.bias + (int64_t)t.e * a.N + t.n0 + ch;
-      bias[0] = *(const f32x4*)b;
-      bias[1] = *(const f32x4*)(b + 4);
-    }
+    const float* const bias = a.bias + ((int64_t)t.e * a.N + t.n0 + (in ? ch : 0));
     turn_out<S, CH>(
         base, *(typename S::acc_t(*)[S::CT][S::TT])acc,
         [&](int r) {
           Row8 row = {};
-          if constexpr (!GATED)
+          if constexpr (kAhead)
             if (a.residual && r < t.rows && in)
               row = *(const u32x4*)(a.residual + first + (uint32_t)r * (uint32_t)a.N + ch);
           return row;
@@ -213,25 +214,39 @@ struct Forward {
 #pragma unroll
               for (int c = 0; c < 8; ++c) v[b][c] *= u[b][c];
           } else {
-            if (a.bias)
+            if (a.bias) {
+              const f32x4 b0 = *(const f32x4*)bias, b1 = *(const f32x4*)(bias + 4);
 #pragma unroll
               for (int b = 0; b < B; ++b)
 #pragma unroll
-                for (int c = 0; c < 8; ++c) v[b][c] += bias[c / 4][c % 4];
+                for (int c = 0; c < 8; ++c) v[b][c] += c < 4 ? b0[c] : b1[c - 4];
+            }
             if (pre)
 #pragma unroll
               for (int b = 0; b < B; ++b)
                 if (r + b * kStep < t.rows && in)
                   *(u32x4*)(pre + ((uint32_t)(r + b * kStep) * (uint32_t)a.N + ch)) = pack8(v[b]);
             act_each(a.act, v);
-            if (a.residual)
+            if (a.residual) {
+              u32x4 row[B];
+#pragma unroll
+              for (int b = 0; b < B; ++b) {
+                if constexpr (kAhead)
+                  row[b] = add[b];
+                else  // past the tile's end: its first row
+                  row[b] = *(const u32x4*)(
+                      a.residual + first +
+                      (r + b * kStep < t.rows && in
+                           ? (uint32_t)(r + b * kStep) * (uint32_t)a.N + ch : 0u));
+              }
 #pragma unroll
               for (int b = 0; b < B; ++b) {
                 float more[8];
-                unpack8(add[b], more);
+                unpack8(row[b], more);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) v[b][c] += more[c];
               }
+            }
           }
 #pragma unroll
           for (int b = 0; b < B; ++b)
@@ -321,6 +336,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
 typedef Shape<32, 4, 4, 2, 2, 2> Big;     // 256 channels x 256 rows
 typedef Shape<32, 4, 2, 2, 2, 3> Big8;    // 256 x 128 (FP8 sums are scaled in vector registers)
 typedef Shape<32, 2, 2, 4, 1, 3> Medium;  // 256 x 64
+typedef Shape<32, 2, 1, 2, 2, 3> Narrow;  // 128 x 64, two workgroups on a compute unit
 typedef Shape<16, 2, 1, 4, 1, 3> Small;   // 128 x 16
 typedef Shape<16, 2, 1, 1, 1, 3, 512, 4> Tiny;  // 32 x 16, the waves share the contraction
 
@@ -349,17 +365,17 @@ static double time_of(const ExpertArgs& a, double stage, double tile) {
 
 // The shape with the least expected time, in units of a stage of Medium; the
 // stages' times are fitted to measurements of every shape at 1 to 128 experts, 1 to
-// 512 rows each (random routing), 648 to 8192 channels.  The choice is 2% off the
-// best shape on average and 28% at worst (FP8 1% and 17%); by rows per expert alone
-// it was 24% off, and 4.9 times at worst (FP8 21%, 4.0 times).  us, bf16, Big / Medium
-// / Small / Tiny:
-//   1 expert, 2048 x 2048, 8 rows:       39 /  20 /   12 /    7
-//   1 expert, 4096 x 8192, 512 rows:     82 /  44 /  124 /  149
-//   8 experts, 1024 x 1024, 512 rows:    33 /  17 /   38 /   60
-//   64 experts, 4096 x 4096, 64 rows:   553 / 400 /  762 /  801
-//   64 experts, 4096 x 4096, 256 rows:  638 / 846 / 2663 / 2646
+// 2,048 rows each (random routing), 648 to 8192 channels.  Narrow is for tiles
+// that all run at once.  The choice is 3% off the best shape on average and 35% at
+// worst (FP8 2% and 48%); by rows per expert alone it was 24% off, and 4.9 times
+// at worst (FP8 21%, 4.0 times).  us, bf16, Big / Medium / Narrow / Small / Tiny:
+//   1 expert, 2048 x 2048, 8 rows:       42 /  20 /  14 /   12 /    7
+//   1 expert, 4096 x 8192, 192 rows:     77 /  38 /  28 /   61 /   60
+//   8 experts, 5584 x 1560, 96 rows:    122 /  70 /  48 /  115 /   71
+//   64 experts, 4096 x 4096, 64 rows:   554 / 444 / 483 /  829 /  882
+//   64 experts, 4096 x 4096, 192 rows:  612 / 762 / 875 / 1900 / 2196
 // A result in FP8 needs its groups of 128 channels whole in a tile, gated or not:
-// only the two larger shapes have them.
+// only the two largest shapes have them.
 template <bool GATED, int Q>
 static void choose(const ExpertArgs& a, hipStream_t st) {
   constexpr bool FP8 = Q != EP_QUANT_NONE;
@@ -368,9 +384,16 @@ static void choose(const ExpertArgs& a, hipStream_t st) {
   const double medium = time_of<Medium, GATED, Q>(a, 1.0, FP8 ? 0.3 : 0.0);
   const double small = time_of<Small, GATED, Q>(a, FP8 ? 0.9 : 0.95, 0.0);
   const double tiny = time_of<Tiny, GATED, Q>(a, FP8 ? 0.4 : 1.1, FP8 ? 3.5 : 1.5);
+  const int64_t wide = (int64_t)a.N * (GATED ? 2 : 1);
+  const double tiles = row_tiles(a.seg, a.rows, Narrow::BM) *
+                       (double)((wide + Narrow::BN - 1) / Narrow::BN);
+  const double narrow = tiles > slots<Narrow, Q>()
+                            ? HUGE_VAL
+                            : time_of<Narrow, GATED, Q>(a, FP8 ? 0.78 : 0.8, FP8 ? 2.0 : 0.0);
   const bool any = a.y_quant == EP_QUANT_NONE;
-  if (any && tiny < std::min({large, medium, small})) launch<Tiny, GATED, Q>(a, st);
-  else if (any && small < std::min(large, medium)) launch<Small, GATED, Q>(a, st);
+  if (any && tiny < std::min({large, medium, narrow, small})) launch<Tiny, GATED, Q>(a, st);
+  else if (any && small < std::min({large, medium, narrow})) launch<Small, GATED, Q>(a, st);
+  else if (any && narrow < std::min(large, medium)) launch<Narrow, GATED, Q>(a, st);
   else if (medium < large) launch<Medium, GATED, Q>(a, st);
   else launch<Large, GATED, Q>(a, st);
 }

@@ -936,12 +936,10 @@ struct TurnLane {
   }
 };
 
-// Rows r, r + kRows, ..: fetch(r) loads what a row's result needs from memory;
-// put(r, turned, fetched) takes kBatch rows.  With two stages the loads go out one
-// turn ahead: a load behind a store waits for the store as well (linear product with
-// residual, 64 experts x 2,048 rows, 2048 x 7168: 4.23 -> 3.72 ms).  The ring's
-// loads of the next tile are already under way and are waited for in any case; there
-// the registers for it cost more (FP8 decode 744 -> 812 us).
+// Rows r, r + kRows, ..: fetch(r) loads what a row's result needs from memory, one turn
+// ahead: a load behind a store waits for the store as well (linear product with
+// residual, 64 experts x 2,048 rows, 2048 x 7168: 4.23 -> 3.72 ms).  put(r, turned,
+// fetched) takes kBatch rows.
 template <class S, int OUT, class Fetch, class Put>
 __device__ __forceinline__ void turn_out(lds_char* lds, const typename S::acc_t (&acc)[S::CT][S::TT],
                                          Fetch fetch, Put put) {
@@ -951,21 +949,20 @@ __device__ __forceinline__ void turn_out(lds_char* lds, const typename S::acc_t 
   const int lane = lane_id(), wave = uniform(threadIdx.x >> 6);
   const S place;
   const Lane at;
-  constexpr int kAhead = S::STAGES == 2 ? 1 : 0;
-  decltype(fetch(0)) fetched[kAhead + 1][kTurns];
+  decltype(fetch(0)) fetched[2][kTurns];
   auto fetch_all = [&](int j) {
 #pragma unroll
     for (int i = 0; i < kTurns; ++i)
-      fetched[j & kAhead][i] = fetch((place.wr * S::TT + j) * MF + at.row + i * Lane::kRows);
+      fetched[j & 1][i] = fetch((place.wr * S::TT + j) * MF + at.row + i * Lane::kRows);
   };
-  if (kAhead) fetch_all(0);
+  fetch_all(0);
   barrier();
   lds_char* mine = lds + wave * (MF * T::kRowBytes);
   const lds_char* from =
       (S::WK > 1 ? lds + at.wc * (MF * T::kRowBytes) : mine) + at.row * T::kRowBytes + at.channel * 2;
 #pragma unroll
   for (int j = 0; j < S::TT; ++j) {
-    if (j + kAhead < S::TT) fetch_all(j + kAhead);
+    if (j + 1 < S::TT) fetch_all(j + 1);
     lds_char* to = mine + (lane % MF) * T::kRowBytes;
 #pragma unroll
     for (int i = 0; i < S::CT; ++i)
@@ -987,7 +984,7 @@ __device__ __forceinline__ void turn_out(lds_char* lds, const typename S::acc_t 
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
           turned[b].at = from + (i + b) * Lane::kRows * T::kRowBytes;
-          own[b] = fetched[j & kAhead][i + b];
+          own[b] = fetched[j & 1][i + b];
         }
         put((place.wr * S::TT + j) * MF + at.row + i * Lane::kRows, turned, own);
       }

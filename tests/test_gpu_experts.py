@@ -850,6 +850,7 @@ def test_wide_gradients(shape):
     (1, 256, 16, 4, N, 1664, 640),
     (1, 200, 64, 4, L, 384, 640),
     (1, 10, 64, 2, L, 2688, 256),
+    (1, 1500, 1, 1, N, 1664, 1024),
 ], ids=lambda s: "-".join(map(str, s)))
 def test_wide_fp8(shape, quant):
     test_fp8_rows_of_a_dispatch(shape, "gated", quant)
