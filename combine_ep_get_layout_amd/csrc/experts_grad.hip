@@ -148,7 +148,7 @@ struct Dx {
   const GradArgs& a;
   const TilePlan& plan;
   lds_char* lds;
-  int nk, nfull, wc, mt, nt;
+  int nk, nfull, mt, nt;
   int64_t z_bytes, w_bytes;
   Chan w_tile;
   Row z_tile;
@@ -157,7 +157,6 @@ struct Dx {
 
   __device__ __forceinline__ Dx(const GradArgs& a_, const TilePlan& p, lds_char* l)
       : a(a_), plan(p), lds(l) {
-    wc = S().wc;
     z_bytes = (int64_t)a.O * 2;
     w_bytes = (int64_t)a.C * 2;
     nk = (a.O + S::KR - 1) / S::KR;
@@ -260,7 +259,7 @@ struct Dw {
 
   const GradArgs& a;
   lds_char* lds;
-  int nk, nfull, wc, e, count, c0, o0;
+  int nk, nfull, e, count, c0, o0;
   int64_t x_bytes, z_bytes;
   Chan x_tile;
   Row z_tile;
@@ -268,7 +267,6 @@ struct Dw {
   typename S::acc_t (*acc)[S::TT];
 
   __device__ __forceinline__ Dw(const GradArgs& a_, lds_char* l) : a(a_), lds(l) {
-    wc = S().wc;
     x_bytes = (int64_t)a.C * 2;
     z_bytes = (int64_t)a.O * 2;
   }
