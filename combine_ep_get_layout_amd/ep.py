@@ -496,8 +496,14 @@ def _rows(p: Problem, t: torch.Tensor, what: str, channels: int | None = None,
         _need(t.dtype in _CODES, f"{what}: FP8 codes are e4m3, or bytes")
         _need(scales.dtype in (torch.float32, torch.uint8), f"{what} scales fp32 or uint8 (UE8M0)")
         quant = QUANT_FP8_F32 if scales.dtype == torch.float32 else QUANT_FP8_UE8M0
-        rows = t.shape[0] if p.mode == MODE_NORMAL else p.E * p.R * p.T
-        _need(scales.numel() >= t.shape[1] // 128 * rows, f"{what} scales")
+        groups, n = t.shape[1] // 128, scales.numel()
+        if p.mode == MODE_NORMAL:
+            # [groups][rows]: the row buffer's length is the stride between groups, so the scales
+            # of a longer buffer would be read at the wrong places (none are read without rows)
+            _need(n == groups * t.shape[0] or t.shape[0] == 0,
+                  f"{what} scales [{what} channels/128][{what} rows]")
+        else:  # [E][groups][R*T]
+            _need(n >= groups * p.E * p.R * p.T, f"{what} scales")
     return CRows(_ptr(t), _ptr(scales), t.shape[0], t.shape[1], quant)
 
 

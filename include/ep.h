@@ -310,7 +310,8 @@ int ep_combine(const ep_problem* p, const ep_layout* layout, const uint16_t* y,
 /* One row buffer. */
 typedef struct ep_rows {
   void* x;          /* [capacity][channels] bf16, or e4m3 codes, 16-byte aligned      */
-  void* scales;     /* FP8: as ep_recv.scales with G = channels / 128, else ignored   */
+  void* scales;     /* FP8: as ep_recv.scales with G = channels / 128 (in normal mode
+                       capacity is the stride between groups), else ignored           */
   int64_t capacity; /* rows; low-latency and messages need >= E*R*T                   */
   int32_t channels;
   int32_t quant;    /* EP_QUANT_* of these rows                                       */
