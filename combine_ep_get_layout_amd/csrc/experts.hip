@@ -19,6 +19,24 @@
 
 namespace ep {
 
+// Replaces the NaNs and infinities of eight bf16 by zeros; their halves come back as
+// 0xFFFF.
+__device__ __forceinline__ u32x4 take_not_finite(u32x4& v) {
+  u32x4 at;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    at[q] = ((v[q] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) |
+            ((v[q] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+    v[q] &= ~at[q];
+  }
+  return at;
+}
+
+// e4m3 NaN codes where the halves of two words are set
+__device__ __forceinline__ uint32_t nan_codes(uint32_t a, uint32_t b) {
+  return (a & 0x7Fu) | (a >> 16 & 0x7Fu) << 8 | (b & 0x7Fu) << 16 | (b >> 16 & 0x7Fu) << 24;
+}
+
 // Nothing to load for a row's result.
 struct NoRow {};
 
@@ -261,14 +279,22 @@ struct Forward {
   }
 
   // FP8 output: eight lanes take 128 channels of a row, quantised as dispatch
-  // does a bf16 row
+  // does a bf16 row.  That takes a group's maximum by bit patterns and saturates, so a
+  // NaN or infinity would turn the group into plausible finite values: each is
+  // quantised as a zero here and gets the NaN code (e4m3 has no infinity).
   __device__ __forceinline__ void store_codes(const Tile& t, lds_char* base) {
     barrier();
     constexpr int kGroups = ON >= 128 ? ON / 128 : 1;
     for (int at = threadIdx.x / 8; at < S::BM * kGroups; at += kGemmThreads / 8) {
       const int r = at / kGroups, g = at % kGroups, l = threadIdx.x % 8;
       const EP_LDS u32x4* from = (const EP_LDS u32x4*)(base + kTurn + r * kRow + g * 256 + l * 32);
-      const u32x4 lo = from[0], hi = from[1];
+      u32x4 lo = from[0], hi = from[1];
+      const bool bad = absmax16(lo, hi) >= 0x7F80u;
+      u32x4 bad_lo = {}, bad_hi = {};
+      if (bad) {
+        bad_lo = take_not_finite(lo);
+        bad_hi = take_not_finite(hi);
+      }
       u32x4 out;
       float scale;
       uint32_t exponent;
@@ -276,6 +302,13 @@ struct Forward {
         quantise_pair<EP_QUANT_FP8_F32>(lo, hi, out, scale, exponent);
       else
         quantise_pair<EP_QUANT_FP8_UE8M0>(lo, hi, out, scale, exponent);
+      if (bad) {  // their codes are zero
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          out[q] |= nan_codes(bad_lo[2 * q], bad_lo[2 * q + 1]);
+          out[2 + q] |= nan_codes(bad_hi[2 * q], bad_hi[2 * q + 1]);
+        }
+      }
       const int ch = t.n0 + g * 128;
       if (r < t.rows && ch < a.N) {
         *(u32x4*)((char*)a.y + (t.row + r) * a.N + ch + l * 16) = out;

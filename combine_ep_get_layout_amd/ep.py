@@ -541,7 +541,7 @@ def expert_gated(p: Problem, layout: Layout, x: torch.Tensor, w: torch.Tensor, h
     x [rows][C], w [E][2 I][C] (gates first), h [rows][I]; `pre` [rows][2 I]
     keeps both projections for expert_gated_backward.  FP8 (codes as bytes):
     x with the dispatch's scales and w with w_scales [E][2 I/128][C/128]; h then
-    may be FP8 too (h_scales, fp32 or uint8)."""
+    may be FP8 too (h_scales, fp32 or uint8), its NaNs and infinities as NaN codes."""
     _invoke(_expert_gated_args(p, layout, x, w, h, act=act, x_scales=x_scales, w_scales=w_scales,
                                h_scales=h_scales, pre=pre), stream)
 

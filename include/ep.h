@@ -336,6 +336,8 @@ typedef struct ep_weights {
  * x: bf16 rows with bf16 weights, or FP8 rows with FP8 weights.
  * h: [capacity][I] bf16; with FP8 rows also FP8: the bf16 result quantised as
  *   dispatch quantises a row (scale per 128 channels), for an FP8 product next.
+ *   A NaN or infinity becomes the NaN code 0x7F (e4m3 has no infinity), and its
+ *   group's scale is that of the finite values.
  * pre: [capacity][2 I] bf16 [g | u], saved for ep_expert_gated_backward, or
  *   NULL. */
 int ep_expert_gated(const ep_problem* p, const ep_layout* layout, const ep_rows* x,
