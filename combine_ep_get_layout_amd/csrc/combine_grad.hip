@@ -21,10 +21,10 @@ __device__ __forceinline__ uint32_t bf16_any(float f) {
 constexpr int kGradThreads = 256;
 
 template <bool RM>
-__global__ __launch_bounds__(kGradThreads) void combine_grad(CombineGradArgs a) {
+__global__ __launch_bounds__(kGradThreads) void combine_grad(CombineGradArgs a, int64_t first) {
   __shared__ float part[64][kGradThreads / kWave];
   const int V = a.g.H / 8, K = a.g.K;
-  const int64_t tok = blockIdx.x;
+  const int64_t tok = first + blockIdx.x;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int myrow = lane < K ? a.send_pos[tok * K + lane] : -1;
   const float myw = !RM && lane < K && a.w ? a.w[tok * K + lane] : 1.0f;
@@ -75,14 +75,21 @@ __global__ __launch_bounds__(kGradThreads) void combine_grad(CombineGradArgs a) 
   }
 }
 
+// Tokens of a launch: a grid holds fewer than 2^32 threads.
+constexpr int64_t kGradTokens = (1ll << 31) / kGradThreads;
+
 hipError_t launch_combine_grad(const CombineGradArgs& a, hipStream_t st) {
   const int64_t N = (int64_t)a.g.R * a.g.T;
-  if (N == 0) return hipSuccess;
-  if (a.rank_major)
-    hipLaunchKernelGGL(combine_grad<true>, dim3((unsigned)N), dim3(kGradThreads), 0, st, a);
-  else
-    hipLaunchKernelGGL(combine_grad<false>, dim3((unsigned)N), dim3(kGradThreads), 0, st, a);
-  return hipGetLastError();
+  for (int64_t first = 0; first < N; first += kGradTokens) {
+    const dim3 grid((unsigned)(N - first < kGradTokens ? N - first : kGradTokens));
+    if (a.rank_major)
+      hipLaunchKernelGGL(combine_grad<true>, grid, dim3(kGradThreads), 0, st, a, first);
+    else
+      hipLaunchKernelGGL(combine_grad<false>, grid, dim3(kGradThreads), 0, st, a, first);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace ep
