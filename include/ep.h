@@ -303,7 +303,9 @@ int ep_combine(const ep_problem* p, const ep_layout* layout, const uint16_t* y,
  * p->hidden and p->quant describe the dispatch and are not used: every
  * operand has its own channel count, a multiple of 8 in [8, 32768], and
  * 128 in FP8.  Sums are kept in fp32 and results rounded to bf16, nearest even,
- * once.  The calls are deterministic and need no workspace.  Row buffers that
+ * once; but of FP8 products eight (consecutive channels of a row) are added at a
+ * time, each cut off 13 bits below the largest of the eight, before they enter the
+ * fp32 sum (a relative error of about 2^-16 on random rows).  The calls are deterministic and need no workspace.  Row buffers that
  * a call reads must not overlap those it writes, but a residual may be the
  * output itself. */
 
