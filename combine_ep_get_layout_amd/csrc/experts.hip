@@ -62,9 +62,9 @@ struct Forward {
   static constexpr int kSlot = Chan::kBytes + Row::kBytes;
   static constexpr int kPasses = Chan::kPasses + Row::kPasses;
   static constexpr int kLoads = kPasses + (FP8 ? GS * S::SLOADS + 1 : 0);
-  static constexpr int kScales = (GS * S::SLOADS + 1) * kWave;
+  static constexpr int kScales = S::kScaleFloats;
   static constexpr int kScaleBytes = Q == EP_QUANT_FP8_F32 ? 4 : 1;
-  static constexpr int kTurn = 4 * MF * Turned<S>::kRowBytes;
+  static constexpr int kTurn = S::kTurnBytes;
   static constexpr int kRow = ON * 2 + 16;  // FP8 output: a row of the tile in bf16
 
   const ExpertArgs& a;
@@ -355,80 +355,43 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
   } else if constexpr (F::FP8) {
     RingEngine8<S, typename F::Chan, typename F::Row, GATED, Q> engine(base, (lds_float*)scales);
     f.acc = engine.acc;
-    run_ring<S, F::kTurn <= F::kSlot>(f, engine, base, block_place(), tiles,
+    run_ring<S, S::kChains>(f, engine, base, block_place(), tiles,
                                       a.y_quant == EP_QUANT_NONE);
   } else {
     RingEngine<S, typename F::Chan, typename F::Row> engine(base);
     f.acc = engine.acc;
-    run_ring<S, F::kTurn <= F::kSlot>(f, engine, base, block_place(), tiles, true);
+    run_ring<S, S::kChains>(f, engine, base, block_place(), tiles, true);
   }
 }
 
-// Large tiles read the LDS least per product; narrow ones waste no products on rows
-// that are not there, and with many of them few rows still fill the chip.
-typedef Shape<32, 4, 4, 2, 2, 2> Big;     // 256 channels x 256 rows
-typedef Shape<32, 4, 2, 2, 2, 3> Big8;    // 256 x 128 (FP8 sums are scaled in vector registers)
-typedef Shape<32, 2, 2, 4, 1, 3> Medium;  // 256 x 64
-typedef Shape<32, 2, 1, 2, 2, 3> Narrow;  // 128 x 64, two workgroups on a compute unit
-typedef Shape<16, 2, 1, 4, 1, 3> Small;   // 128 x 16
-typedef Shape<16, 2, 1, 1, 1, 3, 512, 4> Tiny;  // 32 x 16, the waves share the contraction
-
-// Workgroups of a shape on the chip: by LDS, two a compute unit or one.
-template <class S, int Q>
-constexpr int slots() {
-  const int lds = S::kLds + (int)sizeof(TilePlan) +
-                  (Q == EP_QUANT_NONE ? 0 : S::STAGES * 4 * (S::GS * S::SLOADS + 1) * kWave * 4);
-  return lds <= 80 * 1024 ? 2 * kCus : kCus;
-}
+typedef Shape<BigDims> Big;
+typedef Shape<Big8Dims> Big8;
+typedef Shape<MediumDims> Medium;
+typedef Shape<NarrowDims> Narrow;
+typedef Shape<SmallDims> Small;
+typedef Shape<TinyDims> Tiny;
 
 template <class S, bool GATED, int Q>
 static void launch(const ExpertArgs& a, hipStream_t st) {
   const int on = GATED ? S::BN / 2 : S::BN;
   const int64_t tiles = ((a.rows + S::BM - 1) / S::BM + a.seg.E) * ((a.N + on - 1) / on);
-  hipLaunchKernelGGL((expert_forward<S, GATED, Q>),
-                     dim3((unsigned)std::min(tiles, (int64_t)slots<S, Q>())), dim3(kGemmThreads), 0,
-                     st, a);
+  constexpr int64_t kSlots = forward_slots<S, Q != EP_QUANT_NONE>();
+  hipLaunchKernelGGL((expert_forward<S, GATED, Q>), dim3((unsigned)std::min(tiles, kSlots)),
+                     dim3(kGemmThreads), 0, st, a);
 }
 
-template <class S, bool GATED, int Q>
-static double time_of(const ExpertArgs& a, double stage, double tile) {
-  return shape_time<S>(a.seg, a.rows, (int64_t)a.N * (GATED ? 2 : 1),
-                       (int64_t)a.C * (Q == EP_QUANT_NONE ? 2 : 1), slots<S, Q>(), stage, tile);
-}
-
-// The shape with the least expected time, in units of a stage of Medium; the
-// stages' times are fitted to measurements of every shape at 1 to 128 experts, 1 to
-// 2,048 rows each (random routing), 648 to 8192 channels.  Narrow is for tiles
-// that all run at once.  The choice is 3% off the best shape on average and 35% at
-// worst (FP8 2% and 48%); by rows per expert alone it was 24% off, and 4.9 times
-// at worst (FP8 21%, 4.0 times).  us, bf16, Big / Medium / Narrow / Small / Tiny:
-//   1 expert, 2048 x 2048, 8 rows:       42 /  20 /  14 /   12 /    7
-//   1 expert, 4096 x 8192, 192 rows:     77 /  38 /  28 /   61 /   60
-//   8 experts, 5584 x 1560, 96 rows:    122 /  70 /  48 /  115 /   71
-//   64 experts, 4096 x 4096, 64 rows:   554 / 444 / 483 /  829 /  882
-//   64 experts, 4096 x 4096, 192 rows:  612 / 762 / 875 / 1900 / 2196
-// A result in FP8 needs its groups of 128 channels whole in a tile, gated or not:
-// only the two largest shapes have them.
 template <bool GATED, int Q>
 static void choose(const ExpertArgs& a, hipStream_t st) {
   constexpr bool FP8 = Q != EP_QUANT_NONE;
   typedef typename std::conditional<FP8, Big8, Big>::type Large;
-  const double large = time_of<Large, GATED, Q>(a, FP8 ? 1.55 : 2.0, FP8 ? 0.0 : 1.0);
-  const double medium = time_of<Medium, GATED, Q>(a, 1.0, FP8 ? 0.3 : 0.0);
-  const double small = time_of<Small, GATED, Q>(a, FP8 ? 0.9 : 0.95, 0.0);
-  const double tiny = time_of<Tiny, GATED, Q>(a, FP8 ? 0.4 : 1.1, FP8 ? 3.5 : 1.5);
-  const int64_t wide = (int64_t)a.N * (GATED ? 2 : 1);
-  const double tiles = row_tiles(a.seg, a.rows, Narrow::BM) *
-                       (double)((wide + Narrow::BN - 1) / Narrow::BN);
-  const double narrow = tiles > slots<Narrow, Q>()
-                            ? HUGE_VAL
-                            : time_of<Narrow, GATED, Q>(a, FP8 ? 0.78 : 0.8, FP8 ? 2.0 : 0.0);
-  const bool any = a.y_quant == EP_QUANT_NONE;
-  if (any && tiny < std::min({large, medium, narrow, small})) launch<Tiny, GATED, Q>(a, st);
-  else if (any && small < std::min({large, medium, narrow})) launch<Small, GATED, Q>(a, st);
-  else if (any && narrow < std::min(large, medium)) launch<Narrow, GATED, Q>(a, st);
-  else if (medium < large) launch<Medium, GATED, Q>(a, st);
-  else launch<Large, GATED, Q>(a, st);
+  switch (choose_forward<FP8>(a.seg.E, a.rows, a.C, (int64_t)a.N * (GATED ? 2 : 1),
+                              a.y_quant != EP_QUANT_NONE)) {
+    case kTinyTile: return launch<Tiny, GATED, Q>(a, st);
+    case kSmallTile: return launch<Small, GATED, Q>(a, st);
+    case kNarrowTile: return launch<Narrow, GATED, Q>(a, st);
+    case kMediumTile: return launch<Medium, GATED, Q>(a, st);
+    case kLargeTile: return launch<Large, GATED, Q>(a, st);
+  }
 }
 
 template <bool GATED>

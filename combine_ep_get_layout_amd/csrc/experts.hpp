@@ -7,18 +7,13 @@
 // row and stores them as one 8-byte vector.
 #pragma once
 
-#include <algorithm>
-#include <cmath>
 #include <type_traits>
 
 #include "ep_device.hpp"
 #include "ep_internal.hpp"
+#include "experts_choice.hpp"
 
 namespace ep {
-
-constexpr int kMaxExperts = 2048;
-constexpr int kCus = 256;        // compute units of an MI355X
-constexpr int kGemmThreads = 256;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -471,31 +466,17 @@ __device__ __forceinline__ int channel_of(int q) {
   return MF == 32 ? 8 * q + 4 * (lane_id() / 32) : 4 * (lane_id() / 16);
 }
 
-// Shape of a workgroup's tile: WC x WT x WK waves, each CT x TT matrix-core
-// tiles of MF channels x MF rows; STAGES buffers of KB bytes along the
-// contraction, of which WK waves take a part each.
-template <int MF_, int CT_, int TT_, int WC_, int WT_, int STAGES_, int KB_ = 128, int WK_ = 1>
-struct Shape {
-  static constexpr int KB = KB_, KR = KB / 2;
-  static constexpr int MF = MF_, CT = CT_, TT = TT_, WC = WC_, WT = WT_, WK = WK_;
-  static constexpr int STAGES = STAGES_;
-  static constexpr int BN = WC * CT * MF, BM = WT * TT * MF;
-  static constexpr int KK = KR * MF / 512 / WK;     // bf16 matrix-core steps of a wave's stage
-  static constexpr int GS = KB / 128 / WK;          // FP8 scale groups of a wave's stage
-  static constexpr int KK8 = KB * MF / 2048 / WK;   // FP8 steps
-  static constexpr int kLds = STAGES * (BN + BM) * KB;
-  static constexpr int REGS = MF * MF / kWave;
-  static constexpr int WROWS = TT * MF;    // rows of a wave's tile
-  static constexpr int SLOADS = (WROWS + kWave - 1) / kWave;  // FP8 scale loads of a group
-  static_assert(WC * WT * WK * kWave == kGemmThreads, "four wavefronts");
-  typedef typename Mfma<MF>::acc_t acc_t;
-  // this wave's place
+// A tile's dimensions, and this wave's place in it.
+template <class D>
+struct Shape : D {
+  static_assert(kWavefront == kWave, "");
+  typedef typename Mfma<D::MF>::acc_t acc_t;
   int wc, wr, wk;
   __device__ __forceinline__ Shape() {
     const int wave = uniform(threadIdx.x >> 6);
-    wc = wave % WC;
-    wr = wave / WC % WT;
-    wk = wave / (WC * WT);
+    wc = wave % D::WC;
+    wr = wave / D::WC % D::WT;
+    wk = wave / (D::WC * D::WT);
   }
 };
 
@@ -518,27 +499,6 @@ __device__ __forceinline__ void tile_at(int64_t t, int mt, int nt, int& m, int& 
 __device__ __forceinline__ int block_place() {
   const int g = gridDim.x, b = blockIdx.x;
   return g % kXcds == 0 ? (b % kXcds) * (g / kXcds) + b / kXcds : b;
-}
-
-// ---- choice of a shape ---------------------------------------------------------
-
-// Row tiles of `step` rows that the segments are expected to make.  The counts
-// are on the device: an expert that is hit has the mean number of rows and, unless
-// it has all of them, half a tile more.
-inline double row_tiles(const Segments& s, int64_t rows, int step) {
-  const double hit = (double)std::min<int64_t>(rows, s.E);
-  if (hit <= 1.0) return (double)((rows + step - 1) / step);
-  return hit * std::max(1.0, (double)rows / hit / step + 0.5);
-}
-
-// Relative time of shape S: whole rounds of its workgroups (`slots` of them on the
-// chip) over a product of `channels` results a row and `bytes` of contraction.
-// stage, tile: the time of one of its stages, and of a tile's start and end.
-template <class S>
-inline double shape_time(const Segments& s, int64_t rows, int64_t channels, int64_t bytes,
-                         int slots, double stage, double tile) {
-  const double tiles = row_tiles(s, rows, S::BM) * (double)((channels + S::BN - 1) / S::BN);
-  return std::ceil(tiles / slots) * ((double)((bytes + S::KB - 1) / S::KB) * stage + tile);
 }
 
 // ---- main loop ---------------------------------------------------------------
@@ -572,7 +532,7 @@ __device__ __forceinline__ void clear(typename S::acc_t (&acc)[S::CT][S::TT]) {
 template <class S, bool CHAIN, class Job, class Engine>
 __device__ __forceinline__ void run_ring(Job& job, Engine& engine, lds_char* lds, int64_t t,
                                          int64_t tiles, bool may_chain) {
-  constexpr int N = S::STAGES, kSlot = (S::BN + S::BM) * S::KB;
+  constexpr int N = S::STAGES, kSlot = S::kSlotBytes;
   static_assert(N >= 3, "a stage is loaded while another one waits");
   if (t >= tiles) return;
   auto after = [](int slot) { return slot + 1 == N ? 0 : slot + 1; };
@@ -724,7 +684,7 @@ struct RingEngine8 {
   static constexpr int kSlot = Chan::kBytes + Row::kBytes;
   static constexpr int kPasses = Chan::kPasses + Row::kPasses;
   static constexpr int GS = S::GS, kSteps = S::KK8 / GS;
-  static constexpr int kScales = (GS * S::SLOADS + 1) * kWave;  // floats of a wave and stage
+  static constexpr int kScales = S::kScaleFloats;
   static constexpr int kIssued = kPasses + GS * S::SLOADS + 1;  // all loads
   typename S::acc_t acc[CT][TT];
   lds_char* lds;
@@ -904,8 +864,8 @@ __device__ __forceinline__ void products_deep(const Chan& ct, const Row& rt, lds
 // fall into all banks once.
 template <class S>
 struct Turned {
-  static constexpr int kHalf = S::CT * S::MF * 2;        // bytes
-  static constexpr int kRowBytes = 2 * kHalf + 16;       // 16: rows start four banks apart
+  static constexpr int kHalf = S::kHalfBytes;
+  static constexpr int kRowBytes = S::kTurnRowBytes;  // 16 more than two halves: rows start four banks apart
   const lds_char* at;
   // eight channels, `further` channels on (a multiple of 8); the sum of the
   // waves' parts of the contraction, in their order

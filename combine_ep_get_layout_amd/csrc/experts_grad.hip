@@ -143,8 +143,7 @@ struct Dx {
   typedef RowTile<S::BM, S::KB> Row;
   static constexpr int kSlot = Chan::kBytes + Row::kBytes;
   static constexpr int kPasses = Chan::kPasses + Row::kPasses, kLoads = kPasses;
-  static constexpr int kTurn = 4 * S::MF * Turned<S>::kRowBytes;
-
+  
   const GradArgs& a;
   const TilePlan& plan;
   lds_char* lds;
@@ -239,7 +238,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_dx(GradArgs a) {
   } else {
     RingEngine<S, typename D::Chan, typename D::Row> engine(base);
     d.acc = engine.acc;
-    run_ring<S, D::kTurn <= D::kSlot>(d, engine, base, block_place(), tiles, true);
+    run_ring<S, S::kChains>(d, engine, base, block_place(), tiles, true);
   }
 }
 
@@ -350,11 +349,11 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_dw(GradArgs a) {
 
 // ---- launches ------------------------------------------------------------------
 
-typedef Shape<32, 4, 4, 2, 2, 2> Big;     // 256 channels x 256 rows
-typedef Shape<32, 2, 2, 4, 1, 3> Medium;  // 256 x 64
-typedef Shape<16, 2, 1, 4, 1, 3> Small;   // 128 x 16
-typedef Shape<32, 2, 2, 2, 2, 3> Square;  // 128 x 128, one on a compute unit
-typedef Shape<32, 2, 2, 2, 2, 4, 64> Pair;  // the same in 64 KiB, two on one
+typedef Shape<grad::Big> Big;
+typedef Shape<grad::Medium> Medium;
+typedef Shape<grad::Small> Small;
+typedef Shape<grad::Square> Square;
+typedef Shape<grad::Pair> Pair;
 
 template <int CH>
 static void launch_dbias(const GradArgs& a, hipStream_t st) {
@@ -363,18 +362,10 @@ static void launch_dbias(const GradArgs& a, hipStream_t st) {
 }
 
 template <class S>
-constexpr int dx_slots() { return S::kLds > 70 * 1024 ? kCus : 2 * kCus; }
-
-template <class S>
 static void launch_dx(const GradArgs& a, hipStream_t st) {
   const int64_t tiles = ((a.rows + S::BM - 1) / S::BM + a.seg.E) * ((a.C + S::BN - 1) / S::BN);
   hipLaunchKernelGGL(expert_dx<S>, dim3((unsigned)min(tiles, (int64_t)dx_slots<S>())),
                      dim3(kGemmThreads), 0, st, a);
-}
-
-template <class S>
-static double dx_time(const GradArgs& a, double stage, double tile) {
-  return shape_time<S>(a.seg, a.rows, a.C, (int64_t)a.O * 2, dx_slots<S>(), stage, tile);
 }
 
 template <class S>
@@ -396,38 +387,25 @@ hipError_t launch_expert_grad(const GradArgs& a, hipStream_t st) {
       hipLaunchKernelGGL(expert_dz<false>, grid, dim3(256), 0, st, a);
   }
   if (a.dbias) {
-    // Channels of a workgroup, so that there are enough of them and each has a few
-    // rows a thread.  us, 32 / 64 / 256 channels: 1 expert x 8,192 rows x 4096 channels
-    // 67 / 123 / 479; 4 x 2,048 x 4096 52 / 38 / 128; 64 x 4 x 4096 48 / 22 / 7.
-    const int64_t groups = (int64_t)a.seg.E * ((a.N + 63) / 64);
-    if (groups <= kCus / 2) launch_dbias<32>(a, st);
-    else if (groups >= 4 * kCus && a.rows <= (int64_t)a.seg.E * 128) launch_dbias<256>(a, st);
-    else launch_dbias<64>(a, st);
+    switch (choose_dbias(a.seg.E, a.rows, a.N)) {
+      case 32: launch_dbias<32>(a, st); break;
+      case 64: launch_dbias<64>(a, st); break;
+      default: launch_dbias<256>(a, st);
+    }
   }
   if (a.dx && a.rows > 0) {
-    // as in the forward products, in units of a stage of Medium: 1% off the best
-    // shape on average over the same sizes, 18% by rows per expert alone.  us, Big
-    // / Medium / Small: 1 expert, 2048 x 2048, 512 rows 41 / 20 / 20; 64 experts,
-    // 2048 x 2048, 64 rows 139 / 106 / 215, 512 rows 282 / 432 / 1378.
-    const double big = dx_time<Big>(a, 2.0, 1.0), medium = dx_time<Medium>(a, 1.0, 0.0);
-    const double small = dx_time<Small>(a, 0.95, 0.0);
-    if (small < min(big, medium)) launch_dx<Small>(a, st);
-    else if (medium < big) launch_dx<Medium>(a, st);
-    else launch_dx<Big>(a, st);
+    switch (choose_dx(a.seg.E, a.rows, a.C, a.O)) {
+      case kDxSmall: launch_dx<Small>(a, st); break;
+      case kDxMedium: launch_dx<Medium>(a, st); break;
+      case kDxBig: launch_dx<Big>(a, st); break;
+    }
   }
   if (a.dw) {
-    // The largest tiles that fill the chip; of the smaller ones two on a compute unit
-    // where there are more of them than compute units.  us, Square / Pair: 8 experts of
-    // 1024 x 1024 (512 tiles), 16 rows 12.1 / 8.4, 512 rows 16.3 / 14.6; 1 expert of
-    // 2048 x 2048 (256 tiles), 16 rows 5.7 / 5.4, 8,192 rows 74 / 87.  8 experts of 4096 x
-    // 4096, Big / Square: 64 rows 76 / 118, 2,048 rows 470 / 749; 1 of 2048 x 2048 (64 of
-    // Big's tiles): 12 / 6 and 60 / 22.
-    const auto tiles = [&](int side) {
-      return (int64_t)a.seg.E * ((a.C + side - 1) / side) * ((a.O + side - 1) / side);
-    };
-    if (tiles(Big::BN) >= kCus) launch_dw<Big>(a, st);
-    else if (tiles(Square::BN) <= kCus) launch_dw<Square>(a, st);
-    else launch_dw<Pair>(a, st);
+    switch (choose_dw(a.seg.E, a.C, a.O)) {
+      case kDwBig: launch_dw<Big>(a, st); break;
+      case kDwSquare: launch_dw<Square>(a, st); break;
+      case kDwPair: launch_dw<Pair>(a, st); break;
+    }
   }
   return hipGetLastError();
 }
