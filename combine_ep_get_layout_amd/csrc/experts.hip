@@ -7,7 +7,9 @@
 // With many rows an expert the products are bound by the matrix cores and their
 // power: 64 experts x 2,048 rows, 7168 -> 2 x 2048, take 6.31 ms (1,220 TFLOP/s), the
 // cores busy 77% of the time at 1.6 GHz.  2048 -> 7168 with a residual takes 3.65
-// ms (1,050 TFLOP/s): a quarter of it starts and ends tiles.  With few rows they are
+// ms (1,050 TFLOP/s): a quarter of it starts and ends tiles.  In FP8 the same two take
+// 5.48 and 3.32 ms (1,400 and 1,160): a stage's reads, products and scaling wait for each
+// other (RingEngine8).  With few rows they are
 // bound by reading the weights: 256 experts x 32 rows in FP8, 7168 -> 2 x 2048, 1.29
 // ms (5.9 TB/s); 2048 -> 7168, 0.74 ms (5.2 TB/s, 16 stages a tile).  Eight rows
 // of eight experts, 2048 -> 2 x 768, take 14 us, half of it latency.

@@ -4,7 +4,7 @@
 //
 // Every product is computed transposed, D[channel][row] = sum_k A[channel][k]
 // B[row][k], so that a lane ends up with four consecutive channels of one
-// row and stores them as one 8-byte vector.
+// row; the epilogue turns them around in LDS and stores eight as one 16-byte vector.
 #pragma once
 
 #include <type_traits>
@@ -37,10 +37,11 @@ __device__ __forceinline__ float sigmoid(float v) {
 
 // Gaussian cumulative distribution, 0.5 erfc(-v / sqrt 2), with a relative
 // error below 7e-7 for |v| <= 3, growing with the unit in the last place of
-// v^2 / 2 beyond (1 + erf would cancel for negative v).  For
-// x >= 0, erfc(x) = t exp(-x^2 + Q(t)) with t = 2 / (2 + x); Q is a polynomial
-// fitted to log(erfc(x) exp(x^2) / t) over t in [1/8, 1] (x <= 14, where erfc
-// is far below the smallest float) with an error of 6e-8.  An epilogue of 64
+// v^2 / 2 beyond (2e-6 at 9, 4e-6 at 12; 1 + erf would cancel for negative v).  For
+// x >= 0, erfc(x) = t exp(-x^2 + Q(t)) with t = 2 / (2 + x), the form of Press et al.,
+// "Numerical Recipes", section 6.2; Q is a polynomial of our own fit
+// to log(erfc(x) exp(x^2) / t) over t in [1/8, 1] (x <= 14, where erfc
+// is far below the smallest float) with an error of 1.03e-7 at most.  An epilogue of 64
 // values a lane is bound by instructions, and this is a third of erfcf's.
 __device__ __forceinline__ float gauss_cdf(float v) {
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(v), 0.35355339059327376f, 1.0f));

@@ -11,15 +11,16 @@ namespace ep {
 
 // ---- dz ----------------------------------------------------------------------
 
-// Rows of a work item: 256 vectors of 8 channels at least, one a thread (16 experts x
-// 2,048 rows x 4096 channels 146 us, eight rows an item 170; 1 expert x 512 rows 8.6 and
-// 22 us).
+// Rows of a work item: as many whole rows as make up to 256 vectors of 8 channels, one a
+// thread, or one longer row (16 experts x 2,048 rows x 4096 channels 146 us, eight rows an
+// item 170; 1 expert x 512 rows 8.6 and 22 us).  A row of little more than 1,024 channels
+// leaves nearly half the threads idle.
 __host__ __device__ __forceinline__ int dz_rows(int channels) {
   return channels >= 2048 ? 1 : 2048 / channels;
 }
 
-// Reads dy and the pre-activations once and writes dz: bound by memory (65,536 rows,
-// 2 x 1408 channels: 166 us, 5.6 TB/s).
+// Reads dy and the pre-activations once and writes dz: bound by memory (62,259 rows,
+// 2 x 1408 channels: 166 us, 5.3 TB/s).
 template <bool GATED>
 __global__ __launch_bounds__(256) void expert_dz(GradArgs a) {
   __shared__ TilePlan plan;
@@ -130,7 +131,7 @@ __global__ __launch_bounds__(kBiasWaves* kWave) void expert_dbias(GradArgs a) {
 
 // dx = dz W: the rows run along the contraction (O channels of dz), the
 // weights across it, so they are read transposed from LDS rather than stored
-// transposed in memory.  65,536 rows over 32 experts, 2 x 1408 -> 4096: 1.31 ms, 1,150
+// transposed in memory.  62,259 rows over 32 experts, 2 x 1408 -> 4096: 1.31 ms, 1,100
 // TFLOP/s, bound as the forward products (matrix cores 70% busy).
 struct DxTile {
   int64_t row;
@@ -245,8 +246,10 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_dx(GradArgs a) {
 // ---- dW ----------------------------------------------------------------------
 
 // dW_e = dz_e^T x_e: both operands run across the contraction, the segment's
-// rows (the same sizes: 1.33 ms, 1,130 TFLOP/s).  One workgroup per tile of one expert; an expert without rows gets
-// zeros.  Each die takes 32 consecutive tiles in turn, so the workgroups that
+// rows (the same sizes: 1.33 ms, 1,080 TFLOP/s).  One workgroup per tile of one expert; an
+// expert without rows gets zeros.  A segment's rows are never split, so few tiles with many
+// rows leave most of the chip idle (1 expert, 16,384 rows, dx and dW together: 256 x 256
+// channels 117 us, 512 x 512 130, 1024 x 1024 166, 2048 x 2048 255).  Each die takes 32 consecutive tiles in turn, so the workgroups that
 // run on it together read the same expert's rows and long experts fall on all
 // dies alike.
 template <class S>
