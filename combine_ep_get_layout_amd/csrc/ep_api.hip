@@ -45,11 +45,13 @@ int ep::make_geometry(const ep_problem* p, Geometry* g) {
             K = p->num_topk;
   if (p->reserved != 0) return EP_ERR_SHAPE;
   if (p->mode < EP_MODE_NORMAL || p->mode > EP_MODE_RANK_MAJOR) return EP_ERR_MODE;
-  if (p->quant < EP_QUANT_NONE || p->quant > EP_QUANT_FP8_UE8M0) return EP_ERR_MODE;
+  if (p->quant < EP_QUANT_NONE || p->quant > EP_QUANT_INT8) return EP_ERR_MODE;
+  const bool int8 = p->quant == EP_QUANT_INT8, fp8 = p->quant != EP_QUANT_NONE && !int8;
+  if (int8 && p->mode != EP_MODE_NORMAL && p->mode != EP_MODE_LOW_LATENCY) return EP_ERR_MODE;
   if (R < 1 || R > 256 || T < 0 || K < 1 || K > 64) return EP_ERR_SHAPE;
   if (E < R || E > 2048 || E % R != 0) return EP_ERR_SHAPE;
   if (H < 8 || H % 8 != 0 || H > 32768) return EP_ERR_SHAPE;
-  if (p->quant != EP_QUANT_NONE && H % 128 != 0) return EP_ERR_SHAPE;
+  if ((fp8 && H % 128 != 0) || (int8 && H % 16 != 0)) return EP_ERR_SHAPE;
   if (p->expert_alignment < 1) return EP_ERR_SHAPE;
   const int64_t entries = (int64_t)R * T * K;
   if (entries >= (1ll << 31) || (int64_t)R * T * R >= (1ll << 31)) return EP_ERR_SHAPE;
@@ -101,8 +103,7 @@ int ep::make_geometry(const ep_problem* p, Geometry* g) {
   g->off_msg = off;
   if (p->mode == EP_MODE_MESSAGES) off += up256(message_ws_bytes(R));
   g->off_stage = off;
-  if ((p->mode == EP_MODE_NORMAL || p->mode == EP_MODE_RANK_MAJOR) &&
-      p->quant != EP_QUANT_NONE) {
+  if ((p->mode == EP_MODE_NORMAL || p->mode == EP_MODE_RANK_MAJOR) && fp8) {
     // row-major scale staging for the worst-case number of receive rows
     const int64_t rows = p->mode == EP_MODE_RANK_MAJOR
                              ? (int64_t)R * T * (K < R ? K : R)
@@ -301,8 +302,8 @@ int dispatch_args(const ep_problem* p, const Geometry& g, const ep_layout* layou
   if (p->mode == EP_MODE_LOW_LATENCY && recv->capacity < (int64_t)g.E * g.R * g.T)
     return EP_ERR_CAPACITY;
   const bool rank_major = p->mode == EP_MODE_RANK_MAJOR;
-  const bool staged =
-      (p->mode == EP_MODE_NORMAL || rank_major) && p->quant != EP_QUANT_NONE;
+  const bool staged = (p->mode == EP_MODE_NORMAL || rank_major) &&
+                      p->quant != EP_QUANT_NONE && p->quant != EP_QUANT_INT8;
   if (rank_major && toks) {
     // per-row metadata needs the routing (ids) and, for weights, the weights
     if ((recv->topk_idx || recv->topk_weights) && !topk_idx) return EP_ERR_NULL;
@@ -350,6 +351,10 @@ int dispatch_args(const ep_problem* p, const Geometry& g, const ep_layout* layou
   return EP_OK;
 }
 
+hipError_t launch_any_dispatch(const ep::DispatchArgs& a, hipStream_t s) {
+  return a.quant == EP_QUANT_INT8 ? ep::launch_dispatch_int8(a, s) : ep::launch_dispatch(a, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -380,7 +385,7 @@ int ep_dispatch(const ep_problem* p, const ep_layout* layout, const uint16_t* x,
     st = dispatch_args(p, g, layout, x, topk_idx, topk_weights, recv, workspace,
                        workspace_bytes, &a);
     if (st != EP_OK) return st;
-    if (ep::launch_dispatch(a, (hipStream_t)stream) != hipSuccess) return EP_ERR_HIP;
+    if (launch_any_dispatch(a, (hipStream_t)stream) != hipSuccess) return EP_ERR_HIP;
     return EP_OK;
   }
   // message mode
@@ -436,14 +441,15 @@ int ep_dispatch_fused(const ep_problem* p, const int32_t* topk_idx, const ep_lay
   st = dispatch_args(p, g, layout, x, topk_idx, nullptr, recv, workspace, workspace_bytes, &a);
   if (st != EP_OK) return st;
   hipStream_t s = (hipStream_t)stream;
-  if (g.direct || !toks) {  // small problems: the one-launch layout, then dispatch
+  // small problems: the one-launch layout, then dispatch; 8-bit integers have no fused form
+  if (g.direct || !toks || a.quant == EP_QUANT_INT8) {
     if (ep::launch_layout(la, s) != hipSuccess) return EP_ERR_HIP;
   } else {
     if (ep::launch_layout_counts(la, s) != hipSuccess) return EP_ERR_HIP;
     a.fused = true;
     a.la = la;
   }
-  if (ep::launch_dispatch(a, s) != hipSuccess) return EP_ERR_HIP;
+  if (launch_any_dispatch(a, s) != hipSuccess) return EP_ERR_HIP;
   return EP_OK;
 }
 

@@ -100,6 +100,7 @@ struct DispatchArgs {
 };
 
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t stream);
+hipError_t launch_dispatch_int8(const DispatchArgs& a, hipStream_t stream);
 
 struct CombineArgs {
   Geometry g;
@@ -210,6 +211,17 @@ struct ExpertArgs {
 };
 
 hipError_t launch_expert_forward(const ExpertArgs& a, hipStream_t stream);
+
+struct Int8Args {
+  Segments seg;
+  int64_t rows;            // most rows the segments hold together
+  int C;
+  const uint16_t* x;       // [cap][C]
+  int8_t* codes;           // [cap][C]
+  float* scales;           // [cap]
+};
+
+hipError_t launch_rows_int8(const Int8Args& a, hipStream_t stream);
 
 struct GradArgs {
   Segments seg;

@@ -42,6 +42,28 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t a, uint32_t b) {
 // Nothing to load for a row's result.
 struct NoRow {};
 
+// 8-bit integers: the row's scale, and eight channels of its residual.
+struct Row8 {
+  u32x4 add;
+  float scale;
+};
+
+__device__ __forceinline__ u32x4& residual_of(u32x4& row) { return row; }
+__device__ __forceinline__ const u32x4& residual_of(const u32x4& row) { return row; }
+__device__ __forceinline__ u32x4& residual_of(Row8& row) { return row.add; }
+__device__ __forceinline__ const u32x4& residual_of(const Row8& row) { return row.add; }
+
+// Sums of 8-bit products of B rows to their values: rows' scales times eight channels'.
+template <int B>
+__device__ __forceinline__ void scale8(float (&v)[B][8], const float (&rows)[B],
+                                       const float* channels) {
+  const f32x4 lo = *(const f32x4*)channels, hi = *(const f32x4*)(channels + 4);
+#pragma unroll
+  for (int b = 0; b < B; ++b)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[b][c] *= rows[b] * (c < 4 ? lo[c] : hi[c - 4]);
+}
+
 // What a tile's epilogue needs of it.
 struct Tile {
   int64_t row;     // first row in the row buffers
@@ -52,7 +74,8 @@ struct Tile {
 // One workgroup's state: where its loads read, and the epilogue.  Q: EP_QUANT_*
 template <class S, bool GATED, int Q>
 struct Forward {
-  static constexpr bool FP8 = Q != EP_QUANT_NONE;
+  static constexpr bool INT8 = Q == EP_QUANT_INT8;
+  static constexpr bool FP8 = Q != EP_QUANT_NONE && !INT8;
   static constexpr int MF = S::MF, CT = S::CT;
   // gated: a wave's channel tiles are half gates and half ups of the same channels
   static constexpr int CH = GATED ? CT / 2 : CT;         // channel tiles of the output per wave
@@ -93,7 +116,7 @@ struct Forward {
     wave = uniform(threadIdx.x >> 6);
     wc = place.wc;
     wr = place.wr;
-    row_bytes = (int64_t)a.C * (FP8 ? 1 : 2);
+    row_bytes = (int64_t)a.C * (FP8 || INT8 ? 1 : 2);
     nk = (int)((row_bytes + S::KB - 1) / S::KB);
     nfull = (int)(row_bytes / S::KB);
     mt = uniform(plan.upto[a.seg.E - 1]);
@@ -193,8 +216,10 @@ struct Forward {
     // unused is waited for where its registers are next written, in the main loop,
     // and with it every load of the stages in flight (1 expert, 4096 x 8192, 64
     // rows of Medium: 35 -> 55 us).
+    // An 8-bit row's scale is loaded likewise.
     constexpr bool kAhead = S::STAGES == 2 && !GATED;
-    typedef typename std::conditional<kAhead, u32x4, NoRow>::type Row8;
+    typedef typename std::conditional<
+        INT8, Row8, typename std::conditional<kAhead, u32x4, NoRow>::type>::type Own;
     const bool codes = FP8 && ON >= 128 && a.y_quant != EP_QUANT_NONE;
     const Lane lane;
     const int ch = lane.wc * CH * MF + lane.channel;  // within the tile
@@ -203,23 +228,37 @@ struct Forward {
     uint16_t* const y = (uint16_t*)a.y + first;
     uint16_t* const pre = a.pre ? a.pre + (GATED ? t.row * 2 * a.N + t.n0 : first) : nullptr;
     const float* const bias = a.bias + ((int64_t)t.e * a.N + t.n0 + (in ? ch : 0));
-    turn_out<S, CH>(
+    // 8-bit integers: the rows' and the channels' scales
+    const float* const row_scale = (const float*)a.x_scales + t.row;
+    const float* const chan_scale =
+        a.w_scales + ((int64_t)t.e * (GATED ? 2 : 1) * a.N + t.n0 + (in ? ch : 0));
+    turn_out<S, CH, INT8>(
         base, *(typename S::acc_t(*)[S::CT][S::TT])acc,
         [&](int r) {
-          Row8 row = {};
+          Own row = {};
           if constexpr (kAhead)
             if (a.residual && r < t.rows && in)
-              row = *(const u32x4*)(a.residual + first + (uint32_t)r * (uint32_t)a.N + ch);
+              residual_of(row) = *(const u32x4*)(a.residual + first + (uint32_t)r * (uint32_t)a.N + ch);
+          if constexpr (INT8 && S::STAGES == 2) row.scale = row_scale[min(r, t.rows - 1)];
           return row;
         },
-        [&](int r, const Turned<S>(&turned)[B], const Row8(&add)[B]) {
-          float v[B][8];
+        [&](int r, const Turned<S>(&turned)[B], const Own(&own)[B]) {
+          float v[B][8], sx[B];
 #pragma unroll
           for (int b = 0; b < B; ++b) turned[b].get(0, v[b]);
+          if constexpr (INT8) {
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+              if constexpr (S::STAGES == 2) sx[b] = own[b].scale;
+              else sx[b] = row_scale[min(r + b * kStep, t.rows - 1)];
+            }
+            scale8(v, sx, chan_scale);
+          }
           if constexpr (GATED) {
             float u[B][8];
 #pragma unroll
             for (int b = 0; b < B; ++b) turned[b].get(CH * MF, u[b]);
+            if constexpr (INT8) scale8(u, sx, chan_scale + a.N);
             if (pre)
 #pragma unroll
               for (int b = 0; b < B; ++b)
@@ -252,7 +291,7 @@ struct Forward {
 #pragma unroll
               for (int b = 0; b < B; ++b) {
                 if constexpr (kAhead)
-                  row[b] = add[b];
+                  row[b] = residual_of(own[b]);
                 else  // past the tile's end: its first row
                   row[b] = *(const u32x4*)(
                       a.residual + first +
@@ -348,7 +387,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
     for (int64_t t = block_place(); t < tiles; t += gridDim.x) {
       const Tile tile = f.setup(t);
       clear<S>(acc);
-      products_deep<S>(
+      products_deep<S, F::INT8>(
           f.w_tile, f.x_tile, base, f.nk, f.nfull,
           [&](int k, lds_char* buf, int p) { f.load_at(k, buf, p); },
           [&](int k, lds_char* buf) { f.tail_at(k, buf); }, acc);
@@ -360,7 +399,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) 
     run_ring<S, S::kChains>(f, engine, base, block_place(), tiles,
                                       a.y_quant == EP_QUANT_NONE);
   } else {
-    RingEngine<S, typename F::Chan, typename F::Row> engine(base);
+    RingEngine<S, typename F::Chan, typename F::Row, F::INT8> engine(base);
     f.acc = engine.acc;
     run_ring<S, S::kChains>(f, engine, base, block_place(), tiles, true);
   }
@@ -377,17 +416,18 @@ template <class S, bool GATED, int Q>
 static void launch(const ExpertArgs& a, hipStream_t st) {
   const int on = GATED ? S::BN / 2 : S::BN;
   const int64_t tiles = ((a.rows + S::BM - 1) / S::BM + a.seg.E) * ((a.N + on - 1) / on);
-  constexpr int64_t kSlots = forward_slots<S, Q != EP_QUANT_NONE>();
+  constexpr int64_t kSlots = forward_slots<S, Q != EP_QUANT_NONE && Q != EP_QUANT_INT8>();
   hipLaunchKernelGGL((expert_forward<S, GATED, Q>), dim3((unsigned)std::min(tiles, kSlots)),
                      dim3(kGemmThreads), 0, st, a);
 }
 
 template <bool GATED, int Q>
 static void choose(const ExpertArgs& a, hipStream_t st) {
-  constexpr bool FP8 = Q != EP_QUANT_NONE;
+  constexpr bool INT8 = Q == EP_QUANT_INT8, FP8 = Q != EP_QUANT_NONE && !INT8;
   typedef typename std::conditional<FP8, Big8, Big>::type Large;
-  switch (choose_forward<FP8>(a.seg.E, a.rows, a.C, (int64_t)a.N * (GATED ? 2 : 1),
-                              a.y_quant != EP_QUANT_NONE)) {
+  // 8-bit integers run through the bf16 kernels' tiles with half the contraction's bytes
+  switch (choose_forward<FP8>(a.seg.E, a.rows, INT8 ? a.C / 2 : a.C,
+                              (int64_t)a.N * (GATED ? 2 : 1), a.y_quant != EP_QUANT_NONE)) {
     case kTinyTile: return launch<Tiny, GATED, Q>(a, st);
     case kSmallTile: return launch<Small, GATED, Q>(a, st);
     case kNarrowTile: return launch<Narrow, GATED, Q>(a, st);
@@ -401,6 +441,7 @@ static void choose(const ExpertArgs& a, hipStream_t st) {
   switch (a.quant) {
     case EP_QUANT_NONE: return choose<GATED, EP_QUANT_NONE>(a, st);
     case EP_QUANT_FP8_F32: return choose<GATED, EP_QUANT_FP8_F32>(a, st);
+    case EP_QUANT_INT8: return choose<GATED, EP_QUANT_INT8>(a, st);
     default: return choose<GATED, EP_QUANT_FP8_UE8M0>(a, st);
   }
 }

@@ -21,6 +21,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 #define EP_LDS __attribute__((address_space(3)))
 typedef EP_LDS char lds_char;
@@ -448,6 +449,11 @@ struct Mfma<32> {
   static __device__ __forceinline__ acc_t fp8(i32x8 a, i32x8 b, acc_t c) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
   }
+  static __device__ __forceinline__ acc_t int8(bf16x8 a, bf16x8 b, acc_t c) {
+    return __builtin_bit_cast(acc_t, __builtin_amdgcn_mfma_i32_32x32x32_i8(
+                                         __builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b),
+                                         __builtin_bit_cast(i32x16, c), 0, 0, 0));
+  }
 };
 template <>
 struct Mfma<16> {
@@ -458,7 +464,28 @@ struct Mfma<16> {
   static __device__ __forceinline__ acc_t fp8(i32x8 a, i32x8 b, acc_t c) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
   }
+  static __device__ __forceinline__ acc_t int8(bf16x8 a, bf16x8 b, acc_t c) {
+    return __builtin_bit_cast(acc_t, __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                                         __builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b),
+                                         __builtin_bit_cast(i32x4, c), 0, 0, 0));
+  }
 };
+
+// One product of 16-byte fragments.  8-bit integers take the places of half as many bf16:
+// a lane's 16 consecutive ones of a row, 32x32x32 and 16x16x64.  Their sums are 32-bit
+// integers (exact up to 2^17 channels), kept in the same registers as bits until
+// sum_value converts them.
+template <int MF, bool INT8>
+__device__ __forceinline__ typename Mfma<MF>::acc_t product(bf16x8 a, bf16x8 b,
+                                                            typename Mfma<MF>::acc_t c) {
+  if constexpr (INT8) return Mfma<MF>::int8(a, b, c);
+  else return Mfma<MF>::bf16(a, b, c);
+}
+
+template <bool INT8>
+__device__ __forceinline__ float sum_value(float bits) {
+  return INT8 ? (float)__float_as_int(bits) : bits;
+}
 
 // First of the four consecutive channels that accumulator registers 4 q .. 4 q + 3
 // of a lane hold.
@@ -615,7 +642,7 @@ __device__ __forceinline__ void run_ring(Job& job, Engine& engine, lds_char* lds
 // before the barrier and the reads behind it, which leaves the matrix cores
 // idle for a barrier and an LDS round trip per stage.  A stage's last products
 // cover the barrier and the next stage's first reads.
-template <class S, class Chan, class Row>
+template <class S, class Chan, class Row, bool INT8 = false>
 struct RingEngine {
   static constexpr int CT = S::CT, TT = S::TT, KK = S::KK;
   static constexpr int kSlot = Chan::kBytes + Row::kBytes;
@@ -664,7 +691,7 @@ struct RingEngine {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < TT; ++j)
-          acc[i][j] = Mfma<S::MF>::bf16(fa[from][i], fb[from][j], acc[i][j]);
+          acc[i][j] = product<S::MF, INT8>(fa[from][i], fb[from][j], acc[i][j]);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -763,7 +790,7 @@ struct RingEngine8 {
 // arrive and rows are fetched as whole 128-byte lines.  64-byte stages, four
 // of which fit, were tried first: their loads alone take 1.54 ms at 16
 // experts x 2,048 rows x 7168 x 4096, those of 128 bytes 1.04 ms.
-template <class S, class Chan, class Row, class Load, class Tail>
+template <class S, bool INT8 = false, class Chan, class Row, class Load, class Tail>
 __device__ __forceinline__ void products_deep(const Chan& ct, const Row& rt, lds_char* lds, int nk,
                                               int nfull, Load load, Tail tail,
                                               typename S::acc_t (&acc)[S::CT][S::TT]) {
@@ -820,7 +847,7 @@ __device__ __forceinline__ void products_deep(const Chan& ct, const Row& rt, lds
             load(k, into, (s - 1) * kStepLoads + l);
       }
       __builtin_amdgcn_sched_barrier(0);
-      acc[i][j] = Mfma<S::MF>::bf16(fa[s][i], fb[s][j], acc[i][j]);
+      acc[i][j] = product<S::MF, INT8>(fa[s][i], fb[s][j], acc[i][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -907,7 +934,7 @@ struct TurnLane {
 // ahead: a load behind a store waits for the store as well (linear product with
 // residual, 64 experts x 2,048 rows, 2048 x 7168: 4.23 -> 3.72 ms).  put(r, turned,
 // fetched) takes kBatch rows.
-template <class S, int OUT, class Fetch, class Put>
+template <class S, int OUT, bool INT8 = false, class Fetch, class Put>
 __device__ __forceinline__ void turn_out(lds_char* lds, const typename S::acc_t (&acc)[S::CT][S::TT],
                                          Fetch fetch, Put put) {
   typedef Turned<S> T;
@@ -935,8 +962,9 @@ __device__ __forceinline__ void turn_out(lds_char* lds, const typename S::acc_t 
     for (int i = 0; i < S::CT; ++i)
 #pragma unroll
       for (int q = 0; q < S::REGS / 4; ++q) {
-        const f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                         acc[i][j][4 * q + 3]};
+        const f32x4 v = {
+            sum_value<INT8>(acc[i][j][4 * q]), sum_value<INT8>(acc[i][j][4 * q + 1]),
+            sum_value<INT8>(acc[i][j][4 * q + 2]), sum_value<INT8>(acc[i][j][4 * q + 3])};
         const int quad = (i * MF + channel_of<MF>(q)) / 4;
         *(EP_LDS f32x4*)(to + (quad & 1) * T::kHalf + (quad >> 1) * 16) = v;
       }

@@ -38,13 +38,20 @@ int segments(const ep_problem* p, const Geometry& g, const ep_layout* layout, Se
   return EP_OK;
 }
 
+inline bool is_fp8(int quant) { return quant == EP_QUANT_FP8_F32 || quant == EP_QUANT_FP8_UE8M0; }
+
+// What a row buffer may hold, beside bf16.
+enum { kBf16Rows = 0, kFp8Rows = 1, kInt8Rows = 2 };
+
 // Checks a row buffer of `channels` channels and narrows the segments' cap to it.
-int rows_ok(const ep_rows* r, int channels, const Geometry& g, bool fp8_allowed, Segments* s) {
+int rows_ok(const ep_rows* r, int channels, const Geometry& g, int allowed, Segments* s) {
   if (!r) return EP_ERR_NULL;
   if (r->channels != channels) return EP_ERR_SHAPE;
-  if (r->quant < EP_QUANT_NONE || r->quant > EP_QUANT_FP8_UE8M0) return EP_ERR_MODE;
-  if (r->quant != EP_QUANT_NONE && !fp8_allowed) return EP_ERR_MODE;
-  if (r->quant != EP_QUANT_NONE && channels % 128 != 0) return EP_ERR_SHAPE;
+  if (r->quant < EP_QUANT_NONE || r->quant > EP_QUANT_INT8) return EP_ERR_MODE;
+  if (is_fp8(r->quant) && !(allowed & kFp8Rows)) return EP_ERR_MODE;
+  if (r->quant == EP_QUANT_INT8 && !(allowed & kInt8Rows)) return EP_ERR_MODE;
+  if (is_fp8(r->quant) && channels % 128 != 0) return EP_ERR_SHAPE;
+  if (r->quant == EP_QUANT_INT8 && channels % 16 != 0) return EP_ERR_SHAPE;
   if (r->capacity < 0 || (!s->start && r->capacity < (int64_t)g.E * s->block_rows))
     return EP_ERR_CAPACITY;
   // no rows at all, no buffer needed
@@ -52,7 +59,8 @@ int rows_ok(const ep_rows* r, int channels, const Geometry& g, bool fp8_allowed,
     if (!r->x || (r->quant != EP_QUANT_NONE && !r->scales)) return EP_ERR_NULL;
   }
   if (!aligned(r->x, 16)) return EP_ERR_ALIGN;
-  if (r->quant == EP_QUANT_FP8_F32 && !aligned(r->scales, 4)) return EP_ERR_ALIGN;
+  if ((r->quant == EP_QUANT_FP8_F32 || r->quant == EP_QUANT_INT8) && !aligned(r->scales, 4))
+    return EP_ERR_ALIGN;
   if (r->capacity < s->cap) s->cap = r->capacity;
   return EP_OK;
 }
@@ -60,7 +68,7 @@ int rows_ok(const ep_rows* r, int channels, const Geometry& g, bool fp8_allowed,
 int weights_ok(const ep_weights* w) {
   if (!w) return EP_ERR_NULL;
   if (w->reserved != 0) return EP_ERR_SHAPE;
-  if (w->fp8 != 0 && w->fp8 != 1) return EP_ERR_MODE;
+  if (w->fp8 < EP_WEIGHTS_BF16 || w->fp8 > EP_WEIGHTS_INT8) return EP_ERR_MODE;
   return EP_OK;
 }
 
@@ -88,16 +96,18 @@ int forward(const ep_problem* p, const ep_layout* layout, const ep_rows* x, cons
   const int C = w->in_channels, O = w->out_channels, N = gated ? O / 2 : O;
   if (!channels_ok(C) || !channels_ok(N)) return EP_ERR_SHAPE;
   if (gated && w->bias) return EP_ERR_MODE;
-  EP_TRY(rows_ok(x, C, g, true, &a.seg));
-  const bool fp8 = x->quant != EP_QUANT_NONE;
-  if (fp8 != (w->fp8 != 0)) return EP_ERR_MODE;
+  EP_TRY(rows_ok(x, C, g, kFp8Rows | kInt8Rows, &a.seg));
+  const bool fp8 = is_fp8(x->quant), int8 = x->quant == EP_QUANT_INT8;
+  if (w->fp8 != (fp8 ? EP_WEIGHTS_FP8 : int8 ? EP_WEIGHTS_INT8 : EP_WEIGHTS_BF16))
+    return EP_ERR_MODE;
   if (fp8 && (C % 128 != 0 || N % 128 != 0)) return EP_ERR_SHAPE;
-  if (!w->w || (fp8 && !w->scales)) return EP_ERR_NULL;
-  if (!aligned(w->w, 16) || (fp8 && !aligned(w->scales, 4)) || !aligned(w->bias, 16))
+  if (!w->w || ((fp8 || int8) && !w->scales)) return EP_ERR_NULL;
+  if (!aligned(w->w, 16) || (fp8 && !aligned(w->scales, 4)) || (int8 && !aligned(w->scales, 16)) ||
+      !aligned(w->bias, 16))
     return EP_ERR_ALIGN;
-  EP_TRY(rows_ok(y, N, g, fp8, &a.seg));
-  if (residual) EP_TRY(rows_ok(residual, N, g, false, &a.seg));
-  if (pre) EP_TRY(rows_ok(pre, O, g, false, &a.seg));
+  EP_TRY(rows_ok(y, N, g, fp8 ? kFp8Rows : kBf16Rows, &a.seg));
+  if (residual) EP_TRY(rows_ok(residual, N, g, kBf16Rows, &a.seg));
+  if (pre) EP_TRY(rows_ok(pre, O, g, kBf16Rows, &a.seg));
   a.rows = (int64_t)g.R * g.T * g.K;
   a.gated = gated;
   a.quant = x->quant;
@@ -134,19 +144,19 @@ int backward(const ep_problem* p, const ep_layout* layout, const ep_rows* x, con
   if (gated && w->out_channels % 2 != 0) return EP_ERR_SHAPE;
   const int C = w->in_channels, O = w->out_channels, N = gated ? O / 2 : O;
   if (!channels_ok(C) || !channels_ok(N)) return EP_ERR_SHAPE;
-  EP_TRY(rows_ok(dy, N, g, false, &a.seg));
+  EP_TRY(rows_ok(dy, N, g, kBf16Rows, &a.seg));
   const bool same = !gated && act == EP_ACT_NONE;  // dpre is dy
   if (!same) {
-    EP_TRY(rows_ok(pre, O, g, false, &a.seg));
-    if (dx || dw || dpre || gated) EP_TRY(rows_ok(dpre, O, g, false, &a.seg));
+    EP_TRY(rows_ok(pre, O, g, kBf16Rows, &a.seg));
+    if (dx || dw || dpre || gated) EP_TRY(rows_ok(dpre, O, g, kBf16Rows, &a.seg));
   }
   if (dx) {
-    EP_TRY(rows_ok(dx, C, g, false, &a.seg));
+    EP_TRY(rows_ok(dx, C, g, kBf16Rows, &a.seg));
     if (!w->w) return EP_ERR_NULL;
     if (!aligned(w->w, 16)) return EP_ERR_ALIGN;
   }
   if (dw) {
-    EP_TRY(rows_ok(x, C, g, false, &a.seg));
+    EP_TRY(rows_ok(x, C, g, kBf16Rows, &a.seg));
     if (!aligned(dw, 16)) return EP_ERR_ALIGN;
   }
   if (!aligned(dbias, 4)) return EP_ERR_ALIGN;
@@ -197,6 +207,28 @@ int ep_expert_linear_backward(const ep_problem* p, const ep_layout* layout, cons
                               const ep_rows* dy, const ep_rows* dpre, const ep_rows* dx,
                               uint16_t* dw, float* dbias, void* stream) {
   return backward(p, layout, x, w, act, pre, dy, dpre, dx, dw, dbias, false, stream);
+}
+
+int ep_quantize_rows(const ep_problem* p, const ep_layout* layout, const ep_rows* x,
+                     const ep_rows* q, void* stream) {
+  Geometry g;
+  EP_TRY(ep::make_geometry(p, &g));
+  ep::Int8Args a;
+  memset(&a, 0, sizeof(a));
+  EP_TRY(segments(p, g, layout, &a.seg));
+  if (!x) return EP_ERR_NULL;
+  const int C = x->channels;
+  if (!channels_ok(C) || C % 16 != 0) return EP_ERR_SHAPE;
+  EP_TRY(rows_ok(x, C, g, kBf16Rows, &a.seg));
+  EP_TRY(rows_ok(q, C, g, kInt8Rows, &a.seg));
+  if (q->quant != EP_QUANT_INT8) return EP_ERR_MODE;
+  a.rows = (int64_t)g.R * g.T * g.K;
+  a.C = C;
+  a.x = (const uint16_t*)x->x;
+  a.codes = (int8_t*)q->x;
+  a.scales = (float*)q->scales;
+  if (ep::launch_rows_int8(a, (hipStream_t)stream) != hipSuccess) return EP_ERR_HIP;
+  return EP_OK;
 }
 
 int ep_combine_backward(const ep_problem* p, const ep_layout* layout, const uint16_t* dout,

@@ -18,14 +18,15 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libep.so")
 
 MODE_NORMAL, MODE_LOW_LATENCY, MODE_MESSAGES, MODE_RANK_MAJOR = 0, 1, 2, 3
-QUANT_NONE, QUANT_FP8_F32, QUANT_FP8_UE8M0 = 0, 1, 2
+QUANT_NONE, QUANT_FP8_F32, QUANT_FP8_UE8M0, QUANT_INT8 = 0, 1, 2, 3
+WEIGHTS_BF16, WEIGHTS_FP8, WEIGHTS_INT8 = 0, 1, 2
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = 0, 1, 2, 3
 DEVERR_TOPK_RANGE, DEVERR_LL_OVERFLOW, DEVERR_CAPACITY, DEVERR_MESSAGE = 1, 2, 4, 8
 
 EXPORTS = ["ep_workspace_bytes", "ep_max_recv_rows", "ep_messages_capacity", "ep_get_layout",
            "ep_dispatch", "ep_dispatch_fused", "ep_dispatch_fused_noalloc", "ep_combine",
            "ep_expert_gated", "ep_expert_linear", "ep_expert_gated_backward",
-           "ep_expert_linear_backward", "ep_combine_backward",
+           "ep_expert_linear_backward", "ep_combine_backward", "ep_quantize_rows",
            "ep_messages_execute", "ep_messages_unpack", "ep_status_string"]
 NOALLOC_SCRATCH_BYTES = 64 << 20  # EP_NOALLOC_SCRATCH_BYTES
 ERR_SCRATCH = -8
@@ -121,6 +122,8 @@ def lib() -> ctypes.CDLL:
         l.ep_expert_gated_backward.restype = ctypes.c_int
         l.ep_expert_linear_backward.argtypes = [P, LP, RP, WP, i32, RP, RP, RP, RP, _vp, _vp, _vp]
         l.ep_expert_linear_backward.restype = ctypes.c_int
+        l.ep_quantize_rows.argtypes = [P, LP, RP, RP, _vp]
+        l.ep_quantize_rows.restype = ctypes.c_int
         l.ep_combine_backward.argtypes = [P, LP, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp, _vp]
         l.ep_combine_backward.restype = ctypes.c_int
         l.ep_messages_execute.argtypes = [P, ctypes.POINTER(CMessages), _vp, ctypes.c_int64,
@@ -311,6 +314,9 @@ class Recv:
         if p.quant == QUANT_NONE:
             self.x = torch.empty((self.capacity, p.H), dtype=torch.bfloat16, device=device)
             self.scales = None
+        elif p.quant == QUANT_INT8:
+            self.x = torch.empty((self.capacity, p.H), dtype=torch.int8, device=device)
+            self.scales = torch.empty(self.capacity, dtype=torch.float32, device=device)
         else:
             self.x = torch.empty((self.capacity, p.H), dtype=torch.uint8, device=device)
             n = p.G * (p.E * p.R * p.T if p.mode == MODE_LOW_LATENCY else self.capacity)
@@ -349,6 +355,20 @@ class Messages:
                          _ptr(self.num_descriptors))
 
 
+def _check_payload(p: Problem, recv: Recv) -> None:
+    """The receive rows' element type and their scales."""
+    if p.quant == QUANT_NONE:
+        _need(recv.x.element_size() == 2, "bf16 rows")
+    elif p.quant == QUANT_INT8:
+        _need(recv.x.dtype == torch.int8, "8-bit rows are int8")
+        _need(recv.scales is not None and recv.scales.dtype == torch.float32
+              and recv.scales.numel() >= recv.capacity, "recv scales [capacity] fp32")
+    else:
+        n = p.G * (p.E * p.R * p.T if p.mode == MODE_LOW_LATENCY else recv.capacity)
+        _need(recv.scales is not None and recv.scales.numel() >= n, "recv scales")
+        _need(recv.x.element_size() == 1, "FP8 codes are bytes")
+
+
 def dispatch(p: Problem, layout: Layout, x: torch.Tensor, *, recv: Recv | None = None,
              msgs: Messages | None = None, topk_idx: torch.Tensor | None = None,
              topk_weights: torch.Tensor | None = None, ws: torch.Tensor | None = None,
@@ -374,12 +394,7 @@ def _dispatch_args(p: Problem, layout: Layout, x: torch.Tensor, *, recv: Recv | 
             for t_ in (recv.topk_idx, recv.topk_weights):
                 _need(t_ is None or t_.numel() >= recv.capacity * K, "row metadata [capacity][K]")
         _need(recv.x.shape[0] >= recv.capacity and recv.x.shape[1] == H, "recv x [capacity][H]")
-        if p.quant != QUANT_NONE:
-            n = p.G * (E * R * T if p.mode == MODE_LOW_LATENCY else recv.capacity)
-            _need(recv.scales is not None and recv.scales.numel() >= n, "recv scales")
-            _need(recv.x.element_size() == 1, "FP8 codes are bytes")
-        else:
-            _need(recv.x.element_size() == 2, "bf16 rows")
+        _check_payload(p, recv)
     else:
         _need(msgs is not None and layout.send_head is not None, "message buffers and send_head")
         _need(topk_idx is not None and topk_idx.dtype == torch.int32 and topk_idx.numel() == R * T * K,
@@ -418,12 +433,7 @@ def _check_fused(p: Problem, topk_idx: torch.Tensor, layout: Layout, x: torch.Te
           "recv_src_idx smaller than recv_capacity")
     _need(x.dtype == torch.bfloat16 and x.numel() == R * T * H, "x [R][T][H] bf16")
     _need(recv.x.shape[0] >= recv.capacity and recv.x.shape[1] == H, "recv x [capacity][H]")
-    if p.quant != QUANT_NONE:
-        n = p.G * (E * R * T if p.mode == MODE_LOW_LATENCY else recv.capacity)
-        _need(recv.scales is not None and recv.scales.numel() >= n, "recv scales")
-        _need(recv.x.element_size() == 1, "FP8 codes are bytes")
-    else:
-        _need(recv.x.element_size() == 2, "bf16 rows")
+    _check_payload(p, recv)
 
 
 def _dispatch_fused_args(p: Problem, topk_idx: torch.Tensor, layout: Layout, x: torch.Tensor,
@@ -523,6 +533,38 @@ def _weights(p: Problem, w: torch.Tensor, scales: torch.Tensor | None = None,
                     0 if scales is None else 1, 0)
 
 
+def _int8_rows(t: torch.Tensor, what: str, channels: int,
+               scales: torch.Tensor | None) -> CRows:
+    """A row buffer of 8-bit integers with a scale per row."""
+    _need(t.dim() == 2 and t.shape[1] == channels, f"{what} [rows][{channels}]")
+    _need(t.dtype == torch.int8, f"{what} int8 (as the weights)")
+    _need(scales is not None and scales.dtype == torch.float32
+          and scales.numel() >= t.shape[0], f"{what} scales [{what} rows] fp32")
+    return CRows(_ptr(t), _ptr(scales), t.shape[0], t.shape[1], QUANT_INT8)
+
+
+def _int8_weights(p: Problem, w: torch.Tensor, scales: torch.Tensor | None,
+                  bias: torch.Tensor | None = None) -> CWeights:
+    _need(w.dim() == 3 and w.shape[0] == p.E and w.dtype == torch.int8,
+          "w [E][out channels][in channels] int8")
+    _need(scales is not None and scales.dtype == torch.float32
+          and scales.numel() == p.E * w.shape[1], "w_scales [E][out channels] fp32")
+    if bias is not None:
+        _need(bias.dtype == torch.float32 and bias.numel() == p.E * w.shape[1], "bias [E][N] fp32")
+    return CWeights(_ptr(w), _ptr(scales), _ptr(bias), w.shape[2], w.shape[1], WEIGHTS_INT8, 0)
+
+
+def _operands(p: Problem, x: torch.Tensor, x_scales: torch.Tensor | None, w: torch.Tensor,
+              w_scales: torch.Tensor | None,
+              bias: torch.Tensor | None = None) -> tuple[CRows, CWeights]:
+    """Rows and weights of a forward product: both bf16, both e4m3 codes or both int8."""
+    if w.dtype == torch.int8:
+        cw = _int8_weights(p, w, w_scales, bias)
+        return _int8_rows(x, "x", w.shape[2], x_scales), cw
+    cw = _weights(p, w, w_scales, bias)
+    return _rows(p, x, "x", w.shape[2], x_scales), cw
+
+
 def _check_segments(p: Problem, layout: Layout) -> None:
     _same_device(layout.err, layout.recv_tokens_per_expert, layout.expert_start)
     _need(layout.recv_tokens_per_expert.numel() == p.E and layout.expert_start.numel() == p.E,
@@ -541,7 +583,8 @@ def expert_gated(p: Problem, layout: Layout, x: torch.Tensor, w: torch.Tensor, h
     x [rows][C], w [E][2 I][C] (gates first), h [rows][I]; `pre` [rows][2 I]
     keeps both projections for expert_gated_backward.  FP8 (codes as bytes):
     x with the dispatch's scales and w with w_scales [E][2 I/128][C/128]; h then
-    may be FP8 too (h_scales, fp32 or uint8), its NaNs and infinities as NaN codes."""
+    may be FP8 too (h_scales, fp32 or uint8), its NaNs and infinities as NaN codes.
+    8-bit integers (int8): x with x_scales [rows] and w with w_scales [E][2 I]; h bf16."""
     _invoke(_expert_gated_args(p, layout, x, w, h, act=act, x_scales=x_scales, w_scales=w_scales,
                                h_scales=h_scales, pre=pre), stream)
 
@@ -555,8 +598,7 @@ def _expert_gated_args(p: Problem, layout: Layout, x: torch.Tensor, w: torch.Ten
     _check_segments(p, layout)
     _same_device(x, x_scales, w, w_scales, h, h_scales, pre, layout.err)
     _need(w.dim() == 3 and w.shape[1] % 2 == 0, "w [E][2 I][C]")
-    cw = _weights(p, w, w_scales)
-    cx = _rows(p, x, "x", w.shape[2], x_scales)
+    cx, cw = _operands(p, x, x_scales, w, w_scales)
     ch = _rows(p, h, "h", w.shape[1] // 2, h_scales)
     cpre = _rows(p, pre, "pre", w.shape[1]) if pre is not None else None
     pc, cl = p.c(), layout.c()
@@ -573,7 +615,7 @@ def expert_linear(p: Problem, layout: Layout, x: torch.Tensor, w: torch.Tensor, 
     """Product with bias, activation and residual over the receive rows:
     y = act(x W^T + bias) + residual.  x [rows][C], w [E][N][C], bias [E][N]
     fp32, residual and y [rows][N] (residual may be y); `pre` [rows][N] keeps
-    x W^T + bias for expert_linear_backward.  FP8 as in expert_gated."""
+    x W^T + bias for expert_linear_backward.  FP8 and int8 as in expert_gated."""
     _invoke(_expert_linear_args(p, layout, x, w, y, act=act, bias=bias, residual=residual,
                                 x_scales=x_scales, w_scales=w_scales, y_scales=y_scales, pre=pre),
             stream)
@@ -588,8 +630,7 @@ def _expert_linear_args(p: Problem, layout: Layout, x: torch.Tensor, w: torch.Te
                         pre: torch.Tensor | None = None) -> _Args:
     _check_segments(p, layout)
     _same_device(x, x_scales, w, w_scales, y, y_scales, bias, residual, pre, layout.err)
-    cw = _weights(p, w, w_scales, bias)
-    cx = _rows(p, x, "x", w.shape[2], x_scales)
+    cx, cw = _operands(p, x, x_scales, w, w_scales, bias)
     cy = _rows(p, y, "y", w.shape[1], y_scales)
     cr = _rows(p, residual, "residual", w.shape[1]) if residual is not None else None
     cpre = _rows(p, pre, "pre", w.shape[1]) if pre is not None else None
@@ -597,6 +638,24 @@ def _expert_linear_args(p: Problem, layout: Layout, x: torch.Tensor, w: torch.Te
     return _Args("ep_expert_linear", (ctypes.byref(pc), ctypes.byref(cl), ctypes.byref(cx),
                                       ctypes.byref(cw), int(act), _ref(cr), ctypes.byref(cy),
                                       _ref(cpre)), (pc, cl, cx, cw, cr, cy, cpre))
+
+
+def quantize_rows(p: Problem, layout: Layout, x: torch.Tensor, q: torch.Tensor,
+                  q_scales: torch.Tensor, stream=None) -> None:
+    """bf16 receive rows x [rows][C] to 8-bit integers q (int8) with a scale each,
+    q_scales [rows] fp32: max(amax, 2^-100) / 127."""
+    _invoke(_quantize_rows_args(p, layout, x, q, q_scales), stream)
+
+
+def _quantize_rows_args(p: Problem, layout: Layout, x: torch.Tensor, q: torch.Tensor,
+                        q_scales: torch.Tensor) -> _Args:
+    _check_segments(p, layout)
+    _same_device(x, q, q_scales, layout.err)
+    cx = _rows(p, x, "x")
+    cq = _int8_rows(q, "q", x.shape[1], q_scales)
+    pc, cl = p.c(), layout.c()
+    return _Args("ep_quantize_rows", (ctypes.byref(pc), ctypes.byref(cl), ctypes.byref(cx),
+                                      ctypes.byref(cq)), (pc, cl, cx, cq))
 
 
 def expert_gated_backward(p: Problem, layout: Layout, x: torch.Tensor | None, w: torch.Tensor,
@@ -777,7 +836,7 @@ _ARGS = {get_layout: _get_layout_args, dispatch: _dispatch_args,
          messages_unpack: _messages_unpack_args, expert_gated: _expert_gated_args,
          expert_linear: _expert_linear_args, expert_gated_backward: _expert_gated_backward_args,
          expert_linear_backward: _expert_linear_backward_args,
-         combine_backward: _combine_backward_args}
+         combine_backward: _combine_backward_args, quantize_rows: _quantize_rows_args}
 
 
 def messages_sizes(p: Problem, counts=None) -> tuple[int, int, int]:

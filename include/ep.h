@@ -51,8 +51,8 @@
  *    E = num_experts, K = num_topk, L = E / R, G = H / 128.
  *    Limits: 1 <= R <= 256, R <= E <= 2048, E % R == 0, 1 <= K <= 64,
  *    T >= 0, 8 <= H <= 32768, H % 8 == 0 (bf16 rows are whole 16-byte
- *    vectors), H % 128 == 0 when quantised, R*T*K < 2^31, receive rows
- *    < 2^31.
+ *    vectors), H % 128 == 0 in FP8, H % 16 == 0 in 8-bit integers,
+ *    R*T*K < 2^31, receive rows < 2^31.
  */
 #ifndef EP_H
 #define EP_H
@@ -75,6 +75,13 @@ extern "C" {
 #define EP_QUANT_NONE 0      /* bf16 rows                                      */
 #define EP_QUANT_FP8_F32 1   /* e4m3 codes + fp32 scale (amax / 448) per 128 channels */
 #define EP_QUANT_FP8_UE8M0 2 /* e4m3 codes + power-of-two scale stored as a biased 8-bit exponent */
+#define EP_QUANT_INT8 3      /* 8-bit integers + fp32 scale (amax / 127) per row; normal and
+                                low-latency modes                              */
+
+/* the experts' weights */
+#define EP_WEIGHTS_BF16 0
+#define EP_WEIGHTS_FP8 1  /* e4m3 codes + fp32 scale per 128 x 128 block       */
+#define EP_WEIGHTS_INT8 2 /* 8-bit integers + fp32 scale per output channel    */
 
 /* activations of the experts' products */
 #define EP_ACT_NONE 0 /* v                                                     */
@@ -144,10 +151,11 @@ typedef struct ep_layout {
 
 /* Receive side of normal / low-latency dispatch. */
 typedef struct ep_recv {
-  void* x;          /* [capacity][H]: bf16 (EP_QUANT_NONE) or e4m3 codes (1 byte)          */
-  void* scales;     /* FP8 only, column-major: normal [G][capacity];
+  void* x;          /* [capacity][H]: bf16 (EP_QUANT_NONE), e4m3 codes (1 byte) or int8    */
+  void* scales;     /* FP8, column-major: normal [G][capacity];
                        low-latency [E][G][R*T].  fp32 (FP8_F32) or uint8 exponents
-                       (FP8_UE8M0: scale = 2^(byte - 127)); 4-byte aligned               */
+                       (FP8_UE8M0: scale = 2^(byte - 127)); 4-byte aligned.
+                       8-bit integers: [capacity] fp32, a row's                          */
   int64_t capacity; /* rows of x; low-latency needs >= E*R*T                              */
   int32_t* topk_idx;    /* rank-major only, may be NULL: [capacity][K], the row's token's
                            experts on this rank as local ids (e - d*L), else -1          */
@@ -222,7 +230,10 @@ int ep_get_layout(const ep_problem* p, const int32_t* topk_idx, const ep_layout*
  *   (s, t, k) writes token x[s][t] to row send_pos[s][t][k] of recv->x,
  *   as bf16 or as e4m3 codes with one scale per 128-channel group (the
  *   group's largest magnitude maps to 448; UE8M0 rounds the scale up to a
- *   power of two).  Uses layout->send_pos; `msgs` may be NULL.
+ *   power of two).  Uses layout->send_pos; `msgs` may be NULL.  As 8-bit
+ *   integers (EP_QUANT_INT8) a row has one scale, max(amax, 2^-100) / 127 of
+ *   the token, and the codes rint(x / scale), ties to even, both quotients
+ *   rounded to fp32; a token with a NaN or infinity gets zeros and the scale NaN.
  * messages ("Eaas_server" notes; "ibgda_device.cuh" sec. 1, 3): for every
  *   (s, d) with num_tokens_per_rank[s][d] > 0, one region in s's send arena:
  *   16-byte header {s, d, n, body bytes} (u32 LE), body = codes n*H |
@@ -301,8 +312,10 @@ int ep_combine(const ep_problem* p, const ep_layout* layout, const uint16_t* y,
  * A segment past the smallest capacity of the call's row buffers sets
  * EP_DEVERR_CAPACITY (OR-ed into *layout->err) and is cut there.
  * p->hidden and p->quant describe the dispatch and are not used: every
- * operand has its own channel count, a multiple of 8 in [8, 32768], and
- * 128 in FP8.  Sums are kept in fp32 and results rounded to bf16, nearest even,
+ * operand has its own channel count, a multiple of 8 in [8, 32768], of
+ * 128 in FP8 and of 16 where it is held in 8-bit integers.  Sums of those are exact
+ * 32-bit integers, converted to fp32 (the smallest tile adds four such parts there), and
+ * times the row's and the channel's scale; other sums are kept in fp32 and results rounded to bf16, nearest even,
  * once; but of FP8 products eight (consecutive channels of a row) are added at a
  * time, each cut off 13 bits below the largest of the eight, before they enter the
  * fp32 sum (a relative error of about 2^-16 on random rows).  The calls are deterministic and need no workspace.  Row buffers that
@@ -311,9 +324,10 @@ int ep_combine(const ep_problem* p, const ep_layout* layout, const uint16_t* y,
 
 /* One row buffer. */
 typedef struct ep_rows {
-  void* x;          /* [capacity][channels] bf16, or e4m3 codes, 16-byte aligned      */
+  void* x;          /* [capacity][channels] bf16, e4m3 codes or int8, 16-byte aligned */
   void* scales;     /* FP8: as ep_recv.scales with G = channels / 128 (in normal mode
-                       capacity is the stride between groups), else ignored           */
+                       capacity is the stride between groups); 8-bit integers:
+                       [capacity] fp32, a row's; else ignored                         */
   int64_t capacity; /* rows; low-latency and messages need >= E*R*T                   */
   int32_t channels;
   int32_t quant;    /* EP_QUANT_* of these rows                                       */
@@ -321,13 +335,15 @@ typedef struct ep_rows {
 
 /* The experts' weights. */
 typedef struct ep_weights {
-  const void* w;       /* [E][out_channels][in_channels] bf16 or e4m3 codes, 16-byte aligned */
+  const void* w;       /* [E][out_channels][in_channels] bf16, e4m3 codes or int8, 16-byte
+                          aligned                                                      */
   const float* scales; /* FP8: [E][out_channels/128][in_channels/128], the factor of each
-                          128 x 128 block; else ignored                                */
+                          128 x 128 block; 8-bit integers: [E][out_channels], a channel's,
+                          16-byte aligned; else ignored                                */
   const float* bias;   /* [E][out_channels] fp32, 16-byte aligned, or NULL             */
   int32_t in_channels;
   int32_t out_channels;
-  int32_t fp8;         /* 0: bf16, 1: e4m3 codes with scales                           */
+  int32_t fp8;         /* EP_WEIGHTS_*                                                 */
   int32_t reserved;    /* must be 0                                                    */
 } ep_weights;
 
@@ -335,7 +351,8 @@ typedef struct ep_weights {
  * in one launch.  w holds gate and up projection, [E][2 I][C] (out_channels =
  * 2 I, the gates first; bias must be NULL):
  *   g = x Wg^T,  u = x Wu^T,  h = act(g) * u      for every row x of expert e.
- * x: bf16 rows with bf16 weights, or FP8 rows with FP8 weights.
+ * x: bf16 rows with bf16 weights, FP8 rows with FP8 weights, or 8-bit integers with
+ *   8-bit integers (bf16 result).
  * h: [capacity][I] bf16; with FP8 rows also FP8: the bf16 result quantised as
  *   dispatch quantises a row (scale per 128 channels), for an FP8 product next.
  *   A NaN or infinity becomes the NaN code 0x7F (e4m3 has no infinity), and its
@@ -355,6 +372,12 @@ int ep_expert_gated(const ep_problem* p, const ep_layout* layout, const ep_rows*
 int ep_expert_linear(const ep_problem* p, const ep_layout* layout, const ep_rows* x,
                      const ep_weights* w, int32_t act, const ep_rows* residual,
                      const ep_rows* y, const ep_rows* pre, void* stream);
+
+/* bf16 rows to 8-bit integers with a scale each, as dispatch makes them of tokens: what
+ * stands between two 8-bit products.  x: [capacity][C] bf16, q: [capacity][C] int8 with
+ * scales (quant EP_QUANT_INT8), which must not overlap x.  C % 16 == 0. */
+int ep_quantize_rows(const ep_problem* p, const ep_layout* layout, const ep_rows* x,
+                     const ep_rows* q, void* stream);
 
 /* Gradients of ep_expert_gated (bf16).  pre: the saved [g | u]; dh: [capacity][I].
  *   dpre = [dh * u * act'(g) | dh * act(g)]   written to dpre, [capacity][2 I]
