@@ -21,12 +21,15 @@ MODE_NORMAL, MODE_LOW_LATENCY, MODE_MESSAGES, MODE_RANK_MAJOR = 0, 1, 2, 3
 QUANT_NONE, QUANT_FP8_F32, QUANT_FP8_UE8M0, QUANT_INT8 = 0, 1, 2, 3
 WEIGHTS_BF16, WEIGHTS_FP8, WEIGHTS_INT8 = 0, 1, 2
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = 0, 1, 2, 3
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 DEVERR_TOPK_RANGE, DEVERR_LL_OVERFLOW, DEVERR_CAPACITY, DEVERR_MESSAGE = 1, 2, 4, 8
+DEVERR_LOGITS = 16
 
 EXPORTS = ["ep_workspace_bytes", "ep_max_recv_rows", "ep_messages_capacity", "ep_get_layout",
            "ep_dispatch", "ep_dispatch_fused", "ep_dispatch_fused_noalloc", "ep_combine",
            "ep_expert_gated", "ep_expert_linear", "ep_expert_gated_backward",
            "ep_expert_linear_backward", "ep_combine_backward", "ep_quantize_rows",
+           "ep_route", "ep_route_backward",
            "ep_messages_execute", "ep_messages_unpack", "ep_status_string"]
 NOALLOC_SCRATCH_BYTES = 64 << 20  # EP_NOALLOC_SCRATCH_BYTES
 ERR_SCRATCH = -8
@@ -81,6 +84,13 @@ class CWeights(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class CRouter(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("groups_kept", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("normalize", ctypes.c_int32), ("bf16", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -124,6 +134,11 @@ def lib() -> ctypes.CDLL:
         l.ep_expert_linear_backward.restype = ctypes.c_int
         l.ep_quantize_rows.argtypes = [P, LP, RP, RP, _vp]
         l.ep_quantize_rows.restype = ctypes.c_int
+        OP = ctypes.POINTER(CRouter)
+        l.ep_route.argtypes = [P, OP, _vp, _vp, _vp, _vp, _vp, _vp]
+        l.ep_route.restype = ctypes.c_int
+        l.ep_route_backward.argtypes = [P, OP, _vp, _vp, _vp, _vp, _vp, _vp]
+        l.ep_route_backward.restype = ctypes.c_int
         l.ep_combine_backward.argtypes = [P, LP, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp, _vp]
         l.ep_combine_backward.restype = ctypes.c_int
         l.ep_messages_execute.argtypes = [P, ctypes.POINTER(CMessages), _vp, ctypes.c_int64,
@@ -760,6 +775,76 @@ def _combine_backward_args(p: Problem, layout: Layout, dout: torch.Tensor,
                                          _ptr(dweights)), (pc, cl))
 
 
+# ---- the router ----
+
+def _router(p: Problem, logits: torch.Tensor, score: int, normalize: bool, scale: float,
+            groups: int = 1, groups_kept: int = 1, group_top: int = 1) -> CRouter:
+    _need(logits.dtype in (torch.float32, torch.bfloat16)
+          and logits.numel() == p.R * p.T * p.E, "logits [R][T][E] fp32 or bf16")
+    return CRouter(int(score), int(groups), int(groups_kept), int(group_top), int(normalize),
+                   int(logits.dtype == torch.bfloat16), float(scale), 0)
+
+
+def route(p: Problem, logits: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
+          err: torch.Tensor | None = None, *, score: int = SCORE_SOFTMAX,
+          bias: torch.Tensor | None = None, groups: int = 1, groups_kept: int = 1,
+          group_top: int = 1, normalize: bool = True, scale: float = 1.0, stream=None) -> None:
+    """Top-k expert ids [R][T][K] int32 and weights [R][T][K] fp32 from router logits
+    [R][T][E].  `bias` [E] fp32 counts for the choice alone; of `groups` groups of experts
+    the `groups_kept` best by the sum of their `group_top` (1 or 2) largest choices stay.
+    Experts at -inf are not chosen; entries without an expert are -1 with weight 0.  Error
+    bits are OR-ed into err[0]."""
+    _invoke(_route_args(p, logits, topk_idx, topk_weights, err, score=score, bias=bias,
+                        groups=groups, groups_kept=groups_kept, group_top=group_top,
+                        normalize=normalize, scale=scale), stream)
+
+
+def _route_args(p: Problem, logits: torch.Tensor, topk_idx: torch.Tensor,
+                topk_weights: torch.Tensor, err: torch.Tensor | None = None, *,
+                score: int = SCORE_SOFTMAX, bias: torch.Tensor | None = None, groups: int = 1,
+                groups_kept: int = 1, group_top: int = 1, normalize: bool = True,
+                scale: float = 1.0) -> _Args:
+    n = p.R * p.T * p.K
+    _same_device(logits, bias, topk_idx, topk_weights, err)
+    cr = _router(p, logits, score, normalize, scale, groups, groups_kept, group_top)
+    _need(bias is None or (bias.dtype == torch.float32 and bias.numel() == p.E), "bias [E] fp32")
+    _need(topk_idx.dtype == torch.int32 and topk_idx.numel() == n, "topk_idx [R][T][K] int32")
+    _need(topk_weights.dtype == torch.float32 and topk_weights.numel() == n,
+          "topk_weights [R][T][K] fp32")
+    _need(err is None or (err.dtype == torch.int32 and err.numel() >= 1), "err int32")
+    pc = p.c()
+    return _Args("ep_route", (ctypes.byref(pc), ctypes.byref(cr), _ptr(logits), _ptr(bias),
+                              _ptr(topk_idx), _ptr(topk_weights), _ptr(err)), (pc, cr))
+
+
+def route_backward(p: Problem, logits: torch.Tensor, topk_idx: torch.Tensor,
+                   dweights: torch.Tensor, dlogits: torch.Tensor,
+                   err: torch.Tensor | None = None, *, score: int = SCORE_SOFTMAX,
+                   normalize: bool = True, scale: float = 1.0, stream=None) -> None:
+    """Gradient of route: dlogits [R][T][E] (as the logits, written whole) from
+    combine_backward's dweights [R][T][K] fp32."""
+    _invoke(_route_backward_args(p, logits, topk_idx, dweights, dlogits, err, score=score,
+                                 normalize=normalize, scale=scale), stream)
+
+
+def _route_backward_args(p: Problem, logits: torch.Tensor, topk_idx: torch.Tensor,
+                         dweights: torch.Tensor, dlogits: torch.Tensor,
+                         err: torch.Tensor | None = None, *, score: int = SCORE_SOFTMAX,
+                         normalize: bool = True, scale: float = 1.0) -> _Args:
+    n = p.R * p.T * p.K
+    _same_device(logits, topk_idx, dweights, dlogits, err)
+    cr = _router(p, logits, score, normalize, scale)
+    _need(topk_idx.dtype == torch.int32 and topk_idx.numel() == n, "topk_idx [R][T][K] int32")
+    _need(dweights.dtype == torch.float32 and dweights.numel() == n, "dweights [R][T][K] fp32")
+    _need(dlogits.dtype == logits.dtype and dlogits.numel() == logits.numel(),
+          "dlogits as the logits")
+    _need(err is None or (err.dtype == torch.int32 and err.numel() >= 1), "err int32")
+    pc = p.c()
+    return _Args("ep_route_backward", (ctypes.byref(pc), ctypes.byref(cr), _ptr(logits),
+                                       _ptr(topk_idx), _ptr(dweights), _ptr(dlogits), _ptr(err)),
+                 (pc, cr))
+
+
 def messages_execute(p: Problem, msgs: Messages, recv_arena: torch.Tensor, err: torch.Tensor,
                      stream=None, publish_batch: int = 0) -> None:
     """Loopback delivery of the descriptors of `msgs` into `recv_arena`
@@ -836,7 +921,8 @@ _ARGS = {get_layout: _get_layout_args, dispatch: _dispatch_args,
          messages_unpack: _messages_unpack_args, expert_gated: _expert_gated_args,
          expert_linear: _expert_linear_args, expert_gated_backward: _expert_gated_backward_args,
          expert_linear_backward: _expert_linear_backward_args,
-         combine_backward: _combine_backward_args, quantize_rows: _quantize_rows_args}
+         combine_backward: _combine_backward_args, quantize_rows: _quantize_rows_args,
+         route: _route_args, route_backward: _route_backward_args}
 
 
 def messages_sizes(p: Problem, counts=None) -> tuple[int, int, int]:

@@ -89,6 +89,10 @@ extern "C" {
 #define EP_ACT_SILU 2 /* v / (1 + exp(-v))                                     */
 #define EP_ACT_GELU 3 /* v Phi(v), Phi the Gaussian distribution (erf form)    */
 
+/* a router's scores */
+#define EP_SCORE_SOFTMAX 0 /* exp(l_e) / sum exp(l)                             */
+#define EP_SCORE_SIGMOID 1 /* 1 / (1 + exp(-l_e))                               */
+
 /* host-side status codes */
 #define EP_OK 0
 #define EP_ERR_NULL (-1)        /* a required pointer is NULL              */
@@ -110,6 +114,7 @@ extern "C" {
 #define EP_DEVERR_CAPACITY 4    /* a row or byte offset past the caller's capacity: skipped */
 #define EP_DEVERR_MESSAGE 8     /* a descriptor names a rank outside [0, R), or a received
                                    message's header or completion flag does not match: skipped */
+#define EP_DEVERR_LOGITS 16     /* a router logit that is no number: its token gets no expert */
 
 typedef struct ep_problem {
   int32_t num_ranks;        /* R                                           */
@@ -412,6 +417,45 @@ int ep_expert_linear_backward(const ep_problem* p, const ep_layout* layout, cons
 int ep_combine_backward(const ep_problem* p, const ep_layout* layout, const uint16_t* dout,
                         const float* topk_weights, const uint16_t* y, int64_t y_rows,
                         uint16_t* dy, float* dweights, void* stream);
+
+/* ---- The router: where topk_idx and topk_weights come from ---------------- */
+
+typedef struct ep_router {
+  int32_t score;       /* EP_SCORE_*                                          */
+  int32_t groups;      /* groups of E / groups consecutive experts, 1 .. 64   */
+  int32_t groups_kept; /* of which a token may use, 1 .. groups               */
+  int32_t group_top;   /* largest choices that a group is judged by: 1 or 2, at most E / groups */
+  int32_t normalize;   /* 1: a token's weights add up to `scale`              */
+  int32_t bf16;        /* logits (and their gradient): 0 fp32, 1 bf16         */
+  float scale;         /* finite                                              */
+  int32_t reserved;    /* must be 0                                           */
+} ep_router;
+
+/* Top-k experts and weights of every token.  With s the scores of its logits l:
+ *   choice_e = s_e + bias_e; without a bias, and where no scores are added up, l_e itself;
+ *   a group is judged by the sum of its group_top largest choices (of those that
+ *   there are); the groups_kept best groups stay;
+ *   topk_idx[k] = the k-th largest choice of their experts, ties (of groups as of
+ *   experts) to the lowest index; topk_weights[k] = scale * s / (sum of the chosen s),
+ *   or scale * s.
+ * Choices are compared as their values in 64 bits; weights are computed in fp32.  An expert
+ * whose logit, or bias, is -inf is not to be had; where fewer than K are left the rest of the
+ * entries are -1 with weight 0 (as layout takes them).  A token with a NaN (logit, or bias),
+ * or with a logit of +inf under softmax, gets -1 throughout and sets EP_DEVERR_LOGITS.
+ * logits: [R][T][E], 16-byte aligned.  bias: [E] fp32 or NULL.  topk_idx: [R][T][K].
+ * topk_weights: [R][T][K].  err: [1], bits are OR-ed into it, or NULL.  p->mode, p->quant and
+ * p->hidden are not used. */
+int ep_route(const ep_problem* p, const ep_router* r, const void* logits, const float* bias,
+             int32_t* topk_idx, float* topk_weights, int32_t* err, void* stream);
+
+/* Gradient of topk_weights with respect to the logits, the choice taken as it is (the
+ * bias, which counts for it alone, has none).  dlogits: [R][T][E], as the logits; written
+ * whole.  Entries of -1 have no part in it; an expert that several entries of a token
+ * name gets the sum of theirs; an id outside [-1, E) is skipped and sets
+ * EP_DEVERR_TOPK_RANGE.  r's groups are checked but not used. */
+int ep_route_backward(const ep_problem* p, const ep_router* r, const void* logits,
+                      const int32_t* topk_idx, const float* dweights, void* dlogits,
+                      int32_t* err, void* stream);
 
 /* Loopback delivery of message mode's descriptors ("ibgda_device.cuh" notes,
  * sec. 1; "GPU-Initiated Communication: Dissecting Down to the Bone", WQE

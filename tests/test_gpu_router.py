@@ -1,0 +1,411 @@
+"""The router and its gradient against plain 64-bit forms (tests/router_util.py, where the
+bounds are derived): expert counts that lanes do not divide, ties, groups, masked experts,
+values that are no numbers, the two passes together with the layer that they route."""
+import numpy as np
+import pytest
+import torch
+
+from combine_ep_get_layout_amd import ep
+from expert_util import HALF
+from gpu_util import DEV, say
+from router_util import choices64, grad64, weights64
+
+pytestmark = pytest.mark.gpu
+
+INF, NAN = float("inf"), float("nan")
+SCORES = {"softmax": ep.SCORE_SOFTMAX, "sigmoid": ep.SCORE_SIGMOID}
+
+
+def logits_for(gen, n, E, bf16, masked=0.0, scale=1.5, steps=None):
+    l = torch.randn((n, E), generator=gen) * scale
+    if steps:
+        l = torch.round(l * steps) / steps  # ties
+    if masked:
+        l[torch.rand((n, E), generator=gen) < masked] = -INF
+    return l.to(torch.bfloat16) if bf16 else l
+
+
+def run_route(p, l, bias=None, **kw):
+    n = p.R * p.T
+    idx = torch.full((n, p.K), 777, dtype=torch.int32, device=DEV)
+    w = torch.full((n, p.K), NAN, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ep.route(p, l.to(DEV), idx, w, err, bias=None if bias is None else bias.to(DEV), **kw)
+    torch.cuda.synchronize()
+    return idx.cpu().numpy(), w.cpu().numpy().astype(np.float64), int(err.item())
+
+
+def check_route(R, T, E, K, score, gen, bias=None, groups=1, kept=1, top=1, normalize=True,
+                scale=1.0, l=None, bf16=False, masked=0.0, steps=None, spread=1.5):
+    p = ep.Problem(R, T, 128, E, K)
+    n = R * T
+    if l is None:
+        l = logits_for(gen, n, E, bf16, masked, spread, steps)
+    idx, w, err = run_route(p, l, bias, score=SCORES[score], groups=groups, groups_kept=kept,
+                            group_top=top, normalize=normalize, scale=scale)
+    l64 = l.double().numpy()
+    b64 = None if bias is None else bias.double().numpy()
+    sig = score == "sigmoid"
+    bad = 0
+    for t in range(n):
+        answers = choices64(l64[t], b64, sig, groups, kept, top, K)
+        if not answers:
+            bad = ep.DEVERR_LOGITS
+            assert (idx[t] == -1).all() and (w[t] == 0).all(), t
+            continue
+        want = next((v for v in answers if (idx[t] == v).all()), None)
+        assert want is not None, (t, idx[t], answers[:3])
+        ww, ew = weights64(l64[t], want, sig, normalize, scale)
+        assert (np.abs(w[t] - ww) <= ew).all(), (t, w[t], ww)
+    assert err == bad
+
+
+# R, T, E, K, groups, kept, group_top
+SHAPES = [
+    (1, 1, 1, 1, 1, 1, 1),
+    (1, 3, 3, 2, 1, 1, 1),
+    (1, 1, 64, 8, 1, 1, 1),
+    (1, 7, 5, 5, 5, 2, 1),
+    (1, 9, 60, 6, 4, 2, 2),
+    (1, 33, 78, 3, 6, 5, 2),
+    (2, 20, 64, 15, 16, 3, 2),
+    (2, 20, 64, 16, 32, 7, 2),
+    (1, 18, 64, 64, 64, 64, 1),
+    (1, 18, 64, 64, 64, 5, 1),
+    (4, 25, 128, 8, 8, 3, 1),
+    (4, 25, 100, 7, 25, 3, 2),
+    (8, 130, 256, 8, 8, 4, 2),
+    (3, 11, 201, 8, 3, 1, 2),
+    (1, 40, 256, 20, 16, 4, 2),
+    (1, 21, 384, 8, 12, 4, 2),
+    (1, 21, 512, 12, 64, 9, 2),
+    (1, 10, 513, 9, 9, 4, 2),
+    (1, 6, 1000, 40, 10, 3, 2),
+    (2, 6, 2048, 64, 32, 8, 2),
+]
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "-".join(map(str, s)))
+def test_route(shape, score, bf16):
+    R, T, E, K, groups, kept, top = shape
+    say("route", shape, score, bf16)
+    gen = torch.Generator().manual_seed(41)
+    bias = torch.randn(E, generator=gen) * 0.1
+    for normalize in (True, False):
+        check_route(R, T, E, K, score, gen, bf16=bf16, normalize=normalize)
+        check_route(R, T, E, K, score, gen, bias=bias, bf16=bf16, normalize=normalize, scale=2.5)
+        check_route(R, T, E, K, score, gen, groups=groups, kept=kept, top=top, bf16=bf16,
+                    normalize=normalize)
+        check_route(R, T, E, K, score, gen, bias=bias, groups=groups, kept=kept, top=top,
+                    bf16=bf16, normalize=normalize, masked=0.5, scale=-0.5)
+    # few left, or none
+    check_route(R, T, E, K, score, gen, groups=groups, kept=kept, top=top, bf16=bf16, masked=0.97)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("shape", [(1, 40, 60, 6, 4, 2, 2), (2, 50, 256, 8, 8, 4, 2),
+                                   (1, 60, 132, 9, 11, 4, 2), (1, 30, 512, 40, 32, 4, 2)],
+                         ids=lambda s: "-".join(map(str, s)))
+def test_ties_go_to_the_lowest_index(shape, score):
+    """Logits (and biases) of few values: many equal ones, in every lane and group, zeros of
+    either sign among them."""
+    R, T, E, K, groups, kept, top = shape
+    gen = torch.Generator().manual_seed(42)
+    bias = torch.round(torch.randn(E, generator=gen) * 4) / 64
+    for steps in (0.4, 2, 8):
+        for b in (None, torch.zeros(E), bias):
+            check_route(R, T, E, K, score, gen, bias=b, steps=steps)
+            check_route(R, T, E, K, score, gen, bias=b, steps=steps, groups=groups, kept=kept,
+                        top=top, bf16=True)
+            check_route(R, T, E, K, score, gen, bias=b, steps=steps, groups=groups, kept=kept,
+                        top=1)
+    check_route(R, T, E, K, score, gen, l=torch.zeros((R * T, E)))
+    l = torch.zeros((R * T, E))
+    l[:, 1::2] = -0.0
+    check_route(R, T, E, K, score, gen, l=l)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_choices_closer_than_fp32(score):
+    """Choices that 64 bits tell apart and 32 do not: logits that differ in their last bits
+    under biases that bring their scores next to each other."""
+    E, n = 256, 200
+    gen = torch.Generator().manual_seed(43)
+    base = torch.randn((n, 1), generator=gen)
+    l = base + torch.randint(-3, 4, (n, E), generator=gen) * 2.0 ** -23
+    for bias in (torch.zeros(E), torch.randint(-2, 3, (E,), generator=gen) * 2.0 ** -26,
+                 torch.full((E,), 1.0)):
+        for kw in ({}, dict(groups=8, kept=3, top=2)):
+            check_route(1, n, E, 8, score, gen, bias=bias, l=l, **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_values_that_are_no_numbers(score, bf16):
+    """NaN anywhere (and +inf under softmax) gives the token no expert and an error; its
+    neighbours in the wave stay right.  Rows of nothing but -inf, of one expert, and of the
+    type's lowest value."""
+    E, K = 64, 6
+    gen = torch.Generator().manual_seed(44)
+    l = logits_for(gen, 24, E, bf16)
+    l[1, 5] = NAN
+    l[3, 63] = INF
+    l[4] = -INF
+    l[6] = -INF
+    l[6, 40] = 0.5
+    l[7] = torch.finfo(l.dtype).min
+    l[9, ::2] = torch.finfo(l.dtype).min
+    l[11] = NAN
+    l[13, 0], l[13, 1] = -INF, NAN
+    l[14] = 80.0
+    l[15] = -80.0 - torch.arange(E) / 8
+    l[16] = torch.linspace(-300, 300, E).to(l.dtype)
+    bias = torch.randn(E, generator=gen) * 0.1
+    for b in (None, bias):
+        for normalize in (True, False):
+            check_route(1, 24, E, K, score, gen, l=l, bias=b, normalize=normalize)
+            check_route(1, 24, E, K, score, gen, l=l, bias=b, normalize=normalize, groups=8,
+                        kept=2, top=2)
+    bias[3], bias[60] = -INF, INF
+    check_route(1, 24, E, K, score, gen, l=l, bias=bias)
+    check_route(1, 24, E, K, score, gen, l=l, bias=bias, groups=8, kept=2, top=2)
+    check_route(1, 24, E, K, score, gen, l=l, bias=torch.full((E,), -INF))
+    bias[7] = NAN
+    check_route(1, 24, E, K, score, gen, l=l, bias=bias)
+
+
+def test_no_tokens_and_no_error_word():
+    p = ep.Problem(2, 0, 128, 8, 2)
+    e = lambda *s, **k: torch.empty(s, device=DEV, **k)  # noqa: E731
+    ep.route(p, e(2, 0, 8), e(2, 0, 2, dtype=torch.int32), e(2, 0, 2))
+    ep.route_backward(p, e(2, 0, 8), e(2, 0, 2, dtype=torch.int32), e(2, 0, 2), e(2, 0, 8))
+    p = ep.Problem(1, 2, 128, 8, 2)
+    idx, w = e(2, 2, dtype=torch.int32), e(2, 2)
+    l = torch.full((2, 8), NAN, device=DEV)
+    ep.route(p, l, idx, w)
+    torch.cuda.synchronize()
+    assert (idx == -1).all() and (w == 0).all()
+
+
+# ---- gradient -----------------------------------------------------------------------
+
+def check_grad(n, E, K, score, normalize, scale, bf16, gen, l=None, ids=None, masked=0.0,
+               dup=False):
+    p = ep.Problem(1, n, 128, E, K)
+    if l is None:
+        l = logits_for(gen, n, E, bf16, masked)
+    if ids is None:
+        ids = torch.stack([torch.randperm(E, generator=gen)[:K] if K <= E and not dup
+                           else torch.randint(0, E, (K,), generator=gen) for _ in range(n)])
+        ids[torch.rand((n, K), generator=gen) < 0.15] = -1
+    dw = torch.randn((n, K), generator=gen)
+    dw[ids < 0] = NAN  # of an entry without an expert, whatever it is
+    got = torch.full((n, E), NAN, dtype=l.dtype, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    kw = dict(score=SCORES[score], normalize=normalize, scale=scale)
+    ep.route_backward(p, l.to(DEV), ids.to(torch.int32).to(DEV), dw.to(DEV), got, err, **kw)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    g = got.cpu().double().numpy()
+    half = HALF if bf16 else 0.0
+    for t in range(n):
+        want, bound = grad64(l[t].double().numpy(), ids[t].numpy(), dw[t].double().numpy(),
+                             score == "sigmoid", normalize, scale)
+        bound = bound + half * (np.abs(want) + bound)
+        assert (np.abs(g[t] - want) <= bound).all(), (t, np.abs(g[t] - want).max())
+    return l, ids, dw, got
+
+
+GRADS = [(1, 1, 1), (3, 2, 2), (5, 5, 3), (9, 64, 8), (33, 78, 3), (20, 64, 64), (65, 128, 8),
+         (40, 201, 6), (70, 256, 8), (9, 256, 17), (11, 512, 16), (5, 1000, 12), (4, 2048, 64)]
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("shape", GRADS, ids=lambda s: "-".join(map(str, s)))
+def test_route_backward(shape, score, bf16):
+    n, E, K = shape
+    say("route_backward", shape, score, bf16)
+    gen = torch.Generator().manual_seed(45)
+    for normalize in (True, False):
+        check_grad(n, E, K, score, normalize, 1.5, bf16, gen)
+        check_grad(n, E, K, score, normalize, 1.0, bf16, gen, masked=0.4)
+        check_grad(n, E, K, score, normalize, -2.0, bf16, gen, dup=True)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gradient_of_extreme_logits(score):
+    """Chosen experts far below the best one, all far below zero, and saturated ones: the
+    normalised weights are what they are, so are their gradients."""
+    gen = torch.Generator().manual_seed(46)
+    E, K = 64, 6
+    l = logits_for(gen, 12, E, False)
+    l[0] -= 100
+    l[1, 10:] += 200
+    l[2] = -300 - torch.arange(E).float()
+    l[3] = torch.linspace(-150, 150, E)
+    l[4] = -INF
+    l[5, :6] = -INF
+    ids = torch.arange(K).repeat(12, 1)
+    for normalize in (True, False):
+        check_grad(12, E, K, score, normalize, 1.0, False, gen, l=l, ids=ids)
+
+
+def test_gradient_ids_out_of_range_and_none():
+    E, K = 16, 3
+    gen = torch.Generator().manual_seed(47)
+    p = ep.Problem(1, 4, 128, E, K)
+    l = logits_for(gen, 4, E, False)
+    l[3] = NAN
+    ids = torch.tensor([[1, 16, 2], [-2, 5, -1], [3, 4, 5], [-1, -1, -1]], dtype=torch.int32)
+    dw = torch.randn((4, K), generator=gen)
+    got = torch.full((4, E), NAN, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ep.route_backward(p, l.to(DEV), ids.to(DEV), dw.to(DEV), got, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == ep.DEVERR_TOPK_RANGE
+    ids[(ids < -1) | (ids >= E)] = -1
+    for t in range(4):
+        want, bound = grad64(l[t].double().numpy(), ids[t].numpy(), dw[t].double().numpy(), False,
+                             True, 1.0)
+        assert (np.abs(got[t].cpu().double().numpy() - want) <= bound).all()
+
+
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gradient_against_differences(score, normalize):
+    """<gradient, v> for v its signs against central differences of the 64-bit weights; the
+    difference's own error, O(step^2), is seen by halving the step."""
+    gen = torch.Generator().manual_seed(48)
+    n, E, K = 17, 40, 5
+    l, ids, dw, got = check_grad(n, E, K, score, normalize, 1.25, False, gen)
+    g = got.cpu().double().numpy()
+    v = np.sign(g)
+    dw64 = np.where(ids.numpy() >= 0, dw.double().numpy(), 0)
+
+    def value(step):
+        total = 0.0
+        for t in range(n):
+            at = l[t].double().numpy() + step * v[t]
+            total += (weights64(at, ids[t].numpy(), score == "sigmoid", normalize, 1.25)[0]
+                      * dw64[t]).sum()
+        return total
+    found = [(value(s) - value(-s)) / (2 * s) for s in (1e-3, 5e-4)]
+    error = abs(found[0] - found[1]) / 3  # of the second one
+    assert abs(np.abs(g).sum() - found[1]) <= 4 * error + 2 ** -15 * np.abs(g).sum() + 1e-9
+
+
+# ---- together -------------------------------------------------------------------------
+
+def test_many_tokens_past_a_grid():
+    """More tokens than one round of workgroups takes, the last round ragged."""
+    n, E, K = 40003, 8, 2
+    gen = torch.Generator().manual_seed(49)
+    p = ep.Problem(1, n, 128, E, K)
+    l = logits_for(gen, n, E, True)
+    idx, w, err = run_route(p, l, score=ep.SCORE_SOFTMAX)
+    want = torch.sort(l.float(), dim=1, descending=True, stable=True)
+    assert (idx == want.indices[:, :K].numpy()).all() and err == 0
+    ww = torch.softmax(want.values[:, :K].double(), 1).numpy()
+    assert (np.abs(w - ww) <= 80 * 2.0 ** -23 * ww).all()
+    dw = torch.randn((n, K), generator=gen)
+    got = torch.full((n, E), NAN, dtype=torch.bfloat16, device=DEV)
+    ep.route_backward(p, l.to(DEV), torch.from_numpy(idx).to(DEV), dw.to(DEV), got)
+    d = ww * (dw.double().numpy() - (ww * dw.double().numpy()).sum(1, keepdims=True))
+    full = np.zeros((n, E))
+    np.put_along_axis(full, idx.astype(np.int64), d, 1)
+    lim = HALF * np.abs(full) + 200 * 2.0 ** -23 * np.abs(dw.double().numpy()).sum(1)[:, None]
+    assert (np.abs(got.cpu().double().numpy() - full) <= lim).all()
+
+
+def test_replayed_in_a_graph_on_another_stream():
+    """Both passes captured together and replayed with fresh logits."""
+    R, T, E, K = 2, 150, 64, 4
+    p = ep.Problem(R, T, 128, E, K)
+    gen = torch.Generator().manual_seed(50)
+    n = R * T
+    l, dw = torch.empty((n, E), device=DEV), torch.empty((n, K), device=DEV)
+    idx, w = torch.empty((n, K), dtype=torch.int32, device=DEV), torch.empty((n, K), device=DEV)
+    dl, err = torch.empty_like(l), torch.zeros(1, dtype=torch.int32, device=DEV)
+    bias = torch.randn(E, generator=gen).to(DEV) * 0.1
+    kw = dict(score=ep.SCORE_SIGMOID, scale=2.0)
+
+    def step():
+        ep.route(p, l, idx, w, err, bias=bias, groups=8, groups_kept=3, group_top=2, **kw)
+        ep.route_backward(p, l, idx, dw, dl, err, **kw)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        l.copy_(torch.randn((n, E), generator=gen))
+        dw.zero_()
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for _ in range(4):
+        l.copy_(torch.randn((n, E), generator=gen))
+        dw.copy_(torch.randn((n, K), generator=gen))
+        step()
+        torch.cuda.synchronize()
+        want = [v.clone() for v in (idx, w, dl)]
+        for v in (idx, w, dl):
+            v.fill_(-3)
+        graph.replay()
+        torch.cuda.synchronize()
+        for v, x in zip((idx, w, dl), want):
+            assert torch.equal(v, x)
+
+
+@pytest.mark.parametrize("mode", [ep.MODE_NORMAL, ep.MODE_LOW_LATENCY])
+def test_a_training_step_from_logits_and_back(mode):
+    """route -> layout -> dispatch -> experts -> combine, and combine_backward ->
+    route_backward: the logits' gradient against autograd in 64 bits through the same choice.
+    dweights carries two bf16 roundings of y (its products' inputs and itself), each at most
+    half a step and over many values at most sqrt(1/3) of that in the 2-norm; the gradient
+    passes them on through w (1 - w)-like factors below one, doubled."""
+    R, T, E, K, H, I = 2, 80, 16, 4, 128, 64
+    n = R * T
+    gen = torch.Generator().manual_seed(51)
+    bf = lambda *s, k=1.0: (torch.randn(s, generator=gen) * k).to(torch.bfloat16)  # noqa: E731
+    x, dout = bf(n, H), bf(n, H)
+    w1, w2 = bf(E, 2 * I, H, k=H ** -0.5), bf(E, H, I, k=I ** -0.5)
+    l = torch.randn((n, E), generator=gen)
+    p = ep.Problem(R, T, H, E, K, mode=mode)
+    cap = ep.max_recv_rows(p)
+    i32, f32 = dict(dtype=torch.int32, device=DEV), dict(device=DEV)
+    idx, wt, err = torch.empty((n, K), **i32), torch.empty((n, K), **f32), torch.zeros(1, **i32)
+    kw = dict(score=ep.SCORE_SOFTMAX, normalize=True, scale=1.0)
+    lg, xg, dg, w1g, w2g = (v.to(DEV) for v in (l, x, dout, w1, w2))
+    ep.route(p, lg, idx, wt, err, **kw)
+    lay, ws = ep.Layout(p), ep.workspace(p)
+    ep.get_layout(p, idx, lay, ws)
+    recv = ep.Recv(p, cap)
+    ep.dispatch(p, lay, xg, recv=recv, ws=ws)
+    b = dict(dtype=torch.bfloat16, device=DEV)
+    h, y, out = torch.empty((cap, I), **b), torch.empty((cap, H), **b), torch.empty((n, H), **b)
+    ep.expert_gated(p, lay, recv.x, w1g, h)
+    ep.expert_linear(p, lay, h, w2g, y)
+    ep.combine(p, lay, y, wt, out)
+    dwt, dl = torch.empty((n, K), **f32), torch.empty((n, E), **f32)
+    ep.combine_backward(p, lay, dg, wt, y, dweights=dwt)
+    ep.route_backward(p, lg, idx, dwt, dl, err, **kw)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and int(lay.err.item()) == 0
+
+    ids = idx.cpu().long()
+    assert torch.equal(ids, torch.sort(l, dim=1, descending=True, stable=True).indices[:, :K])
+    leaf = l.double().requires_grad_()
+    weights = torch.softmax(leaf.gather(1, ids), 1)
+    x64 = x.double()
+    ref = torch.zeros((n, H), dtype=torch.float64)
+    for e in range(E):
+        t, k = torch.nonzero(ids == e, as_tuple=True)
+        z = x64[t] @ w1[e].double().t()
+        o = (torch.nn.functional.silu(z[:, :I]) * z[:, I:]) @ w2[e].double().t()
+        ref = ref.index_add(0, t, o * weights[t, k][:, None])
+    ref.backward(dout.double())
+    d = dl.cpu().double() - leaf.grad
+    assert float(d.norm() / leaf.grad.norm()) <= 2 * (2 / 3) ** 0.5 * HALF * 2
