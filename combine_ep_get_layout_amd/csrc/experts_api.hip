@@ -1,11 +1,12 @@
-// C ABI of the experts' products and of combine's gradient: argument
-// validation and launches.  Declarations and semantics: include/ep.h.
+// C ABI of the experts' products, of combine's gradient and of the layer for a few
+// tokens: argument validation and launches.  Declarations and semantics: include/ep.h.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <string.h>
 
 #include "../../include/ep.h"
 #include "ep_internal.hpp"
+#include "layer.hpp"
 
 using ep::Geometry;
 using ep::Segments;
@@ -179,6 +180,17 @@ int backward(const ep_problem* p, const ep_layout* layout, const ep_rows* x, con
   return EP_OK;
 }
 
+// The layer's sizes.
+int layer_ok(const Geometry& g, int inner) {
+  if (!channels_ok(inner)) return EP_ERR_SHAPE;
+  return (int64_t)g.R * g.T * g.K > EP_LAYER_MAX_ENTRIES ? EP_ERR_SHAPE : EP_OK;
+}
+
+size_t layer_bytes(const Geometry& g, int inner) {  // h
+  const size_t bytes = (size_t)g.R * g.T * g.K * inner * 2;
+  return bytes < 256 ? 256 : (bytes + 255) & ~(size_t)255;
+}
+
 }  // namespace
 
 extern "C" {
@@ -260,6 +272,64 @@ int ep_combine_backward(const ep_problem* p, const ep_layout* layout, const uint
   a.dw = dweights;
   a.err = layout->err;
   if (ep::launch_combine_grad(a, (hipStream_t)stream) != hipSuccess) return EP_ERR_HIP;
+  return EP_OK;
+}
+
+size_t ep_expert_layer_workspace_bytes(const ep_problem* p, int32_t inner) {
+  Geometry g;
+  if (ep::make_geometry(p, &g) != EP_OK || layer_ok(g, inner) != EP_OK) return 0;
+  return layer_bytes(g, inner);
+}
+
+int ep_expert_layer(const ep_problem* p, const uint16_t* x, const int32_t* topk_idx,
+                    const float* topk_weights, const ep_weights* w13, int32_t act,
+                    const ep_weights* w2, uint16_t* out, int32_t* err, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  Geometry g;
+  EP_TRY(ep::make_geometry(p, &g));
+  EP_TRY(act_ok(act));
+  EP_TRY(weights_ok(w13));
+  EP_TRY(weights_ok(w2));
+  const int H = g.H, I = w2->in_channels, kind = w13->fp8;
+  EP_TRY(layer_ok(g, I));
+  if (w13->in_channels != H || w2->out_channels != H || w13->out_channels != 2 * I)
+    return EP_ERR_SHAPE;
+  if (w2->fp8 != kind || w13->bias || w2->bias) return EP_ERR_MODE;
+  const int step = kind == EP_WEIGHTS_FP8 ? 128 : kind == EP_WEIGHTS_INT8 ? 16 : 8;
+  if (H % step != 0 || I % step != 0) return EP_ERR_SHAPE;
+  const bool toks = (int64_t)g.R * g.T > 0;
+  if (!w13->w || !w2->w || (kind != EP_WEIGHTS_BF16 && (!w13->scales || !w2->scales)))
+    return EP_ERR_NULL;
+  if (toks && (!x || !topk_idx || !topk_weights || !out || !workspace)) return EP_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(out, 16) || !aligned(w13->w, 16) || !aligned(w2->w, 16) ||
+      !aligned(workspace, 16) || !aligned(topk_idx, 4) || !aligned(topk_weights, 4) ||
+      !aligned(err, 4))
+    return EP_ERR_ALIGN;
+  const int scales = kind == EP_WEIGHTS_INT8 ? 16 : 4;
+  if (kind != EP_WEIGHTS_BF16 && (!aligned(w13->scales, scales) || !aligned(w2->scales, scales)))
+    return EP_ERR_ALIGN;
+  if (toks && workspace_bytes < layer_bytes(g, I)) return EP_ERR_WORKSPACE;
+  ep::LayerArgs a;
+  memset(&a, 0, sizeof(a));
+  a.tokens = g.R * g.T;
+  a.K = g.K;
+  a.entries = a.tokens * g.K;
+  a.E = g.E;
+  a.H = H;
+  a.I = I;
+  a.kind = kind;
+  a.act = act;
+  a.x = x;
+  a.idx = topk_idx;
+  a.weights = topk_weights;
+  a.w13 = (const char*)w13->w;
+  a.s13 = w13->scales;
+  a.w2 = (const char*)w2->w;
+  a.s2 = w2->scales;
+  a.h = (uint16_t*)workspace;
+  a.out = out;
+  a.err = err;
+  if (ep::launch_layer(a, (hipStream_t)stream) != hipSuccess) return EP_ERR_HIP;
   return EP_OK;
 }
 

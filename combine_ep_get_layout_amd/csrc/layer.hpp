@@ -1,0 +1,29 @@
+// Arguments of the layer for a few tokens.
+#pragma once
+
+#include "ep_device.hpp"
+
+namespace ep {
+
+constexpr int kLayerEntries = EP_LAYER_MAX_ENTRIES;
+
+struct LayerArgs {
+  int tokens, K, entries, E;
+  int H, I;                // channels of x and out; of h
+  int kind, act;           // EP_WEIGHTS_*, EP_ACT_*
+  int slots;               // places for an entry's result in a workgroup's LDS
+  const uint16_t* x;       // [tokens][H]
+  const int32_t* idx;      // [tokens][K]
+  const float* weights;    // [tokens][K]
+  const char* w13;         // [E][2 I][H]
+  const float* s13;
+  const char* w2;          // [E][H][I]
+  const float* s2;
+  uint16_t* h;             // workspace: [entries][I]
+  uint16_t* out;           // [tokens][H]
+  int32_t* err;
+};
+
+hipError_t launch_layer(LayerArgs a, hipStream_t stream);
+
+}  // namespace ep

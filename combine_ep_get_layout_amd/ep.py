@@ -29,9 +29,10 @@ EXPORTS = ["ep_workspace_bytes", "ep_max_recv_rows", "ep_messages_capacity", "ep
            "ep_dispatch", "ep_dispatch_fused", "ep_dispatch_fused_noalloc", "ep_combine",
            "ep_expert_gated", "ep_expert_linear", "ep_expert_gated_backward",
            "ep_expert_linear_backward", "ep_combine_backward", "ep_quantize_rows",
-           "ep_route", "ep_route_backward",
+           "ep_route", "ep_route_backward", "ep_expert_layer", "ep_expert_layer_workspace_bytes",
            "ep_messages_execute", "ep_messages_unpack", "ep_status_string"]
 NOALLOC_SCRATCH_BYTES = 64 << 20  # EP_NOALLOC_SCRATCH_BYTES
+LAYER_MAX_ENTRIES = 1024  # EP_LAYER_MAX_ENTRIES
 ERR_SCRATCH = -8
 
 
@@ -139,6 +140,11 @@ def lib() -> ctypes.CDLL:
         l.ep_route.restype = ctypes.c_int
         l.ep_route_backward.argtypes = [P, OP, _vp, _vp, _vp, _vp, _vp, _vp]
         l.ep_route_backward.restype = ctypes.c_int
+        l.ep_expert_layer_workspace_bytes.argtypes = [P, i32]
+        l.ep_expert_layer_workspace_bytes.restype = ctypes.c_size_t
+        l.ep_expert_layer.argtypes = [P, _vp, _vp, _vp, WP, i32, WP, _vp, _vp, _vp,
+                                      ctypes.c_size_t, _vp]
+        l.ep_expert_layer.restype = ctypes.c_int
         l.ep_combine_backward.argtypes = [P, LP, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp, _vp]
         l.ep_combine_backward.restype = ctypes.c_int
         l.ep_messages_execute.argtypes = [P, ctypes.POINTER(CMessages), _vp, ctypes.c_int64,
@@ -775,6 +781,55 @@ def _combine_backward_args(p: Problem, layout: Layout, dout: torch.Tensor,
                                          _ptr(dweights)), (pc, cl))
 
 
+# ---- the whole layer, for a few tokens ----
+
+def layer_workspace(p: Problem, inner: int, device="cuda") -> torch.Tensor:
+    """Scratch memory of expert_layer with `inner` channels between its two products."""
+    n = int(lib().ep_expert_layer_workspace_bytes(ctypes.byref(p.c()), int(inner)))
+    if n == 0:
+        raise EPError(-3, "workspace size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def expert_layer(p: Problem, x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
+                 w13: torch.Tensor, w2: torch.Tensor, out: torch.Tensor,
+                 err: torch.Tensor | None, ws: torch.Tensor, *, act: int = ACT_SILU,
+                 w13_scales: torch.Tensor | None = None, w2_scales: torch.Tensor | None = None,
+                 stream=None) -> None:
+    """An MoE layer for a few tokens (R*T*K <= LAYER_MAX_ENTRIES) in two launches, without
+    layout or dispatch: out = sum_k topk_weights * (act(x Wg^T) * (x Wu^T)) W2^T.
+    x and out [R][T][H] bf16, topk_idx [R][T][K] int32 (-1: none), topk_weights [R][T][K]
+    fp32, w13 [E][2 I][H] (gates first), w2 [E][H][I]: bf16, FP8 codes (scales per 128 x 128
+    block) or int8 (scales [E][2 I] and [E][H]).  Error bits are OR-ed into err[0]."""
+    _invoke(_expert_layer_args(p, x, topk_idx, topk_weights, w13, w2, out, err, ws, act=act,
+                               w13_scales=w13_scales, w2_scales=w2_scales), stream)
+
+
+def _expert_layer_args(p: Problem, x: torch.Tensor, topk_idx: torch.Tensor,
+                       topk_weights: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor,
+                       out: torch.Tensor, err: torch.Tensor | None, ws: torch.Tensor, *,
+                       act: int = ACT_SILU, w13_scales: torch.Tensor | None = None,
+                       w2_scales: torch.Tensor | None = None) -> _Args:
+    n = p.R * p.T
+    _same_device(x, topk_idx, topk_weights, w13, w13_scales, w2, w2_scales, out, err, ws)
+    for t, name in (x, "x"), (out, "out"):
+        _need(t.dtype == torch.bfloat16 and t.numel() == n * p.H, f"{name} [R][T][H] bf16")
+    _need(topk_idx.dtype == torch.int32 and topk_idx.numel() == n * p.K, "topk_idx [R][T][K] int32")
+    _need(topk_weights.dtype == torch.float32 and topk_weights.numel() == n * p.K,
+          "topk_weights [R][T][K] fp32")
+    _need(err is None or (err.dtype == torch.int32 and err.numel() >= 1), "err int32")
+    of = [_int8_weights(p, w, s) if w.dtype == torch.int8 else _weights(p, w, s)
+          for w, s in ((w13, w13_scales), (w2, w2_scales))]
+    _need(w13.shape[2] == p.H and w2.shape[1] == p.H and w13.shape[1] == 2 * w2.shape[2],
+          "w13 [E][2 I][H], w2 [E][H][I]")
+    _need(ws.dtype == torch.uint8, "ws bytes")
+    pc = p.c()
+    return _Args("ep_expert_layer",
+                 (ctypes.byref(pc), _ptr(x), _ptr(topk_idx), _ptr(topk_weights),
+                  ctypes.byref(of[0]), int(act), ctypes.byref(of[1]), _ptr(out), _ptr(err),
+                  _ptr(ws), ws.numel()), (pc, *of))
+
+
 # ---- the router ----
 
 def _router(p: Problem, logits: torch.Tensor, score: int, normalize: bool, scale: float,
@@ -922,7 +977,8 @@ _ARGS = {get_layout: _get_layout_args, dispatch: _dispatch_args,
          expert_linear: _expert_linear_args, expert_gated_backward: _expert_gated_backward_args,
          expert_linear_backward: _expert_linear_backward_args,
          combine_backward: _combine_backward_args, quantize_rows: _quantize_rows_args,
-         route: _route_args, route_backward: _route_backward_args}
+         route: _route_args, route_backward: _route_backward_args,
+         expert_layer: _expert_layer_args}
 
 
 def messages_sizes(p: Problem, counts=None) -> tuple[int, int, int]:

@@ -418,6 +418,33 @@ int ep_combine_backward(const ep_problem* p, const ep_layout* layout, const uint
                         const float* topk_weights, const uint16_t* y, int64_t y_rows,
                         uint16_t* dy, float* dweights, void* stream);
 
+/* ---- The whole layer, for a few tokens ------------------------------------ */
+
+/* Most entries (R*T*K) of ep_expert_layer. */
+#define EP_LAYER_MAX_ENTRIES 1024
+
+/* Bytes of scratch device memory ep_expert_layer needs for inner channels I (0 on invalid
+ * input).  Any 256-byte aligned buffer of this size; its contents need not be initialised
+ * and are dead after the stream reaches the end of the call.  Calls whose work may overlap,
+ * and graphs that may be replayed at once, need one each. */
+size_t ep_expert_layer_workspace_bytes(const ep_problem* p, int32_t inner);
+
+/* An MoE layer from routing to weighted sum, in two launches, without layout, dispatch
+ * or combine: what decoding a few tokens takes, whose time is reading the weights.
+ *   h[t][k] = act(x_t Wg_e^T) * (x_t Wu_e^T),   e = topk_idx[t][k], rounded to bf16
+ *   out_t = bf16( sum_k topk_weights[t][k] * (h[t][k] W2_e^T) )
+ * sums in fp32, over k in order; every token of every rank meets every expert.  An entry of
+ * -1 has no part in it (whatever its weight); an id outside [-1, E) is skipped and sets
+ * EP_DEVERR_TOPK_RANGE.  A token without entries gets 0.
+ * x, out: [R][T][H] bf16, not overlapping.  w13: [E][2 I][H], the gates first, w2:
+ * [E][H][I], as for ep_expert_gated and ep_expert_linear, both of one type (bf16, FP8 or
+ * 8-bit integers; the rows stay bf16), without bias.  err: [1], bits are OR-ed into it, or
+ * NULL.  R*T*K <= EP_LAYER_MAX_ENTRIES.  p->mode and p->quant are not used. */
+int ep_expert_layer(const ep_problem* p, const uint16_t* x, const int32_t* topk_idx,
+                    const float* topk_weights, const ep_weights* w13, int32_t act,
+                    const ep_weights* w2, uint16_t* out, int32_t* err, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
 /* ---- The router: where topk_idx and topk_weights come from ---------------- */
 
 typedef struct ep_router {
