@@ -186,9 +186,16 @@ int layer_ok(const Geometry& g, int inner) {
   return (int64_t)g.R * g.T * g.K > EP_LAYER_MAX_ENTRIES ? EP_ERR_SHAPE : EP_OK;
 }
 
-size_t layer_bytes(const Geometry& g, int inner) {  // h
-  const size_t bytes = (size_t)g.R * g.T * g.K * inner * 2;
-  return bytes < 256 ? 256 : (bytes + 255) & ~(size_t)255;
+// The layer's workspace: h, and the entries' results where they do not fit the LDS.
+size_t layer_h_bytes(const Geometry& g, int inner) {
+  return ((size_t)g.R * g.T * g.K * inner * 2 + 255) & ~(size_t)255;
+}
+
+size_t layer_bytes(const Geometry& g, int inner) {
+  const size_t entries = (size_t)g.R * g.T * g.K, row = (size_t)(g.H + 15) / 16 * 16;
+  const size_t bytes = layer_h_bytes(g, inner) +
+                       (entries > ep::kLayerPlaces ? entries * row * sizeof(float) : 0);
+  return bytes < 256 ? 256 : bytes;
 }
 
 }  // namespace
@@ -327,6 +334,7 @@ int ep_expert_layer(const ep_problem* p, const uint16_t* x, const int32_t* topk_
   a.w2 = (const char*)w2->w;
   a.s2 = w2->scales;
   a.h = (uint16_t*)workspace;
+  a.y = (float*)((char*)workspace + layer_h_bytes(g, I));
   a.out = out;
   a.err = err;
   if (ep::launch_layer(a, (hipStream_t)stream) != hipSuccess) return EP_ERR_HIP;

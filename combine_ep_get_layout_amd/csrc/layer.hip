@@ -3,11 +3,14 @@
 //   h = act(x Wg_e^T) * (x Wu_e^T),  rounded to bf16,        (layer_gated)
 //   out_t = sum_k w_k h W2_e^T,      in fp32, in k order.    (layer_down)
 //
-// With few tokens the time is that of reading the weights of the experts that are hit, so
-// each is read once, straight into the registers of the matrix instructions (16 rows of
-// weights x 64 bytes a load), while the tokens' rows come from the cache.  Rows stay bf16
-// whatever the weights' type: e4m3 and 8-bit codes are converted (both fit bf16 exactly),
-// and their scales are applied to the fp32 sums.
+// With few tokens the time is that of reading the weights of the experts that are hit.  A
+// wave multiplies 16 rows of weights (a strip) with up to 16 rows of one expert's entries.
+// It streams both through a ring of its own in LDS, by asynchronous loads that never stop:
+// towards the end of a strip they are the next one's.  Weights come as whole 128-byte lines of
+// eight rows a load: straight into the registers of the matrix instructions, which take 16
+// rows x 64 bytes, they came at 4.1 TB/s instead.  Rows stay bf16 whatever the weights' type:
+// e4m3 and 8-bit codes are converted (both fit bf16 exactly), and their scales are applied to
+// the fp32 sums.
 #include <algorithm>
 
 #include "experts.hpp"
@@ -15,9 +18,7 @@
 
 namespace ep {
 
-constexpr int kUpWaves = 4;    // of a workgroup of layer_gated, which share a contraction
-constexpr int kDownWaves = 8;  // of a workgroup of layer_down, an expert each
-constexpr int kTileRows = 64;  // entries of an expert that are multiplied at once
+constexpr int kMost = 16;  // entries of an expert that are multiplied at once, at most
 
 // ---- who is hit ------------------------------------------------------------------
 
@@ -69,41 +70,101 @@ struct Hits {
   }
 };
 
-// Expert e's entries (t * K + k) in their order; a wave's own list.
-__device__ __forceinline__ int entries_of(const LayerArgs& a, const Routing& r, int e,
-                                          uint16_t* list) {
+// Expert e's entries (t * K + k), in their order: how many, and from the at-th on up to `room`
+// of them to `list`, the wave's own.
+__device__ __forceinline__ int entries_of(const LayerArgs& a, const Routing& r, int e, int at,
+                                          int room, uint16_t* list) {
   const int lane = lane_id();
   int n = 0;
   for (int c = 0; c < a.entries; c += kWave) {
     const bool is = r.ids[c + lane] == e;
     const uint64_t mask = __ballot(is);
-    if (is) list[n + rank_below(mask)] = (uint16_t)(c + lane);
+    const int place = n + rank_below(mask) - at;
+    if (is && place >= 0 && place < room) list[place] = (uint16_t)(c + lane);
     n += __popcll(mask);
   }
   wave_lds_sync();
   return n;
 }
 
-// ---- 16 rows of weights times up to 64 rows --------------------------------------------
+// ---- a stream of lines -----------------------------------------------------------------
 
-// A line is 128 bytes of a row of weights: two loads of 16 bytes a lane, lane l taking row
-// l % 16 and bytes 16 (l / 16) of either half.  The products follow from that: in bf16 a load
-// is one step of 32 channels, in 8 bits two, of each lane's first and last eight codes.
-template <int KIND, int TT>
-struct Strip {
+// What a wave multiplies next: up to a slot's room of an expert's entries, from the at-th
+// on, with one strip.
+struct Unit {
+  int e, strip, at, rows, n;  // n: the expert's entries in all
+  uint16_t* list;             // the unit's
+};
+
+// A line is 128 bytes of each of a strip's 16 rows of weights and the channels that these
+// multiply of the rows, which is 128 bytes of each in bf16 and 256 where the weights have 8
+// bits.  A slot of the ring holds one: two loads (2 KiB) of weights and NB of rows.  In LDS
+// chunk c (16 bytes) of row r stands at c ^ turn(r), so that 16 lanes' reads of one chunk of
+// 16 rows fall into different banks.
+template <int KIND, int NB, int D>
+struct Stream {
   static constexpr bool kBytes = KIND != EP_WEIGHTS_BF16;
-  // lines in flight: as many as leave the registers for 16 waves on a compute unit
-  static constexpr int U = TT == 1 ? (kBytes ? 2 : 4) : TT == 2 ? (kBytes ? 1 : 2) : 1;
-  static constexpr int kRowLoads = kBytes ? 4 : 2;  // of a line, for a lane's row
+  static constexpr int kSize = kBytes ? 1 : 2;
+  static constexpr int kChunks = kBytes ? 16 : 8;           // of a row in a line
+  static constexpr int kRows = NB * kWave / kChunks;        // that a slot has room for
+  static constexpr int kSlot = (2 + NB) * 1024;
+  static constexpr int kLoads = 2 + NB;
+  static constexpr int kSteps = kBytes ? 4 : 2;             // matrix steps of a line
+  static_assert(kRows <= kMost, "");
 
-  const char* w;           // the lane's row of weights, at its 16 bytes
-  const char* x[TT];       // the lane's rows, likewise
-  const float* scale;      // FP8: the lane's row's blocks along the contraction
-  f32x4 acc[TT];
+  lds_char* ring;
+  int lines, left;         // of a row of weights, and the last one's bytes
+  const char *w, *x;       // of the unit that is loaded: uniform, with the lanes' offsets
+  uint32_t w_off[2], x_off[NB];
+  f32x4 acc;
 
-  __device__ __forceinline__ void clear() {
+  __device__ __forceinline__ Stream(lds_char* r, int channels)
+      : ring(r), lines((channels * kSize + 127) / 128),
+        left(channels * kSize - (lines - 1) * 128) {}
+
+  static __device__ __forceinline__ int w_turn(int r) { return r / 2 & 7; }
+  static __device__ __forceinline__ int x_turn(int r) { return kBytes ? r : r / 2 & 7; }
+
+  // row(r): byte offset from w of the strip's row r; entry(r): from x of the unit's row r
+  template <class Row, class Entry>
+  __device__ __forceinline__ void point(const char* w_, const char* x_, Row row, Entry entry) {
+    const int lane = lane_id();
+    w = w_;
+    x = x_;
 #pragma unroll
-    for (int j = 0; j < TT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < 2; ++i) {
+      const int r = 8 * i + lane / 8;
+      w_off[i] = row(r) + ((lane % 8 ^ w_turn(r)) << 4);
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int r = i * (kWave / kChunks) + lane / kChunks;
+      x_off[i] = entry(r) + ((lane % kChunks ^ x_turn(r)) << 4);
+    }
+  }
+  __device__ __forceinline__ void load(int line, int slot) const {
+    lds_char* to = ring + slot * kSlot;
+    const char* wl = w + (int64_t)line * 128;
+    const char* xl = x + (int64_t)line * (16 * kChunks);
+    if (KIND == EP_WEIGHTS_FP8 || line < lines - 1 || left == 128) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) load_lds16(wl, w_off[i], to + 1024 * i);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) load_lds16(xl, x_off[i], to + 2048 + 1024 * i);
+    } else {  // chunks past the end are zeros on both sides
+      const int lane = lane_id(), chunks = left / 16 * (kBytes ? 2 : 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool in = (lane % 8 ^ w_turn(8 * i + lane / 8)) * 16 < left;
+        load_lds16(in ? wl + w_off[i] : (const char*)k_zeros, to + 1024 * i);
+      }
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const int r = i * (kWave / kChunks) + lane / kChunks;
+        const bool in = (lane % kChunks ^ x_turn(r)) < chunks;
+        load_lds16(in ? xl + x_off[i] : (const char*)k_zeros, to + 2048 + 1024 * i);
+      }
+    }
   }
 
   static __device__ __forceinline__ bf16x8 codes(uint32_t lo, uint32_t hi) {
@@ -128,259 +189,336 @@ struct Strip {
     return u.v;
   }
 
-  struct Weights {
-    u32x4 v[2];
-    float s;
-  };
-  struct Rows {
-    u32x4 v[TT][kRowLoads];
-  };
-
-  __device__ __forceinline__ void load(int line, Weights& to) const {
+  // Lane l holds row l % 16 of both operands.  In bf16 a step is 32 channels, in 8 bits a
+  // lane's 16 codes are two steps, the first eight of every lane and the last.
+  // scale: FP8, of this line's 128 channels
+  __device__ __forceinline__ void multiply(int slot, float scale) {
+    const lds_char* from = ring + slot * kSlot;
+    const int lane = lane_id(), r = lane % 16, q = lane / 16;
+    // rows past the slot's room repeat its last one; their columns are not used
+    const int xr = kRows < 16 ? min(r, kRows - 1) : r;
+    i32x4 wv[2];
+    bf16x8 xv[kSteps];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      to.v[i] = __builtin_nontemporal_load((const u32x4*)(w + (int64_t)line * 128 + 64 * i));
-    if (KIND == EP_WEIGHTS_FP8) to.s = scale[line];
-  }
-  __device__ __forceinline__ void load(int line, Rows& to) const {
+      wv[i] = *(const EP_LDS i32x4*)(from + r * 128 + ((q + 4 * i ^ w_turn(r)) << 4));
 #pragma unroll
-    for (int j = 0; j < TT; ++j)
-#pragma unroll
-      for (int i = 0; i < kRowLoads; ++i)
-        to.v[j][i] = *(const u32x4*)(x[j] + (int64_t)line * (kBytes ? 256 : 128) +
-                                     (kBytes ? 128 * (i / 2) + 16 * (i % 2) : 64 * i));
-  }
-  __device__ __forceinline__ void multiply(const Weights& a, const Rows& b) {
-    bf16x8 f[kRowLoads];
-#pragma unroll
-    for (int i = 0; i < kRowLoads; ++i) {
-      if constexpr (kBytes) f[i] = codes(a.v[i / 2][2 * (i % 2)], a.v[i / 2][2 * (i % 2) + 1]);
-      else f[i] = __builtin_bit_cast(bf16x8, a.v[i]);
+    for (int i = 0; i < kSteps; ++i) {
+      const int c = kBytes ? 8 * (i / 2) + 2 * q + i % 2 : q + 4 * i;
+      xv[i] = __builtin_bit_cast(bf16x8, *(const EP_LDS i32x4*)(from + 2048 + xr * 16 * kChunks +
+                                                                ((c ^ x_turn(xr)) << 4)));
     }
+    f32x4 sum = KIND == EP_WEIGHTS_FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc;
 #pragma unroll
-    for (int j = 0; j < TT; ++j) {
-      f32x4 sum = KIND == EP_WEIGHTS_FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[j];
+    for (int i = 0; i < kSteps; ++i) {
+      bf16x8 f;
+      if constexpr (kBytes)
+        f = codes((uint32_t)wv[i / 2][2 * (i % 2)], (uint32_t)wv[i / 2][2 * (i % 2) + 1]);
+      else
+        f = __builtin_bit_cast(bf16x8, wv[i]);
+      sum = Mfma<16>::bf16(f, xv[i], sum);
+    }
+    if (KIND == EP_WEIGHTS_FP8) {
 #pragma unroll
-      for (int i = 0; i < kRowLoads; ++i)
-        sum = Mfma<16>::bf16(f[i], __builtin_bit_cast(bf16x8, b.v[j][i]), sum);
-      if (KIND == EP_WEIGHTS_FP8) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[j][q] = __builtin_fmaf(sum[q], a.s, acc[j][q]);
-      } else {
-        acc[j] = sum;
-      }
+      for (int q4 = 0; q4 < 4; ++q4) acc[q4] = __builtin_fmaf(sum[q4], scale, acc[q4]);
+    } else {
+      acc = sum;
     }
   }
 
-  // Lines first, first + step, .. of a row of `bytes` bytes.  The next U lines of weights are
-  // on their way while these are multiplied; the rows' loads come out of the cache, and are
-  // issued before those so that waiting for them waits for nothing else.
-  __device__ __forceinline__ void run(int bytes, int first, int step) {
-    const int lines = bytes / 128;
-    const int n = first < lines ? (lines - first + step - 1) / step : 0;
-    const int last = first + (n - 1) * step;
-    if (n > 0) {
-      Weights now[U];
-      Rows rows[U];
+  // Unit after unit; of each the lines part, part + parts, ..
+  //   next(unit): the wave's next unit, false after the last
+  //   aim(unit): calls point()
+  //   scales(unit, line): FP8, the line's scale
+  //   done(unit): takes acc
+  template <class Next, class Aim, class Scales, class Done>
+  __device__ __forceinline__ void run(int part, int parts, Next next, Aim aim, Scales scales,
+                                      Done done) {
+    const int n = part < lines ? (lines - part + parts - 1) / parts : 0;
+    Unit now, then;
+    if (!next(now)) return;
+    aim(now);
+    const bool chain = n >= D - 1;
+    int slot = 0;
+    auto after = [](int s) { return s + 1 == D ? 0 : s + 1; };
+    bool fresh = true;
+    for (;;) {
+      if (fresh) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) load(min(first + i * step, last), now[i]);
-      int at = first;
-      for (int done = U; done < n; done += U, at += U * step) {
-        Weights next[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) load(at + i * step, rows[i]);
-#pragma unroll
-        for (int i = 0; i < U; ++i) load(min(at + (U + i) * step, last), next[i]);
-#pragma unroll
-        for (int i = 0; i < U; ++i) multiply(now[i], rows[i]);
-#pragma unroll
-        for (int i = 0; i < U; ++i) now[i] = next[i];
+        for (int i = 0; i < D - 1; ++i)
+          if (i < n) load(part + i * parts, i);
+        slot = 0;
       }
-#pragma unroll
-      for (int i = 0; i < U; ++i) load(min(at + i * step, last), rows[i]);
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (at + i * step <= last) multiply(now[i], rows[i]);
-    }
-    // less than a line is left (never in FP8): chunks past the end are zeros on both sides
-    if (KIND != EP_WEIGHTS_FP8 && bytes % 128 != 0 && lines % step == first % step) {
-      Weights a;
-      Rows b;
-      const u32x4 zero = {0u, 0u, 0u, 0u};
-      const int left = bytes % 128 - 16 * (lane_id() / 16);
-      a.s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        a.v[i] = 64 * i < left ? *(const u32x4*)(w + (int64_t)lines * 128 + 64 * i) : zero;
-#pragma unroll
-      for (int j = 0; j < TT; ++j)
-#pragma unroll
-        for (int i = 0; i < kRowLoads; ++i)
-          b.v[j][i] = 64 * (kBytes ? i / 2 : i) < left
-                          ? *(const u32x4*)(x[j] + (int64_t)lines * (kBytes ? 256 : 128) +
-                                            (kBytes ? 128 * (i / 2) + 16 * (i % 2) : 64 * i))
-                          : zero;
-      multiply(a, b);
+      acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      bool more = false;
+      float scale = scales(now, min(part, lines - 1));
+      for (int i = 0; i < n; ++i) {
+        const int ahead = i + D - 1, into = slot == 0 ? D - 1 : slot - 1;
+        // the line before has been read out of the slot that is loaded
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (ahead < n) {
+          load(part + ahead * parts, into);
+          wait_loads<kLoads*(D - 1)>();
+        } else {
+          if (ahead == n && chain) {
+            more = next(then);
+            if (more) aim(then);
+          }
+          if (more) {
+            load(part + (ahead - n) * parts, into);
+            wait_loads<kLoads*(D - 1)>();
+          } else {
+            wait_loads<0>();
+          }
+        }
+        const float own = scale;  // the next line's is on its way during this one's products
+        scale = scales(now, min(part + (i + 1) * parts, lines - 1));
+        multiply(slot, own);
+        slot = after(slot);
+      }
+      done(now);
+      if (!chain) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        more = next(then);
+        if (more) aim(then);
+      }
+      if (!more) return;
+      now = then;
+      fresh = !chain;
     }
   }
 };
 
-// ---- gated block -------------------------------------------------------------------
-
-// A workgroup's unit: eight channels of one expert, their gates and ups the 16 rows of
-// weights, the contraction's lines dealt to its four waves in turn.
-constexpr int kUpStride = 20;  // floats of a column of partial sums, 16 and a gap
-
-template <int KIND, int TT>
-__device__ __forceinline__ void up_tile(const LayerArgs& a, int e, int n0, const uint16_t* list,
-                                        int rows, float* parts) {
-  const int lane = lane_id(), wave = uniform(threadIdx.x / kWave), row = lane % 16;
-  constexpr int kSize = KIND == EP_WEIGHTS_BF16 ? 2 : 1;
-  Strip<KIND, TT> s;
-  const int channel = row < 8 ? n0 + row : a.I + n0 + row - 8;
-  s.w = a.w13 + ((int64_t)e * 2 * a.I + channel) * a.H * kSize + 16 * (lane / 16);
-#pragma unroll
-  for (int j = 0; j < TT; ++j) {
-    const int token = list[min(16 * j + row, rows - 1)] / a.K;
-    s.x[j] = (const char*)(a.x + (int64_t)token * a.H) + (kSize == 2 ? 16 : 32) * (lane / 16);
-  }
-  // sums are of rows 4 (lane / 16) ..: the first half of the lanes has the gates
-  if (KIND == EP_WEIGHTS_FP8)
-    s.scale = a.s13 + ((int64_t)e * (2 * a.I / 128) + ((lane < 32 ? 0 : a.I) + n0) / 128) * (a.H / 128);
-  s.clear();
-  s.run(a.H * kSize, wave, kUpWaves);
-#pragma unroll
-  for (int j = 0; j < TT; ++j)
-    *(f32x4*)(parts + (wave * kTileRows + 16 * j + row) * kUpStride + 4 * (lane / 16)) = s.acc[j];
-  __syncthreads();
-  for (int o = threadIdx.x; o < TT * 16 * 8; o += kUpWaves * kWave) {
-    const int col = o / 8, ch = o % 8;
-    float g = 0.0f, u = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kUpWaves; ++w) {
-      g += parts[(w * kTileRows + col) * kUpStride + ch];
-      u += parts[(w * kTileRows + col) * kUpStride + 8 + ch];
-    }
-    if (KIND == EP_WEIGHTS_INT8) {
-      const float* scale = a.s13 + (int64_t)e * 2 * a.I + n0 + ch;
-      g *= scale[0];
-      u *= scale[a.I];
-    }
-    float value, slope;
-    act_both(a.act, g, value, slope);
-    if (col < rows) ((__bf16*)a.h)[(int64_t)list[col] * a.I + n0 + ch] = (__bf16)(value * u);
-  }
-  __syncthreads();
+// FP8 scales are the same for the whole wave and do not change: scalar loads, since a vector
+// load would be waited for together with every asynchronous load before it.
+__device__ __forceinline__ float fixed_float(const float* p) {
+  return *(const __attribute__((address_space(4))) float*)p;
 }
 
-template <int KIND>
-__global__ __launch_bounds__(kUpWaves* kWave, 4) void layer_gated(LayerArgs a) {
+// a: v in the lower half of the wave, b: in the upper one, in all lanes
+__device__ __forceinline__ void halves(float v, float& a, float& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                  false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+
+// ---- gated block -------------------------------------------------------------------
+
+constexpr int kUpWaves = 4;    // of a workgroup
+constexpr int kUpStride = 20;  // floats of a column of partial sums, 16 and a gap
+
+// A strip is eight channels of one expert, their gates and ups.  WK waves share a strip, its
+// lines dealt to them in turn; a wave's sums of rows 4 (lane / 16) .. are gates in the lower
+// half of its lanes and ups in the upper one.
+template <int KIND, int NB, int D, int WK>
+__global__ __launch_bounds__(kUpWaves* kWave) void layer_gated(LayerArgs a) {
+  typedef Stream<KIND, NB, D> S;
   __shared__ Routing routing;
-  __shared__ uint16_t lists[kUpWaves][kLayerEntries];
-  __shared__ __align__(16) float parts[kUpWaves * kTileRows * kUpStride];
+  __shared__ uint16_t lists[kUpWaves][2][kMost];
+  __shared__ __align__(16) char rings[kUpWaves][D * S::kSlot];
+  __shared__ __align__(16) float parts[WK > 1 ? WK * kMost * kUpStride : 1];
   read_routing<kUpWaves * kWave>(a, routing);
   const Hits hits(routing);
-  const int tiles = a.I / 8, units = hits.total * tiles;
-  uint16_t* list = lists[uniform(threadIdx.x / kWave)];
-  int held = -1, n = 0;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int e = hits.expert(u / tiles), n0 = u % tiles * 8;
-    if (e != held) n = entries_of(a, routing, e, list);
-    held = e;
-    for (int at = 0; at < n; at += kTileRows) {
-      const int rows = min(n - at, kTileRows);
-      if (rows <= 16) up_tile<KIND, 1>(a, e, n0, list + at, rows, parts);
-      else if (rows <= 32) up_tile<KIND, 2>(a, e, n0, list + at, rows, parts);
-      else up_tile<KIND, 4>(a, e, n0, list + at, rows, parts);
-    }
-  }
+  const int wave = uniform(threadIdx.x / kWave), lane = lane_id(), row = lane % 16;
+  const int strips = a.I / 8, units = hits.total * strips;
+  const int64_t w_row = (int64_t)a.H * S::kSize;
+  constexpr int kTeams = kUpWaves / WK;
+  int u = blockIdx.x * kTeams + wave / WK - gridDim.x * kTeams, turn = 0;
+  Unit last;
+  last.n = 0;
+  last.at = last.e = -1;
+  S stream((lds_char*)rings[wave], a.H);
+  stream.run(
+      WK > 1 ? wave % WK : 0, WK,
+      [&](Unit& unit) {
+        const int e = last.e, at = last.at;
+        last.at += S::kRows;  // more entries of the same expert
+        if (e < 0 || last.at >= last.n) {
+          u += gridDim.x * kTeams;
+          if (u >= units) return false;
+          last.e = hits.expert(u / strips);
+          last.strip = u % strips;
+          last.at = 0;
+        }
+        if (last.e != e || last.at != at) {
+          last.list = lists[wave][turn ^= 1];
+          last.n = entries_of(a, routing, last.e, last.at, S::kRows, last.list);
+        }
+        last.rows = min(last.n - last.at, S::kRows);
+        unit = last;
+        return true;
+      },
+      [&](const Unit& unit) {
+        stream.point(
+            a.w13 + ((int64_t)unit.e * 2 * a.I + unit.strip * 8) * w_row, (const char*)a.x,
+            [&](int r) { return (uint32_t)((r < 8 ? r : a.I + r - 8) * w_row); },
+            [&](int r) {
+              return (uint32_t)(unit.list[min(r, unit.rows - 1)] / a.K) * (uint32_t)(a.H * 2);
+            });
+      },
+      [&](const Unit& unit, int line) {
+        if (KIND != EP_WEIGHTS_FP8) return 1.0f;
+        const int64_t groups = a.H / 128;
+        const float* s = a.s13 + ((int64_t)unit.e * (2 * a.I / 128) + unit.strip / 16) * groups + line;
+        const float gate = fixed_float(s), up = fixed_float(s + a.I / 128 * groups);
+        return lane < 32 ? gate : up;
+      },
+      [&](const Unit& unit) {
+        const int ch = 4 * (lane / 16 % 2);
+        const float* scale = a.s13 + (int64_t)unit.e * 2 * a.I + unit.strip * 8;
+        float g[4], up[4];
+        if constexpr (WK > 1) {
+          *(f32x4*)(parts + (wave % WK * kMost + row) * kUpStride + 4 * (lane / 16)) = stream.acc;
+          barrier();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) g[q] = up[q] = 0.0f;
+#pragma unroll
+          for (int w = 0; w < WK; ++w) {
+            const float* from = parts + (w * kMost + row) * kUpStride + ch;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) g[q] += from[q], up[q] += from[8 + q];
+          }
+          barrier();
+          if (wave % WK != 0) return;
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) halves(stream.acc[q], g[q], up[q]);
+        }
+        bf16x2 out[2];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (KIND == EP_WEIGHTS_INT8) {
+            const float g0 = fixed_float(scale + q), g1 = fixed_float(scale + 4 + q);
+            const float u0 = fixed_float(scale + a.I + q), u1 = fixed_float(scale + a.I + 4 + q);
+            g[q] *= ch == 0 ? g0 : g1;
+            up[q] *= ch == 0 ? u0 : u1;
+          }
+          float value, slope;
+          act_both(a.act, g[q], value, slope);
+          out[q / 2][q % 2] = (__bf16)(value * up[q]);
+        }
+        if (lane < 32 && row < unit.rows)
+          *(uint2*)(a.h + (int64_t)unit.list[row] * a.I + unit.strip * 8 + ch) =
+              __builtin_bit_cast(uint2, out);
+      });
 }
 
 // ---- down projection and the weighted sum ---------------------------------------------
 
-template <int KIND, int TT>
-__device__ __forceinline__ void down_tile(const LayerArgs& a, int e, int n0, const uint16_t* list,
-                                          int rows, int part, int parts, float* y) {
-  const int lane = lane_id(), row = lane % 16;
-  constexpr int kSize = KIND == EP_WEIGHTS_BF16 ? 2 : 1;
-  Strip<KIND, TT> s;
-  const int channel = min(n0 + row, a.H - 1);  // past the last one: not stored
-  s.w = a.w2 + ((int64_t)e * a.H + channel) * a.I * kSize + 16 * (lane / 16);
-#pragma unroll
-  for (int j = 0; j < TT; ++j)
-    s.x[j] = (const char*)(a.h + (int64_t)list[min(16 * j + row, rows - 1)] * a.I) +
-             (kSize == 2 ? 16 : 32) * (lane / 16);
-  if (KIND == EP_WEIGHTS_FP8) s.scale = a.s2 + ((int64_t)e * (a.H / 128) + n0 / 128) * (a.I / 128);
-  s.clear();
-  s.run(a.I * kSize, part, parts);
-  f32x4 scale = {1.0f, 1.0f, 1.0f, 1.0f};
-  if (KIND == EP_WEIGHTS_INT8)
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      scale[q] = a.s2[(int64_t)e * a.H + min(n0 + 4 * (lane / 16) + q, a.H - 1)];
-#pragma unroll
-  for (int j = 0; j < TT; ++j)
-    if (16 * j + row < rows)
-      *(f32x4*)(y + list[16 * j + row] * 16 + 4 * (lane / 16)) = s.acc[j] * scale;
-}
-
-// A workgroup has 16 channels of every token: its waves take an expert each in turn (or parts
-// of its contraction, where there are fewer experts than waves) and put every entry's
-// result into its own place in LDS; then they are summed in k order.
-template <int KIND>
-__global__ __launch_bounds__(kDownWaves* kWave, 4) void layer_down(LayerArgs a) {
-  extern __shared__ __align__(16) float y[];  // [parts][entries][16]
+// A workgroup has a strip of 16 channels of every token.  Its waves take an expert each in
+// turn (or parts of the contraction, where there are fewer experts than waves) and put
+// every entry's result into a place of its own, in LDS or in the workspace; then they are
+// summed in k order.
+template <int KIND, int NB, int D, int WAVES, bool IN_LDS>
+__global__ __launch_bounds__(WAVES* kWave) void layer_down(LayerArgs a) {
+  typedef Stream<KIND, NB, D> S;
   __shared__ Routing routing;
-  __shared__ uint16_t lists[kDownWaves][kLayerEntries];
-  read_routing<kDownWaves * kWave>(a, routing);
+  __shared__ uint16_t lists[WAVES][2][kMost];
+  __shared__ __align__(16) char rings[WAVES][D * S::kSlot];
+  __shared__ __align__(16) float places[IN_LDS ? kLayerPlaces * 16 : 1];
+  read_routing<WAVES * kWave>(a, routing);
   const Hits hits(routing);
-  const int n0 = blockIdx.x * 16, wave = uniform(threadIdx.x / kWave);
-  uint16_t* list = lists[wave];
+  const int wave = uniform(threadIdx.x / kWave), lane = lane_id(), row = lane % 16;
+  const int n0 = blockIdx.x * 16;
+  const int64_t w_row = (int64_t)a.I * S::kSize;
   // parts that every expert's contraction is cut into
   int parts = 1;
-  while (2 * parts * hits.total <= kDownWaves && 2 * parts * a.entries <= a.slots) parts *= 2;
-  for (int u = wave; u < hits.total * parts; u += kDownWaves) {
-    const int e = hits.expert(u / parts), part = u % parts;
-    const int n = entries_of(a, routing, e, list);
-    float* to = y + part * a.entries * 16;
-    for (int at = 0; at < n; at += kTileRows) {
-      const int rows = min(n - at, kTileRows);
-      if (rows <= 16) down_tile<KIND, 1>(a, e, n0, list + at, rows, part, parts, to);
-      else if (rows <= 32) down_tile<KIND, 2>(a, e, n0, list + at, rows, part, parts, to);
-      else down_tile<KIND, 4>(a, e, n0, list + at, rows, part, parts, to);
-    }
-  }
+  if (IN_LDS)
+    while (2 * parts * hits.total <= WAVES && 2 * parts * a.entries <= kLayerPlaces) parts *= 2;
+  const int part = wave % parts;
+  float* const y = IN_LDS ? places + part * a.entries * 16 : a.y + n0;
+  const int64_t y_row = IN_LDS ? 16 : (a.H + 15) / 16 * 16;
+  int u = wave / parts - WAVES / parts, turn = 0;
+  Unit last;
+  last.n = 0;
+  last.at = last.e = -1;
+  last.strip = blockIdx.x;
+  S stream((lds_char*)rings[wave], a.I);
+  stream.run(
+      part, parts,
+      [&](Unit& unit) {
+        last.at += S::kRows;
+        if (last.e < 0 || last.at >= last.n) {
+          u += WAVES / parts;
+          if (u >= hits.total) return false;
+          last.e = hits.expert(u);
+          last.at = 0;
+        }
+        last.list = lists[wave][turn ^= 1];
+        last.n = entries_of(a, routing, last.e, last.at, S::kRows, last.list);
+        last.rows = min(last.n - last.at, S::kRows);
+        unit = last;
+        return true;
+      },
+      [&](const Unit& unit) {
+        stream.point(
+            a.w2 + ((int64_t)unit.e * a.H + n0) * w_row, (const char*)a.h,
+            // past the last channel: that one again, not stored
+            [&](int r) { return (uint32_t)(min(r, a.H - 1 - n0) * w_row); },
+            [&](int r) {
+              return (uint32_t)unit.list[min(r, unit.rows - 1)] * (uint32_t)(a.I * 2);
+            });
+      },
+      [&](const Unit& unit, int line) {
+        if (KIND != EP_WEIGHTS_FP8) return 1.0f;
+        return fixed_float(a.s2 + ((int64_t)unit.e * (a.H / 128) + n0 / 128) * (a.I / 128) + line);
+      },
+      [&](const Unit& unit) {
+        if (row < unit.rows)
+          *(f32x4*)(y + unit.list[row] * y_row + 4 * (lane / 16)) = stream.acc;
+      });
   __syncthreads();
-  for (int o = threadIdx.x; o < a.tokens * 16; o += kDownWaves * kWave) {
+  for (int o = threadIdx.x; o < a.tokens * 16; o += WAVES * kWave) {
     const int t = o / 16, ch = o % 16;
     float sum = 0.0f;
     for (int k = 0; k < a.K; ++k) {
-      const int i = t * a.K + k;
-      if (routing.ids[i] < 0) continue;
+      const int i = t * a.K + k, e = routing.ids[i];
+      if (e < 0) continue;
       float v = 0.0f;
-      for (int p = 0; p < parts; ++p) v += y[(p * a.entries + i) * 16 + ch];
+      for (int p = 0; p < parts; ++p)
+        v += IN_LDS ? places[(p * a.entries + i) * 16 + ch] : y[i * y_row + ch];
+      if (KIND == EP_WEIGHTS_INT8) v *= a.s2[(int64_t)e * a.H + min(n0 + ch, a.H - 1)];
       sum = __builtin_fmaf(a.weights[i], v, sum);
     }
     if (n0 + ch < a.H) ((__bf16*)a.out)[(int64_t)t * a.H + n0 + ch] = (__bf16)sum;
   }
 }
 
-template <int KIND>
+// ---- launches ------------------------------------------------------------------------
+
+template <int KIND, int NB, int D, int DW, int DD>
 static void launch(const LayerArgs& a, hipStream_t st) {
   const int64_t units = (int64_t)std::min(a.E, a.entries) * (a.I / 8);
-  hipLaunchKernelGGL((layer_gated<KIND>), dim3((unsigned)std::min<int64_t>(units, 4 * kCus)),
-                     dim3(kUpWaves * kWave), 0, st, a);
-  hipLaunchKernelGGL((layer_down<KIND>), dim3((a.H + 15) / 16), dim3(kDownWaves * kWave),
-                     (size_t)a.slots * 16 * sizeof(float), st, a);
+  const int64_t room = 3 * kCus;  // workgroups at once
+  if (units < room * kUpWaves)
+    hipLaunchKernelGGL((layer_gated<KIND, NB, D, kUpWaves>),
+                       dim3((unsigned)std::min<int64_t>(units, 4 * kCus)), dim3(kUpWaves * kWave), 0, st, a);
+  else
+    hipLaunchKernelGGL((layer_gated<KIND, NB, D, 1>), dim3((unsigned)room),
+                       dim3(kUpWaves * kWave), 0, st, a);
+  const int strips = (a.H + 15) / 16;
+  const bool in_lds = a.entries <= kLayerPlaces;
+  if (in_lds)
+    hipLaunchKernelGGL((layer_down<KIND, NB, DD, DW, true>), dim3(strips), dim3(DW * kWave), 0, st, a);
+  else
+    hipLaunchKernelGGL((layer_down<KIND, NB, DD, 4, false>), dim3(strips), dim3(4 * kWave), 0, st, a);
 }
 
-hipError_t launch_layer(LayerArgs a, hipStream_t st) {
+template <int KIND>
+static void choose(const LayerArgs& a, hipStream_t st) {
+  constexpr bool kBytes = KIND != EP_WEIGHTS_BF16;
+  // rows of an expert, on average, and the fewest that a slot has room for
+  if (2 * a.entries <= 3 * std::min(a.E, a.entries) * (kBytes ? 2 : 4)) launch<KIND, 1, 4, 8, 5>(a, st);
+  else launch<KIND, kBytes ? 4 : 2, 3, 4, 3>(a, st);
+}
+
+hipError_t launch_layer(const LayerArgs& a, hipStream_t st) {
   if (a.tokens == 0) return hipSuccess;
-  a.slots = std::max(a.entries, std::min(kDownWaves * a.entries, 256));
   switch (a.kind) {
-    case EP_WEIGHTS_BF16: launch<EP_WEIGHTS_BF16>(a, st); break;
-    case EP_WEIGHTS_FP8: launch<EP_WEIGHTS_FP8>(a, st); break;
-    default: launch<EP_WEIGHTS_INT8>(a, st); break;
+    case EP_WEIGHTS_BF16: choose<EP_WEIGHTS_BF16>(a, st); break;
+    case EP_WEIGHTS_FP8: choose<EP_WEIGHTS_FP8>(a, st); break;
+    default: choose<EP_WEIGHTS_INT8>(a, st); break;
   }
   return hipGetLastError();
 }

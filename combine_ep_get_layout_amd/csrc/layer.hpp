@@ -6,12 +6,12 @@
 namespace ep {
 
 constexpr int kLayerEntries = EP_LAYER_MAX_ENTRIES;
+constexpr int kLayerPlaces = 256;  // entries' results that a workgroup of layer_down has in LDS
 
 struct LayerArgs {
   int tokens, K, entries, E;
   int H, I;                // channels of x and out; of h
   int kind, act;           // EP_WEIGHTS_*, EP_ACT_*
-  int slots;               // places for an entry's result in a workgroup's LDS
   const uint16_t* x;       // [tokens][H]
   const int32_t* idx;      // [tokens][K]
   const float* weights;    // [tokens][K]
@@ -20,10 +20,11 @@ struct LayerArgs {
   const char* w2;          // [E][H][I]
   const float* s2;
   uint16_t* h;             // workspace: [entries][I]
+  float* y;                // and, for more than kLayerPlaces entries, [entries][H up to 16]
   uint16_t* out;           // [tokens][H]
   int32_t* err;
 };
 
-hipError_t launch_layer(LayerArgs a, hipStream_t stream);
+hipError_t launch_layer(const LayerArgs& a, hipStream_t stream);
 
 }  // namespace ep

@@ -23,7 +23,7 @@ def test_workspace():
     assert of(64) == 2 * 8 * 2 * 64 * 2
     assert of(8, T=0) == 256
     assert of(72, R=1, T=1) == 512
-    assert of(64, R=1, T=512) == 1024 * 64 * 2
+    assert of(64, R=1, T=512) == 1024 * (64 * 2 + 128 * 4)  # and the entries' results in fp32
     assert of(64, R=1, T=513) == 0                       # more than 1,024 entries
     assert of(64, E=5) == 0
     for inner in (0, 4, 12, -8, 32776):
