@@ -18,7 +18,7 @@
 
 namespace ep {
 
-constexpr int kMost = 16;  // entries of an expert that are multiplied at once, at most
+constexpr int kMost = 64;  // entries of an expert that are multiplied at once, at most
 
 // ---- who is hit ------------------------------------------------------------------
 
@@ -108,28 +108,30 @@ struct Unit {
   uint16_t* list;             // the unit's
 };
 
-// A line is 128 bytes of each of a strip's 16 rows of weights and the channels that these
+// A line is 128 bytes of each of 16 CT rows of weights and the channels that these
 // multiply of the rows, which is 128 bytes of each in bf16 and 256 where the weights have 8
-// bits.  A slot of the ring holds one: two loads (2 KiB) of weights and NB of rows.  In LDS
-// chunk c (16 bytes) of row r stands at c ^ turn(r), so that 16 lanes' reads of one chunk of
-// 16 rows fall into different banks.
-template <int KIND, int NB, int D>
+// bits.  A slot of the ring holds one: two loads (2 KiB) of weights a strip and NB of rows.  In
+// LDS chunk c (16 bytes) of row r stands at c ^ turn(r), so that 16 lanes' reads of one chunk
+// of 16 rows fall into different banks.
+template <int KIND, int CT, int NB, int D>
 struct Stream {
   static constexpr bool kBytes = KIND != EP_WEIGHTS_BF16;
   static constexpr int kSize = kBytes ? 1 : 2;
   static constexpr int kChunks = kBytes ? 16 : 8;           // of a row in a line
   static constexpr int kRows = NB * kWave / kChunks;        // that a slot has room for
-  static constexpr int kSlot = (2 + NB) * 1024;
-  static constexpr int kLoads = 2 + NB;
+  static constexpr int TT = (kRows + 15) / 16;              // in matrix-core tiles
+  static constexpr int kRowsAt = CT * 2048;                 // in a slot
+  static constexpr int kSlot = kRowsAt + NB * 1024;
+  static constexpr int kLoads = 2 * CT + NB;
   static constexpr int kSteps = kBytes ? 4 : 2;             // matrix steps of a line
-  static_assert(kRows <= kMost, "");
+  static_assert(kRows <= kMost && (kRows < 16 || kRows % 16 == 0), "");
 
   lds_char* ring;
   int lines, left;         // of a row of weights, and the last one's bytes
   bool turns;              // strips start at different lines
   const char *w, *x;       // of the unit that is loaded: uniform, with the lanes' offsets
-  uint32_t w_off[2], x_off[NB];
-  f32x4 acc;
+  uint32_t w_off[2 * CT], x_off[NB];
+  f32x4 acc[CT][TT];
 
   __device__ __forceinline__ Stream(lds_char* r, int channels)
       : ring(r), lines((channels * kSize + 127) / 128),
@@ -137,16 +139,16 @@ struct Stream {
         turns(channels * kSize % 4096 == 0) {}
 
   static __device__ __forceinline__ int w_turn(int r) { return r / 2 & 7; }
-  static __device__ __forceinline__ int x_turn(int r) { return kBytes ? r : r / 2 & 7; }
+  static __device__ __forceinline__ int x_turn(int r) { return kBytes ? r & 15 : r / 2 & 7; }
 
-  // row(r): byte offset from w of the strip's row r; entry(r): from x of the unit's row r
+  // row(r): byte offset from w of weight row r; entry(r): from x of the unit's row r
   template <class Row, class Entry>
   __device__ __forceinline__ void point(const char* w_, const char* x_, Row row, Entry entry) {
     const int lane = lane_id();
     w = w_;
     x = x_;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 * CT; ++i) {
       const int r = 8 * i + lane / 8;
       w_off[i] = row(r) + ((lane % 8 ^ w_turn(r)) << 4);
     }
@@ -162,13 +164,13 @@ struct Stream {
     const char* xl = x + (int64_t)line * (16 * kChunks);
     if (KIND == EP_WEIGHTS_FP8 || line < lines - 1 || left == 128) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) stream_lds16(wl, w_off[i], to + 1024 * i);
+      for (int i = 0; i < 2 * CT; ++i) stream_lds16(wl, w_off[i], to + 1024 * i);
 #pragma unroll
-      for (int i = 0; i < NB; ++i) load_lds16(xl, x_off[i], to + 2048 + 1024 * i);
+      for (int i = 0; i < NB; ++i) load_lds16(xl, x_off[i], to + kRowsAt + 1024 * i);
     } else {  // chunks past the end are zeros on both sides
       const int lane = lane_id(), chunks = left / 16 * (kBytes ? 2 : 1);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 2 * CT; ++i) {
         const bool in = (lane % 8 ^ w_turn(8 * i + lane / 8)) * 16 < left;
         load_lds16(in ? wl + w_off[i] : (const char*)k_zeros, to + 1024 * i);
       }
@@ -176,7 +178,7 @@ struct Stream {
       for (int i = 0; i < NB; ++i) {
         const int r = i * (kWave / kChunks) + lane / kChunks;
         const bool in = (lane % kChunks ^ x_turn(r)) < chunks;
-        load_lds16(in ? xl + x_off[i] : (const char*)k_zeros, to + 2048 + 1024 * i);
+        load_lds16(in ? xl + x_off[i] : (const char*)k_zeros, to + kRowsAt + 1024 * i);
       }
     }
   }
@@ -209,34 +211,45 @@ struct Stream {
   __device__ __forceinline__ void multiply(int slot, float scale) {
     const lds_char* from = ring + slot * kSlot;
     const int lane = lane_id(), r = lane % 16, q = lane / 16;
-    // rows past the slot's room repeat its last one; their columns are not used
-    const int xr = kRows < 16 ? min(r, kRows - 1) : r;
-    i32x4 wv[2];
-    bf16x8 xv[kSteps];
+    i32x4 wv[CT][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      wv[i] = *(const EP_LDS i32x4*)(from + r * 128 + ((q + 4 * i ^ w_turn(r)) << 4));
+    for (int c = 0; c < CT; ++c)
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int c = kBytes ? 8 * (i / 2) + 2 * q + i % 2 : q + 4 * i;
-      xv[i] = __builtin_bit_cast(bf16x8, *(const EP_LDS i32x4*)(from + 2048 + xr * 16 * kChunks +
-                                                                ((c ^ x_turn(xr)) << 4)));
-    }
-    f32x4 sum = KIND == EP_WEIGHTS_FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc;
+      for (int i = 0; i < 2; ++i)
+        wv[c][i] = *(const EP_LDS i32x4*)(from + (16 * c + r) * 128 + ((q + 4 * i ^ w_turn(r)) << 4));
+    bf16x8 f[CT][kSteps];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      bf16x8 f;
-      if constexpr (kBytes)
-        f = codes((uint32_t)wv[i / 2][2 * (i % 2)], (uint32_t)wv[i / 2][2 * (i % 2) + 1]);
-      else
-        f = __builtin_bit_cast(bf16x8, wv[i]);
-      sum = Mfma<16>::bf16(f, xv[i], sum);
-    }
-    if (KIND == EP_WEIGHTS_FP8) {
+    for (int c = 0; c < CT; ++c)
 #pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4) acc[q4] = __builtin_fmaf(sum[q4], scale, acc[q4]);
-    } else {
-      acc = sum;
+      for (int i = 0; i < kSteps; ++i) {
+        if constexpr (kBytes)
+          f[c][i] = codes((uint32_t)wv[c][i / 2][2 * (i % 2)], (uint32_t)wv[c][i / 2][2 * (i % 2) + 1]);
+        else
+          f[c][i] = __builtin_bit_cast(bf16x8, wv[c][i]);
+      }
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+      // rows past the slot's room repeat its last one; their columns are not used
+      const int xr = kRows < 16 ? min(r, kRows - 1) : 16 * j + r;
+      bf16x8 xv[kSteps];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int c = kBytes ? 8 * (i / 2) + 2 * q + i % 2 : q + 4 * i;
+        xv[i] = __builtin_bit_cast(bf16x8, *(const EP_LDS i32x4*)(from + kRowsAt + xr * 16 * kChunks +
+                                                                  ((c ^ x_turn(xr)) << 4)));
+      }
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        f32x4 sum = KIND == EP_WEIGHTS_FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[c][j];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) sum = Mfma<16>::bf16(f[c][i], xv[i], sum);
+        if (KIND == EP_WEIGHTS_FP8) {
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) acc[c][j][q4] = __builtin_fmaf(sum[q4], scale, acc[c][j][q4]);
+        } else {
+          acc[c][j] = sum;
+        }
+      }
     }
   }
 
@@ -274,7 +287,10 @@ struct Stream {
           if (i < n) load(line_of(now, i), i);
         slot = 0;
       }
-      acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int j = 0; j < TT; ++j) acc[c][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       bool more = false;
       float scale = n > 0 ? scales(now, line_of(now, 0)) : 0.0f;
       for (int i = 0; i < n; ++i) {
@@ -333,20 +349,22 @@ __device__ __forceinline__ void halves(float v, float& a, float& b) {
 constexpr int kUpWaves = 4;    // of a workgroup
 constexpr int kUpStride = 20;  // floats of a column of partial sums, 16 and a gap
 
-// A strip is eight channels of one expert, their gates and ups.  WK waves share a strip, its
-// lines dealt to them in turn; a wave's sums of rows 4 (lane / 16) .. are gates in the lower
-// half of its lanes and ups in the upper one.
-template <int KIND, int NB, int D, int WK>
+// A strip is eight channels of one expert, their gates and ups.  WK waves share CT strips,
+// the lines dealt to them in turn; a wave's sums of rows 4 (lane / 16) .. are gates in the
+// lower half of its lanes and ups in the upper one.
+template <int KIND, int CT, int NB, int D, int WK>
 __global__ __launch_bounds__(kUpWaves* kWave) void layer_gated(LayerArgs a) {
-  typedef Stream<KIND, NB, D> S;
+  typedef Stream<KIND, CT, NB, D> S;
+  static_assert(WK == 1 || WK == kUpWaves, "a workgroup's barriers");
+  constexpr int kCols = 16 * S::TT;
   __shared__ Routing routing;
-  __shared__ uint16_t lists[kUpWaves][2][kMost];
+  __shared__ uint16_t lists[kUpWaves][2][S::kRows];
   __shared__ __align__(16) char rings[kUpWaves][D * S::kSlot];
-  __shared__ __align__(16) float parts[WK > 1 ? WK * kMost * kUpStride : 1];
+  __shared__ __align__(16) float parts[WK > 1 ? WK * kCols * kUpStride : 1];
   read_routing<kUpWaves * kWave>(a, routing, nullptr);
   const Hits hits(routing);
   const int wave = uniform(threadIdx.x / kWave), lane = lane_id(), row = lane % 16;
-  const int strips = a.I / 8, units = hits.total * strips;
+  const int strips = (a.I + 8 * CT - 1) / (8 * CT), units = hits.total * strips;
   const int64_t w_row = (int64_t)a.H * S::kSize;
   constexpr int kTeams = kUpWaves / WK;
   int u = blockIdx.x * kTeams + wave / WK - gridDim.x * kTeams, turn = 0;
@@ -375,9 +393,13 @@ __global__ __launch_bounds__(kUpWaves* kWave) void layer_gated(LayerArgs a) {
         return true;
       },
       [&](const Unit& unit) {
+        const int n0 = unit.strip * 8 * CT;
         stream.point(
-            a.w13 + ((int64_t)unit.e * 2 * a.I + unit.strip * 8) * w_row, (const char*)a.x,
-            [&](int r) { return (uint32_t)((r < 8 ? r : a.I + r - 8) * w_row); },
+            a.w13 + ((int64_t)unit.e * 2 * a.I + n0) * w_row, (const char*)a.x,
+            [&](int r) {  // past the last channel: that one again, not stored
+              const int ch = min(r / 16 * 8 + r % 8, a.I - 1 - n0);
+              return (uint32_t)((r % 16 < 8 ? ch : a.I + ch) * w_row);
+            },
             [&](int r) {
               return (uint32_t)(unit.list[min(r, unit.rows - 1)] / a.K) * (uint32_t)(a.H * 2);
             });
@@ -385,68 +407,83 @@ __global__ __launch_bounds__(kUpWaves* kWave) void layer_gated(LayerArgs a) {
       [&](const Unit& unit, int line) {
         if (KIND != EP_WEIGHTS_FP8) return 1.0f;
         const int64_t groups = a.H / 128;
-        const float* s = a.s13 + ((int64_t)unit.e * (2 * a.I / 128) + unit.strip / 16) * groups + line;
+        const float* s = a.s13 + ((int64_t)unit.e * (2 * a.I / 128) + unit.strip * CT / 16) * groups + line;
         const float gate = fixed_float(s), up = fixed_float(s + a.I / 128 * groups);
         return lane < 32 ? gate : up;
       },
       [&](const Unit& unit) {
         const int ch = 4 * (lane / 16 % 2);
-        const float* scale = a.s13 + (int64_t)unit.e * 2 * a.I + unit.strip * 8;
-        float g[4], up[4];
-        if constexpr (WK > 1) {
-          *(f32x4*)(parts + (wave % WK * kMost + row) * kUpStride + 4 * (lane / 16)) = stream.acc;
-          barrier();
 #pragma unroll
-          for (int q = 0; q < 4; ++q) g[q] = up[q] = 0.0f;
+        for (int c = 0; c < CT; ++c) {
+          const int n0 = (unit.strip * CT + c) * 8;
+          if (WK > 1) {
 #pragma unroll
-          for (int w = 0; w < WK; ++w) {
-            const float* from = parts + (w * kMost + row) * kUpStride + ch;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) g[q] += from[q], up[q] += from[8 + q];
+            for (int j = 0; j < S::TT; ++j)
+              *(f32x4*)(parts + (wave % WK * kCols + 16 * j + row) * kUpStride + 4 * (lane / 16)) =
+                  stream.acc[c][j];
+            barrier();
           }
-          barrier();
-          if (wave % WK != 0) return;
-        } else {
+          if (n0 < a.I) {
+            const float* scale = a.s13 + (int64_t)unit.e * 2 * a.I + n0;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) halves(stream.acc[q], g[q], up[q]);
-        }
-        bf16x2 out[2];
+            for (int j = 0; j < S::TT; ++j) {
+              if (WK > 1 && j % WK != wave) continue;  // a tile each
+              float g[4], up[4];
+              if (WK > 1) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (KIND == EP_WEIGHTS_INT8) {
-            const float g0 = fixed_float(scale + q), g1 = fixed_float(scale + 4 + q);
-            const float u0 = fixed_float(scale + a.I + q), u1 = fixed_float(scale + a.I + 4 + q);
-            g[q] *= ch == 0 ? g0 : g1;
-            up[q] *= ch == 0 ? u0 : u1;
+                for (int q = 0; q < 4; ++q) g[q] = up[q] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < WK; ++w) {
+                  const float* from = parts + (w * kCols + 16 * j + row) * kUpStride + ch;
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) g[q] += from[q], up[q] += from[8 + q];
+                }
+              } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) halves(stream.acc[c][j][q], g[q], up[q]);
+              }
+              bf16x2 out[2];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (KIND == EP_WEIGHTS_INT8) {
+                  const float g0 = fixed_float(scale + q), g1 = fixed_float(scale + 4 + q);
+                  const float u0 = fixed_float(scale + a.I + q), u1 = fixed_float(scale + a.I + 4 + q);
+                  g[q] *= ch == 0 ? g0 : g1;
+                  up[q] *= ch == 0 ? u0 : u1;
+                }
+                float value, slope;
+                act_both(a.act, g[q], value, slope);
+                out[q / 2][q % 2] = (__bf16)(value * up[q]);
+              }
+              const int r = 16 * j + row;
+              if (lane < 32 && r < unit.rows)
+                *(uint2*)(a.h + (int64_t)unit.list[r] * a.I + n0 + ch) = __builtin_bit_cast(uint2, out);
+            }
           }
-          float value, slope;
-          act_both(a.act, g[q], value, slope);
-          out[q / 2][q % 2] = (__bf16)(value * up[q]);
+          if (WK > 1) barrier();
         }
-        if (lane < 32 && row < unit.rows)
-          *(uint2*)(a.h + (int64_t)unit.list[row] * a.I + unit.strip * 8 + ch) =
-              __builtin_bit_cast(uint2, out);
       });
 }
 
 // ---- down projection and the weighted sum ---------------------------------------------
 
-// A workgroup has a strip of 16 channels of every token.  Its waves take an expert each in
+// A workgroup has CT strips of 16 channels of every token.  Its waves take an expert each in
 // turn (or parts of the contraction, where there are fewer experts than waves) and put
 // every entry's result into a place of its own, in LDS or in the workspace; then they are
 // summed in k order.
-template <int KIND, int NB, int D, int WAVES, bool IN_LDS>
+template <int KIND, int CT, int NB, int D, int WAVES, bool IN_LDS>
 __global__ __launch_bounds__(WAVES* kWave) void layer_down(LayerArgs a) {
-  typedef Stream<KIND, NB, D> S;
+  typedef Stream<KIND, CT, NB, D> S;
+  static_assert(!IN_LDS || CT == 1, "a place has 16 channels");
   __shared__ Routing routing;
-  __shared__ uint16_t lists[WAVES][2][kMost];
+  __shared__ uint16_t lists[WAVES][2][S::kRows];
   __shared__ __align__(16) char rings[WAVES][D * S::kSlot];
   __shared__ float weights[kLayerEntries];
   __shared__ __align__(16) float places[IN_LDS ? kLayerPlaces * 16 : 1];
   read_routing<WAVES * kWave>(a, routing, weights);
   const Hits hits(routing);
   const int wave = uniform(threadIdx.x / kWave), lane = lane_id(), row = lane % 16;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = blockIdx.x * 16 * CT;
   const int64_t w_row = (int64_t)a.I * S::kSize;
   // parts that every expert's contraction is cut into
   int parts = 1;
@@ -491,12 +528,19 @@ __global__ __launch_bounds__(WAVES* kWave) void layer_down(LayerArgs a) {
         return fixed_float(a.s2 + ((int64_t)unit.e * (a.H / 128) + n0 / 128) * (a.I / 128) + line);
       },
       [&](const Unit& unit) {
-        if (row < unit.rows)
-          *(f32x4*)(y + unit.list[row] * y_row + 4 * (lane / 16)) = stream.acc;
+#pragma unroll
+        for (int j = 0; j < S::TT; ++j)
+          if (16 * j + row < unit.rows)
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+              if (c == 0 || n0 + 16 * c < a.H)
+                *(f32x4*)(y + unit.list[16 * j + row] * y_row + 16 * c + 4 * (lane / 16)) =
+                    stream.acc[c][j];
       });
   __syncthreads();
-  for (int o = threadIdx.x; o < a.tokens * 16; o += WAVES * kWave) {
-    const int t = o / 16, ch = o % 16;
+  for (int o = threadIdx.x; o < a.tokens * 16 * CT; o += WAVES * kWave) {
+    const int t = o / (16 * CT), ch = o % (16 * CT);
+    if (n0 + ch >= a.H) continue;
     float sum = 0.0f;
     for (int k = 0; k < a.K; ++k) {
       const int i = t * a.K + k, e = routing.ids[i];
@@ -504,39 +548,61 @@ __global__ __launch_bounds__(WAVES* kWave) void layer_down(LayerArgs a) {
       float v = 0.0f;
       for (int p = 0; p < parts; ++p)
         v += IN_LDS ? places[(p * a.entries + i) * 16 + ch] : y[i * y_row + ch];
-      if (KIND == EP_WEIGHTS_INT8) v *= a.s2[(int64_t)e * a.H + min(n0 + ch, a.H - 1)];
+      if (KIND == EP_WEIGHTS_INT8) v *= a.s2[(int64_t)e * a.H + n0 + ch];
       sum = __builtin_fmaf(weights[i], v, sum);
     }
-    if (n0 + ch < a.H) ((__bf16*)a.out)[(int64_t)t * a.H + n0 + ch] = (__bf16)sum;
+    ((__bf16*)a.out)[(int64_t)t * a.H + n0 + ch] = (__bf16)sum;
   }
 }
 
 // ---- launches ------------------------------------------------------------------------
 
-template <int KIND, int NB, int D, int DW, int DD>
-static void launch(const LayerArgs& a, hipStream_t st) {
-  const int64_t units = (int64_t)std::min(a.E, a.entries) * (a.I / 8);
+// D, TD: slots of the ring where a wave has its own strips, and where four share them
+template <int KIND, int CT, int NB, int D, int TD>
+static void launch_gated(const LayerArgs& a, hipStream_t st) {
+  const int64_t units = (int64_t)std::min(a.E, a.entries) * ((a.I + 8 * CT - 1) / (8 * CT));
   const int64_t room = 3 * kCus;  // workgroups at once
   if (units < room * kUpWaves)
-    hipLaunchKernelGGL((layer_gated<KIND, NB, D, kUpWaves>),
-                       dim3((unsigned)std::min<int64_t>(units, 4 * kCus)), dim3(kUpWaves * kWave), 0, st, a);
+    hipLaunchKernelGGL((layer_gated<KIND, CT, NB, TD, kUpWaves>),
+                       dim3((unsigned)std::min<int64_t>(units, 4 * kCus)), dim3(kUpWaves * kWave),
+                       0, st, a);
   else
-    hipLaunchKernelGGL((layer_gated<KIND, NB, D, 1>), dim3((unsigned)room),
+    hipLaunchKernelGGL((layer_gated<KIND, CT, NB, D, 1>), dim3((unsigned)room),
                        dim3(kUpWaves * kWave), 0, st, a);
-  const int strips = (a.H + 15) / 16;
-  const bool in_lds = a.entries <= kLayerPlaces;
-  if (in_lds)
-    hipLaunchKernelGGL((layer_down<KIND, NB, DD, DW, true>), dim3(strips), dim3(DW * kWave), 0, st, a);
-  else
-    hipLaunchKernelGGL((layer_down<KIND, NB, DD, 4, false>), dim3(strips), dim3(4 * kWave), 0, st, a);
 }
 
+template <int KIND, int CT, int NB, int D, int WAVES, bool IN_LDS>
+static void launch_down(const LayerArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((layer_down<KIND, CT, NB, D, WAVES, IN_LDS>),
+                     dim3((a.H + 16 * CT - 1) / (16 * CT)), dim3(WAVES * kWave), 0, st, a);
+}
+
+// How many entries a slot has room for goes by how many an expert has on average: a wave
+// reads its weights once for each slot full of them.  us (gated and down together, bf16
+// 4096 -> 1408, 16 experts with 8 / 16 / 32 / 64 entries each): slots of 16 entries 104 / 151 /
+// 308 / 590, of 64 with two strips - / 160 / 190 / 283.  In 8 bits a slot's rows are as many
+// bytes as its weights, or more, so two strips share them: 32 experts with 4 / 16 entries 140 /
+// 255 with one strip, 112 / 220 with two.  With more than about 12 entries an expert layout,
+// dispatch, the experts' products and combine take less (136 / 152 / 150 us for 16 / 32 / 64).
 template <int KIND>
 static void choose(const LayerArgs& a, hipStream_t st) {
   constexpr bool kBytes = KIND != EP_WEIGHTS_BF16;
-  // rows of an expert, on average, and the fewest that a slot has room for
-  if (2 * a.entries <= 3 * std::min(a.E, a.entries) * (kBytes ? 2 : 4)) launch<KIND, 1, 3, 8, 3>(a, st);
-  else launch<KIND, kBytes ? 4 : 2, 3, 4, 3>(a, st);
+  const bool in_lds = a.entries <= kLayerPlaces;
+  const int experts = std::min(a.E, a.entries);
+  if (2 * a.entries <= 3 * experts * (kBytes ? 2 : 4)) {  // 4 entries a slot, in bf16 8
+    launch_gated<KIND, 1, 1, 3, 3>(a, st);
+    if (in_lds) launch_down<KIND, 1, 1, 3, 8, true>(a, st);
+    else launch_down<KIND, 1, 1, 3, 4, false>(a, st);
+  } else if (a.entries <= 16 * experts) {  // 16
+    constexpr int NB = kBytes ? 4 : 2, D = kBytes ? 2 : 3;
+    launch_gated<KIND, kBytes ? 2 : 1, NB, D, D>(a, st);
+    if (in_lds) launch_down<KIND, 1, NB, D, kBytes ? 6 : 4, true>(a, st);
+    else launch_down<KIND, 1, NB, D, 4, false>(a, st);
+  } else {  // 32, in bf16 64
+    launch_gated<KIND, 2, 8, 3, 2>(a, st);
+    if (in_lds) launch_down<KIND, 1, 8, 3, 4, true>(a, st);
+    else launch_down<KIND, 1, 8, 3, 4, false>(a, st);
+  }
 }
 
 hipError_t launch_layer(const LayerArgs& a, hipStream_t st) {
