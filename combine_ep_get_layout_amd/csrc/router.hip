@@ -12,12 +12,14 @@
 //   softmax:     dl_e = scale s_e (dw_e - sum_k dw_k s_k), for every expert.
 //
 // LPT lanes take a token, PER consecutive experts each, so that the first lane with the
-// largest value also has its lowest index.
+// largest value also has its lowest index.  Choices are compared in fp32, and where two that
+// decide are nearer to each other than that tells, again in 64 bits, a token at a time: all
+// in 64 bits took 61 us for 32,768 tokens over 256 experts (8 groups, bias).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 
-#include "experts_choice.hpp"
+#include "experts.hpp"
 #include "router.hpp"
 
 namespace ep {
@@ -190,42 +192,51 @@ __device__ __forceinline__ void load_logits(const char* row, int first, int E, f
              : 0.0f + (BF16 ? (i % 2 ? bf16_hi(u.w[i / 2]) : bf16_lo(u.w[i / 2]))
                             : __uint_as_float(u.w[i]));
   } else {
+    // one lane's address, not one for each expert: that many registers would halve the waves
+    const char* from = row + (int64_t)first * (BF16 ? 2 : 4);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int e = first + i < E ? first + i : 0;
-      const float v = BF16 ? __uint_as_float((uint32_t)((const uint16_t*)row)[e] << 16)
-                           : ((const float*)row)[e];
-      l[i] = first + i < E ? 0.0f + v : fill;
+      l[i] = fill;
+      if (first + i < E)
+        l[i] = 0.0f + (BF16 ? __uint_as_float((uint32_t)((const uint16_t*)from)[i] << 16)
+                            : ((const float*)from)[i]);
     }
   }
 }
 
-__device__ __forceinline__ float exponential(float v) { return expf(v); }
-__device__ __forceinline__ double exponential(double v) { return exp(v); }
+// In fp32 the hardware's exponential and reciprocal, for choices and gradients: the
+// exponential's argument times log2 e is rounded to 2^-24 of itself.
+__device__ __forceinline__ float exponential(float v) { return __expf(v); }
+__device__ __forceinline__ float inverse(float v) { return __builtin_amdgcn_rcpf(v); }
 
 // 1 / (1 + exp(-v)), relatively exact for large negative v too
-template <class V>
-__device__ __forceinline__ V sigmoid_of(V v) {
-  const V z = exponential(v < (V)0 ? v : -v);
-  return (v < (V)0 ? z : (V)1) / ((V)1 + z);
+__device__ __forceinline__ float sigmoid_of(float v) {
+  const float z = exponential(v < 0.0f ? v : -v);
+  return (v < 0.0f ? z : 1.0f) * inverse(1.0f + z);
+}
+
+// for weights: each step rounded correctly, or to a unit in the last place
+__device__ __forceinline__ float sigmoid_exact(float v) {
+  const float z = expf(v < 0.0f ? v : -v);
+  return (v < 0.0f ? z : 1.0f) / (1.0f + z);
 }
 
 // ---- the choice -------------------------------------------------------------------
 
-// One token's experts in LPT lanes.  V: the type that choices are compared in.
-template <int LPT, int PER, class V>
+// One token's experts in LPT lanes, in fp32.
+template <int LPT, int PER>
 struct Choice {
   const RouteArgs& a;
   const int at, first;     // lane of the token, and its first expert
-  V c[PER];
-  V most = 0, total = 1;   // softmax: the largest logit and the sum of exp(l - most)
+  float c[PER];
+  float most = 0, total = 1, part = 1;  // softmax: the largest logit, the sum of exp(l - most), its inverse
 
   __device__ __forceinline__ explicit Choice(const RouteArgs& a_)
       : a(a_), at(lane_id() & (LPT - 1)), first(at * PER) {}
 
-  __device__ __forceinline__ V score(float l) const {
-    if (a.sigmoid) return sigmoid_of((V)l);
-    return exponential((V)l - most) / total;
+  __device__ __forceinline__ float score(float l) const {
+    if (a.sigmoid) return sigmoid_of(l);
+    return exponential(l - most) * part;
   }
 
   __device__ __forceinline__ void softmax_sums(const float (&l)[PER]) {
@@ -233,11 +244,12 @@ struct Choice {
 #pragma unroll
     for (int i = 1; i < PER; ++i) m = fmaxf(m, l[i]);
     m = all_max<LPT>(m);
-    most = (V)(m > low_inf() ? m : 0.0f);
-    V sum = 0;
+    most = m > low_inf() ? m : 0.0f;
+    float sum = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) sum += exponential((V)l[i] - most);
+    for (int i = 0; i < PER; ++i) sum += exponential(l[i] - most);
     total = all_sum<LPT>(sum);
+    part = inverse(total);
   }
 
   // c of every expert; whether some is not a number
@@ -246,25 +258,25 @@ struct Choice {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       if (a.scored) {
-        c[i] = l[i] > low_inf() ? score(l[i]) + (V)bias[i] : (V)low_inf();
+        c[i] = l[i] > low_inf() ? score(l[i]) + bias[i] : low_inf();
         bad |= c[i] != c[i];
       } else {
-        c[i] = (V)l[i];
+        c[i] = l[i];
       }
     }
     return bad;
   }
 
-  // Experts outside the kept groups to -inf.  Returns by how much the last kept group is
-  // ahead of the first one left.
-  __device__ __forceinline__ V keep_groups() {
+  // Experts outside the kept groups to -inf.  close: whether the last kept group is no more
+  // than `sure` and 2^-21 of both ahead of the first one left.
+  __device__ __forceinline__ bool keep_groups(float sure) {
     const int size = a.group_size, lanes = size / PER;
-    V mine;       // the score of group at / lanes, or of group `at`
+    float mine;       // the score of group at / lanes, or of group `at`
     bool stays[PER];
-    V lowest = (V)__builtin_inff(), highest = (V)low_inf();
+    float lowest = __builtin_inff(), highest = low_inf();
     if (size % PER == 0 && (lanes & (lanes - 1)) == 0 && lanes <= LPT) {
       // a group is a power of two of lanes
-      Top2<V> top{c[0], (V)low_inf()};
+      Top2<float> top{c[0], low_inf()};
 #pragma unroll
       for (int i = 1; i < PER; ++i) top.add(c[i]);
       top.template join<LPT>(lanes);
@@ -272,7 +284,7 @@ struct Choice {
       const int own = at / lanes;
       int rank = 0;
       for (int g = 0; g < a.groups; ++g) {
-        const V other = of_lane<LPT>(mine, g * lanes);
+        const float other = of_lane<LPT>(mine, g * lanes);
         rank += other > mine || (other == mine && g < own);
       }
       const bool in = own < a.groups, stay = in && rank < a.groups_kept;
@@ -281,20 +293,20 @@ struct Choice {
       if (stay) lowest = mine;
       else if (in) highest = mine;
     } else {
-      mine = (V)low_inf();
+      mine = low_inf();
       for (int g = 0; g < a.groups; ++g) {
-        Top2<V> top{(V)low_inf(), (V)low_inf()};
+        Top2<float> top{low_inf(), low_inf()};
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
           const int e = first + i - g * size;
-          top.add(e >= 0 && e < size ? c[i] : (V)low_inf());
+          top.add(e >= 0 && e < size ? c[i] : low_inf());
         }
         top.template join<LPT>(LPT);
         if (g == at) mine = top.sum(a.group_top);
       }
       int rank = 0;
       for (int g = 0; g < a.groups; ++g) {
-        const V other = of_lane<LPT>(mine, g);
+        const float other = of_lane<LPT>(mine, g);
         rank += other > mine || (other == mine && g < at);
       }
       const bool in = at < a.groups, stay = in && rank < a.groups_kept;
@@ -310,187 +322,352 @@ struct Choice {
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (!stays[i]) c[i] = (V)low_inf();
-    return -all_max<LPT>(-lowest) - all_max<LPT>(highest);
+      if (!stays[i]) c[i] = low_inf();
+    lowest = -all_max<LPT>(-lowest);
+    highest = all_max<LPT>(highest);
+    const float size_of = fabsf(lowest) + fabsf(highest);
+    return highest > low_inf() && !(lowest - highest > sure + 0x1p-21f * size_of);
   }
 
   // The n largest, one a lane: id -1 where there are no more.
-  __device__ __forceinline__ void largest(int n, V& value, int& id) {
-    value = (V)low_inf();
+  __device__ __forceinline__ void largest(int n, float& value, int& id) {
+    value = low_inf();
     id = -1;
     for (int k = 0; k < n; ++k) {
-      V best = c[0];
+      float best = c[0];
 #pragma unroll
       for (int i = 1; i < PER; ++i) best = larger(best, c[i]);
-      const V top = all_max<LPT>(best);
-      const bool any = top > (V)low_inf();
+      const float top = all_max<LPT>(best);
+      const bool any = top > low_inf();
       if (__ballot(any) == 0) return;
       const int from = first_lane<LPT>(token_bits<LPT>(__ballot(any && best == top)));
       // the lane's first expert of that value, taken out
       int which = PER;
-      bool open = at == from && any;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const bool hit = open && c[i] == top;
-        if (hit) c[i] = (V)low_inf(), which = i;
-        open = open && !hit;
-      }
+      for (int i = PER - 1; i >= 0; --i) which = c[i] == top ? i : which;
       const int e = of_lane<LPT>(first + which, from);
+      which = at == from && any ? which : PER;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c[i] = i == which ? low_inf() : c[i];
       if (at == k && any) value = top, id = e;
     }
   }
 };
 
+template <bool BF16>
+__device__ __forceinline__ float logit_at(const char* row, int e) {
+  return 0.0f + (BF16 ? __uint_as_float((uint32_t)((const uint16_t*)row)[e] << 16)
+                      : ((const float*)row)[e]);
+}
+
+// Writes a token's entries, entry k's expert (or -1) in its lane k.  most, total: softmax.
+template <int LPT, bool BF16>
+__device__ __forceinline__ void store_entries(const RouteArgs& a, const char* row, int64_t t, int id,
+                                              float most, float total) {
+  const int at = lane_id() & (LPT - 1);
+  const bool has = id >= 0;
+  const float mine = has ? logit_at<BF16>(row, id) : low_inf();
+  const float top = all_max<LPT>(mine);
+  float w = 0.0f;
+  if (has) {
+    // sigmoids so small that they might vanish are exponentials
+    if (a.sigmoid && !(a.normalize && top < -30.0f)) w = sigmoid_exact(mine);
+    else if (a.normalize) w = expf(mine - top);
+    else w = expf(mine - most) / total;
+  }
+  if (a.normalize) {
+    const float sum = all_sum<LPT>(w);
+    if (has) w = w / sum;
+  }
+  if (t < a.tokens && at < a.K) {
+    a.idx[t * a.K + at] = id;
+    a.weights[t * a.K + at] = w * a.scale;
+  }
+}
+
+// A token chosen in 64 bits, by the whole wave; c: its choices in LDS.  Lane l has experts
+// per l .. as above.  Few tokens come here (of 32,768 tens), but the last of them ends the
+// kernel: what counts is one token's latency.
+template <bool BF16>
+__device__ __forceinline__ void route_exactly(const RouteArgs& a, int64_t t, double* c) {
+  const char* row = (const char*)a.logits + t * a.E * (BF16 ? 2 : 4);
+  const int lane = lane_id(), per = (a.E + kWave - 1) / kWave;
+  const int first = min(lane * per, a.E), end = min(first + per, a.E);
+  double most = 0.0, total = 1.0;
+  if (!a.sigmoid) {
+    float m = low_inf();
+#pragma unroll 4
+    for (int e = first; e < end; ++e) m = fmaxf(m, logit_at<BF16>(row, e));
+    m = all_max<64>(m);
+    if (m > low_inf()) most = m;
+    total = 0.0;
+#pragma unroll 4
+    for (int e = first; e < end; ++e) total += exp((double)logit_at<BF16>(row, e) - most);
+    total = all_sum<64>(total);
+  }
+#pragma unroll 4
+  for (int e = first; e < end; ++e) {
+    const float l = logit_at<BF16>(row, e);
+    const double x = a.sigmoid ? (l < 0.0f ? (double)l : -(double)l) : (double)l - most;
+    const double z = exp(x);
+    const double score = a.sigmoid ? (l < 0.0f ? z : 1.0) / (1.0 + z) : z / total;
+    c[e] = l > low_inf() ? score + (a.bias ? (double)a.bias[e] : 0.0) : (double)low_inf();
+  }
+  wave_lds_sync();
+  if (a.groups_kept < a.groups) {
+    Top2<double> top{(double)low_inf(), (double)low_inf()};
+    if (lane < a.groups)
+#pragma unroll 8
+      for (int i = 0; i < a.group_size; ++i) top.add(c[lane * a.group_size + i]);
+    const double mine = top.sum(a.group_top);
+    int rank = 0;
+#pragma unroll 1
+    for (int g = 0; g < a.groups; ++g) {
+      const double other = of_lane<64>(mine, g);
+      rank += other > mine || (other == mine && g < lane);
+    }
+    const uint64_t kept = __ballot(lane < a.groups && rank < a.groups_kept);
+    wave_lds_sync();
+#pragma unroll 4
+    for (int e = first; e < end; ++e) {
+      if (!(kept >> e / a.group_size & 1)) c[e] = (double)low_inf();
+      else if (!a.bias) c[e] = (double)logit_at<BF16>(row, e);
+    }
+    wave_lds_sync();
+  }
+  int id = -1;
+#pragma unroll 1
+  for (int k = 0; k < a.K; ++k) {
+    double best = (double)low_inf();
+    int at = first;
+#pragma unroll 4
+    for (int e = first; e < end; ++e)
+      if (c[e] > best) best = c[e], at = e;
+    const double top = all_max<64>(best);
+    if (!(top > (double)low_inf())) break;
+    const int e = __builtin_amdgcn_readlane(at, __builtin_ctzll(__ballot(best == top)));
+    if (lane == k) id = e;
+    if (lane == 0) c[e] = (double)low_inf();
+    wave_lds_sync();
+  }
+  store_entries<64, BF16>(a, row, t, id, (float)most, (float)total);
+}
+
+// How far off a score in fp32 may be.  Sigmoid: z = exp(-|l|) is off by 2^-23 of itself and
+// by |l| z 2^-24 <= 0.37 2^-24 for its rounded argument, one plus it by 2^-24, the reciprocal
+// by 2^-23: together less than 1.6 2^-23.  Softmax: the exponential likewise, and their sum, of
+// 32 values a lane one after another and in six steps between lanes, by 38 2^-24 of itself
+// beside, so less than 2^-18 of the largest score.
+__device__ __forceinline__ float score_error(const RouteArgs& a, float largest) {
+  return a.sigmoid ? 0x1p-22f : 0x1p-18f * largest;
+}
+
+// The first part of a wave's tokens in fp32; false for a token that has to be chosen again.
 template <int LPT, int PER, bool BF16>
-__global__ __launch_bounds__(kRouteThreads) void route(RouteArgs a) {
-  constexpr int kTokens = kRouteThreads / LPT;
-  typedef Choice<LPT, PER, double> Exact;
+__device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t) {
   const int at = lane_id() & (LPT - 1), first = at * PER;
-  float bias[PER];
+  const bool in = t < a.tokens;  // lanes without a token repeat the last one
+  const int64_t token = in ? t : a.tokens - 1;
+  const char* row = (const char*)a.logits + token * a.E * (BF16 ? 2 : 4);
+  float l[PER], bias[PER];
+  load_logits<PER, BF16>(row, first, a.E, low_inf(), l);
+  if (a.bias) {
+    load_logits<PER, false>((const char*)a.bias, first, a.E, 0.0f, bias);
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) bias[i] = 0.0f;
+  }
+  bool bad = false;
 #pragma unroll
   for (int i = 0; i < PER; ++i)
-    bias[i] = a.bias && first + i < a.E ? a.bias[first + i] : 0.0f;
-  for (int64_t base = (int64_t)blockIdx.x * kTokens; base < a.tokens;
-       base += (int64_t)gridDim.x * kTokens) {
-    const int64_t t = base + threadIdx.x / LPT;
-    const bool in = t < a.tokens;  // lanes without a token repeat the last one
-    const int64_t token = in ? t : a.tokens - 1;
-    const char* row = (const char*)a.logits + token * a.E * (BF16 ? 2 : 4);
-    float l[PER];
-    load_logits<PER, BF16>(row, first, a.E, low_inf(), l);
-    bool bad = false;
+    bad |= l[i] != l[i] || (!a.sigmoid && l[i] == __builtin_inff());
+
+  Choice<LPT, PER> choice(a);
+  if (!a.sigmoid && (a.scored || !a.normalize)) choice.softmax_sums(l);
+  bad |= choice.fill(l, bias);
+  bad = token_bits<LPT>(__ballot(bad)) != 0;
+  // two choices have to be this far apart, four (a group's sum of two) twice as far
+  const float sure = a.scored ? 2.0f * score_error(a, choice.part) : 0.0f;
+  bool close = false;
+  if (a.groups_kept < a.groups) close = choice.keep_groups(2.0f * sure) && a.scored;
+  if (a.scored && !a.bias)  // the logits are in the scores' order, and told apart where those are 1
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      bad |= l[i] != l[i] || (!a.sigmoid && l[i] == __builtin_inff());
+      if (choice.c[i] > low_inf()) choice.c[i] = l[i];
+  // one more than asked for: the last one's distance counts too
+  const bool check = a.bias != nullptr, fits = a.K < LPT;
+  float value;
+  int id;
+  choice.largest(check && fits ? a.K + 1 : a.K, value, id);
+  if (check) {
+    // Equal logits and biases make equal choices, in any number of bits; of the last one
+    // and the first that is left out that says nothing of the others left out.
+    const float mine = id >= 0 ? logit_at<BF16>(row, id) : low_inf();
+    const float own = id >= 0 ? a.bias[id] : 0.0f;
+    const int next = (at + 1) & (LPT - 1);
+    const float below = of_lane<LPT>(value, next), l_below = of_lane<LPT>(mine, next);
+    const float b_below = of_lane<LPT>(own, next);
+    close |= at < a.K && at + 1 < LPT && id >= 0 && below > low_inf() &&
+             !(value - below > sure + 0x1p-23f * (fabsf(value) + fabsf(below))) &&
+             !(at + 1 < a.K && mine == l_below && own == b_below);
+    close |= !fits;
+  }
+  if (bad || at >= a.K) id = -1;
+  store_entries<LPT, BF16>(a, row, t, id, choice.most, choice.total);
+  if (bad && in && at == 0) set_err(a.err, EP_DEVERR_LOGITS);
+  return !in || bad || token_bits<LPT>(__ballot(close)) == 0;
+}
 
-    Exact exact(a);
-    if (!a.sigmoid && (a.scored || !a.normalize)) exact.softmax_sums(l);
-    bad |= exact.fill(l, bias);
-    bad = token_bits<LPT>(__ballot(bad)) != 0;
-    if (a.groups_kept < a.groups) exact.keep_groups();
-    if (a.scored && !a.bias)  // the logits are in the scores' order, and told apart where those are 1
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (exact.c[i] > (double)low_inf()) exact.c[i] = l[i];
-    double value;
-    int id;
-    exact.largest(a.K, value, id);
-    if (bad) id = -1;
-
-    // weights: lane k has entry k
-    const bool has = id >= 0;
-    float mine = low_inf();
-    if (has)
-      mine = BF16 ? __uint_as_float((uint32_t)((const uint16_t*)row)[id] << 16)
-                  : ((const float*)row)[id];
-    const float top = all_max<LPT>(mine);
-    float w = 0.0f;
-    if (has) {
-      // sigmoids so small that they might vanish are exponentials
-      if (a.sigmoid && !(a.normalize && top < -30.0f)) w = sigmoid_of(mine);
-      else if (a.normalize) w = expf(mine - top);
-      else w = expf(mine - (float)exact.most) / (float)exact.total;
+template <int LPT, int PER, bool BF16>
+__global__ __launch_bounds__(kRouteThreads, PER <= 16 ? 4 : 1) void route(RouteArgs a) {
+  constexpr int kTokens = kRouteThreads / LPT, kWaveTokens = kWave / LPT;
+  extern __shared__ double choices[];  // where choices are scores: [waves][E]
+  const int wave = uniform(threadIdx.x / kWave);
+  const int64_t step = (int64_t)gridDim.x * kTokens;
+  const int64_t mine = (int64_t)blockIdx.x * kTokens + wave * kWaveTokens;
+  for (int64_t base = mine; base < a.tokens;) {
+    // as many rounds as a word has bits for their tokens, then those that have to be chosen
+    // again: their code keeps its registers out of the loop that all tokens take
+    uint64_t again = 0;
+    const int64_t start = base;
+    for (int r = 0; r < LPT && base < a.tokens; ++r, base += step) {
+      const bool sure = route_fast<LPT, PER, BF16>(a, base + lane_id() / LPT);
+      uint64_t at = __ballot(!sure && (lane_id() & (LPT - 1)) == 0);
+      for (; at; at &= at - 1)
+        again |= 1ull << (r * kWaveTokens + __builtin_ctzll(at) / LPT);
     }
-    if (a.normalize) {
-      const float sum = all_sum<LPT>(w);
-      if (has) w = w / sum;
+    for (; again; again &= again - 1) {  // rarely
+      const int bit = __builtin_ctzll(again);
+      route_exactly<BF16>(a, start + (bit / kWaveTokens) * step + bit % kWaveTokens,
+                          choices + wave * a.E);
     }
-    if (in && at < a.K) {
-      a.idx[t * a.K + at] = id;
-      a.weights[t * a.K + at] = w * a.scale;
-    }
-    if (bad && in && at == 0) set_err(a.err, EP_DEVERR_LOGITS);
   }
 }
 
 // ---- gradient -----------------------------------------------------------------------
 
+// PER consecutive values of a row, as one vector where all lanes' are whole
 template <int PER, bool BF16>
 __device__ __forceinline__ void store_logits(char* row, int first, int E, const float (&g)[PER]) {
+  constexpr int kBytes = PER * (BF16 ? 2 : 4);
+  if (PER > 1 && E % PER == 0) {
+    if (first >= E) return;
+    uint32_t w[kBytes / 4];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    if (first + i < E) {
-      if (BF16) ((__bf16*)row)[first + i] = (__bf16)g[i];
-      else ((float*)row)[first + i] = g[i];
+    for (int i = 0; i < kBytes / 4; ++i)
+      w[i] = BF16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(
+                                                     (f32x2){g[2 * i], g[2 * i + 1]}, bf16x2))
+                  : __float_as_uint(g[i]);
+    char* to = row + (int64_t)first * (BF16 ? 2 : 4);
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i)
+        ((uint4*)to)[i] = uint4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+    } else if constexpr (kBytes == 8) {
+      *(uint2*)to = uint2{w[0], w[1]};
+    } else {
+      *(uint32_t*)to = w[0];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (first + i < E) {
+        if (BF16) ((__bf16*)row)[first + i] = (__bf16)g[i];
+        else ((float*)row)[first + i] = g[i];
+      }
     }
   }
 }
 
+// Entry k's terms are computed in the token's lane k and spread over the row in LDS.
 template <int LPT, int PER, bool BF16>
 __global__ __launch_bounds__(kRouteThreads) void route_grad(RouteGradArgs a) {
   constexpr int kTokens = kRouteThreads / LPT;
+  __shared__ __align__(16) float rows[kTokens][LPT * PER];
   const int at = lane_id() & (LPT - 1), first = at * PER;
+  float* const spread = rows[threadIdx.x / LPT];
+  const bool dense = !a.sigmoid && !a.normalize;  // every expert has a gradient
+#pragma unroll
+  for (int i = 0; i < PER; ++i) spread[first + i] = 0.0f;
+  wave_lds_sync();
   for (int64_t base = (int64_t)blockIdx.x * kTokens; base < a.tokens;
        base += (int64_t)gridDim.x * kTokens) {
     const int64_t t = base + threadIdx.x / LPT;
     const bool in = t < a.tokens;
     const int64_t token = in ? t : a.tokens - 1;
     const int64_t size = BF16 ? 2 : 4;
-    float l[PER];
-    load_logits<PER, BF16>((const char*)a.logits + token * a.E * size, first, a.E, low_inf(), l);
+    const char* row = (const char*)a.logits + token * a.E * size;
     int id = at < a.K ? a.idx[token * a.K + at] : -1;
     float dw = at < a.K ? a.dweights[token * a.K + at] : 0.0f;
+    float l[PER];
+    if (dense) load_logits<PER, BF16>(row, first, a.E, low_inf(), l);
     if (id < -1 || id >= a.E) {
       if (in) set_err(a.err, EP_DEVERR_TOPK_RANGE);
       id = -1;
     }
-    // an expert's part of the entries: how many name it, and the sum of their gradients
-    float count[PER], d[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) count[i] = d[i] = 0.0f;
-    bool any = false;
-    for (int k = 0; k < a.K; ++k) {
-      const int e = of_lane<LPT>(id, k);
-      const float g = of_lane<LPT>(dw, k);
-      any |= e >= 0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (e == first + i) count[i] += 1.0f, d[i] += g;
-    }
-    float g[PER];
-    // softmax over the chosen experts where it is normalised, over all otherwise
-    float most = low_inf();
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (!a.normalize || count[i] > 0.0f) most = fmaxf(most, l[i]);
-    most = all_max<LPT>(most);
-    if (!(most > low_inf())) most = 0.0f;
-    const bool small = a.sigmoid && a.normalize && most < -30.0f;
-    float s[PER], rest[PER], sum = 0.0f, dot = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
+    const bool has = id >= 0;
+    if (!has) dw = 0.0f;
+    const bool any = token_bits<LPT>(__ballot(has)) != 0;
+    float g = dw;
+    if (!dense) {
+      const float mine = has ? logit_at<BF16>(row, id) : low_inf();
+      float s = 0.0f, rest = 1.0f, part = 1.0f, mean = 0.0f;
+      float top = all_max<LPT>(mine);
       if (a.sigmoid) {
-        const float z = expf(l[i] < 0.0f ? l[i] : -l[i]), r = 1.0f / (1.0f + z);
-        s[i] = l[i] < 0.0f ? z * r : r;
-        rest[i] = l[i] < 0.0f ? r : z * r;  // 1 - s
-        if (small) s[i] = expf(l[i] - most);
-      } else {
-        s[i] = expf(l[i] - most);
-        rest[i] = 1.0f;
+        const float z = exponential(mine < 0.0f ? mine : -mine), r = inverse(1.0f + z);
+        s = mine < 0.0f ? z * r : r;
+        rest = mine < 0.0f ? r : z * r;  // 1 - s
       }
       if (a.normalize) {
-        s[i] = count[i] > 0.0f ? s[i] : 0.0f;
-        sum += count[i] * s[i];
-      } else if (!a.sigmoid) {
-        sum += s[i];
+        // softmax over the chosen; sigmoids so small that they might vanish are exponentials
+        if (!(top > low_inf())) top = 0.0f;
+        if (!a.sigmoid || top < -30.0f) s = exponential(mine - top);
+        if (!has) s = 0.0f;
+        const float sum = all_sum<LPT>(s);
+        part = sum > 0.0f ? 1.0f / sum : 0.0f;
+        mean = all_sum<LPT>(dw * s) * part;
       }
-      dot += d[i] * s[i];
+      g = has ? a.scale * (s * part) * (dw - mean) * rest : 0.0f;
     }
-    float part = 1.0f, mean = 0.0f;
-    if (a.normalize || !a.sigmoid) {
-      sum = all_sum<LPT>(sum);
-      part = sum > 0.0f ? 1.0f / sum : 0.0f;
-      mean = all_sum<LPT>(dot) * part;
+    // an expert that several entries name gets their sum, from the first of them
+    float all = 0.0f;
+    bool again = false;
+    for (int k = 0; k < a.K; ++k) {
+      const bool same = of_lane<LPT>(id, k) == id;
+      const float other = of_lane<LPT>(g, k);
+      all += same ? other : 0.0f;
+      again |= same && k < at;
     }
+    const bool writes = has && !again;
+    if (writes) spread[id] = all;
+    wave_lds_sync();
+    float d[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const float less = a.normalize ? count[i] * mean : a.sigmoid ? 0.0f : mean;
-      g[i] = a.scale * (s[i] * part) * (d[i] - less) * rest[i];
-      // without a chosen expert there is no gradient, whatever the logits hold
-      if (!any || ((a.normalize || a.sigmoid) && count[i] == 0.0f)) g[i] = 0.0f;
+    for (int i = 0; i < PER; ++i) d[i] = spread[first + i];
+    wave_lds_sync();
+    if (writes) spread[id] = 0.0f;
+    wave_lds_sync();
+    if (dense) {
+      float most = l[0];
+#pragma unroll
+      for (int i = 1; i < PER; ++i) most = fmaxf(most, l[i]);
+      most = all_max<LPT>(most);
+      if (!(most > low_inf())) most = 0.0f;
+      float sum = 0.0f, dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        l[i] = exponential(l[i] - most);
+        sum += l[i];
+        dot = __builtin_fmaf(d[i], l[i], dot);
+      }
+      sum = all_sum<LPT>(sum);
+      dot = all_sum<LPT>(dot);
+      const float part = sum > 0.0f ? 1.0f / sum : 0.0f, mean = dot * part;
+      const float factor = any ? a.scale * part : 0.0f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) d[i] = any ? (l[i] * factor) * (d[i] - mean) : 0.0f;
     }
-    if (in)
-      store_logits<PER, BF16>((char*)a.dlogits + token * a.E * size, first, a.E, g);
+    if (in) store_logits<PER, BF16>((char*)a.dlogits + token * a.E * size, first, a.E, d);
   }
 }
 
@@ -516,11 +693,12 @@ constexpr int64_t kRouteBlocks = 8 * kCus;
   hipLaunchKernelGGL((KERNEL<LPT, PER, BF16>),                                                \
                      dim3((unsigned)std::min((a.tokens * LPT + kRouteThreads - 1) /           \
                                                  kRouteThreads, kRouteBlocks)),               \
-                     dim3(kRouteThreads), 0, st, a)
+                     dim3(kRouteThreads), lds, st, a)
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t st) {
   if (a.tokens == 0) return hipSuccess;
   const bool narrow = a.K < 16 && (a.groups_kept == a.groups || a.groups <= 16);
+  const size_t lds = a.scored ? kRouteThreads / kWave * a.E * sizeof(double) : 0;
   EP_ROUTE_FORMS(route);
   return hipGetLastError();
 }
@@ -528,6 +706,7 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t st) {
 hipError_t launch_route_grad(const RouteGradArgs& a, hipStream_t st) {
   if (a.tokens == 0) return hipSuccess;
   const bool narrow = a.K <= 16;
+  const size_t lds = 0;
   EP_ROUTE_FORMS(route_grad);
   return hipGetLastError();
 }

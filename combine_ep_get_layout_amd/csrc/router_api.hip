@@ -39,7 +39,7 @@ int ep_route(const ep_problem* p, const ep_router* r, const void* logits, const 
   if (st == EP_OK) st = router_ok(r, g);
   if (st != EP_OK) return st;
   if ((int64_t)g.R * g.T > 0 && (!logits || !topk_idx || !topk_weights)) return EP_ERR_NULL;
-  if (!aligned(logits, 16) || !aligned(bias, 4) || !aligned(topk_idx, 4) ||
+  if (!aligned(logits, 16) || !aligned(bias, 16) || !aligned(topk_idx, 4) ||
       !aligned(topk_weights, 4) || !aligned(err, 4))
     return EP_ERR_ALIGN;
   ep::RouteArgs a;

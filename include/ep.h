@@ -469,7 +469,7 @@ typedef struct ep_router {
  * whose logit, or bias, is -inf is not to be had; where fewer than K are left the rest of the
  * entries are -1 with weight 0 (as layout takes them).  A token with a NaN (logit, or bias),
  * or with a logit of +inf under softmax, gets -1 throughout and sets EP_DEVERR_LOGITS.
- * logits: [R][T][E], 16-byte aligned.  bias: [E] fp32 or NULL.  topk_idx: [R][T][K].
+ * logits: [R][T][E], bias: [E] fp32 or NULL, both 16-byte aligned.  topk_idx: [R][T][K].
  * topk_weights: [R][T][K].  err: [1], bits are OR-ed into it, or NULL.  p->mode, p->quant and
  * p->hidden are not used. */
 int ep_route(const ep_problem* p, const ep_router* r, const void* logits, const float* bias,

@@ -49,7 +49,7 @@ def test_router(call):
 def test_arrays():
     assert route(w=None) == NULL
     assert route(w=A + 2) == ALIGN
-    assert route(bias=A + 2) == ALIGN
+    assert route(bias=A + 4) == ALIGN
     assert route_bwd(dw=None) == NULL
     assert route_bwd(dl=None) == NULL
     assert route_bwd(dw=A + 2) == ALIGN
