@@ -121,6 +121,9 @@ struct Top2 {
       }
     }
   }
+  __device__ __forceinline__ V magnitude() const {
+    return (first > (V)low_inf() ? fabs(first) : (V)0) + (second > (V)low_inf() ? fabs(second) : (V)0);
+  }
   // the sum of the `top` largest that there are
   __device__ __forceinline__ V sum(int top) const {
     return top == 2 && second > (V)low_inf() ? first + second : first;
@@ -159,6 +162,14 @@ __device__ __forceinline__ double of_lane(double v, int from) {
 
 // ---- values ---------------------------------------------------------------------
 
+// The same value, of which the compiler knows nothing: what rare branches compute from it
+// stays in them instead of being kept in registers for all tokens (of 32,768 over 256
+// experts, with those of all rare branches a quarter of the instructions).
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // PER consecutive logits as fp32, `fill` past the last expert; -0 becomes 0, which it equals.
 template <int PER, bool BF16>
 __device__ __forceinline__ void load_logits(const char* row, int first, int E, float fill,
@@ -193,11 +204,12 @@ __device__ __forceinline__ void load_logits(const char* row, int first, int E, f
                             : __uint_as_float(u.w[i]));
   } else {
     // one lane's address, not one for each expert: that many registers would halve the waves
-    const char* from = row + (int64_t)first * (BF16 ? 2 : 4);
+    const int f = here(first);
+    const char* from = row + (int64_t)f * (BF16 ? 2 : 4);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       l[i] = fill;
-      if (first + i < E)
+      if (f + i < E)
         l[i] = 0.0f + (BF16 ? __uint_as_float((uint32_t)((const uint16_t*)from)[i] << 16)
                             : ((const float*)from)[i]);
     }
@@ -205,13 +217,15 @@ __device__ __forceinline__ void load_logits(const char* row, int first, int E, f
 }
 
 // In fp32 the hardware's exponential and reciprocal, for choices and gradients: the
-// exponential's argument times log2 e is rounded to 2^-24 of itself.
-__device__ __forceinline__ float exponential(float v) { return __expf(v); }
+// exponential's argument times log2 e is rounded to 2^-24 of itself, results below 2^-126 are 0.
+__device__ __forceinline__ float exponential(float v) {
+  return __builtin_amdgcn_exp2f(v * 1.4426950408889634f);
+}
 __device__ __forceinline__ float inverse(float v) { return __builtin_amdgcn_rcpf(v); }
 
 // 1 / (1 + exp(-v)), relatively exact for large negative v too
 __device__ __forceinline__ float sigmoid_of(float v) {
-  const float z = exponential(v < 0.0f ? v : -v);
+  const float z = exponential(-fabsf(v));
   return (v < 0.0f ? z : 1.0f) * inverse(1.0f + z);
 }
 
@@ -234,11 +248,6 @@ struct Choice {
   __device__ __forceinline__ explicit Choice(const RouteArgs& a_)
       : a(a_), at(lane_id() & (LPT - 1)), first(at * PER) {}
 
-  __device__ __forceinline__ float score(float l) const {
-    if (a.sigmoid) return sigmoid_of(l);
-    return exponential(l - most) * part;
-  }
-
   __device__ __forceinline__ void softmax_sums(const float (&l)[PER]) {
     float m = l[0];
 #pragma unroll
@@ -252,28 +261,45 @@ struct Choice {
     part = inverse(total);
   }
 
-  // c of every expert; whether some is not a number
-  __device__ __forceinline__ bool fill(const float (&l)[PER], const float (&bias)[PER]) {
+  // c of every expert; whether some is not a number.  One branch for all values.
+  __device__ __forceinline__ bool fill(const float (&l)[PER], const float* bias_row) {
+    if (!a.scored) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c[i] = l[i];
+    } else {
+      float bias[PER];
+      if (bias_row) {
+        load_logits<PER, false>((const char*)bias_row, first, a.E, 0.0f, bias);
+      } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) bias[i] = 0.0f;
+      }
+      if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) c[i] = sigmoid_of(l[i]) + bias[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) c[i] = __builtin_fmaf(exponential(l[i] - most), part, bias[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c[i] = l[i] == low_inf() ? low_inf() : c[i];
+    }
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (a.scored) {
-        c[i] = l[i] > low_inf() ? score(l[i]) + bias[i] : low_inf();
-        bad |= c[i] != c[i];
-      } else {
-        c[i] = l[i];
-      }
-    }
+    for (int i = 0; i < PER; ++i) bad |= c[i] != c[i];
+    if (!a.sigmoid)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) bad |= l[i] == __builtin_inff();
     return bad;
   }
 
-  // Experts outside the kept groups to -inf.  close: whether the last kept group is no more
-  // than `sure` and 2^-21 of both ahead of the first one left.
+  // Experts outside the kept groups to -inf.  Whether the last kept group is no more than
+  // `sure` and 2^-22 of the choices in a sum (its additions) ahead of the first one left.
   __device__ __forceinline__ bool keep_groups(float sure) {
     const int size = a.group_size, lanes = size / PER;
     float mine;       // the score of group at / lanes, or of group `at`
     bool stays[PER];
-    float lowest = __builtin_inff(), highest = low_inf();
+    float lowest = __builtin_inff(), highest = low_inf(), size_of = 0.0f;
     if (size % PER == 0 && (lanes & (lanes - 1)) == 0 && lanes <= LPT) {
       // a group is a power of two of lanes
       Top2<float> top{c[0], low_inf()};
@@ -281,6 +307,7 @@ struct Choice {
       for (int i = 1; i < PER; ++i) top.add(c[i]);
       top.template join<LPT>(lanes);
       mine = top.sum(a.group_top);
+      size_of = top.magnitude();
       const int own = at / lanes;
       int rank = 0;
       for (int g = 0; g < a.groups; ++g) {
@@ -296,13 +323,15 @@ struct Choice {
       mine = low_inf();
       for (int g = 0; g < a.groups; ++g) {
         Top2<float> top{low_inf(), low_inf()};
+        const int f = here(first) - g * size;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          const int e = first + i - g * size;
+          const int e = f + i;
           top.add(e >= 0 && e < size ? c[i] : low_inf());
         }
         top.template join<LPT>(LPT);
         if (g == at) mine = top.sum(a.group_top);
+        size_of = fmaxf(size_of, top.magnitude());
       }
       int rank = 0;
       for (int g = 0; g < a.groups; ++g) {
@@ -311,7 +340,8 @@ struct Choice {
       }
       const bool in = at < a.groups, stay = in && rank < a.groups_kept;
       const uint64_t kept = token_bits<LPT>(__ballot(stay));
-      int group = first / size, rest = first - group * size;
+      const int f = here(first);
+      int group = f / size, rest = f - group * size;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         stays[i] = group < a.groups && (kept >> group & 1) != 0;
@@ -325,8 +355,7 @@ struct Choice {
       if (!stays[i]) c[i] = low_inf();
     lowest = -all_max<LPT>(-lowest);
     highest = all_max<LPT>(highest);
-    const float size_of = fabsf(lowest) + fabsf(highest);
-    return highest > low_inf() && !(lowest - highest > sure + 0x1p-21f * size_of);
+    return highest > low_inf() && !(lowest - highest > sure + 0x1p-22f * all_max<LPT>(size_of));
   }
 
   // The n largest, one a lane: id -1 where there are no more.
@@ -453,6 +482,96 @@ __device__ __forceinline__ void route_exactly(const RouteArgs& a, int64_t t, dou
   store_entries<64, BF16>(a, row, t, id, (float)most, (float)total);
 }
 
+// A token's candidates, one in each of its 16 lanes: value (-inf: none) and expert.
+struct Candidate {
+  float value;
+  int id;
+};
+
+// v of the token's lane `by` places on, in turn
+template <int BY>
+__device__ __forceinline__ float rotated(float v) {
+  return __uint_as_float(dpp<0x120 + BY>(__float_as_uint(v)));
+}
+template <int BY>
+__device__ __forceinline__ int rotated(int v) {
+  return (int)dpp<0x120 + BY>((uint32_t)v);
+}
+template <int BY>
+__device__ __forceinline__ double rotated(double v) {
+  const uint64_t bits = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp<0x120 + BY>((uint32_t)(bits >> 32)) << 32 |
+                                        dpp<0x120 + BY>((uint32_t)bits));
+}
+
+// Calls f with 1 .. 15, as constants.
+template <int BY = 1, class F>
+__device__ __forceinline__ void each_rotation(F f) {
+  if constexpr (BY < 16) {
+    f(std::integral_constant<int, BY>());
+    each_rotation<BY + 1>(f);
+  }
+}
+
+// How many of the token's candidates come before this lane's.
+template <class V>
+__device__ __forceinline__ int rank_of(V value, int id) {
+  int rank = 0;
+  each_rotation([&](auto by) {
+    const V v = rotated<decltype(by)::value>(value);
+    const int e = rotated<decltype(by)::value>(id);
+    rank += v > value || (v == value && e < id);
+  });
+  return rank;
+}
+
+// The candidates of 16 lanes with PER choices each: the n largest (n <= 16), or all that there
+// are, and, with sure > 0, all that are no more than sure and 2^-23 of both below the n-th.
+// False where they are more than 16.  Of the lanes' two largest the n-th is found by counting;
+// it is no larger than the n-th of all.  (One round for each of the n largest over all lanes takes three times the instructions.)
+template <int PER>
+__device__ __forceinline__ bool candidates(const float (&c)[PER], int first, int n, float sure,
+                                           Candidate* slots, Candidate& mine) {
+  const int at = lane_id() & 15;
+  Top2<float> top{c[0], low_inf()};
+#pragma unroll
+  for (int i = 1; i < PER; ++i) top.add(c[i]);
+  int above_first = 0, above_second = 1;
+  each_rotation([&](auto by) {
+    const float a = rotated<decltype(by)::value>(top.first);
+    const float b = rotated<decltype(by)::value>(top.second);
+    above_first += a > top.first;
+    above_first += b > top.first;
+    above_second += a > top.second;
+    above_second += b > top.second;
+  });
+  // the smallest of those with fewer than n above them
+  const float least = above_second < n ? top.second : above_first < n ? top.first : __builtin_inff();
+  float from = -all_max<16>(-least);
+  // the n-th of all lies between this and the largest
+  if (sure > 0.0f) from -= sure + 0x1p-21f * (fabsf(from) + fabsf(all_max<16>(top.first)));
+  if (!(from > low_inf())) from = -__FLT_MAX__;  // every number
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) count += c[i] >= from;
+  int upto = count;
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) {
+    const int v = __shfl_up(upto, d, 16);
+    if (at >= d) upto += v;
+  }
+  const int total = of_lane<16>(upto, 15);
+  Candidate* to = slots + upto - count;
+  if (total <= 16)
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (c[i] >= from) *to++ = Candidate{c[i], first + i};
+  wave_lds_sync();
+  mine = at < total && total <= 16 ? slots[at] : Candidate{low_inf(), -1};
+  wave_lds_sync();
+  return total <= 16;
+}
+
 // How far off a score in fp32 may be.  Sigmoid: z = exp(-|l|) is off by 2^-23 of itself and
 // by |l| z 2^-24 <= 0.37 2^-24 for its rounded argument, one plus it by 2^-24, the reciprocal
 // by 2^-23: together less than 1.6 2^-23.  Softmax: the exponential likewise, and their sum, of
@@ -464,28 +583,16 @@ __device__ __forceinline__ float score_error(const RouteArgs& a, float largest) 
 
 // The first part of a wave's tokens in fp32; false for a token that has to be chosen again.
 template <int LPT, int PER, bool BF16>
-__device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t) {
+__device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t, Candidate* slots) {
   const int at = lane_id() & (LPT - 1), first = at * PER;
   const bool in = t < a.tokens;  // lanes without a token repeat the last one
   const int64_t token = in ? t : a.tokens - 1;
   const char* row = (const char*)a.logits + token * a.E * (BF16 ? 2 : 4);
-  float l[PER], bias[PER];
+  float l[PER];
   load_logits<PER, BF16>(row, first, a.E, low_inf(), l);
-  if (a.bias) {
-    load_logits<PER, false>((const char*)a.bias, first, a.E, 0.0f, bias);
-  } else {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) bias[i] = 0.0f;
-  }
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < PER; ++i)
-    bad |= l[i] != l[i] || (!a.sigmoid && l[i] == __builtin_inff());
-
   Choice<LPT, PER> choice(a);
   if (!a.sigmoid && (a.scored || !a.normalize)) choice.softmax_sums(l);
-  bad |= choice.fill(l, bias);
-  bad = token_bits<LPT>(__ballot(bad)) != 0;
+  const bool bad = token_bits<LPT>(__ballot(choice.fill(l, a.bias))) != 0;
   // two choices have to be this far apart, four (a group's sum of two) twice as far
   const float sure = a.scored ? 2.0f * score_error(a, choice.part) : 0.0f;
   bool close = false;
@@ -494,23 +601,64 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t) {
 #pragma unroll
     for (int i = 0; i < PER; ++i)
       if (choice.c[i] > low_inf()) choice.c[i] = l[i];
-  // one more than asked for: the last one's distance counts too
-  const bool check = a.bias != nullptr, fits = a.K < LPT;
+  const bool check = a.bias != nullptr;
   float value;
   int id;
-  choice.largest(check && fits ? a.K + 1 : a.K, value, id);
-  if (check) {
-    // Equal logits and biases make equal choices, in any number of bits; of the last one
-    // and the first that is left out that says nothing of the others left out.
-    const float mine = id >= 0 ? logit_at<BF16>(row, id) : low_inf();
-    const float own = id >= 0 ? a.bias[id] : 0.0f;
-    const int next = (at + 1) & (LPT - 1);
-    const float below = of_lane<LPT>(value, next), l_below = of_lane<LPT>(mine, next);
-    const float b_below = of_lane<LPT>(own, next);
-    close |= at < a.K && at + 1 < LPT && id >= 0 && below > low_inf() &&
-             !(value - below > sure + 0x1p-23f * (fabsf(value) + fabsf(below))) &&
-             !(at + 1 < a.K && mine == l_below && own == b_below);
-    close |= !fits;
+  bool chosen = false;
+  if constexpr (LPT == 16) {
+    // n candidates and those that might be as large as the last of them
+    Candidate mine;
+    chosen = __ballot(!candidates<PER>(choice.c, first, a.K, check ? sure : 0.0f, slots, mine)) == 0;
+    if (chosen) {
+      int rank = rank_of(mine.value, mine.id);
+      if (check) {
+        // two that are nearer to each other than fp32 tells, one of them among the first K
+        bool near = false;
+        each_rotation([&](auto by) {
+          const float other = rotated<decltype(by)::value>(mine.value);
+          near |= other > low_inf() && !(fabsf(mine.value - other) >
+                                         sure + 0x1p-23f * (fabsf(mine.value) + fabsf(other)));
+        });
+        near = near && mine.id >= 0 && rank < a.K && !bad;
+        if (__ballot(near) != 0) {
+          if (a.sigmoid) {
+            const double l = mine.id >= 0 ? (double)logit_at<BF16>(row, mine.id) : 0.0;
+            const double z = exp(l < 0.0 ? l : -l);
+            const double by = mine.id >= 0 ? (l < 0.0 ? z : 1.0) / (1.0 + z) + (double)a.bias[mine.id]
+                                           : (double)low_inf();
+            rank = rank_of(by, mine.id);
+          } else {
+            close |= near;  // the sum of all in 64 bits
+          }
+        }
+      }
+      // lanes without a candidate come after all that have one, each at a rank of its own
+      if (mine.id < 0) rank = at;
+      slots[at].id = -1;
+      wave_lds_sync();
+      if (mine.id >= 0) slots[rank].id = mine.id;
+      wave_lds_sync();
+      id = slots[at].id;
+      wave_lds_sync();
+    }
+  }
+  if (!chosen) {
+    // one more than asked for: the last one's distance counts too
+    const bool fits = a.K < LPT;
+    choice.largest(check && fits ? a.K + 1 : a.K, value, id);
+    if (check) {
+      // Equal logits and biases make equal choices, in any number of bits; of the last one
+      // and the first that is left out that says nothing of the others left out.
+      const float mine = id >= 0 ? logit_at<BF16>(row, id) : low_inf();
+      const float own = id >= 0 ? a.bias[id] : 0.0f;
+      const int next = (at + 1) & (LPT - 1);
+      const float below = of_lane<LPT>(value, next), l_below = of_lane<LPT>(mine, next);
+      const float b_below = of_lane<LPT>(own, next);
+      close |= at < a.K && at + 1 < LPT && id >= 0 && below > low_inf() &&
+               !(value - below > sure + 0x1p-23f * (fabsf(value) + fabsf(below))) &&
+               !(at + 1 < a.K && mine == l_below && own == b_below);
+      close |= !fits;
+    }
   }
   if (bad || at >= a.K) id = -1;
   store_entries<LPT, BF16>(a, row, t, id, choice.most, choice.total);
@@ -519,8 +667,9 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t) {
 }
 
 template <int LPT, int PER, bool BF16>
-__global__ __launch_bounds__(kRouteThreads, PER <= 16 ? 4 : 1) void route(RouteArgs a) {
+__global__ __launch_bounds__(kRouteThreads, PER <= 16 ? 3 : 1) void route(RouteArgs a) {
   constexpr int kTokens = kRouteThreads / LPT, kWaveTokens = kWave / LPT;
+  __shared__ Candidate slots[LPT == 16 ? kTokens : 1][16];
   extern __shared__ double choices[];  // where choices are scores: [waves][E]
   const int wave = uniform(threadIdx.x / kWave);
   const int64_t step = (int64_t)gridDim.x * kTokens;
@@ -531,7 +680,8 @@ __global__ __launch_bounds__(kRouteThreads, PER <= 16 ? 4 : 1) void route(RouteA
     uint64_t again = 0;
     const int64_t start = base;
     for (int r = 0; r < LPT && base < a.tokens; ++r, base += step) {
-      const bool sure = route_fast<LPT, PER, BF16>(a, base + lane_id() / LPT);
+      const bool sure = route_fast<LPT, PER, BF16>(a, base + lane_id() / LPT,
+                                                   slots[LPT == 16 ? threadIdx.x / LPT : 0]);
       uint64_t at = __ballot(!sure && (lane_id() & (LPT - 1)) == 0);
       for (; at; at &= at - 1)
         again |= 1ull << (r * kWaveTokens + __builtin_ctzll(at) / LPT);
@@ -569,11 +719,13 @@ __device__ __forceinline__ void store_logits(char* row, int first, int E, const 
       *(uint32_t*)to = w[0];
     }
   } else {
+    const int f = here(first);
+    char* to = row + (int64_t)f * (BF16 ? 2 : 4);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      if (first + i < E) {
-        if (BF16) ((__bf16*)row)[first + i] = (__bf16)g[i];
-        else ((float*)row)[first + i] = g[i];
+      if (f + i < E) {
+        if (BF16) ((__bf16*)to)[i] = (__bf16)g[i];
+        else ((float*)to)[i] = g[i];
       }
     }
   }
