@@ -71,8 +71,9 @@ struct Tile {
   int e, rows, n0;
 };
 
-// One workgroup's state: where its loads read, and the epilogue.  Q: EP_QUANT_*
-template <class S, bool GATED, int Q>
+// One workgroup's state: where its loads read, and the epilogue.  Q: EP_QUANT_*; ONCE: the
+// weights are read by one tile each.
+template <class S, bool GATED, int Q, bool ONCE>
 struct Forward {
   static constexpr bool INT8 = Q == EP_QUANT_INT8;
   static constexpr bool FP8 = Q != EP_QUANT_NONE && !INT8;
@@ -188,7 +189,7 @@ struct Forward {
   __device__ __forceinline__ void load_at(int k, lds_char* buf, int p) {
     const int64_t at = (int64_t)turned(k) * S::KB;
     if (p < Chan::kPasses)
-      w_tile.template load<kPeriod>(p, gate_base + at, up_base + at, buf);
+      w_tile.template load<kPeriod, ONCE>(p, gate_base + at, up_base + at, buf);
     else
       x_tile.template load<1 << 20>(p - Chan::kPasses, x_base + at, nullptr, buf + Chan::kBytes);
   }
@@ -365,9 +366,9 @@ struct Forward {
   }
 };
 
-template <class S, bool GATED, int Q>
+template <class S, bool GATED, int Q, bool ONCE = false>
 __global__ __launch_bounds__(kGemmThreads, 1) void expert_forward(ExpertArgs a) {
-  typedef Forward<S, GATED, Q> F;
+  typedef Forward<S, GATED, Q, ONCE> F;
   __shared__ __align__(16) char lds[S::STAGES][F::kSlot];
   // FP8: every wave's own copy of its rows' scales and, behind them, of its two
   // weight blocks'.  They come by the same asynchronous loads as the tiles: a
@@ -412,22 +413,21 @@ typedef Shape<NarrowDims> Narrow;
 typedef Shape<SmallDims> Small;
 typedef Shape<TinyDims> Tiny;
 
-template <class S, bool GATED, int Q>
+template <class S, bool GATED, int Q, bool ONCE = false>
 static void launch(const ExpertArgs& a, hipStream_t st) {
   const int on = GATED ? S::BN / 2 : S::BN;
   const int64_t tiles = ((a.rows + S::BM - 1) / S::BM + a.seg.E) * ((a.N + on - 1) / on);
   constexpr int64_t kSlots = forward_slots<S, Q != EP_QUANT_NONE && Q != EP_QUANT_INT8>();
-  hipLaunchKernelGGL((expert_forward<S, GATED, Q>), dim3((unsigned)std::min(tiles, kSlots)),
+  hipLaunchKernelGGL((expert_forward<S, GATED, Q, ONCE>), dim3((unsigned)std::min(tiles, kSlots)),
                      dim3(kGemmThreads), 0, st, a);
 }
 
 template <bool GATED, int Q>
 static void choose(const ExpertArgs& a, hipStream_t st) {
-  constexpr bool INT8 = Q == EP_QUANT_INT8, FP8 = Q != EP_QUANT_NONE && !INT8;
+  constexpr bool FP8 = Q != EP_QUANT_NONE;
   typedef typename std::conditional<FP8, Big8, Big>::type Large;
-  // 8-bit integers run through the bf16 kernels' tiles with half the contraction's bytes
-  switch (choose_forward<FP8>(a.seg.E, a.rows, INT8 ? a.C / 2 : a.C,
-                              (int64_t)a.N * (GATED ? 2 : 1), a.y_quant != EP_QUANT_NONE)) {
+  switch (choose_forward<FP8>(a.seg.E, a.rows, a.C, (int64_t)a.N * (GATED ? 2 : 1),
+                              a.y_quant != EP_QUANT_NONE)) {
     case kTinyTile: return launch<Tiny, GATED, Q>(a, st);
     case kSmallTile: return launch<Small, GATED, Q>(a, st);
     case kNarrowTile: return launch<Narrow, GATED, Q>(a, st);
@@ -436,12 +436,37 @@ static void choose(const ExpertArgs& a, hipStream_t st) {
   }
 }
 
+// 8-bit integers.  Where an expert has half a tile's rows or fewer, most have one tile, which
+// alone reads the weights: they go past the caches (256 experts, 7168 -> 2 x 2048, 2 / 8 / 32
+// rows each: 1055 -> 939, 1274 -> 1161, 1321 -> 1235 us; with 64 rows, 4096 -> 2 x 2048, 880
+// -> 981).
+template <class S, bool GATED>
+static void launch_int8(const ExpertArgs& a, hipStream_t st) {
+  if (2 * a.rows <= std::min<int64_t>(a.rows, a.seg.E) * S::BM)
+    launch<S, GATED, EP_QUANT_INT8, true>(a, st);
+  else
+    launch<S, GATED, EP_QUANT_INT8>(a, st);
+}
+
+template <bool GATED>
+static void choose_int8(const ExpertArgs& a, hipStream_t st) {
+  switch (choose_forward_int8(a.seg.E, a.rows, a.C, a.N, GATED)) {
+    case kTinyTile: return launch_int8<Tiny, GATED>(a, st);
+    case kSmallTile: return launch_int8<Small, GATED>(a, st);
+    case kNarrowTile: return launch_int8<Narrow, GATED>(a, st);
+    case kMediumTile: return launch_int8<Medium, GATED>(a, st);
+    case kLargeTile:
+      if (short_int8(a.C, GATED)) return launch<Big8, GATED, EP_QUANT_INT8>(a, st);
+      return launch<Big, GATED, EP_QUANT_INT8>(a, st);
+  }
+}
+
 template <bool GATED>
 static void choose(const ExpertArgs& a, hipStream_t st) {
   switch (a.quant) {
     case EP_QUANT_NONE: return choose<GATED, EP_QUANT_NONE>(a, st);
     case EP_QUANT_FP8_F32: return choose<GATED, EP_QUANT_FP8_F32>(a, st);
-    case EP_QUANT_INT8: return choose<GATED, EP_QUANT_INT8>(a, st);
+    case EP_QUANT_INT8: return choose_int8<GATED>(a, st);
     default: return choose<GATED, EP_QUANT_FP8_UE8M0>(a, st);
   }
 }

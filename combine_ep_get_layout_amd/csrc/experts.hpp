@@ -248,6 +248,15 @@ __device__ __forceinline__ void load_lds16(const char* base, uint32_t off, const
                : "memory");
 }
 
+// The same of what is read once: past the caches, which other operands are read from.
+__device__ __forceinline__ void stream_lds16(const char* base, uint32_t off, const lds_char* dst) {
+  const char* from;
+  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0 nt"
+               : "=&s"(from)
+               : "s"(lds_offset(dst)), "v"(off), "s"(base)
+               : "memory");
+}
+
 // 4 bytes a lane, or one byte zero-extended to four
 template <bool BYTE>
 __device__ __forceinline__ void load_lds4(const char* base, uint32_t off, const lds_char* dst) {
@@ -317,15 +326,19 @@ struct RowTile {
       off[p] = row_of((p * kPassRows + tid / kChunks) % ROWS) + chunk(p) * 16;
   }
   // Pass p's load.  base: the tile's first byte of this step; the second half
-  // of every PERIOD rows comes from `other` (a gated block's ups).
-  template <int PERIOD>
+  // of every PERIOD rows comes from `other` (a gated block's ups).  ONCE: nobody else reads it.
+  template <int PERIOD, bool ONCE = false>
   __device__ __forceinline__ void load(int p, const char* base, const char* other,
                                        lds_char* lds) const {
     const int wave = uniform(threadIdx.x >> 6);
     // a wave's rows of a pass are all in one half
     const int r = p * kPassRows + (PERIOD / 2 % kPassRows == 0 ? 0 : wave * kWaveRows);
-    load_lds16(r % PERIOD >= PERIOD / 2 ? other : base, off[p],
-               lds + (p * 4096 + wave * 1024) % kBytes);
+    if constexpr (ONCE)
+      stream_lds16(r % PERIOD >= PERIOD / 2 ? other : base, off[p],
+                   lds + (p * 4096 + wave * 1024) % kBytes);
+    else
+      load_lds16(r % PERIOD >= PERIOD / 2 ? other : base, off[p],
+                 lds + (p * 4096 + wave * 1024) % kBytes);
   }
   // the last step of rows with fewer than KB bytes left
   template <int PERIOD>

@@ -121,6 +121,17 @@ ForwardShape choose_forward(int experts, int64_t rows, int C, int64_t wide, bool
   return medium < large ? kMediumTile : kLargeTile;
 }
 
+// 8-bit integers run through bf16's tiles with half the contraction's bytes.
+inline ForwardShape choose_forward_int8(int experts, int64_t rows, int C, int64_t N, bool gated) {
+  return choose_forward<false>(experts, rows, C / 2, gated ? 2 * N : N, false);
+}
+
+// And of the largest: a contraction of few stages takes the 256 x 128 ring (Big8Dims), whose
+// tiles start and end sooner, instead of 256 x 256.  us, 64 experts x 2,048 rows, Big /
+// Big8: to 4096 channels from 512 1009 / 717, 2048 1743 / 1484, 4096 2749 / 2688, 7168 4448 /
+// 4660; gated to 2 x 2048 from 512 675 / 597, 2048 1368 / 1340, 4096 2265 / 2451.
+inline bool short_int8(int C, bool gated) { return C <= (gated ? 2048 : 4096); }
+
 // ---- gradients -------------------------------------------------------------------
 
 namespace grad {

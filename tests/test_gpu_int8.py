@@ -8,8 +8,9 @@ follows is as in expert_util: activations (4 + |z|) 2^-22 relative and 1.13 time
 argument's error, bias, gate and residual a rounding of 2^-24 each (2^-23 is allowed), one
 rounding to bf16 (2^-8).
 
-The lists are those of the bf16 tests with twice the channels, so with the same bytes a row:
-every tile is taken through the same paths (tests/test_experts_choice.py)."""
+The lists are those of the bf16 tests with twice the channels, so with the same bytes a row,
+and LONG; tests/test_int8_choice.py asks the library's own choice whether they take every tile
+through every path of its loop."""
 import numpy as np
 import pytest
 import torch
@@ -284,7 +285,23 @@ def test_linear(shape, extras):
     check_linear(shape, extras)
 
 
-@pytest.mark.parametrize("shape", doubled(base.WIDE + tiles.BF16), ids=name)
+# more tiles of the two largest kinds than run at once, of contractions that each is chosen
+# for, with and without a rest; and many experts of one tile
+LONG = [
+    (1, 9000, 28, 4, N, 0.0, 2064, 272),
+    (1, 9000, 28, 4, N, 0.0, 2048, 272),
+    (1, 9000, 28, 4, N, 0.0, 4112, 272),
+    (1, 9000, 28, 4, N, 0.0, 4224, 272),
+    (1, 300, 96, 8, N, 0.0, 1296, 1032),
+    (1, 40, 96, 2, L, 0.0, 2320, 2056),
+    (1, 250, 24, 4, N, 0.0, 1312, 1304),
+    (1, 250, 24, 1, N, 0.0, 256, 1760),
+    (1, 12, 16, 2, N, 0.0, 1888, 584),
+    (1, 64, 64, 2, N, 0.0, 1824, 296),
+]
+
+
+@pytest.mark.parametrize("shape", doubled(base.WIDE + tiles.BF16) + LONG, ids=name)
 def test_wide(shape):
     say("wide int8", shape)
     check_gated(shape, "silu")
