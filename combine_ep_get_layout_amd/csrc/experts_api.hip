@@ -188,7 +188,7 @@ int layer_ok(const Geometry& g, int inner) {
 
 // The layer's workspace: h, and the entries' results where they do not fit the LDS.
 size_t layer_h_bytes(const Geometry& g, int inner) {
-  return ((size_t)g.R * g.T * g.K * inner * 2 + 255) & ~(size_t)255;
+  return ((size_t)g.R * g.T * g.K * inner * 4 + 255) & ~(size_t)255;
 }
 
 size_t layer_bytes(const Geometry& g, int inner) {

@@ -1,7 +1,10 @@
 // A whole MoE layer for a few tokens on gfx950, in two launches and without layout or
 // dispatch: for every token t and its entries (e, w),
-//   h = act(x Wg_e^T) * (x Wu_e^T),  rounded to bf16,        (layer_gated)
+//   h = act(x Wg_e^T) * (x Wu_e^T),                          (layer_gated)
 //   out_t = sum_k w_k h W2_e^T,      in fp32, in k order.    (layer_down)
+// h is kept as two bf16, its value rounded and what that leaves, 16 bits together: in one,
+// its rounding alone would be as large an error of the result as the result's own.  They are
+// two rows of the second product, whose sums are added.
 //
 // With few tokens the time is that of reading the weights of the experts that are hit.  A
 // wave multiplies 16 rows of weights (a strip) with up to 16 rows of one expert's entries.
@@ -335,6 +338,11 @@ __device__ __forceinline__ void halves(float v, float& a, float& b) {
   b = __uint_as_float(r[1]);
 }
 
+// What rounding leaves of h; nothing of a NaN or infinity, which is its rounded value alone.
+__device__ __forceinline__ float rest_of(float h, float rounded) {
+  return fabsf(rounded) < __builtin_inff() ? h - rounded : 0.0f;
+}
+
 // ---- gated block -------------------------------------------------------------------
 
 constexpr int kUpWaves = 4;    // of a workgroup
@@ -433,7 +441,7 @@ __global__ __launch_bounds__(kUpWaves* kWave) void layer_gated(LayerArgs a) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) halves(stream.acc[c][j][q], g[q], up[q]);
               }
-              bf16x2 out[2];
+              bf16x2 high[2], low[2];
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 if (KIND == EP_WEIGHTS_INT8) {
@@ -444,16 +452,27 @@ __global__ __launch_bounds__(kUpWaves* kWave) void layer_gated(LayerArgs a) {
                 }
                 float value, slope;
                 act_both(a.act, g[q], value, slope);
-                out[q / 2][q % 2] = (__bf16)(value * up[q]);
+                const float h = value * up[q];
+                high[q / 2][q % 2] = (__bf16)h;
+                low[q / 2][q % 2] = (__bf16)rest_of(h, (float)high[q / 2][q % 2]);
               }
               const int r = 16 * j + row;
-              if (lane < 32 && r < unit.rows)
-                *(uint2*)(a.h + (int64_t)unit.list[r] * a.I + n0 + ch) = __builtin_bit_cast(uint2, out);
+              if (lane < 32 && r < unit.rows) {
+                uint16_t* to = a.h + (int64_t)unit.list[r] * 2 * a.I + n0 + ch;
+                *(uint2*)to = __builtin_bit_cast(uint2, high);
+                *(uint2*)(to + a.I) = __builtin_bit_cast(uint2, low);
+              }
             }
           }
           if (WK > 1) barrier();
         }
       });
+}
+
+// v of the lane beside: even and odd ones in pairs
+__device__ __forceinline__ float neighbour(float v) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false));  // quad_perm 1,0,3,2
 }
 
 // ---- down projection and the weighted sum ---------------------------------------------
@@ -467,7 +486,8 @@ __global__ __launch_bounds__(WAVES* kWave) void layer_down(LayerArgs a) {
   typedef Stream<KIND, CT, NB, D> S;
   static_assert(!IN_LDS || CT == 1, "a place has 16 channels");
   __shared__ Routing routing;
-  __shared__ uint16_t lists[WAVES][2][S::kRows];
+  constexpr int kEntries = S::kRows / 2;  // a slot's, two rows each
+  __shared__ uint16_t lists[WAVES][2][kEntries];
   __shared__ __align__(16) char rings[WAVES][D * S::kSlot];
   __shared__ float weights[kLayerEntries];
   __shared__ __align__(16) float places[IN_LDS ? kLayerPlaces * 16 : 1];
@@ -492,7 +512,7 @@ __global__ __launch_bounds__(WAVES* kWave) void layer_down(LayerArgs a) {
   stream.run(
       part, parts,
       [&](Unit& unit) {
-        last.at += S::kRows;
+        last.at += kEntries;
         if (last.e < 0 || last.at >= last.n) {
           u += WAVES / parts;
           if (u >= hits.total) return false;
@@ -500,8 +520,8 @@ __global__ __launch_bounds__(WAVES* kWave) void layer_down(LayerArgs a) {
           last.at = 0;
         }
         last.list = lists[wave][turn ^= 1];
-        last.n = entries_of(a, routing, last.e, last.at, S::kRows, last.list);
-        last.rows = min(last.n - last.at, S::kRows);
+        last.n = entries_of(a, routing, last.e, last.at, kEntries, last.list);
+        last.rows = min(last.n - last.at, kEntries);
         unit = last;
         return true;
       },
@@ -511,7 +531,7 @@ __global__ __launch_bounds__(WAVES* kWave) void layer_down(LayerArgs a) {
             // past the last channel: that one again, not stored
             [&](int r) { return (uint32_t)(min(r, a.H - 1 - n0) * w_row); },
             [&](int r) {
-              return (uint32_t)unit.list[min(r, unit.rows - 1)] * (uint32_t)(a.I * 2);
+              return (unit.list[min(r / 2, unit.rows - 1)] * 2u + r % 2) * (uint32_t)(a.I * 2);
             });
       },
       [&](const Unit& unit, int line) {
@@ -521,12 +541,15 @@ __global__ __launch_bounds__(WAVES* kWave) void layer_down(LayerArgs a) {
       [&](const Unit& unit) {
 #pragma unroll
         for (int j = 0; j < S::TT; ++j)
-          if (16 * j + row < unit.rows)
 #pragma unroll
-            for (int c = 0; c < CT; ++c)
-              if (c == 0 || n0 + 16 * c < a.H)
-                *(f32x4*)(y + unit.list[16 * j + row] * y_row + 16 * c + 4 * (lane / 16)) =
-                    stream.acc[c][j];
+          for (int c = 0; c < CT; ++c) {
+            f32x4 sum = stream.acc[c][j];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sum[q] += neighbour(sum[q]);
+            const int r = (16 * j + row) / 2;
+            if (row % 2 == 0 && r < unit.rows && (c == 0 || n0 + 16 * c < a.H))
+              *(f32x4*)(y + unit.list[r] * y_row + 16 * c + 4 * (lane / 16)) = sum;
+          }
       });
   __syncthreads();
   for (int o = threadIdx.x; o < a.tokens * 16 * CT; o += WAVES * kWave) {
@@ -569,31 +592,49 @@ static void launch_down(const LayerArgs& a, hipStream_t st) {
 }
 
 // How many entries a slot has room for goes by how many an expert has on average: a wave
-// reads its weights once for each slot full of them.  us (gated and down together, bf16
-// 4096 -> 1408, 16 experts with 8 / 16 / 32 / 64 entries each): slots of 16 entries 104 / 151 /
-// 308 / 590, of 64 with two strips - / 160 / 190 / 283.  In 8 bits a slot's rows are as many
-// bytes as its weights, or more, so two strips share them: 32 experts with 4 / 16 entries 140 /
-// 255 with one strip, 112 / 220 with two.  With more than about 12 entries an expert layout,
-// dispatch, the experts' products and combine take less (136 / 152 / 150 us for 16 / 32 / 64).
+// reads its weights once for each slot full of them.  us (gated and down together with one row
+// of h an entry, bf16 4096 -> 1408, 16 experts with 8 / 16 / 32 / 64 entries each): slots of 16
+// entries 104 / 151 / 308 / 590, of 64 with two strips - / 160 / 190 / 283.  In 8 bits a slot's
+// rows are as many bytes as its weights, or more, so two strips share them: 32 experts with
+// 4 / 16 entries 140 / 255 with one strip, 112 / 220 with two.
 template <int KIND>
-static void choose(const LayerArgs& a, hipStream_t st) {
+static void choose_gated(const LayerArgs& a, int experts, hipStream_t st) {
   constexpr bool kBytes = KIND != EP_WEIGHTS_BF16;
-  const bool in_lds = a.entries <= kLayerPlaces;
-  const int experts = std::min(a.E, a.entries);
   if (2 * a.entries <= 3 * experts * (kBytes ? 2 : 4)) {  // 4 entries a slot, in bf16 8
     launch_gated<KIND, 1, 1, 3, 3>(a, st);
-    if (in_lds) launch_down<KIND, 1, 1, 3, 8, true>(a, st);
-    else launch_down<KIND, 1, 1, 3, 4, false>(a, st);
   } else if (a.entries <= 16 * experts) {  // 16
     constexpr int NB = kBytes ? 4 : 2, D = kBytes ? 2 : 3;
     launch_gated<KIND, kBytes ? 2 : 1, NB, D, D>(a, st);
-    if (in_lds) launch_down<KIND, 1, NB, D, kBytes ? 6 : 4, true>(a, st);
-    else launch_down<KIND, 1, NB, D, 4, false>(a, st);
   } else {  // 32, in bf16 64
     launch_gated<KIND, 2, 8, 3, 2>(a, st);
-    if (in_lds) launch_down<KIND, 1, 8, 3, 4, true>(a, st);
-    else launch_down<KIND, 1, 8, 3, 4, false>(a, st);
   }
+}
+
+// An entry has two rows here, a workgroup as many waves as the LDS has rings for, up to 8: slots
+// of 8 entries with 4 waves take 326 us for 128 experts with 4 entries each (bf16 2048 -> 768,
+// the whole layer), with 8 276; more (12 in FP8 for 4 entries) gain under 1%.  With more than
+// about 12 entries an expert layout, dispatch, the experts' products and combine are the faster
+// way (16 experts with 8 / 16 / 32 / 64: 128 / 136 / 152 / 150 us, this 112 / 162 / 207 / 339).
+template <int KIND, bool IN_LDS>
+static void choose_down(const LayerArgs& a, int experts, hipStream_t st) {
+  constexpr bool kBytes = KIND != EP_WEIGHTS_BF16;
+  if (a.entries <= 3 * experts) {  // 4 entries a slot
+    launch_down<KIND, 1, kBytes ? 2 : 1, 3, 8, IN_LDS>(a, st);
+  } else if (a.entries <= 5 * experts) {  // 8
+    launch_down<KIND, 1, kBytes ? 4 : 2, kBytes ? 2 : 3, 8, IN_LDS>(a, st);
+  } else if (kBytes || a.entries <= 12 * experts) {  // 16
+    launch_down<KIND, 1, kBytes ? 8 : 4, kBytes ? 2 : 3, IN_LDS ? 6 : 7, IN_LDS>(a, st);
+  } else {  // 32
+    launch_down<KIND, 1, 8, 2, IN_LDS ? 6 : 7, IN_LDS>(a, st);
+  }
+}
+
+template <int KIND>
+static void choose(const LayerArgs& a, hipStream_t st) {
+  const int experts = std::min(a.E, a.entries);
+  choose_gated<KIND>(a, experts, st);
+  if (a.entries <= kLayerPlaces) choose_down<KIND, true>(a, experts, st);
+  else choose_down<KIND, false>(a, experts, st);
 }
 
 hipError_t launch_layer(const LayerArgs& a, hipStream_t st) {

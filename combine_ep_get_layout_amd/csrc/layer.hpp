@@ -19,7 +19,7 @@ struct LayerArgs {
   const float* s13;
   const char* w2;          // [E][H][I]
   const float* s2;
-  uint16_t* h;             // workspace: [entries][I]
+  uint16_t* h;             // workspace: [entries][2][I], h rounded and the rest of it
   float* y;                // and, for more than kLayerPlaces entries, [entries][H up to 16]
   uint16_t* out;           // [tokens][H]
   int32_t* err;

@@ -20,10 +20,10 @@ def call(p=None, x=A, idx=A, wt=A, w13="w13", act=2, w2="w2", out=A, err=A, ws=A
 def test_workspace():
     def of(inner, **kw):
         return ep.lib().ep_expert_layer_workspace_bytes(ref(problem(**kw).c()), inner)
-    assert of(64) == 2 * 8 * 2 * 64 * 2
+    assert of(64) == 2 * 8 * 2 * 64 * 4
     assert of(8, T=0) == 256
-    assert of(72, R=1, T=1) == 512
-    assert of(64, R=1, T=512) == 1024 * (64 * 2 + 128 * 4)  # and the entries' results in fp32
+    assert of(72, R=1, T=1) == 768
+    assert of(64, R=1, T=512) == 1024 * (64 * 4 + 128 * 4)  # and the entries' results in fp32
     assert of(64, R=1, T=513) == 0                       # more than 1,024 entries
     assert of(64, E=5) == 0
     for inner in (0, 4, 12, -8, 32776):
@@ -59,7 +59,7 @@ def test_operands():
     assert call(w13=weights(128, 2 * I, reserved=1)) == SHAPE
     assert call(w2=weights(I, 128, fp8=3)) == MODE
     assert call(w2=weights(I, 128, fp8=1)) == MODE       # the two of different types
-    assert call(ws_bytes=2 * 8 * 2 * I * 2 - 1) == WS
+    assert call(ws_bytes=2 * 8 * 2 * I * 4 - 1) == WS
 
 
 @no_gpu
