@@ -186,7 +186,7 @@ int layer_ok(const Geometry& g, int inner) {
   return (int64_t)g.R * g.T * g.K > EP_LAYER_MAX_ENTRIES ? EP_ERR_SHAPE : EP_OK;
 }
 
-// The layer's workspace: h, and the entries' results where they do not fit the LDS.
+// The layer's workspace: h, and with many entries their results.
 size_t layer_h_bytes(const Geometry& g, int inner) {
   return ((size_t)g.R * g.T * g.K * inner * 4 + 255) & ~(size_t)255;
 }
@@ -194,7 +194,7 @@ size_t layer_h_bytes(const Geometry& g, int inner) {
 size_t layer_bytes(const Geometry& g, int inner) {
   const size_t entries = (size_t)g.R * g.T * g.K, row = (size_t)(g.H + 15) / 16 * 16;
   const size_t bytes = layer_h_bytes(g, inner) +
-                       (entries > ep::kLayerPlaces ? entries * row * sizeof(float) : 0);
+                       (ep::layer_many(entries, g.E, inner) ? entries * row * sizeof(float) : 0);
   return bytes < 256 ? 256 : bytes;
 }
 

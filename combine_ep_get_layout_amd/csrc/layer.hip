@@ -1,7 +1,7 @@
-// A whole MoE layer for a few tokens on gfx950, in two launches and without layout or
-// dispatch: for every token t and its entries (e, w),
-//   h = act(x Wg_e^T) * (x Wu_e^T),                          (layer_gated)
-//   out_t = sum_k w_k h W2_e^T,      in fp32, in k order.    (layer_down)
+// A whole MoE layer for a few tokens on gfx950, in two or three launches and without layout
+// or dispatch: for every token t and its entries (e, w),
+//   h = act(x Wg_e^T) * (x Wu_e^T),                       (layer_gated, many_gated)
+//   out_t = sum_k w_k h W2_e^T,   in fp32, in k order.    (layer_down, many_down + many_sum)
 // h is kept as two bf16, its value rounded and what that leaves, 16 bits together: in one,
 // its rounding alone would be as large an error of the result as the result's own.  They are
 // two rows of the second product, whose sums are added.
@@ -28,7 +28,7 @@ constexpr int kMost = 64;  // entries of an expert that are multiplied at once, 
 
 // The ids in LDS, and a bit for each expert with an entry: lane l's word has experts 32 l ...
 struct Routing {
-  int ids[kLayerEntries];
+  int16_t ids[kLayerEntries];  // -1 or below kMaxExperts
   uint32_t hit[kMaxExperts / 32];
 };
 
@@ -99,6 +99,7 @@ __device__ __forceinline__ int entries_of(const LayerArgs& a, const Routing& r, 
 // on, with one strip.
 struct Unit {
   int e, strip, at, rows, n;  // n: the expert's entries in all
+  int start;                  // the line that it begins with, of the wave's
   uint16_t* list;             // the unit's
 };
 
@@ -107,34 +108,41 @@ struct Unit {
 // bits.  A slot of the ring holds one: two loads (2 KiB) of weights a strip and NB of rows.  In
 // LDS chunk c (16 bytes) of row r stands at c ^ turn(r), so that 16 lanes' reads of one chunk
 // of 16 rows fall into different banks.
-template <int KIND, int CT, int NB, int D>
+// SHARE waves of a workgroup may have the rows in common: then each loads a part of them, and
+// they meet at every line.  ONCE: weights are not kept in the caches.
+template <int KIND, int CT, int NB, int D, int SHARE = 1, bool ONCE = true>
 struct Stream {
   static constexpr bool kBytes = KIND != EP_WEIGHTS_BF16;
   static constexpr int kSize = kBytes ? 1 : 2;
   static constexpr int kChunks = kBytes ? 16 : 8;           // of a row in a line
   static constexpr int kRows = NB * kWave / kChunks;        // that a slot has room for
   static constexpr int TT = (kRows + 15) / 16;              // in matrix-core tiles
-  static constexpr int kRowsAt = CT * 2048;                 // in a slot
-  static constexpr int kSlot = kRowsAt + NB * 1024;
-  static constexpr int kLoads = 2 * CT + NB;
+  static constexpr int kWSlot = CT * 2048, kXSlot = NB * 1024;
+  static constexpr int kMine = NB / SHARE;                  // loads of rows, a wave's
+  static constexpr int kLoads = 2 * CT + kMine;
   static constexpr int kSteps = kBytes ? 4 : 2;             // matrix steps of a line
-  static_assert(kRows <= kMost && (kRows < 16 || kRows % 16 == 0), "");
+  static_assert(kRows <= kMost && (kRows < 16 || kRows % 16 == 0) && NB % SHARE == 0, "");
 
-  lds_char* ring;
+  lds_char *w_ring, *x_ring;
+  int member;              // of those that share rows
   int lines, left;         // of a row of weights, and the last one's bytes
   bool turns;              // strips start at different lines
   const char *w, *x;       // of the unit that is loaded: uniform, with the lanes' offsets
-  uint32_t w_off[2 * CT], x_off[NB];
+  uint32_t w_off[2 * CT], x_off[kMine];
   f32x4 acc[CT][TT];
 
-  __device__ __forceinline__ Stream(lds_char* r, int channels)
-      : ring(r), lines((channels * kSize + 127) / 128),
+  __device__ __forceinline__ Stream(lds_char* w_r, lds_char* x_r, int m, int channels)
+      : w_ring(w_r), x_ring(x_r), member(m), lines((channels * kSize + 127) / 128),
         left(channels * kSize - (lines - 1) * 128),
         turns(channels * kSize % 4096 == 0) {}
 
   static __device__ __forceinline__ int w_turn(int r) { return r / 2 & 7; }
   static __device__ __forceinline__ int x_turn(int r) { return kBytes ? r & 15 : r / 2 & 7; }
 
+  // the row that the lane loads in the wave's i-th load of rows
+  __device__ __forceinline__ int x_row(int i) const {
+    return (i * SHARE + member) * (kWave / kChunks) + lane_id() / kChunks;
+  }
   // row(r): byte offset from w of weight row r; entry(r): from x of the unit's row r
   template <class Row, class Entry>
   __device__ __forceinline__ void point(const char* w_, const char* x_, Row row, Entry entry) {
@@ -147,20 +155,24 @@ struct Stream {
       w_off[i] = row(r) + ((lane % 8 ^ w_turn(r)) << 4);
     }
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int r = i * (kWave / kChunks) + lane / kChunks;
+    for (int i = 0; i < kMine; ++i) {
+      const int r = x_row(i);
       x_off[i] = entry(r) + ((lane % kChunks ^ x_turn(r)) << 4);
     }
   }
   __device__ __forceinline__ void load(int line, int slot) const {
-    lds_char* to = ring + slot * kSlot;
+    lds_char* to = w_ring + slot * kWSlot;
+    lds_char* x_to = x_ring + slot * kXSlot + 1024 * member;
     const char* wl = w + (int64_t)line * 128;
     const char* xl = x + (int64_t)line * (16 * kChunks);
     if (KIND == EP_WEIGHTS_FP8 || line < lines - 1 || left == 128) {
 #pragma unroll
-      for (int i = 0; i < 2 * CT; ++i) stream_lds16(wl, w_off[i], to + 1024 * i);
+      for (int i = 0; i < 2 * CT; ++i) {
+        if (ONCE) stream_lds16(wl, w_off[i], to + 1024 * i);
+        else load_lds16(wl, w_off[i], to + 1024 * i);
+      }
 #pragma unroll
-      for (int i = 0; i < NB; ++i) load_lds16(xl, x_off[i], to + kRowsAt + 1024 * i);
+      for (int i = 0; i < kMine; ++i) load_lds16(xl, x_off[i], x_to + 1024 * SHARE * i);
     } else {  // chunks past the end are zeros on both sides
       const int lane = lane_id(), chunks = left / 16 * (kBytes ? 2 : 1);
 #pragma unroll
@@ -169,10 +181,9 @@ struct Stream {
         load_lds16(in ? wl + w_off[i] : (const char*)k_zeros, to + 1024 * i);
       }
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const int r = i * (kWave / kChunks) + lane / kChunks;
-        const bool in = (lane % kChunks ^ x_turn(r)) < chunks;
-        load_lds16(in ? xl + x_off[i] : (const char*)k_zeros, to + kRowsAt + 1024 * i);
+      for (int i = 0; i < kMine; ++i) {
+        const bool in = (lane % kChunks ^ x_turn(x_row(i))) < chunks;
+        load_lds16(in ? xl + x_off[i] : (const char*)k_zeros, x_to + 1024 * SHARE * i);
       }
     }
   }
@@ -203,7 +214,7 @@ struct Stream {
   // lane's 16 codes are two steps, the first eight of every lane and the last.
   // scale: FP8, of this line's 128 channels
   __device__ __forceinline__ void multiply(int slot, float scale) {
-    const lds_char* from = ring + slot * kSlot;
+    const lds_char *from = w_ring + slot * kWSlot, *x_from = x_ring + slot * kXSlot;
     const int lane = lane_id(), r = lane % 16, q = lane / 16;
     i32x4 wv[CT][2];
 #pragma unroll
@@ -229,7 +240,7 @@ struct Stream {
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
         const int c = kBytes ? 8 * (i / 2) + 2 * q + i % 2 : q + 4 * i;
-        xv[i] = __builtin_bit_cast(bf16x8, *(const EP_LDS i32x4*)(from + kRowsAt + xr * 16 * kChunks +
+        xv[i] = __builtin_bit_cast(bf16x8, *(const EP_LDS i32x4*)(x_from + xr * 16 * kChunks +
                                                                   ((c ^ x_turn(xr)) << 4)));
       }
 #pragma unroll
@@ -260,16 +271,17 @@ struct Stream {
     // length is a multiple of 4 KiB those share few memory channels: there every strip begins
     // somewhere else (rows of 8 KiB, 32 tokens over 16 experts: 67 -> 63 us; of 2 and 7 KiB
     // 2% slower).
+    auto begin = [&](Unit& unit) {
+      unit.start = turns ? uniform((uint32_t)(unit.strip / SHARE * 11 + unit.e * 7) % (uint32_t)n) : 0;
+      aim(unit);
+    };
     auto line_of = [&](const Unit& unit, int i) {
-      if (turns) {
-        i += (int)((uint32_t)(unit.strip * 11 + unit.e * 7) % (uint32_t)n);
-        if (i >= n) i -= n;
-      }
-      return part + i * parts;
+      i += unit.start;
+      return part + (i >= n ? i - n : i) * parts;
     };
     Unit now, then;
     if (!next(now)) return;
-    aim(now);
+    begin(now);
     const bool chain = n >= D - 1;
     int slot = 0;
     auto after = [](int s) { return s + 1 == D ? 0 : s + 1; };
@@ -290,19 +302,25 @@ struct Stream {
       for (int i = 0; i < n; ++i) {
         const int ahead = i + D - 1, into = slot == 0 ? D - 1 : slot - 1;
         // the line before has been read out of the slot that is loaded
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (SHARE > 1) {  // by all, and all have their part of this one
+          if (ahead - 1 < n || more) wait_loads<kLoads*(D - 2)>();
+          else wait_loads<0>();
+          barrier();
+        } else {
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
         if (ahead < n) {
           load(line_of(now, ahead), into);
-          wait_loads<kLoads*(D - 1)>();
+          if (SHARE == 1) wait_loads<kLoads*(D - 1)>();
         } else {
           if (ahead == n && chain) {
             more = next(then);
-            if (more) aim(then);
+            if (more) begin(then);
           }
           if (more) {
             load(line_of(then, ahead - n), into);
-            wait_loads<kLoads*(D - 1)>();
-          } else {
+            if (SHARE == 1) wait_loads<kLoads*(D - 1)>();
+          } else if (SHARE == 1) {
             wait_loads<0>();
           }
         }
@@ -313,9 +331,10 @@ struct Stream {
       }
       done(now);
       if (!chain) {
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (SHARE > 1) barrier();
+        else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         more = next(then);
-        if (more) aim(then);
+        if (more) begin(then);
       }
       if (!more) return;
       now = then;
@@ -348,6 +367,60 @@ __device__ __forceinline__ float rest_of(float h, float rounded) {
 constexpr int kUpWaves = 4;    // of a workgroup
 constexpr int kUpStride = 20;  // floats of a column of partial sums, 16 and a gap
 
+// The stream's next loads: strips of 8 gates and ups from channel n0 on, and the unit's rows
+template <class S>
+__device__ __forceinline__ void aim_gated(const LayerArgs& a, S& stream, const Unit& unit, int n0,
+                                          int64_t w_row) {
+  stream.point(
+      a.w13 + ((int64_t)unit.e * 2 * a.I + n0) * w_row, (const char*)a.x,
+      [&](int r) {  // past the last channel: that one again, not stored
+        const int ch = min(r / 16 * 8 + r % 8, a.I - 1 - n0);
+        return (uint32_t)((r % 16 < 8 ? ch : a.I + ch) * w_row);
+      },
+      [&](int r) {
+        return (uint32_t)(unit.list[min(r, unit.rows - 1)] / a.K) * (uint32_t)(a.H * 2);
+      });
+}
+
+// FP8: the scale of expert e's channels n0 .. in a line, of its gates in the lower half of the
+// wave and of its ups in the upper one
+template <int KIND>
+__device__ __forceinline__ float gated_scale(const LayerArgs& a, int e, int n0, int line) {
+  if (KIND != EP_WEIGHTS_FP8) return 1.0f;
+  const int64_t groups = a.H / 128;
+  const float* s = a.s13 + ((int64_t)e * (2 * a.I / 128) + n0 / 128) * groups + line;
+  const float gate = fixed_float(s), up = fixed_float(s + a.I / 128 * groups);
+  return lane_id() < 32 ? gate : up;
+}
+
+// h of the unit's r-th row: channels n0 + ch (0 or 4) and three more, of the sums of their
+// gates and ups
+template <int KIND>
+__device__ __forceinline__ void store_h(const LayerArgs& a, const Unit& unit, int r, int n0,
+                                        int ch, float (&g)[4], float (&up)[4]) {
+  const float* scale = a.s13 + (int64_t)unit.e * 2 * a.I + n0;
+  bf16x2 high[2], low[2];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (KIND == EP_WEIGHTS_INT8) {
+      const float g0 = fixed_float(scale + q), g1 = fixed_float(scale + 4 + q);
+      const float u0 = fixed_float(scale + a.I + q), u1 = fixed_float(scale + a.I + 4 + q);
+      g[q] *= ch == 0 ? g0 : g1;
+      up[q] *= ch == 0 ? u0 : u1;
+    }
+    float value, slope;
+    act_both(a.act, g[q], value, slope);
+    const float h = value * up[q];
+    high[q / 2][q % 2] = (__bf16)h;
+    low[q / 2][q % 2] = (__bf16)rest_of(h, (float)high[q / 2][q % 2]);
+  }
+  if (r < unit.rows) {
+    uint16_t* to = a.h + (int64_t)unit.list[r] * 2 * a.I + n0 + ch;
+    *(uint2*)to = __builtin_bit_cast(uint2, high);
+    *(uint2*)(to + a.I) = __builtin_bit_cast(uint2, low);
+  }
+}
+
 // A strip is eight channels of one expert, their gates and ups.  WK waves share CT strips,
 // the lines dealt to them in turn; a wave's sums of rows 4 (lane / 16) .. are gates in the
 // lower half of its lanes and ups in the upper one.
@@ -358,7 +431,7 @@ __global__ __launch_bounds__(kUpWaves* kWave) void layer_gated(LayerArgs a) {
   constexpr int kCols = 16 * S::TT;
   __shared__ Routing routing;
   __shared__ uint16_t lists[kUpWaves][2][S::kRows];
-  __shared__ __align__(16) char rings[kUpWaves][D * S::kSlot];
+  __shared__ __align__(16) char rings[kUpWaves][D * (S::kWSlot + S::kXSlot)];
   __shared__ __align__(16) float parts[WK > 1 ? WK * kCols * kUpStride : 1];
   read_routing<kUpWaves * kWave>(a, routing, nullptr);
   const Hits hits(routing);
@@ -370,7 +443,7 @@ __global__ __launch_bounds__(kUpWaves* kWave) void layer_gated(LayerArgs a) {
   Unit last;
   last.n = 0;
   last.at = last.e = -1;
-  S stream((lds_char*)rings[wave], a.H);
+  S stream((lds_char*)rings[wave], (lds_char*)rings[wave] + D * S::kWSlot, 0, a.H);
   stream.run(
       WK > 1 ? wave % WK : 0, WK,
       [&](Unit& unit) {
@@ -392,24 +465,9 @@ __global__ __launch_bounds__(kUpWaves* kWave) void layer_gated(LayerArgs a) {
         return true;
       },
       [&](const Unit& unit) {
-        const int n0 = unit.strip * 8 * CT;
-        stream.point(
-            a.w13 + ((int64_t)unit.e * 2 * a.I + n0) * w_row, (const char*)a.x,
-            [&](int r) {  // past the last channel: that one again, not stored
-              const int ch = min(r / 16 * 8 + r % 8, a.I - 1 - n0);
-              return (uint32_t)((r % 16 < 8 ? ch : a.I + ch) * w_row);
-            },
-            [&](int r) {
-              return (uint32_t)(unit.list[min(r, unit.rows - 1)] / a.K) * (uint32_t)(a.H * 2);
-            });
+        aim_gated(a, stream, unit, unit.strip * 8 * CT, w_row);
       },
-      [&](const Unit& unit, int line) {
-        if (KIND != EP_WEIGHTS_FP8) return 1.0f;
-        const int64_t groups = a.H / 128;
-        const float* s = a.s13 + ((int64_t)unit.e * (2 * a.I / 128) + unit.strip * CT / 16) * groups + line;
-        const float gate = fixed_float(s), up = fixed_float(s + a.I / 128 * groups);
-        return lane < 32 ? gate : up;
-      },
+      [&](const Unit& unit, int line) { return gated_scale<KIND>(a, unit.e, unit.strip * 8 * CT, line); },
       [&](const Unit& unit) {
         const int ch = 4 * (lane / 16 % 2);
 #pragma unroll
@@ -423,7 +481,6 @@ __global__ __launch_bounds__(kUpWaves* kWave) void layer_gated(LayerArgs a) {
             barrier();
           }
           if (n0 < a.I) {
-            const float* scale = a.s13 + (int64_t)unit.e * 2 * a.I + n0;
 #pragma unroll
             for (int j = 0; j < S::TT; ++j) {
               if (WK > 1 && j % WK != wave) continue;  // a tile each
@@ -441,27 +498,7 @@ __global__ __launch_bounds__(kUpWaves* kWave) void layer_gated(LayerArgs a) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) halves(stream.acc[c][j][q], g[q], up[q]);
               }
-              bf16x2 high[2], low[2];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if (KIND == EP_WEIGHTS_INT8) {
-                  const float g0 = fixed_float(scale + q), g1 = fixed_float(scale + 4 + q);
-                  const float u0 = fixed_float(scale + a.I + q), u1 = fixed_float(scale + a.I + 4 + q);
-                  g[q] *= ch == 0 ? g0 : g1;
-                  up[q] *= ch == 0 ? u0 : u1;
-                }
-                float value, slope;
-                act_both(a.act, g[q], value, slope);
-                const float h = value * up[q];
-                high[q / 2][q % 2] = (__bf16)h;
-                low[q / 2][q % 2] = (__bf16)rest_of(h, (float)high[q / 2][q % 2]);
-              }
-              const int r = 16 * j + row;
-              if (lane < 32 && r < unit.rows) {
-                uint16_t* to = a.h + (int64_t)unit.list[r] * 2 * a.I + n0 + ch;
-                *(uint2*)to = __builtin_bit_cast(uint2, high);
-                *(uint2*)(to + a.I) = __builtin_bit_cast(uint2, low);
-              }
+              if (lane < 32) store_h<KIND>(a, unit, 16 * j + row, n0, ch, g, up);
             }
           }
           if (WK > 1) barrier();
@@ -477,38 +514,67 @@ __device__ __forceinline__ float neighbour(float v) {
 
 // ---- down projection and the weighted sum ---------------------------------------------
 
-// A workgroup has CT strips of 16 channels of every token.  Its waves take an expert each in
-// turn (or parts of the contraction, where there are fewer experts than waves) and put
-// every entry's result into a place of its own, in LDS or in the workspace; then they are
-// summed in k order.
-template <int KIND, int CT, int NB, int D, int WAVES, bool IN_LDS>
+template <int KIND>
+__device__ __forceinline__ float down_scale(const LayerArgs& a, int e, int n0, int line) {
+  if (KIND != EP_WEIGHTS_FP8) return 1.0f;
+  return fixed_float(a.s2 + ((int64_t)e * (a.H / 128) + n0 / 128) * (a.I / 128) + line);
+}
+
+// The stream's next loads: strips of 16 channels from n0 on, and the unit's rows of h
+template <class S>
+__device__ __forceinline__ void aim_down(const LayerArgs& a, S& stream, const Unit& unit, int n0,
+                                         int64_t w_row) {
+  stream.point(
+      a.w2 + ((int64_t)unit.e * a.H + n0) * w_row, (const char*)a.h,
+      // past the last channel: that one again, not stored
+      [&](int r) { return (uint32_t)(min(r, a.H - 1 - n0) * w_row); },
+      [&](int r) {
+        return (unit.list[min(r / 2, unit.rows - 1)] * 2u + r % 2) * (uint32_t)(a.I * 2);
+      });
+}
+
+// The results of a unit's entries in one strip, from the sums of their two rows
+template <int TT>
+__device__ __forceinline__ void store_y(float* y, int64_t y_row, const Unit& unit,
+                                        const f32x4 (&acc)[TT]) {
+  const int row = lane_id() % 16, ch = 4 * (lane_id() / 16);
+#pragma unroll
+  for (int j = 0; j < TT; ++j) {
+    f32x4 sum = acc[j];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum[q] += neighbour(sum[q]);
+    const int r = (16 * j + row) / 2;
+    if (row % 2 == 0 && r < unit.rows) *(f32x4*)(y + unit.list[r] * y_row + ch) = sum;
+  }
+}
+
+// A workgroup has a strip of 16 channels of every token.  Its waves take an expert each in turn
+// (or parts of the contraction, where there are fewer experts than waves) and put every
+// entry's result into a place of its own; then they are summed in k order.
+template <int KIND, int NB, int D, int WAVES>
 __global__ __launch_bounds__(WAVES* kWave) void layer_down(LayerArgs a) {
-  typedef Stream<KIND, CT, NB, D> S;
-  static_assert(!IN_LDS || CT == 1, "a place has 16 channels");
+  typedef Stream<KIND, 1, NB, D> S;
   __shared__ Routing routing;
   constexpr int kEntries = S::kRows / 2;  // a slot's, two rows each
   __shared__ uint16_t lists[WAVES][2][kEntries];
-  __shared__ __align__(16) char rings[WAVES][D * S::kSlot];
-  __shared__ float weights[kLayerEntries];
-  __shared__ __align__(16) float places[IN_LDS ? kLayerPlaces * 16 : 1];
+  __shared__ __align__(16) char rings[WAVES][D * (S::kWSlot + S::kXSlot)];
+  __shared__ float weights[kLayerPlaces];
+  __shared__ __align__(16) float places[kLayerPlaces * 16];
   read_routing<WAVES * kWave>(a, routing, weights);
   const Hits hits(routing);
-  const int wave = uniform(threadIdx.x / kWave), lane = lane_id(), row = lane % 16;
-  const int n0 = blockIdx.x * 16 * CT;
+  const int wave = uniform(threadIdx.x / kWave), n0 = blockIdx.x * 16;
   const int64_t w_row = (int64_t)a.I * S::kSize;
   // parts that every expert's contraction is cut into
   int parts = 1;
-  if (IN_LDS)
-    while (2 * parts * hits.total <= WAVES && 2 * parts * a.entries <= kLayerPlaces) parts *= 2;
+  while (2 * parts * hits.total <= WAVES && 2 * parts * a.entries <= kLayerPlaces) parts *= 2;
   const int part = wave % parts;
-  float* const y = IN_LDS ? places + part * a.entries * 16 : a.y + n0;
-  const int64_t y_row = IN_LDS ? 16 : (a.H + 15) / 16 * 16;
+  float* const y = places + part * a.entries * 16;
   int u = wave / parts - WAVES / parts, turn = 0;
   Unit last;
   last.n = 0;
   last.at = last.e = -1;
   last.strip = blockIdx.x;
-  S stream((lds_char*)rings[wave], a.I);
+  S stream((lds_char*)rings[wave], (lds_char*)rings[wave] + D * S::kWSlot, 0, a.I);
   stream.run(
       part, parts,
       [&](Unit& unit) {
@@ -525,48 +591,188 @@ __global__ __launch_bounds__(WAVES* kWave) void layer_down(LayerArgs a) {
         unit = last;
         return true;
       },
-      [&](const Unit& unit) {
-        stream.point(
-            a.w2 + ((int64_t)unit.e * a.H + n0) * w_row, (const char*)a.h,
-            // past the last channel: that one again, not stored
-            [&](int r) { return (uint32_t)(min(r, a.H - 1 - n0) * w_row); },
-            [&](int r) {
-              return (unit.list[min(r / 2, unit.rows - 1)] * 2u + r % 2) * (uint32_t)(a.I * 2);
-            });
-      },
-      [&](const Unit& unit, int line) {
-        if (KIND != EP_WEIGHTS_FP8) return 1.0f;
-        return fixed_float(a.s2 + ((int64_t)unit.e * (a.H / 128) + n0 / 128) * (a.I / 128) + line);
-      },
-      [&](const Unit& unit) {
-#pragma unroll
-        for (int j = 0; j < S::TT; ++j)
-#pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            f32x4 sum = stream.acc[c][j];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) sum[q] += neighbour(sum[q]);
-            const int r = (16 * j + row) / 2;
-            if (row % 2 == 0 && r < unit.rows && (c == 0 || n0 + 16 * c < a.H))
-              *(f32x4*)(y + unit.list[r] * y_row + 16 * c + 4 * (lane / 16)) = sum;
-          }
-      });
+      [&](const Unit& unit) { aim_down(a, stream, unit, n0, w_row); },
+      [&](const Unit& unit, int line) { return down_scale<KIND>(a, unit.e, n0, line); },
+      [&](const Unit& unit) { store_y(y, 16, unit, stream.acc[0]); });
   __syncthreads();
-  for (int o = threadIdx.x; o < a.tokens * 16 * CT; o += WAVES * kWave) {
-    const int t = o / (16 * CT), ch = o % (16 * CT);
+  for (int o = threadIdx.x; o < a.tokens * 16; o += WAVES * kWave) {
+    const int t = o / 16, ch = o % 16;
     if (n0 + ch >= a.H) continue;
     float sum = 0.0f;
     for (int k = 0; k < a.K; ++k) {
       const int i = t * a.K + k, e = routing.ids[i];
       if (e < 0) continue;
       float v = 0.0f;
-      for (int p = 0; p < parts; ++p)
-        v += IN_LDS ? places[(p * a.entries + i) * 16 + ch] : y[i * y_row + ch];
+      for (int p = 0; p < parts; ++p) v += places[(p * a.entries + i) * 16 + ch];
       if (KIND == EP_WEIGHTS_INT8) v *= a.s2[(int64_t)e * a.H + n0 + ch];
       sum = __builtin_fmaf(weights[i], v, sum);
     }
     ((__bf16*)a.out)[(int64_t)t * a.H + n0 + ch] = (__bf16)sum;
   }
+}
+
+// ---- many entries an expert ------------------------------------------------------------
+
+// kTeam waves share the rows of up to a slot's room of one expert's entries (a chunk), each with
+// CT strips of its own; entries' results go to the workspace, and a third launch sums them.
+// A wave alone would read the rows for one or two strips: 16 experts with 16 / 32 / 64 entries
+// (bf16 4096 -> 1408) take 118 / 131 / 174 us, waves alone 162 / 207 / 339; 256 with 2 in FP8
+// (7168 -> 2048) 1480 and 1770 us.  Layout, dispatch, the experts' products and combine take 136
+// / 152 / 150 us for those 16.
+constexpr int kTeam = 4;
+
+template <int ROWS>
+struct Chunks {
+  uint16_t expert[kLayerEntries], at[kLayerEntries];  // every one has an entry
+  int sums[kTeam], total;
+  // count: room for kMaxExperts
+  __device__ __forceinline__ void find(const LayerArgs& a, const Routing& r, int* count) {
+    constexpr int kEach = kMaxExperts / (kTeam * kWave);
+    const int first = threadIdx.x * kEach, lane = lane_id(), wave = threadIdx.x / kWave;
+    for (int i = threadIdx.x; i < kMaxExperts; i += kTeam * kWave) count[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.entries; i += kTeam * kWave)
+      if (r.ids[i] >= 0) atomicAdd(&count[r.ids[i]], 1);
+    __syncthreads();
+    int own = 0;
+    for (int e = first; e < first + kEach; ++e) own += (count[e] + ROWS - 1) / ROWS;
+    int place = own;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int v = __shfl_up(place, d);
+      if (lane >= d) place += v;
+    }
+    if (lane == kWave - 1) sums[wave] = place;
+    __syncthreads();
+    place -= own;
+    for (int w = 0; w < wave; ++w) place += sums[w];
+    for (int e = first; e < first + kEach; ++e)
+      for (int n = 0; n < count[e]; n += ROWS, ++place) expert[place] = e, at[place] = n;
+    if (threadIdx.x == kTeam * kWave - 1) total = place;
+    __syncthreads();
+  }
+};
+
+// A workgroup's next unit of `groups` groups of strips by all chunks, of it the part of this
+// wave; false after the last.  A die takes a run of units, chunks of the same weights one after
+// the other.
+template <int ROWS>
+__device__ __forceinline__ bool team_next(const LayerArgs& a, const Routing& routing,
+                                          const Chunks<ROWS>& chunks, int groups, int& u,
+                                          uint16_t* list, Unit& unit) {
+  const int total = uniform(chunks.total), units = total * groups;
+  int v;
+  do {
+    u += gridDim.x;
+    if (u >= xcd_blocks(units)) return false;
+    v = uniform(xcd_run(u, units));
+  } while (v >= units);
+  const int group = uniform(v / total), c = v - group * total;
+  unit.e = uniform(chunks.expert[c]);
+  unit.at = uniform(chunks.at[c]);
+  unit.strip = group * kTeam + uniform(threadIdx.x / kWave);
+  unit.list = list;
+  unit.n = entries_of(a, routing, unit.e, unit.at, ROWS, list);
+  unit.rows = min(unit.n - unit.at, ROWS);
+  return true;
+}
+
+template <int KIND, int CT, int NB, int D, bool ONCE>
+__global__ __launch_bounds__(kTeam* kWave) void many_gated(LayerArgs a) {
+  typedef Stream<KIND, CT, NB, D, kTeam, ONCE> S;
+  __shared__ Routing routing;
+  __shared__ Chunks<S::kRows> chunks;
+  __shared__ uint16_t lists[kTeam][2][S::kRows];
+  __shared__ __align__(16) char w_rings[kTeam][D * S::kWSlot], x_ring[D * S::kXSlot];
+  read_routing<kTeam * kWave>(a, routing, nullptr);
+  chunks.find(a, routing, (int*)w_rings);
+  const int wave = uniform(threadIdx.x / kWave), lane = lane_id(), row = lane % 16;
+  const int64_t w_row = (int64_t)a.H * S::kSize;
+  int u = blockIdx.x - gridDim.x, turn = 0;
+  S stream((lds_char*)w_rings[wave], (lds_char*)x_ring, wave, a.H);
+  stream.run(
+      0, 1,
+      [&](Unit& unit) {
+        return team_next(a, routing, chunks, (a.I + 8 * CT * kTeam - 1) / (8 * CT * kTeam), u,
+                         lists[wave][turn ^= 1], unit);
+      },
+      [&](const Unit& unit) {
+        aim_gated(a, stream, unit, min(unit.strip * 8 * CT, a.I - 1), w_row);
+      },
+      [&](const Unit& unit, int line) { return gated_scale<KIND>(a, unit.e, unit.strip * 8 * CT, line); },
+      [&](const Unit& unit) {
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          const int n0 = (unit.strip * CT + c) * 8;
+          if (n0 >= a.I) continue;
+#pragma unroll
+          for (int j = 0; j < S::TT; ++j) {
+            float g[4], up[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) halves(stream.acc[c][j][q], g[q], up[q]);
+            if (lane < 32) store_h<KIND>(a, unit, 16 * j + row, n0, 4 * (lane / 16 % 2), g, up);
+          }
+        }
+      });
+}
+
+template <int KIND, int CT, int NB, int D, bool ONCE>
+__global__ __launch_bounds__(kTeam* kWave) void many_down(LayerArgs a) {
+  typedef Stream<KIND, CT, NB, D, kTeam, ONCE> S;
+  constexpr int kEntries = S::kRows / 2;
+  __shared__ Routing routing;
+  __shared__ Chunks<kEntries> chunks;
+  __shared__ uint16_t lists[kTeam][2][kEntries];
+  __shared__ __align__(16) char w_rings[kTeam][D * S::kWSlot], x_ring[D * S::kXSlot];
+  read_routing<kTeam * kWave>(a, routing, nullptr);
+  chunks.find(a, routing, (int*)w_rings);
+  const int wave = uniform(threadIdx.x / kWave);
+  const int64_t w_row = (int64_t)a.I * S::kSize, y_row = (a.H + 15) / 16 * 16;
+  int u = blockIdx.x - gridDim.x, turn = 0;
+  S stream((lds_char*)w_rings[wave], (lds_char*)x_ring, wave, a.I);
+  stream.run(
+      0, 1,
+      [&](Unit& unit) {
+        return team_next(a, routing, chunks, (a.H + 16 * CT * kTeam - 1) / (16 * CT * kTeam), u,
+                         lists[wave][turn ^= 1], unit);
+      },
+      [&](const Unit& unit) {
+        aim_down(a, stream, unit, min(unit.strip * 16 * CT, a.H - 1), w_row);
+      },
+      [&](const Unit& unit, int line) { return down_scale<KIND>(a, unit.e, unit.strip * 16 * CT, line); },
+      [&](const Unit& unit) {
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          const int n0 = (unit.strip * CT + c) * 16;
+          if (n0 < a.H) store_y(a.y + n0, y_row, unit, stream.acc[c]);
+        }
+      });
+}
+
+// Four channels of a token a thread
+template <int KIND>
+__global__ __launch_bounds__(kWave * 4) void many_sum(LayerArgs a) {
+  const int t = blockIdx.x, ch = (blockIdx.y * kWave * 4 + threadIdx.x) * 4;
+  if (ch >= a.H) return;
+  const int64_t y_row = (a.H + 15) / 16 * 16;
+  f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int k = 0; k < a.K; ++k) {
+    const int i = t * a.K + k, e = a.idx[i];
+    if (e < 0 || e >= a.E) continue;
+    f32x4 v = *(const f32x4*)(a.y + i * y_row + ch);
+    if (KIND == EP_WEIGHTS_INT8) {
+      const f32x4 scale = *(const f32x4*)(a.s2 + (int64_t)e * a.H + ch);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] *= scale[q];
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum[q] = __builtin_fmaf(a.weights[i], v[q], sum[q]);
+  }
+  bf16x2 out[2];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) out[q / 2][q % 2] = (__bf16)sum[q];
+  *(uint2*)(a.out + (int64_t)t * a.H + ch) = __builtin_bit_cast(uint2, out);
 }
 
 // ---- launches ------------------------------------------------------------------------
@@ -585,18 +791,18 @@ static void launch_gated(const LayerArgs& a, hipStream_t st) {
                        dim3(kUpWaves * kWave), 0, st, a);
 }
 
-template <int KIND, int CT, int NB, int D, int WAVES, bool IN_LDS>
+template <int KIND, int NB, int D, int WAVES>
 static void launch_down(const LayerArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((layer_down<KIND, CT, NB, D, WAVES, IN_LDS>),
-                     dim3((a.H + 16 * CT - 1) / (16 * CT)), dim3(WAVES * kWave), 0, st, a);
+  hipLaunchKernelGGL((layer_down<KIND, NB, D, WAVES>), dim3((a.H + 15) / 16), dim3(WAVES * kWave),
+                     0, st, a);
 }
 
 // How many entries a slot has room for goes by how many an expert has on average: a wave
 // reads its weights once for each slot full of them.  us (gated and down together with one row
-// of h an entry, bf16 4096 -> 1408, 16 experts with 8 / 16 / 32 / 64 entries each): slots of 16
-// entries 104 / 151 / 308 / 590, of 64 with two strips - / 160 / 190 / 283.  In 8 bits a slot's
-// rows are as many bytes as its weights, or more, so two strips share them: 32 experts with
-// 4 / 16 entries 140 / 255 with one strip, 112 / 220 with two.
+// of h an entry, bf16 4096 -> 1408, 16 experts with 16 / 32 / 64 entries each): slots of 16
+// entries 151 / 308 / 590, of 64 with two strips 160 / 190 / 283.  In 8 bits a slot's rows are
+// as many bytes as its weights, or more, so two strips share them: 32 experts with 4 / 16
+// entries 140 / 255 with one strip, 112 / 220 with two.
 template <int KIND>
 static void choose_gated(const LayerArgs& a, int experts, hipStream_t st) {
   constexpr bool kBytes = KIND != EP_WEIGHTS_BF16;
@@ -610,31 +816,59 @@ static void choose_gated(const LayerArgs& a, int experts, hipStream_t st) {
   }
 }
 
-// An entry has two rows here, a workgroup as many waves as the LDS has rings for, up to 8: slots
-// of 8 entries with 4 waves take 326 us for 128 experts with 4 entries each (bf16 2048 -> 768,
-// the whole layer), with 8 276; more (12 in FP8 for 4 entries) gain under 1%.  With more than
-// about 12 entries an expert layout, dispatch, the experts' products and combine are the faster
-// way (16 experts with 8 / 16 / 32 / 64: 128 / 136 / 152 / 150 us, this 112 / 162 / 207 / 339).
-template <int KIND, bool IN_LDS>
+// An entry has two rows here, a workgroup as many waves as the LDS has rings for, up to 8 (4
+// entries an expert, bf16 4096 -> 1408, 16 experts, the whole layer: 102 us, with 4 waves 108).
+template <int KIND>
 static void choose_down(const LayerArgs& a, int experts, hipStream_t st) {
   constexpr bool kBytes = KIND != EP_WEIGHTS_BF16;
   if (a.entries <= 3 * experts) {  // 4 entries a slot
-    launch_down<KIND, 1, kBytes ? 2 : 1, 3, 8, IN_LDS>(a, st);
+    launch_down<KIND, kBytes ? 2 : 1, 3, 8>(a, st);
   } else if (a.entries <= 5 * experts) {  // 8
-    launch_down<KIND, 1, kBytes ? 4 : 2, kBytes ? 2 : 3, 8, IN_LDS>(a, st);
+    launch_down<KIND, kBytes ? 4 : 2, kBytes ? 2 : 3, 8>(a, st);
   } else if (kBytes || a.entries <= 12 * experts) {  // 16
-    launch_down<KIND, 1, kBytes ? 8 : 4, kBytes ? 2 : 3, IN_LDS ? 6 : 7, IN_LDS>(a, st);
+    launch_down<KIND, kBytes ? 8 : 4, kBytes ? 2 : 3, 6>(a, st);
   } else {  // 32
-    launch_down<KIND, 1, 8, 2, IN_LDS ? 6 : 7, IN_LDS>(a, st);
+    launch_down<KIND, 8, 2, 6>(a, st);
   }
+}
+
+template <int KIND, int CT, int NB, int D, bool ONCE>
+static void launch_many(const LayerArgs& a, hipStream_t st) {
+  constexpr int kRows = NB * (KIND == EP_WEIGHTS_BF16 ? 8 : 4);
+  const dim3 threads(kTeam * kWave);
+  auto grid = [&](int entries, int channels, int strip) {
+    const int64_t chunks = a.entries / entries + std::min(a.E, a.entries);
+    const int64_t groups = (channels + strip * CT * kTeam - 1) / (strip * CT * kTeam);
+    const int64_t room = (NB == 4 ? 3 : 2) * kCus;  // workgroups at once
+    return dim3((unsigned)std::min<int64_t>(xcd_blocks(chunks * groups), room));
+  };
+  hipLaunchKernelGGL((many_gated<KIND, CT, NB, D, ONCE>), grid(kRows, a.I, 8), threads, 0, st, a);
+  hipLaunchKernelGGL((many_down<KIND, CT, NB, D, ONCE>), grid(kRows / 2, a.H, 16), threads, 0, st, a);
+  hipLaunchKernelGGL((many_sum<KIND>), dim3(a.tokens, (a.H + 4 * 4 * kWave - 1) / (4 * 4 * kWave)),
+                     dim3(4 * kWave), 0, st, a);
+}
+
+// us of the layer with tiles of 16 rows (32 in bf16) / of 64: 256 experts with 2 entries in
+// FP8 (7168 -> 2048) 1480 / 1875, 128 with 4 in bf16 (2048 -> 768) 200 / 227, 32 with 12 in FP8
+// (4096 -> 1408) 144 / 132.  Tiles of 64 rows with one strip a wave / two, where there are few:
+// 256 entries of one expert (bf16 4096 -> 1408) 53 / 59.  Weights past the caches / through
+// them: 16 experts with 16 / 64 entries (bf16 4096 -> 1408) 119 / 128 and 211 / 200.
+template <int KIND>
+static void choose_many(const LayerArgs& a, hipStream_t st) {
+  constexpr bool kBytes = KIND != EP_WEIGHTS_BF16;
+  constexpr int NB = kBytes ? 16 : 8;
+  if (layer_tiles(a.entries, a.E, a.I) < kCus) launch_many<KIND, 1, NB, kBytes ? 3 : 4, false>(a, st);
+  else if (a.entries <= 8 * a.E) launch_many<KIND, 2, 4, 2, true>(a, st);
+  else if (a.entries <= 32 * a.E) launch_many<KIND, 2, NB, kBytes ? 2 : 3, true>(a, st);
+  else launch_many<KIND, 2, NB, kBytes ? 2 : 3, false>(a, st);
 }
 
 template <int KIND>
 static void choose(const LayerArgs& a, hipStream_t st) {
+  if (layer_many(a.entries, a.E, a.I)) return choose_many<KIND>(a, st);
   const int experts = std::min(a.E, a.entries);
   choose_gated<KIND>(a, experts, st);
-  if (a.entries <= kLayerPlaces) choose_down<KIND, true>(a, experts, st);
-  else choose_down<KIND, false>(a, experts, st);
+  choose_down<KIND>(a, experts, st);
 }
 
 hipError_t launch_layer(const LayerArgs& a, hipStream_t st) {

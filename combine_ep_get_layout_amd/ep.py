@@ -796,8 +796,8 @@ def expert_layer(p: Problem, x: torch.Tensor, topk_idx: torch.Tensor, topk_weigh
                  err: torch.Tensor | None, ws: torch.Tensor, *, act: int = ACT_SILU,
                  w13_scales: torch.Tensor | None = None, w2_scales: torch.Tensor | None = None,
                  stream=None) -> None:
-    """An MoE layer for a few tokens (R*T*K <= LAYER_MAX_ENTRIES) in two launches, without
-    layout or dispatch: out = sum_k topk_weights * (act(x Wg^T) * (x Wu^T)) W2^T.
+    """An MoE layer for a few tokens (R*T*K <= LAYER_MAX_ENTRIES) in two or three launches,
+    without layout or dispatch: out = sum_k topk_weights * (act(x Wg^T) * (x Wu^T)) W2^T.
     x and out [R][T][H] bf16, topk_idx [R][T][K] int32 (-1: none), topk_weights [R][T][K]
     fp32, w13 [E][2 I][H] (gates first), w2 [E][H][I]: bf16, FP8 codes (scales per 128 x 128
     block) or int8 (scales [E][2 I] and [E][H]).  Error bits are OR-ed into err[0]."""

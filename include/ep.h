@@ -429,8 +429,8 @@ int ep_combine_backward(const ep_problem* p, const ep_layout* layout, const uint
  * and graphs that may be replayed at once, need one each. */
 size_t ep_expert_layer_workspace_bytes(const ep_problem* p, int32_t inner);
 
-/* An MoE layer from routing to weighted sum, in two launches, without layout, dispatch
- * or combine: what decoding a few tokens takes, whose time is reading the weights.
+/* An MoE layer from routing to weighted sum, in two or three launches, without layout,
+ * dispatch or combine: what decoding a few tokens takes, whose time is reading the weights.
  *   h[t][k] = act(x_t Wg_e^T) * (x_t Wu_e^T),   e = topk_idx[t][k], to 16 bits
  *   out_t = bf16( sum_k topk_weights[t][k] * (h[t][k] W2_e^T) )
  * sums in fp32, over k in order; every token of every rank meets every expert.  An entry of

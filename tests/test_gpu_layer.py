@@ -107,6 +107,21 @@ SHAPES = [
 ]
 
 
+# many entries an expert, whose rows workgroups share: rows of whole 4 KiB in either product
+# (lines then begin at different places), channels that end inside a strip and a group of them,
+# chunks of one entry, in tiles of 16 (32) rows and of 64, of one strip a wave and of two
+MANY = [
+    (1, 130, 2, 1, 4096, 264, 0.0),
+    (2, 65, 2, 1, 264, 4096, 0.0),
+    (1, 24, 32, 6, 2048, 520, 0.0),
+    (1, 129, 1, 1, 72, 40, 0.0),
+    (4, 256, 4, 1, 264, 1032, 0.1),
+    (1, 96, 16, 2, 200, 1096, 0.0),
+    (1, 200, 6, 5, 1032, 520, 0.4),
+    (1, 16, 64, 64, 136, 200, 0.0),
+]
+
+
 def sized(shape, kind):
     """The shape with channels that the type has: 128 in FP8, 16 in 8-bit integers."""
     step = {"bf16": 8, "fp8": 128, "int8": 16}[kind]
@@ -116,7 +131,7 @@ def sized(shape, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "-".join(map(str, s)))
+@pytest.mark.parametrize("shape", SHAPES + MANY, ids=lambda s: "-".join(map(str, s)))
 def test_layer(shape, kind):
     R, T, E, K, H, I, masked = sized(shape, kind)
     say("layer", shape, kind)
