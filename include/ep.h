@@ -435,7 +435,7 @@ size_t ep_expert_layer_workspace_bytes(const ep_problem* p, int32_t inner);
  *   out_t = bf16( sum_k topk_weights[t][k] * (h[t][k] W2_e^T) )
  * sums in fp32, over k in order; every token of every rank meets every expert.  An entry of
  * -1 has no part in it (whatever its weight); an id outside [-1, E) is skipped and sets
- * EP_DEVERR_TOPK_RANGE.  A token without entries gets 0.
+ * EP_DEVERR_TOPK_RANGE.  A token without entries gets 0.  An infinity in w2 may give NaN.
  * x, out: [R][T][H] bf16, not overlapping.  w13: [E][2 I][H], the gates first, w2:
  * [E][H][I], as for ep_expert_gated and ep_expert_linear, both of one type (bf16, FP8 or
  * 8-bit integers; the rows stay bf16), without bias.  err: [1], bits are OR-ed into it, or

@@ -135,6 +135,26 @@ def test_dispatch(case, fused):
     same_bits(recv.scales, want_s, "scales")
 
 
+@pytest.mark.parametrize("mode", [N, L])
+def test_dispatch_without_a_workspace(mode):
+    R, T, H, E, K = 2, 33, 272, 8, 3
+    p, lay, topk = routed(R, T, E, K, mode, seed=32, masked=0.1, H=H, quant=ep.QUANT_INT8)
+    x = rand(torch.Generator().manual_seed(32), R * T, H)
+    want = ep.Recv(p, capacity(p))
+    got = ep.Recv(p, capacity(p))
+    for r in (want, got):
+        r.x.fill_(0x5A)
+        r.scales.fill_(-7.0)
+    ep.dispatch(p, lay, x.to(DEV), recv=want)
+    lay = ep.Layout(p)
+    tk = torch.from_numpy(np.ascontiguousarray(topk)).to(DEV)
+    ep.dispatch_fused_noalloc(p, tk, lay, x.to(DEV), got)
+    torch.cuda.synchronize()
+    assert int(lay.err.item()) == 0
+    same_bits(got.x, want.x.cpu(), "codes")
+    same_bits(got.scales, want.scales.cpu(), "scales")
+
+
 def special_rows(H):
     """Rows that quantisation can go wrong at, bf16."""
     x = torch.zeros((14, H), dtype=torch.bfloat16)

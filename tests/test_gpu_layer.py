@@ -239,10 +239,32 @@ def test_no_tokens():
 
 
 @pytest.mark.parametrize("kind", KINDS)
-def test_special_values_stay_in_their_tokens(kind):
+def test_ids_of_no_expert_among_many(kind):
+    """The same where workgroups share rows: ids out of range, tokens without any, no token
+    with any."""
+    R, T, E, K, H, I, masked = sized((1, 150, 9, 2, 72, 40, 0.2), kind)
+    topk = routing(R, T, E, K, masked, 76)
+    m = Made(R, T, E, K, H, I, kind, topk)
+    m.wt[topk < 0] = NAN
+    bad = topk.clone()
+    bad[3, 1], bad[149, 0], bad[77, 1], bad[78] = E, -2, 1 << 30, -1
+    out = m.call(topk=bad)
+    torch.cuda.synchronize()
+    assert int(m.err.item()) == ep.DEVERR_TOPK_RANGE
+    bad[(bad < -1) | (bad >= E)] = -1
+    m.check(out, topk=bad, wt=torch.where(bad < 0, 0.0, m.wt))
+    assert (out[78] == 0).all()
+    out = m.call(topk=torch.full_like(topk, -1))
+    torch.cuda.synchronize()
+    assert (out == 0).all()
+
+
+@pytest.mark.parametrize("T", [40, 140])
+@pytest.mark.parametrize("kind", KINDS)
+def test_special_values_stay_in_their_tokens(kind, T):
     """An infinity or NaN in one token's row, or in the weights of one expert, reaches the
     tokens that have it and no others."""
-    R, T, E, K, H, I, _ = sized((1, 40, 6, 2, 264, 72, 0.0), kind)
+    R, T, E, K, H, I, _ = sized((1, T, 6, 2, 264, 72, 0.0), kind)
     topk = routing(R, T, E, K, 0.0, 67)
     m = Made(R, T, E, K, H, I, kind, topk)
     clean = m.call()
@@ -301,11 +323,12 @@ def test_weights_past_32_bit_offsets():
 
 # ---- together ---------------------------------------------------------------------
 
+@pytest.mark.parametrize("T", [24, 100])
 @pytest.mark.parametrize("kind", KINDS)
-def test_routed_and_replayed_in_a_graph(kind):
+def test_routed_and_replayed_in_a_graph(kind, T):
     """route and expert_layer captured together, replayed with fresh rows and logits, eager
     work of the same buffers in between; every replay equals the eager run bit for bit."""
-    R, T, E, K, H, I, _ = sized((1, 24, 16, 4, 256, 128, 0.0), kind)
+    R, T, E, K, H, I, _ = sized((1, T, 16, 4, 256, 128, 0.0), kind)
     m = Made(R, T, E, K, H, I, kind, routing(R, T, E, K, 0.0, 69))
     gen = torch.Generator().manual_seed(69)
     x, l = torch.empty((T, H), dtype=torch.bfloat16, device=DEV), torch.empty((T, E), device=DEV)
@@ -368,11 +391,12 @@ def test_two_streams_and_prepared_calls():
         assert torch.equal(alone.view(torch.int16), out.view(torch.int16))
 
 
+@pytest.mark.parametrize("T", [16, 64])
 @pytest.mark.parametrize("kind", ["bf16"])
-def test_against_the_separate_calls(kind):
+def test_against_the_separate_calls(kind, T):
     """layout, dispatch, the two products and combine of the same tokens: the same layer but
     for the rounding of h and y to bf16, so within four half steps (2-norm, doubled as above)."""
-    R, T, E, K, H, I = 2, 16, 8, 3, 264, 136
+    R, E, K, H, I = 2, 8, 3, 264, 136
     topk = routing(R, T, E, K, 0.1, 72)
     m = Made(R, T, E, K, H, I, kind, topk)
     out = m.call()
