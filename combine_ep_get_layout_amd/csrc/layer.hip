@@ -832,40 +832,52 @@ static void choose_down(const LayerArgs& a, int experts, hipStream_t st) {
   }
 }
 
-template <int KIND, int CT, int NB, int D, bool ONCE>
+template <int KIND, bool GATED, int CT, int NB, int D, bool ONCE>
 static void launch_many(const LayerArgs& a, hipStream_t st) {
-  constexpr int kRows = NB * (KIND == EP_WEIGHTS_BF16 ? 8 : 4);
-  const dim3 threads(kTeam * kWave);
-  auto grid = [&](int entries, int channels, int strip) {
-    const int64_t chunks = a.entries / entries + std::min(a.E, a.entries);
-    const int64_t groups = (channels + strip * CT * kTeam - 1) / (strip * CT * kTeam);
-    const int64_t room = (NB == 4 ? 3 : 2) * kCus;  // workgroups at once
-    return dim3((unsigned)std::min<int64_t>(xcd_blocks(chunks * groups), room));
-  };
-  hipLaunchKernelGGL((many_gated<KIND, CT, NB, D, ONCE>), grid(kRows, a.I, 8), threads, 0, st, a);
-  hipLaunchKernelGGL((many_down<KIND, CT, NB, D, ONCE>), grid(kRows / 2, a.H, 16), threads, 0, st, a);
-  hipLaunchKernelGGL((many_sum<KIND>), dim3(a.tokens, (a.H + 4 * 4 * kWave - 1) / (4 * 4 * kWave)),
-                     dim3(4 * kWave), 0, st, a);
+  constexpr int kEntries = NB * (KIND == EP_WEIGHTS_BF16 ? 8 : 4) / (GATED ? 1 : 2);
+  constexpr int kGroup = (GATED ? 8 : 16) * CT * kTeam;  // channels
+  const int64_t chunks = a.entries / kEntries + std::min(a.E, a.entries);
+  const int64_t units = chunks * (((GATED ? a.I : a.H) + kGroup - 1) / kGroup);
+  const int64_t room = (NB == 4 ? 3 : 2) * kCus;  // workgroups at once
+  const dim3 grid((unsigned)std::min<int64_t>(xcd_blocks(units), room)), threads(kTeam * kWave);
+  if (GATED) hipLaunchKernelGGL((many_gated<KIND, CT, NB, D, ONCE>), grid, threads, 0, st, a);
+  else hipLaunchKernelGGL((many_down<KIND, CT, NB, D, ONCE>), grid, threads, 0, st, a);
 }
 
 // us of the layer with tiles of 16 rows (32 in bf16) / of 64: 256 experts with 2 entries in
 // FP8 (7168 -> 2048) 1480 / 1875, 128 with 4 in bf16 (2048 -> 768) 200 / 227, 32 with 12 in FP8
-// (4096 -> 1408) 144 / 132.  Tiles of 64 rows with one strip a wave / two, where there are few:
-// 256 entries of one expert (bf16 4096 -> 1408) 53 / 59.  Weights past the caches / through
-// them: 16 experts with 16 / 64 entries (bf16 4096 -> 1408) 119 / 128 and 211 / 200.
-template <int KIND>
+// (4096 -> 1408) 144 / 132.  One strip a wave / two, where there are few tiles: 256 entries of
+// one expert (bf16 4096 -> 1408) 53 / 59, 24 of 8 (bf16 2280 -> 2952) 89 / 124.  Weights past
+// the caches / through them: 16 experts with 16 / 64 entries (bf16 4096 -> 1408) 119 / 128 and
+// 211 / 200.
+template <int KIND, bool GATED>
 static void choose_many(const LayerArgs& a, hipStream_t st) {
   constexpr bool kBytes = KIND != EP_WEIGHTS_BF16;
   constexpr int NB = kBytes ? 16 : 8;
-  if (layer_tiles(a.entries, a.E, a.I) < kCus) launch_many<KIND, 1, NB, kBytes ? 3 : 4, false>(a, st);
-  else if (a.entries <= 8 * a.E) launch_many<KIND, 2, 4, 2, true>(a, st);
-  else if (a.entries <= 32 * a.E) launch_many<KIND, 2, NB, kBytes ? 2 : 3, true>(a, st);
-  else launch_many<KIND, 2, NB, kBytes ? 2 : 3, false>(a, st);
+  const int64_t tiles = GATED ? layer_tiles(a.entries, a.E, a.I, 64)
+                              : layer_tiles(2 * a.entries, a.E, a.H, 128);
+  if (a.entries <= 8 * a.E) {
+    if (tiles < 2 * kCus) launch_many<KIND, GATED, 1, 4, 3, true>(a, st);
+    else launch_many<KIND, GATED, 2, 4, 2, true>(a, st);
+  } else if (tiles < kCus) {
+    launch_many<KIND, GATED, 1, NB, kBytes ? 3 : 4, false>(a, st);
+  } else if (a.entries <= 32 * a.E) {
+    launch_many<KIND, GATED, 2, NB, kBytes ? 2 : 3, true>(a, st);
+  } else {
+    launch_many<KIND, GATED, 2, NB, kBytes ? 2 : 3, false>(a, st);
+  }
 }
 
 template <int KIND>
 static void choose(const LayerArgs& a, hipStream_t st) {
-  if (layer_many(a.entries, a.E, a.I)) return choose_many<KIND>(a, st);
+  if (layer_many(a.entries, a.E, a.I)) {
+    choose_many<KIND, true>(a, st);
+    choose_many<KIND, false>(a, st);
+    hipLaunchKernelGGL((many_sum<KIND>),
+                       dim3(a.tokens, (a.H + 4 * 4 * kWave - 1) / (4 * 4 * kWave)),
+                       dim3(4 * kWave), 0, st, a);
+    return;
+  }
   const int experts = std::min(a.E, a.entries);
   choose_gated<KIND>(a, experts, st);
   choose_down<KIND>(a, experts, st);
