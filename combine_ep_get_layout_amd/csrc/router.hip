@@ -172,12 +172,13 @@ __device__ __forceinline__ int here(int v) {
   return v;
 }
 
-// PER consecutive logits as fp32, `fill` past the last expert; -0 becomes 0, which it equals.
+// `per` consecutive logits as fp32, `fill` behind them and past the last expert; -0 becomes 0,
+// which it equals.
 template <int PER, bool BF16>
 __device__ __forceinline__ void load_logits(const char* row, int first, int E, float fill,
-                                            float (&l)[PER]) {
+                                            float (&l)[PER], int per = PER) {
   constexpr int kBytes = PER * (BF16 ? 2 : 4);
-  if (PER > 1 && E % PER == 0) {  // whole and aligned in every lane that has any
+  if (PER > 1 && E % PER == 0 && per == PER) {  // whole and aligned in every lane that has any
     union {
       uint32_t w[kBytes / 4];
       uint16_t b[kBytes / 2];
@@ -211,7 +212,7 @@ __device__ __forceinline__ void load_logits(const char* row, int first, int E, f
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       l[i] = fill;
-      if (f + i < E)
+      if (i < per && f + i < E)
         l[i] = 0.0f + (BF16 ? __uint_as_float((uint32_t)((const uint16_t*)from)[i] << 16)
                             : ((const float*)from)[i]);
     }
@@ -248,7 +249,7 @@ struct Choice {
   float most = 0, total = 1, part = 1;  // softmax: the largest logit, the sum of exp(l - most), its inverse
 
   __device__ __forceinline__ explicit Choice(const RouteArgs& a_)
-      : a(a_), at(lane_id() & (LPT - 1)), first(at * PER) {}
+      : a(a_), at(lane_id() & (LPT - 1)), first(at * a_.per) {}
 
   __device__ __forceinline__ void softmax_sums(const float (&l)[PER]) {
     float m = l[0];
@@ -271,7 +272,7 @@ struct Choice {
     } else {
       float bias[PER];
       if (bias_row) {
-        load_logits<PER, false>((const char*)bias_row, first, a.E, 0.0f, bias);
+        load_logits<PER, false>((const char*)bias_row, first, a.E, 0.0f, bias, a.per);
       } else {
 #pragma unroll
         for (int i = 0; i < PER; ++i) bias[i] = 0.0f;
@@ -298,11 +299,11 @@ struct Choice {
   // Experts outside the kept groups to -inf.  Whether the last kept group is no more than
   // `sure` and 2^-22 of the choices in a sum (its additions) ahead of the first one left.
   __device__ __forceinline__ bool keep_groups(float sure) {
-    const int size = a.group_size, lanes = size / PER;
+    const int size = a.group_size, lanes = size / a.per;
     float mine;       // the score of group at / lanes, or of group `at`
     bool stays[PER];
     float lowest = __builtin_inff(), highest = low_inf(), size_of = 0.0f;
-    if (size % PER == 0 && (lanes & (lanes - 1)) == 0 && lanes <= LPT) {
+    if (size % a.per == 0 && (lanes & (lanes - 1)) == 0 && lanes <= LPT) {
       // a group is a power of two of lanes
       Top2<float> top{c[0], low_inf()};
 #pragma unroll
@@ -587,12 +588,12 @@ __device__ __forceinline__ float score_error(const RouteArgs& a, float largest) 
 // The first part of a wave's tokens in fp32; false for a token that has to be chosen again.
 template <int LPT, int PER, bool BF16>
 __device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t, Candidate* slots) {
-  const int at = lane_id() & (LPT - 1), first = at * PER;
+  const int at = lane_id() & (LPT - 1), first = at * a.per;
   const bool in = t < a.tokens;  // lanes without a token repeat the last one
   const int64_t token = in ? t : a.tokens - 1;
   const char* row = (const char*)a.logits + token * a.E * (BF16 ? 2 : 4);
   float l[PER];
-  load_logits<PER, BF16>(row, first, a.E, low_inf(), l);
+  load_logits<PER, BF16>(row, first, a.E, low_inf(), l, a.per);
   Choice<LPT, PER> choice(a);
   if (!a.sigmoid && (a.scored || !a.normalize)) choice.softmax_sums(l);
   const bool bad = token_bits<LPT>(__ballot(choice.fill(l, a.bias))) != 0;
@@ -828,9 +829,25 @@ __global__ __launch_bounds__(kRouteThreads) void route_grad(RouteGradArgs a) {
 
 // ---- launches -------------------------------------------------------------------------
 
-// Up to 256 experts 16 lanes take a token, so that a wave has four of them in a butterfly's
-// steps (32,768 tokens over 256 experts: 64 lanes 57 us); they hold 16 candidates.
+// Up to 512 experts 16 lanes take a token's choice, so that a wave has four of them in a
+// butterfly's steps; they hold 16 candidates (32,768 tokens over 256 / 384 / 512 experts: 64
+// lanes 57 / 141 / 230 us, 16 lanes 30 / 42 / 55).  The gradient's 64 from 257 on (384: 18 us,
+// with 16 lanes 24).
 constexpr int64_t kRouteBlocks = 8 * kCus;
+
+// A lane has fewer than `most` experts where a power of two of lanes then has a group each
+// (32,768 tokens over 160 experts in 8 groups: 47 us with 16 a lane, 38 with 10).
+static RouteArgs with_lanes(RouteArgs a, int lanes, int most) {
+  a.per = most;
+  if (a.groups_kept < a.groups)
+    for (int of = 1; of * a.groups <= lanes; of *= 2)
+      if (a.group_size % of == 0 && a.group_size / of <= most) {
+        a.per = a.group_size / of;
+        break;
+      }
+  return a;
+}
+static const RouteGradArgs& with_lanes(const RouteGradArgs& a, int, int) { return a; }
 
 #define EP_ROUTE_FORMS(KERNEL)                                                                \
   do {                                                                                        \
@@ -850,13 +867,18 @@ constexpr int64_t kRouteBlocks = 8 * kCus;
   hipLaunchKernelGGL((KERNEL<LPT, PER, BF16>),                                                \
                      dim3((unsigned)std::min((a.tokens * LPT + kRouteThreads - 1) /           \
                                                  kRouteThreads, kRouteBlocks)),               \
-                     dim3(kRouteThreads), lds, st, a)
+                     dim3(kRouteThreads), lds, st, with_lanes(a, LPT, PER))
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t st) {
   if (a.tokens == 0) return hipSuccess;
   const bool narrow = a.K < 16 && (a.groups_kept == a.groups || a.groups <= 16);
   const size_t lds = a.scored ? kRouteThreads / kWave * a.E * sizeof(double) : 0;
-  EP_ROUTE_FORMS(route);
+  if (narrow && a.E > 256 && a.E <= 512) {
+    if (a.bf16) EP_ROUTE_LAUNCH(route, 16, 32, true);
+    else EP_ROUTE_LAUNCH(route, 16, 32, false);
+  } else {
+    EP_ROUTE_FORMS(route);
+  }
   return hipGetLastError();
 }
 

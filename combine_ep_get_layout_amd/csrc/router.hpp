@@ -11,6 +11,7 @@ struct RouteArgs {
   bool bf16, sigmoid, normalize;
   bool scored;             // choices are scores (with a bias, or summed over a group)
   int groups, groups_kept, group_top, group_size;
+  int per;                 // experts a lane (set by launch_route)
   float scale;
   const void* logits;      // [tokens][E]
   const float* bias;       // [E] or NULL

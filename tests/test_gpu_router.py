@@ -82,6 +82,12 @@ SHAPES = [
     (1, 10, 513, 9, 9, 4, 2),
     (1, 6, 1000, 40, 10, 3, 2),
     (2, 6, 2048, 64, 32, 8, 2),
+    # groups of a power of two of lanes with fewer experts than a lane has room for, or of none
+    (1, 37, 160, 6, 8, 3, 2),
+    (2, 20, 48, 4, 16, 5, 1),
+    (1, 30, 192, 8, 4, 2, 2),
+    (1, 21, 170, 3, 10, 7, 2),
+    (1, 9, 320, 8, 8, 3, 2),
 ]
 
 
