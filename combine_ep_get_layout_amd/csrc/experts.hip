@@ -55,7 +55,10 @@ __device__ __forceinline__ const u32x4& residual_of(const u32x4& row) { return r
 __device__ __forceinline__ u32x4& residual_of(Row8& row) { return row.add; }
 __device__ __forceinline__ const u32x4& residual_of(const Row8& row) { return row.add; }
 
-// Sums of 8-bit products of B rows to their values: rows' scales times eight channels'.
+// Sums of 8-bit products of B rows to their values, times eight channels' scales and then the
+// rows': the scales' own product may be an infinity where the sum is 0, or lose its bits below
+// 2^-126 where the value does not.  A sum is an integer below 2^30, so it times a channel's
+// scale (up to 2^98) is neither.
 template <int B>
 __device__ __forceinline__ void scale8(float (&v)[B][8], const float (&rows)[B],
                                        const float* channels) {
@@ -63,7 +66,7 @@ __device__ __forceinline__ void scale8(float (&v)[B][8], const float (&rows)[B],
 #pragma unroll
   for (int b = 0; b < B; ++b)
 #pragma unroll
-    for (int c = 0; c < 8; ++c) v[b][c] *= rows[b] * (c < 4 ? lo[c] : hi[c - 4]);
+    for (int c = 0; c < 8; ++c) v[b][c] = v[b][c] * (c < 4 ? lo[c] : hi[c - 4]) * rows[b];
 }
 
 // What a tile's epilogue needs of it.

@@ -344,7 +344,7 @@ typedef struct ep_weights {
                           aligned                                                      */
   const float* scales; /* FP8: [E][out_channels/128][in_channels/128], the factor of each
                           128 x 128 block; 8-bit integers: [E][out_channels], a channel's,
-                          16-byte aligned; else ignored                                */
+                          below 2^98, 16-byte aligned; else ignored                    */
   const float* bias;   /* [E][out_channels] fp32, 16-byte aligned, or NULL             */
   int32_t in_channels;
   int32_t out_channels;

@@ -444,6 +444,48 @@ def test_rows_past_32_bit_offsets():
     untouched(y, segs, 0x5A5A)
 
 
+@pytest.mark.parametrize("rows", [3, 40, 600])
+@pytest.mark.parametrize("gated", [False, True])
+def test_scales_whose_product_is_no_normal_number(gated, rows):
+    """A row's and a channel's scale whose product is subnormal, or an infinity: values that are
+    normal numbers lose no more than elsewhere, and sums of 0 are 0.  The integer sum is rounded
+    once to fp32 (in up to four parts, added) and once with either scale, the gate's likewise,
+    their product once, and the result once to bf16."""
+    C, I = 32768, 64
+    p, lay, _ = routed(1, rows, 1, 1, N, seed=39, H=C, quant=ep.QUANT_INT8)
+    x = torch.full((rows, C), 127, dtype=torch.int8)
+    low = torch.arange(rows) % 3 != 1
+    sx = torch.where(low, 2.0 ** -107, 2.0 ** 120)
+    # channels 0 .. 31: times 2^-107 below the smallest subnormal number, or a few of them;
+    # sums of 2^29, so values of 2^-119.  From 32 on: sums of 0, times 2^120 an infinity
+    w = torch.full((1, I, C), 127, dtype=torch.int8)
+    sw = 2.0 ** -41 * (1 + (torch.arange(I) % 32) / 37.0)
+    sw[:16] /= 4
+    w[0, 32:], sw[32:] = 0, 2.0 ** 12
+    z = (x[:1].double() @ w[0].double().t()) * sw.double() * sx.double()[:, None]
+    other = torch.ones_like(z)
+    y = poisoned(rows, I)
+    kw = dict(act=ep.ACT_NONE, x_scales=sx.to(DEV))
+    if gated:
+        # the other factor near 1 in the rows that each channel is for; gates and ups by turns
+        v = torch.full((1, I, C), 127, dtype=torch.int8)
+        sv = torch.full((I,), 2.0 ** 78)
+        sv[32:] = 2.0 ** -149
+        other = (x[:1].double() @ v[0].double().t()) * sv.double() * sx.double()[:, None]
+        turn = torch.arange(I) % 2 == 0
+        gates, ups = torch.where(turn[:, None], w, v), torch.where(turn[:, None], v, w)
+        scales = torch.cat([torch.where(turn, sw, sv), torch.where(turn, sv, sw)])
+        ep.expert_gated(p, lay, x.to(DEV), torch.cat([gates, ups], 1).to(DEV), y,
+                        w_scales=scales[None].to(DEV), **kw)
+    else:
+        ep.expert_linear(p, lay, x.to(DEV), w.to(DEV), y, w_scales=sw[None].to(DEV), **kw)
+    torch.cuda.synchronize()
+    want, got = (z * other)[low, :32], y.double().cpu()
+    assert (want.abs() > 2.0 ** -124).all()
+    assert ((got[low, :32] - want).abs() <= (HALF * (1 + HALF) + 20 * 2.0 ** -24) * want.abs()).all()
+    assert (got[~low, 32:] == 0).all() and (gated or (got[low, 32:] == 0).all())
+
+
 @pytest.mark.parametrize("mode", [N, L])
 def test_whole_layer_and_its_replays(mode):
     """layout -> dispatch -> gated -> quantize_rows -> linear -> combine in 8-bit integers,
