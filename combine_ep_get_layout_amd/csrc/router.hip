@@ -219,8 +219,9 @@ __device__ __forceinline__ void load_logits(const char* row, int first, int E, f
   }
 }
 
-// In fp32 the hardware's exponential and reciprocal, for choices and gradients: the
-// exponential's argument times log2 e is rounded to 2^-24 of itself, results below 2^-126 are 0.
+// In fp32 the hardware's exponential and reciprocal, for choices, gradients and the sum that
+// softmax weights which are not normalised are divided by: the exponential's argument times
+// log2 e is rounded to 2^-24 of itself, results below 2^-126 are 0.
 __device__ __forceinline__ float exponential(float v) {
   return __builtin_amdgcn_exp2f(v * 1.4426950408889634f);
 }
@@ -232,7 +233,8 @@ __device__ __forceinline__ float sigmoid_of(float v) {
   return (v < 0.0f ? z : 1.0f) * inverse(1.0f + z);
 }
 
-// for weights: each step rounded correctly, or to a unit in the last place
+// for weights, as expf and their quotients are: each step rounded correctly, or to a unit in the
+// last place
 __device__ __forceinline__ float sigmoid_exact(float v) {
   const float z = expf(v < 0.0f ? v : -v);
   return (v < 0.0f ? z : 1.0f) / (1.0f + z);
@@ -392,7 +394,10 @@ __device__ __forceinline__ float logit_at(const char* row, int e) {
                       : ((const float*)row)[e]);
 }
 
-// Writes a token's entries, entry k's expert (or -1) in its lane k.  most, total: softmax.
+// Writes a token's entries, entry k's expert (or -1) in its lane k.  most, total: softmax, as
+// softmax_sums has them, so that weights go by the logits alone and not by how the token was
+// chosen.  The sum is within 2^-18 of itself (score_error), which is as large an error of weights
+// that are not normalised; all others are within a few units in the last place.
 template <int LPT, bool BF16>
 __device__ __forceinline__ void store_entries(const RouteArgs& a, const char* row, int64_t t, int id,
                                               float most, float total) {
@@ -417,11 +422,12 @@ __device__ __forceinline__ void store_entries(const RouteArgs& a, const char* ro
   }
 }
 
-// A token chosen in 64 bits, by the whole wave; c: its choices in LDS.  Lane l has experts
+// A token chosen in 64 bits, by the whole wave; c: its choices in LDS, total32: its sum in fp32.  Lane l has experts
 // per l .. as above.  Few tokens come here (of 32,768 tens), but the last of them ends the
 // kernel: what counts is one token's latency.
 template <bool BF16>
-__device__ __forceinline__ void route_exactly(const RouteArgs& a, int64_t t, double* c) {
+__device__ __forceinline__ void route_exactly(const RouteArgs& a, int64_t t, float total32,
+                                              double* c) {
   const char* row = (const char*)a.logits + t * a.E * (BF16 ? 2 : 4);
   const int lane = lane_id(), per = (a.E + kWave - 1) / kWave;
   const int first = min(lane * per, a.E), end = min(first + per, a.E);
@@ -482,7 +488,7 @@ __device__ __forceinline__ void route_exactly(const RouteArgs& a, int64_t t, dou
     if (lane == 0) c[e] = (double)low_inf();
     wave_lds_sync();
   }
-  store_entries<64, BF16>(a, row, t, id, (float)most, (float)total);
+  store_entries<64, BF16>(a, row, t, id, (float)most, total32);
 }
 
 // A token's candidates, one in each of its 16 lanes: value (-inf: none) and expert.
@@ -586,8 +592,10 @@ __device__ __forceinline__ float score_error(const RouteArgs& a, float largest) 
 }
 
 // The first part of a wave's tokens in fp32; false for a token that has to be chosen again.
+// total: softmax, the sum that its weights are divided by
 template <int LPT, int PER, bool BF16>
-__device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t, Candidate* slots) {
+__device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t, Candidate* slots,
+                                           float& total) {
   const int at = lane_id() & (LPT - 1), first = at * a.per;
   const bool in = t < a.tokens;  // lanes without a token repeat the last one
   const int64_t token = in ? t : a.tokens - 1;
@@ -596,6 +604,7 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t, Candid
   load_logits<PER, BF16>(row, first, a.E, low_inf(), l, a.per);
   Choice<LPT, PER> choice(a);
   if (!a.sigmoid && (a.scored || !a.normalize)) choice.softmax_sums(l);
+  total = choice.total;
   const bool bad = token_bits<LPT>(__ballot(choice.fill(l, a.bias))) != 0;
   // two choices have to be this far apart, four (a group's sum of two) twice as far
   const float sure = a.scored ? 2.0f * score_error(a, choice.part) : 0.0f;
@@ -674,6 +683,7 @@ template <int LPT, int PER, bool BF16>
 __global__ __launch_bounds__(kRouteThreads, PER <= 16 ? 3 : 1) void route(RouteArgs a) {
   constexpr int kTokens = kRouteThreads / LPT, kWaveTokens = kWave / LPT;
   __shared__ Candidate slots[LPT == 16 ? kTokens : 1][16];
+  __shared__ float totals[kRouteThreads / kWave][kWave];  // of tokens that are chosen again
   extern __shared__ double choices[];  // where choices are scores: [waves][E]
   const int wave = uniform(threadIdx.x / kWave);
   const int64_t step = (int64_t)gridDim.x * kTokens;
@@ -684,16 +694,20 @@ __global__ __launch_bounds__(kRouteThreads, PER <= 16 ? 3 : 1) void route(RouteA
     uint64_t again = 0;
     const int64_t start = base;
     for (int r = 0; r < LPT && base < a.tokens; ++r, base += step) {
-      const bool sure = route_fast<LPT, PER, BF16>(a, base + lane_id() / LPT,
-                                                   slots[LPT == 16 ? threadIdx.x / LPT : 0]);
-      uint64_t at = __ballot(!sure && (lane_id() & (LPT - 1)) == 0);
+      float total;
+      const bool sure = route_fast<LPT, PER, BF16>(
+          a, base + lane_id() / LPT, slots[LPT == 16 ? threadIdx.x / LPT : 0], total);
+      const bool redo = !sure && (lane_id() & (LPT - 1)) == 0;
+      if (redo) totals[wave][r * kWaveTokens + lane_id() / LPT] = total;
+      uint64_t at = __ballot(redo);
       for (; at; at &= at - 1)
         again |= 1ull << (r * kWaveTokens + __builtin_ctzll(at) / LPT);
     }
+    wave_lds_sync();
     for (; again; again &= again - 1) {  // rarely
       const int bit = __builtin_ctzll(again);
       route_exactly<BF16>(a, start + (bit / kWaveTokens) * step + bit % kWaveTokens,
-                          choices + wave * a.E);
+                          totals[wave][bit], choices + wave * a.E);
     }
   }
 }

@@ -182,6 +182,30 @@ def test_values_that_are_no_numbers(score, bf16):
     check_route(1, 24, E, K, score, gen, l=l, bias=bias)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("E, K", [(64, 6), (128, 8), (256, 8), (512, 12)])
+def test_weights_do_not_depend_on_the_tokens_beside(E, K, bf16):
+    """Softmax weights that are not normalised are divided by a sum over all experts: the same
+    bits whichever way the token is chosen.  With logits equal at the border of the choice and
+    within it that goes by the other tokens of the wave, here by rows of one value."""
+    n = 160
+    gen = torch.Generator().manual_seed(52)
+    p, bias = ep.Problem(1, n, 128, E, K), torch.zeros(E)
+    l = logits_for(gen, n, E, bf16)
+    order = torch.argsort(l.float(), dim=1, descending=True)
+    at = torch.arange(n)
+    l[at[1::2], order[1::2, K]] = l[at[1::2], order[1::2, K - 1]]
+    l[at[::2], order[::2, 1]] = l[at[::2], order[::2, 0]]
+    kw = dict(score=ep.SCORE_SOFTMAX, normalize=False)
+    idx, w, _ = run_route(p, l, bias, **kw)
+    flat = l.clone()
+    flat[::4] = 0.5
+    idx2, w2, _ = run_route(p, flat, bias, **kw)
+    other = np.arange(n) % 4 != 0
+    assert (idx[other] == idx2[other]).all()
+    assert (w[other] == w2[other]).all()
+
+
 def test_no_tokens_and_no_error_word():
     p = ep.Problem(2, 0, 128, 8, 2)
     e = lambda *s, **k: torch.empty(s, device=DEV, **k)  # noqa: E731
