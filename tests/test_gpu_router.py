@@ -350,6 +350,40 @@ def test_many_tokens_past_a_grid():
     assert (np.abs(got.cpu().double().numpy() - full) <= lim).all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_equal_choices_take_no_longer(score):
+    """Tokens of many equal logits under a bias of zeros (as at the start of training with a
+    balancing bias), against logits that are all different: equal choices are told apart by their
+    index, without 64 bits.  Chosen again one by one under softmax they took 4.9 times as long;
+    three times is allowed."""
+    n, E, K = 65536, 256, 8
+    p = ep.Problem(1, n, 128, E, K)
+    gen = torch.Generator().manual_seed(53)
+    far = torch.stack([torch.randperm(E, generator=gen) for _ in range(64)]).float() / 32 - 4
+    same = far.clone()
+    same[:, ::2] = same[:, 1::2]  # each twice
+    bias = torch.zeros(E, device=DEV)
+    idx = torch.empty((n, K), dtype=torch.int32, device=DEV)
+    w = torch.empty((n, K), device=DEV)
+    times = []
+    for l in far, same:
+        l = l.repeat(n // 64, 1).to(DEV)
+        call = ep.prepare(ep.route, p, l, idx, w, score=SCORES[score], bias=bias)
+        call()
+        each = []
+        for _ in range(5):
+            a, b = torch.cuda.Event(True), torch.cuda.Event(True)
+            a.record()
+            call()
+            b.record()
+            torch.cuda.synchronize()
+            each.append(a.elapsed_time(b))
+        times.append(sorted(each)[2])
+        want = torch.sort(l[:64], dim=1, descending=True, stable=True).indices[:, :K]
+        assert torch.equal(idx.view(-1, 64, K), want.to(torch.int32).expand(n // 64, 64, K))
+    assert times[1] <= 3 * times[0], times
+
+
 def test_replayed_in_a_graph_on_another_stream():
     """Both passes captured together and replayed with fresh logits."""
     R, T, E, K = 2, 150, 64, 4
