@@ -122,6 +122,21 @@ MANY = [
 ]
 
 
+# few entries of experts with many channels, whose strips waves take alone, several of them one
+# after the other; slots of 8 entries in the second product; 8 to 32 entries an expert with rows
+# in common and many channels to give
+FORMS = [
+    (1, 3, 24, 8, 72, 1032, 0.0),
+    (1, 3, 24, 8, 1032, 1096, 0.0),
+    (1, 2, 16, 8, 200, 4136, 0.0),
+    (1, 1, 8, 8, 136, 8200, 0.1),
+    (1, 9, 8, 4, 264, 72, 0.0),
+    (1, 20, 5, 1, 136, 1032, 0.1),
+    (1, 128, 16, 2, 4096, 136, 0.0),
+    (1, 100, 12, 3, 2824, 200, 0.2),
+]
+
+
 def sized(shape, kind):
     """The shape with channels that the type has: 128 in FP8, 16 in 8-bit integers."""
     step = {"bf16": 8, "fp8": 128, "int8": 16}[kind]
@@ -154,6 +169,25 @@ def test_layer(shape, kind):
             y = (torch.nn.functional.silu(z[:, :I]) * z[:, I:]) @ m.v2[e].t()
             full.index_add_(0, t, y * m.wt[t, k].double()[:, None])
         assert relative([out], [full]) <= 2 * (1 / 3) ** 0.5 * HALF
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape", FORMS, ids=lambda s: "-".join(map(str, s)))
+def test_every_form(shape, kind):
+    test_layer(shape, kind)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_strips_of_a_wave_alone_with_several_slots(kind):
+    """Two experts have all entries, more than a slot holds, of a size whose strips waves take
+    alone: they go over a strip's weights again for the rest of the entries."""
+    R, T, E, K, H, I, _ = sized((1, 24, 24, 1, 200, 1032, 0.0), kind)
+    topk = torch.tensor([3, 5, 3, 3, 5, 3] * 4, dtype=torch.int32)[:, None]
+    m = Made(R, T, E, K, H, I, kind, topk)
+    out = m.call()
+    torch.cuda.synchronize()
+    m.check(out)
+    assert int(m.err.item()) == 0
 
 
 @pytest.mark.parametrize("kind", KINDS)
