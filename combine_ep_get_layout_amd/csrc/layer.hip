@@ -367,7 +367,6 @@ __device__ __forceinline__ float rest_of(float h, float rounded) {
 
 // ---- gated block -------------------------------------------------------------------
 
-constexpr int kUpWaves = 4;    // of a workgroup
 constexpr int kUpStride = 20;  // floats of a column of partial sums, 16 and a gap
 
 // The stream's next loads: strips of 8 gates and ups from channel n0 on, and the unit's rows
@@ -780,18 +779,13 @@ __global__ __launch_bounds__(kWave * 4) void many_sum(LayerArgs a) {
 
 // ---- launches ------------------------------------------------------------------------
 
-// D, TD: slots of the ring where a wave has its own strips, and where four share them
-template <int KIND, int CT, int NB, int D, int TD>
+// WK: waves that a strip's lines are dealt to
+template <int KIND, int CT, int NB, int D, int WK>
 static void launch_gated(const LayerArgs& a, hipStream_t st) {
-  const int64_t units = (int64_t)std::min(a.E, a.entries) * ((a.I + 8 * CT - 1) / (8 * CT));
-  const int64_t room = 3 * kCus;  // workgroups at once
-  if (units < room * kUpWaves)
-    hipLaunchKernelGGL((layer_gated<KIND, CT, NB, TD, kUpWaves>),
-                       dim3((unsigned)std::min<int64_t>(units, 4 * kCus)), dim3(kUpWaves * kWave),
-                       0, st, a);
-  else
-    hipLaunchKernelGGL((layer_gated<KIND, CT, NB, D, 1>), dim3((unsigned)room),
-                       dim3(kUpWaves * kWave), 0, st, a);
+  const int64_t strips = (int64_t)std::min(a.E, a.entries) * ((a.I + 8 * CT - 1) / (8 * CT));
+  const int64_t blocks = WK == 1 ? kUpRoom : std::min<int64_t>(strips, 4 * kCus);
+  hipLaunchKernelGGL((layer_gated<KIND, CT, NB, D, WK>), dim3((unsigned)blocks),
+                     dim3(kUpWaves * kWave), 0, st, a);
 }
 
 template <int KIND, int NB, int D, int WAVES>
@@ -800,38 +794,29 @@ static void launch_down(const LayerArgs& a, hipStream_t st) {
                      0, st, a);
 }
 
-// How many entries a slot has room for goes by how many an expert has on average: a wave
-// reads its weights once for each slot full of them.  us (gated and down together with one row
-// of h an entry, bf16 4096 -> 1408, 16 experts with 16 / 32 / 64 entries each): slots of 16
-// entries 151 / 308 / 590, of 64 with two strips 160 / 190 / 283.  In 8 bits a slot's rows are
-// as many bytes as its weights, or more, so two strips share them: 32 experts with 4 / 16
-// entries 140 / 255 with one strip, 112 / 220 with two.
+// In 8 bits a slot's rows are as many bytes as its weights, or more, so two strips share them.
 template <int KIND>
-static void choose_gated(const LayerArgs& a, int experts, hipStream_t st) {
+static void choose_gated(const LayerArgs& a, hipStream_t st) {
   constexpr bool kBytes = KIND != EP_WEIGHTS_BF16;
-  if (2 * a.entries <= 3 * experts * (kBytes ? 2 : 4)) {  // 4 entries a slot, in bf16 8
-    launch_gated<KIND, 1, 1, 3, 3>(a, st);
-  } else if (a.entries <= 16 * experts) {  // 16
-    constexpr int NB = kBytes ? 4 : 2, D = kBytes ? 2 : 3;
-    launch_gated<KIND, kBytes ? 2 : 1, NB, D, D>(a, st);
-  } else {  // 32, in bf16 64
-    launch_gated<KIND, 2, 8, 3, 2>(a, st);
+  switch (choose_layer_gated(kBytes, a.entries, a.E, a.I)) {
+    case kGatedFew: return launch_gated<KIND, 1, 1, 3, 1>(a, st);
+    case kGatedFewSplit: return launch_gated<KIND, 1, 1, 3, kUpWaves>(a, st);
+    case kGatedSome:
+      return launch_gated<KIND, kBytes ? 2 : 1, kBytes ? 4 : 2, kBytes ? 2 : 3, kUpWaves>(a, st);
+    case kGatedMost: return launch_gated<KIND, 2, 8, 2, kUpWaves>(a, st);
   }
 }
 
-// An entry has two rows here, a workgroup as many waves as the LDS has rings for, up to 8 (4
-// entries an expert, bf16 4096 -> 1408, 16 experts, the whole layer: 102 us, with 4 waves 108).
+// An entry has two rows here, a workgroup as many waves as the LDS has rings for, up to 8.
 template <int KIND>
-static void choose_down(const LayerArgs& a, int experts, hipStream_t st) {
+static void choose_down(const LayerArgs& a, hipStream_t st) {
   constexpr bool kBytes = KIND != EP_WEIGHTS_BF16;
-  if (a.entries <= 3 * experts) {  // 4 entries a slot
-    launch_down<KIND, kBytes ? 2 : 1, 3, 8>(a, st);
-  } else if (a.entries <= 5 * experts) {  // 8
-    launch_down<KIND, kBytes ? 4 : 2, kBytes ? 2 : 3, 8>(a, st);
-  } else if (kBytes || a.entries <= 12 * experts) {  // 16
-    launch_down<KIND, kBytes ? 8 : 4, kBytes ? 2 : 3, 6>(a, st);
-  } else {  // 32
-    launch_down<KIND, 8, 2, 6>(a, st);
+  switch (choose_layer_down(kBytes, a.entries, a.E)) {
+    case kDown4: return launch_down<KIND, kBytes ? 2 : 1, 3, 8>(a, st);
+    case kDown8: return launch_down<KIND, kBytes ? 4 : 2, kBytes ? 2 : 3, 8>(a, st);
+    case kDown16: return launch_down<KIND, kBytes ? 8 : 4, kBytes ? 2 : 3, 6>(a, st);
+    case kDown32:
+      if constexpr (!kBytes) return launch_down<KIND, 8, 2, 6>(a, st);
   }
 }
 
@@ -847,27 +832,16 @@ static void launch_many(const LayerArgs& a, hipStream_t st) {
   else hipLaunchKernelGGL((many_down<KIND, CT, NB, D, ONCE>), grid, threads, 0, st, a);
 }
 
-// us of the layer with tiles of 16 rows (32 in bf16) / of 64: 256 experts with 2 entries in
-// FP8 (7168 -> 2048) 1480 / 1875, 128 with 4 in bf16 (2048 -> 768) 200 / 227, 32 with 12 in FP8
-// (4096 -> 1408) 144 / 132.  One strip a wave / two, where there are few tiles: 256 entries of
-// one expert (bf16 4096 -> 1408) 53 / 59, 24 of 8 (bf16 2280 -> 2952) 89 / 124.  Weights past
-// the caches / through them: 16 experts with 16 / 64 entries (bf16 4096 -> 1408) 119 / 128 and
-// 211 / 200.
 template <int KIND, bool GATED>
 static void choose_many(const LayerArgs& a, hipStream_t st) {
   constexpr bool kBytes = KIND != EP_WEIGHTS_BF16;
   constexpr int NB = kBytes ? 16 : 8;
-  const int64_t tiles = GATED ? layer_tiles(a.entries, a.E, a.I, 64)
-                              : layer_tiles(2 * a.entries, a.E, a.H, 128);
-  if (a.entries <= 8 * a.E) {
-    if (tiles < 2 * kCus) launch_many<KIND, GATED, 1, 4, 3, true>(a, st);
-    else launch_many<KIND, GATED, 2, 4, 2, true>(a, st);
-  } else if (tiles < kCus) {
-    launch_many<KIND, GATED, 1, NB, kBytes ? 3 : 4, false>(a, st);
-  } else if (a.entries <= 32 * a.E) {
-    launch_many<KIND, GATED, 2, NB, kBytes ? 2 : 3, true>(a, st);
-  } else {
-    launch_many<KIND, GATED, 2, NB, kBytes ? 2 : 3, false>(a, st);
+  switch (choose_layer_many(GATED, a.entries, a.E, GATED ? a.I : a.H)) {
+    case kManyFew1: return launch_many<KIND, GATED, 1, 4, 3, true>(a, st);
+    case kManyFew2: return launch_many<KIND, GATED, 2, 4, 2, true>(a, st);
+    case kManyRows1: return launch_many<KIND, GATED, 1, NB, kBytes ? 3 : 4, false>(a, st);
+    case kManyRows2Once: return launch_many<KIND, GATED, 2, NB, kBytes ? 2 : 3, true>(a, st);
+    case kManyRows2: return launch_many<KIND, GATED, 2, NB, kBytes ? 2 : 3, false>(a, st);
   }
 }
 
@@ -881,9 +855,8 @@ static void choose(const LayerArgs& a, hipStream_t st) {
                        dim3(4 * kWave), 0, st, a);
     return;
   }
-  const int experts = std::min(a.E, a.entries);
-  choose_gated<KIND>(a, experts, st);
-  choose_down<KIND>(a, experts, st);
+  choose_gated<KIND>(a, st);
+  choose_down<KIND>(a, st);
 }
 
 hipError_t launch_layer(const LayerArgs& a, hipStream_t st) {

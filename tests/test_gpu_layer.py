@@ -124,7 +124,8 @@ MANY = [
 
 # few entries of experts with many channels, whose strips waves take alone, several of them one
 # after the other; slots of 8 entries in the second product; 8 to 32 entries an expert with rows
-# in common and many channels to give
+# in common and many channels to give (tests/test_layer_choice.py asks the library's own choice
+# which kernels all these lists run)
 FORMS = [
     (1, 3, 24, 8, 72, 1032, 0.0),
     (1, 3, 24, 8, 1032, 1096, 0.0),
