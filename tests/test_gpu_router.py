@@ -350,6 +350,34 @@ def test_many_tokens_past_a_grid():
     assert (np.abs(got.cpu().double().numpy() - full) <= lim).all()
 
 
+# a round of workgroups takes 32,768 tokens in 16 lanes each, 8,192 in 64; after 16 rounds (64)
+# the tokens of those are chosen again
+@pytest.mark.parametrize("n, E, K", [(33001, 16, 2), (16 * 32768 + 333, 16, 2),
+                                     (8199, 32, 16), (3 * 8192 + 77, 32, 16)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_tokens_chosen_again_past_a_grid(n, E, K, score):
+    """Every token, of several rounds, has choices that fp32 does not tell apart, within the
+    chosen and at their border: logits next to each other under a bias of zeros, in whose order
+    the scores are."""
+    p = ep.Problem(1, n, 128, E, K)
+    gen = torch.Generator().manual_seed(54)
+    l = torch.randn((n, E), generator=gen)
+    order = torch.argsort(l, dim=1, descending=True)
+    for above, below in (0, 1), (K - 1, K):
+        top = l.gather(1, order[:, above:above + 1])
+        l.scatter_(1, order[:, below:below + 1], torch.nextafter(top, torch.tensor(-INF)))
+    idx, w, err = run_route(p, l, torch.zeros(E), score=SCORES[score], normalize=False)
+    assert err == 0
+    want = torch.sort(l, dim=1, descending=True, stable=True)
+    # sigmoids of distinct logits near 1 may be equal in 64 bits too, not these
+    assert torch.equal(torch.from_numpy(idx), want.indices[:, :K].to(torch.int32))
+    s = (torch.softmax if score == "softmax" else lambda v, _: torch.sigmoid(v))(l.double(), 1)
+    ww = s.gather(1, want.indices[:, :K])
+    far = l.max(1, keepdim=True).values - l.min(1, keepdim=True).values
+    off = (torch.from_numpy(w) - ww).abs()
+    assert (off <= (64 + far) * 2.0 ** -23 * ww).all(), float((off / ww).max())
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_equal_choices_take_no_longer(score):
     """Tokens of many equal logits under a bias of zeros (as at the start of training with a
