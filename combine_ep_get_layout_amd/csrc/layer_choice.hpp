@@ -44,19 +44,27 @@ enum LayerGated {
 };
 
 // How many entries a slot has room for goes by how many an expert has on average: a wave reads
-// its weights once for each slot full of them.  (bytes: weights of 8 bits.)
+// its weights once for each slot full of them, and multiplies the whole slot.  (bytes: weights
+// of 8 bits.)  us of the layer, few / some / most: in bf16 24 entries of 8 experts (4096 -> 896)
+// 41 / 41 / 50, 64 of them 53 / 45 / 53, 64 of 4 (4096 -> 1408) 71 / 58 / 58, of 2 60 / 43 / 34;
+// in 8-bit integers 16, 24 and 64 of 8 (4096 -> 896) 26 / 26 / 36, 34 / 28 / 38 and 50 / 33 / 41,
+// 64 of 4 (4096 -> 1408) 75 / 52 / 49, of 2 81 / 41 / 35; FP8 as the integers, a tenth less.
 inline LayerGated choose_layer_gated(bool bytes, int64_t entries, int experts, int inner) {
   const int64_t hit = std::min<int64_t>(experts, entries);
-  if (2 * entries <= 3 * hit * (bytes ? 2 : 4))
+  if (entries <= hit * (bytes ? 2 : 6))
     return layer_strips(entries, experts, inner) < kUpRoom * kUpWaves ? kGatedFewSplit : kGatedFew;
   return entries <= 16 * hit ? kGatedSome : kGatedMost;
 }
 
 enum LayerDown { kDown4, kDown8, kDown16, kDown32 };  // entries of a slot
 
+// us of the layer, slots of 4 / 8 / 16 / 32 (4096 -> 896): in bf16 12, 16, 40 and 64 entries of 8
+// experts 32 / 32 / 35 / 39, 36 / 34 / 37 / 41, 46 / 41 / 43 / 49 and 53 / 46 / 45 / 50, 64 of 4
+// (4096 -> 1408) 72 / 59 / 61 / 58; in 8-bit integers, up to 16, 12, 16, 40 and 64 of 8
+// 24 / 24 / 27, 26 / 25 / 28, 32 / 29 / 32 and 37 / 33 / 33, 64 of 2 (4096 -> 1408) 47 / 37 / 35.
 inline LayerDown choose_layer_down(bool bytes, int64_t entries, int experts) {
   const int64_t hit = std::min<int64_t>(experts, entries);
-  if (entries <= 3 * hit) return kDown4;
+  if (entries < 2 * hit) return kDown4;
   if (entries <= 5 * hit) return kDown8;
   return bytes || entries <= 12 * hit ? kDown16 : kDown32;
 }
