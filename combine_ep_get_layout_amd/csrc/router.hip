@@ -145,7 +145,7 @@ __device__ __forceinline__ int first_lane(uint64_t bits) {
   return LPT == 64 ? uniform(lane) : lane;
 }
 
-// v of the token's lane `from`
+// v of the token's lane `from`, which is the same in all lanes of the token
 template <int LPT>
 __device__ __forceinline__ int of_lane(int v, int from) {
   if (LPT == 64) return __builtin_amdgcn_readlane(v, from);
@@ -161,6 +161,12 @@ __device__ __forceinline__ double of_lane(double v, int from) {
   const uint32_t lo = (uint32_t)of_lane<LPT>((int)(uint32_t)bits, from);
   const uint32_t hi = (uint32_t)of_lane<LPT>((int)(uint32_t)(bits >> 32), from);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// v of the lane after this one; of the token's last lane whatever
+__device__ __forceinline__ float of_next(float v) {
+  return __int_as_float(
+      __builtin_amdgcn_ds_bpermute(((lane_id() + 1) & (kWave - 1)) << 2, __float_as_int(v)));
 }
 
 // ---- values ---------------------------------------------------------------------
@@ -678,9 +684,7 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t, Candid
       // and the first that is left out that says nothing of the others left out.
       const float mine = id >= 0 ? logit_at<BF16>(row, id) : low_inf();
       const float own = id >= 0 ? a.bias[id] : 0.0f;
-      const int next = (at + 1) & (LPT - 1);
-      const float below = of_lane<LPT>(value, next), l_below = of_lane<LPT>(mine, next);
-      const float b_below = of_lane<LPT>(own, next);
+      const float below = of_next(value), l_below = of_next(mine), b_below = of_next(own);
       close |= at < a.K && at + 1 < LPT && id >= 0 && below > low_inf() &&
                !(value - below > sure + 0x1p-23f * (fabsf(value) + fabsf(below))) &&
                !(at + 1 < a.K && mine == l_below && own == b_below);
