@@ -13,8 +13,8 @@
 // bound by reading the weights: 256 experts x 32 rows in FP8, 7168 -> 2 x 2048, 1.29
 // ms (5.9 TB/s); 2048 -> 7168, 0.74 ms (5.2 TB/s, 16 stages a tile).  Eight rows
 // of eight experts, 2048 -> 2 x 768, take 14 us, half of it latency.  In 8-bit integers the
-// first takes 3.50 ms (2.2 POP/s, the cores busy 68% of the time), the second 2.60 (1.48, 37%),
-// the gated decode step 1.22 ms (6.2 TB/s): its weights pass the caches.
+// first takes 3.6 to 3.7 ms (2.1 POP/s, the cores busy 68% of the time), the second 2.7 (1.4,
+// 37%), the gated decode step 1.24 ms (6.05 TB/s): its weights pass the caches.
 #include <algorithm>
 #include <type_traits>
 

@@ -14,10 +14,10 @@
 // LPT lanes take a token, PER consecutive experts each, so that the first lane with the
 // largest value also has its lowest index.  Choices are compared in fp32, and where two that
 // decide are nearer to each other than that tells, again in 64 bits, a token at a time: all
-// in 64 bits took 61 us for 32,768 tokens over 256 experts (8 groups, bias).  These take 29
-// us now, 1.2 TB/s, bound by vector instructions (82% of what the busy compute units can
+// in 64 bits took 61 us for 32,768 tokens over 256 experts (8 groups, bias).  These take 28
+// to 31 us now, 1.2 TB/s, bound by vector instructions (82% of what the busy compute units can
 // issue); one token over 64 experts 4.4 us, latency.  The gradient, softmax over 128 experts,
-// 131,072 tokens in bf16: 16 to 18 us, 4.3 to 4.7 TB/s.
+// 131,072 tokens in bf16: 16 to 18 us, 4.3 to 4.6 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -403,7 +403,8 @@ __device__ __forceinline__ float logit_at(const char* row, int e) {
 // Writes a token's entries, entry k's expert (or -1) in its lane k.  most, total: softmax, as
 // softmax_sums has them, so that weights go by the logits alone and not by how the token was
 // chosen.  The sum is within 2^-18 of itself (score_error), which is as large an error of weights
-// that are not normalised; all others are within a few units in the last place.
+// that are not normalised; all others are within a few units in the last place, and half of one
+// for each unit that the logit is below the largest (its difference is rounded).
 template <int LPT, bool BF16>
 __device__ __forceinline__ void store_entries(const RouteArgs& a, const char* row, int64_t t, int id,
                                               float most, float total) {
@@ -430,7 +431,9 @@ __device__ __forceinline__ void store_entries(const RouteArgs& a, const char* ro
 
 // A token chosen in 64 bits, by the whole wave; c: its choices in LDS, total32: its sum in fp32.  Lane l has experts
 // per l .. as above.  Few tokens come here (of 32,768 tens), but the last of them ends the
-// kernel: what counts is one token's latency.
+// kernel: what counts is one token's latency.  More do where equal choices stand at the border
+// of a choice in 64 lanes (32,768 tokens over 1,024 experts in bf16, softmax: 194 us under a random
+// bias, 328 under one of zeros).
 template <bool BF16>
 __device__ __forceinline__ void route_exactly(const RouteArgs& a, int64_t t, float total32,
                                               double* c) {
@@ -863,7 +866,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_grad(RouteGradArgs a) {
 
 // Up to 512 experts 16 lanes take a token's choice, so that a wave has four of them in a
 // butterfly's steps; they hold 16 candidates (32,768 tokens over 256 / 384 / 512 experts: 64
-// lanes 57 / 141 / 230 us, 16 lanes 30 / 42 / 55).  The gradient's 64 from 257 on (384: 18 us,
+// lanes 79 / 65 / 84 us, 16 lanes 30 / 42 / 55).  The gradient's 64 from 257 on (384: 18 us,
 // with 16 lanes 24).
 constexpr int64_t kRouteBlocks = 8 * kCus;
 

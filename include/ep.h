@@ -465,10 +465,12 @@ typedef struct ep_router {
  *   topk_idx[k] = the k-th largest choice of their experts, ties (of groups as of
  *   experts) to the lowest index; topk_weights[k] = scale * s / (sum of the chosen s),
  *   or scale * s.
- * Choices are compared as their values in 64 bits; weights are computed in fp32.  An expert
+ * Choices are compared as their values in 64 bits; weights are computed in fp32 from the
+ * token's logits alone (softmax without normalising to 2^-18 of themselves).  An expert
  * whose logit, or bias, is -inf is not to be had; where fewer than K are left the rest of the
- * entries are -1 with weight 0 (as layout takes them).  A token with a NaN (logit, or bias),
- * or with a logit of +inf under softmax, gets -1 throughout and sets EP_DEVERR_LOGITS.
+ * entries are -1 with weight 0 (as layout takes them).
+ * A token with a NaN (a logit, or the bias of an expert whose logit is not -inf), or with a
+ * logit of +inf under softmax, gets -1 throughout and sets EP_DEVERR_LOGITS.
  * logits: [R][T][E], bias: [E] fp32 or NULL, both 16-byte aligned.  topk_idx: [R][T][K].
  * topk_weights: [R][T][K].  err: [1], bits are OR-ed into it, or NULL.  p->mode, p->quant and
  * p->hidden are not used. */
