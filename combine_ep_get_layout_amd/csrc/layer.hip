@@ -10,10 +10,10 @@
 // tokens over 256 experts (FP8, 7168 -> 2048) take 1.45 to 1.48 ms, 6.7 TB/s, in 8-bit integers
 // 1.44; 32 over 16 experts (bf16, 4096 -> 1408) 97 us, 5.6 TB/s; one token over 8 (bf16, 2048 ->
 // 768) 21.9 us, of which two launches' start and end are 7.8 and the second product 10 to 11: a
-// workgroup has 16 channels of the result there, so with fewer than 4096 some units are idle.  A wave multiplies strips of 16 rows of weights with up to
-// 64 rows of one expert's entries.  It streams both through a ring in LDS (of its own, or with
-// the rows in common to four waves), by asynchronous loads that never stop: towards the end of
-// a strip they are the next one's.  Weights come as whole 128-byte lines of eight rows a load:
+// workgroup has 16 channels of the result there, so with fewer than 4096 some units are idle.
+// A wave multiplies strips of 16 rows of weights with up to 64 rows of one expert's entries.  It
+// streams both through a ring in LDS (of its own, or with the rows in common to four waves), by
+// asynchronous loads that never stop: towards the end of a strip they are the next one's.  Weights come as whole 128-byte lines of eight rows a load:
 // straight into the registers of the matrix instructions, which take 16 rows x 64 bytes, they
 // came at 4.1 TB/s instead.  Rows stay bf16 whatever the weights' type: e4m3 and 8-bit codes
 // are converted (both fit bf16 exactly), and their scales are applied to the fp32 sums.

@@ -429,11 +429,11 @@ __device__ __forceinline__ void store_entries(const RouteArgs& a, const char* ro
   }
 }
 
-// A token chosen in 64 bits, by the whole wave; c: its choices in LDS, total32: its sum in fp32.  Lane l has experts
-// per l .. as above.  Few tokens come here (of 32,768 tens), but the last of them ends the
-// kernel: what counts is one token's latency.  More do where equal choices stand at the border
-// of a choice in 64 lanes (32,768 tokens over 1,024 experts in bf16, softmax: 194 us under a random
-// bias, 328 under one of zeros).
+// A token chosen in 64 bits, by the whole wave; c: its choices in LDS, total32: its sum in
+// fp32.  Lane l has experts per l .. as above.  Few tokens come here (of 32,768 tens), but the
+// last of them ends the kernel: what counts is one token's latency.  More do where equal choices
+// stand at the border of a choice in 64 lanes (32,768 tokens over 1,024 experts in bf16, softmax:
+// 194 us under a random bias, 328 under one of zeros).
 template <bool BF16>
 __device__ __forceinline__ void route_exactly(const RouteArgs& a, int64_t t, float total32,
                                               double* c) {

@@ -1,7 +1,8 @@
 // The layer's choice of kernels.  Prints for each call on standard input, one a line,
 //   bytes entries E H I
-// the kernels that it is launched with; with an argument instead those that any call can take:
-//   own <gated> <down>  or  many <gated> <down>, after the weights' size (1: 8 bits)
+// the two that its products are launched with, a line each:
+//   bytes gated|down|many_gated|many_down form        (bytes 1: weights of 8 bits)
+// and with an argument instead those that any call can take.
 #include <stdio.h>
 
 #include <set>
